@@ -1,0 +1,91 @@
+// FP32 -> E4M3 for values that a kernel computes itself (a weighted row, an activation, a
+// gradient), and E4M3 -> FP32.  Same definition as the BF16 quantizer:
+//   s = fl32(amax / 448), 1 if that is 0;  q = E4M3_rn_satfinite(fl32(x / s)).
+// amax is an FP32 maximum here, so s may be any FP32; with amax below 448 times the least
+// subnormal the quotient amax / 448 rounds to 0 and s = 1 (every code is then 0).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "quant_e4m3.cuh"
+
+namespace dg {
+
+__device__ __forceinline__ BlockScale block_scale_f32(float amax) {
+    BlockScale b;
+    const float q = __fdiv_rn(amax, 448.0f);
+    b.s = (q == 0.0f) ? 1.0f : q;
+    const float r = __frcp_rn(b.s);
+    b.fast_ok = isfinite(r);
+    const float rlo = __fmul_rn(r, 1.0f - 0x1p-21f), rhi = __fmul_rn(r, 1.0f + 0x1p-21f);
+    b.rlo2 = make_float2(rlo, rlo);
+    b.rhi2 = make_float2(rhi, rhi);
+    return b;
+}
+
+// quantize8 (quant_e4m3.cuh) for eight FP32 values: the bracket's proof takes any FP32 x.
+__device__ __forceinline__ uint2 quantize8_f32(const float2 (&x)[4], const BlockScale &b) {
+    float2 lo[4], hi[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        lo[j] = __fmul2_rn(x[j], b.rlo2);
+        hi[j] = __fmul2_rn(x[j], b.rhi2);
+    }
+    uint2 out;
+    out.x = e4m3x4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
+    out.y = e4m3x4(hi[2].x, hi[2].y, hi[3].x, hi[3].y);
+    const uint32_t lx = e4m3x4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
+    const uint32_t ly = e4m3x4(lo[2].x, lo[2].y, lo[3].x, lo[3].y);
+    if (__builtin_expect(((out.x ^ lx) | (out.y ^ ly)) != 0u || !b.fast_ok, 0)) {
+        float2 y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = make_float2(__fdiv_rn(x[j].x, b.s), __fdiv_rn(x[j].y, b.s));
+        out.x = e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y);
+        out.y = e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y);
+    }
+    return out;
+}
+
+// Four E4M3 codes (lowest byte first) as FP32, exact: every E4M3 value is an FP16 value.
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t q, float2 &lo, float2 &hi) {
+    uint32_t a, b;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(q));
+    lo = __half22float2(*reinterpret_cast<__half2 *>(&a));
+    hi = __half22float2(*reinterpret_cast<__half2 *>(&b));
+}
+
+// Eight BF16 of a 16-byte group as FP32.
+__device__ __forceinline__ void bf16x8_to_f32(uint4 v, float2 (&x)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        x[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+}
+
+// |x| folded into an FP32 magnitude kept as bits: the order of non-negative FP32 is that of
+// their bits, and a NaN is above infinity, so a NaN in a block reaches its scale.
+__device__ __forceinline__ uint32_t amax_fold_f32(uint32_t m, float2 x) {
+    m = max(m, __float_as_uint(x.x) & 0x7FFFFFFFu);
+    return max(m, __float_as_uint(x.y) & 0x7FFFFFFFu);
+}
+
+// The maximum of `v` over the CTA's warps.  red: one word per warp, not in use by an
+// earlier call that some thread may still read.
+template <int WARPS>
+__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t *red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    if ((threadIdx.x & 31u) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    uint32_t m = red[0];
+#pragma unroll
+    for (int i = 1; i < WARPS; ++i) m = max(m, red[i]);
+    return m;
+}
+
+}  // namespace dg

@@ -280,6 +280,214 @@ dg_status_t dg_fp8_gemm_1x128_select(const uint8_t *A, const float *sA_t,
                                      int64_t M, int64_t N, int64_t K, dg_kernel_t kernel,
                                      cudaStream_t stream);
 
+/*
+ * ---------------------------------------------------------------- expert layer
+ * What an MoE layer needs around the grouped products, and its backward pass.  A step of
+ * training, T tokens with k experts each, hidden size H, expert width F:
+ *
+ *   forward   dg_moe_sort                          topk_ids -> group_offsets, row maps
+ *             dg_moe_dispatch_quantize             x -> XQ, sX
+ *             dg_fp8_grouped_gemm_contiguous       XQ, W1 -> h = [gate | up]
+ *             dg_swiglu_quantize                   h -> AQ, sA and the checkpoint H8, sH
+ *             dg_fp8_grouped_gemm_contiguous       AQ, W2 -> y
+ *             dg_moe_combine                       y, weights -> out
+ *   backward  dg_moe_combine_backward              dout, y -> dweights
+ *             dg_moe_dispatch_quantize (weights)   dout -> dYQ, sdY
+ *             dg_fp8_grouped_wgrad_contiguous      dYQ, AQ -> dW2
+ *             dg_fp8_grouped_dgrad_contiguous      dYQ, W2 -> dA
+ *             dg_swiglu_quantize_backward          H8, dA -> dHQ, sdH
+ *             dg_fp8_grouped_wgrad_contiguous      dHQ, XQ -> dW1
+ *             dg_fp8_grouped_dgrad_contiguous      dHQ, W1 -> dx rows
+ *             dg_moe_combine (no weights)          dx rows -> dx
+ *
+ * Kept from forward to backward: codes and scales only (XQ, AQ, H8), the row maps and y.
+ * The masked forms serve decoding, where only device counts say how many rows each expert
+ * has.  All calls follow the conventions at the top of this file; inputs and outputs of a
+ * call must not overlap.
+ */
+
+/*
+ * Tokens sorted by expert (nxmr.cn/news/132300 §2.2: experts stored contiguously by
+ * expert id).  Slot s = t * k + j sends token t to expert topk_ids[t][j]; an id
+ * outside [0, G) drops the slot.  An expert's rows hold its slots in ascending
+ * order and start at a multiple of 128; a token may name an expert twice.
+ *
+ * topk_ids      : [T][k] int32, or int64 when ids_64bit is not 0; aligned to its type.
+ * group_offsets : int32 [G+1] out, as dg_fp8_grouped_gemm_contiguous reads it.
+ * row_of_slot   : int32 [T][k] out, the slot's row, -1 when dropped.
+ * slot_of_row   : int32 [M_total_capacity] out, the row's slot, -1 for padding rows
+ *                 and every row at or past group_offsets[G].
+ * k >= 1, T * k <= 2^30, 1 <= G <= 1024; M_total_capacity a multiple of 128 that
+ * holds the worst case: at least (S + 127 min(G, S)) / 128 * 128 for S = T * k
+ * slots.  T == 0 writes empty groups.
+ */
+dg_status_t dg_moe_sort(const void *topk_ids, int ids_64bit, int64_t T, int k, int G,
+                        int32_t *group_offsets, int32_t *row_of_slot, int32_t *slot_of_row,
+                        int64_t M_total_capacity, cudaStream_t stream);
+
+/*
+ * dg_moe_sort into the masked layout: expert g's slots take rows g * M_max, ... in
+ * ascending order; those past M_max are dropped (row -1).
+ *
+ * masked_m    : int32 [G] out, min(slots of the expert, M_max).
+ * row_of_slot : int32 [T][k] out.   slot_of_row : int32 [G * M_max] out, -1 past a count.
+ * M_max >= 0, G * M_max < 2^31; the rest as in dg_moe_sort.
+ */
+dg_status_t dg_moe_sort_masked(const void *topk_ids, int ids_64bit, int64_t T, int k, int G,
+                               int32_t *masked_m, int32_t *row_of_slot, int32_t *slot_of_row,
+                               int64_t M_max, cudaStream_t stream);
+
+/*
+ * Gather by expert and quantize: row r of the sorted layout is x[slot_of_row[r] / k],
+ * multiplied in FP32 by weights[slot_of_row[r]] when weights is not null, and zero where
+ * slot_of_row[r] is not in [0, T * k).  The codes and scales are dg_quantize_blockwise's
+ * definition on that matrix (without weights, bit for bit its output on the gathered BF16
+ * rows; a block whose amax / 448 rounds to 0 has scale 1).  Rows at or past
+ * group_offsets[G] (taken to lie in [0, M_total_capacity]) are not written.
+ * With weights this is the gradient of dg_moe_combine with respect to Y, quantized.
+ *
+ * X_bf16 : [T][H] BF16, 16-byte aligned.    weights : [T][k] FP32 or null.
+ * slot_of_row : int32 [M_total_capacity].   group_offsets : int32 [G+1].
+ * Q : [M_total_capacity][H] E4M3 out, 16-byte aligned.
+ * S : [M_total_capacity/128][ceil(H/128)] FP32 out.
+ * H % 16 == 0, M_total_capacity % 128 == 0.  M_total_capacity == 0 or H == 0 is a no-op.
+ */
+dg_status_t dg_moe_dispatch_quantize(const void *X_bf16, const float *weights,
+                                     const int32_t *slot_of_row, const int32_t *group_offsets,
+                                     int64_t T, int k, int64_t H, int64_t M_total_capacity, int G,
+                                     uint8_t *Q, float *S, cudaStream_t stream);
+
+/*
+ * The same into the masked layout, as dg_quantize_blockwise_masked quantizes each slab: only
+ * the first masked_m[g] rows of slab g (clamped to [0, M_max]) are written, and the scales of
+ * the row blocks that hold them.
+ * Q : [G][M_max][H] E4M3 out.  S : [G][ceil(M_max/128)][ceil(H/128)] FP32 out.
+ */
+dg_status_t dg_moe_dispatch_quantize_masked(const void *X_bf16, const int32_t *slot_of_row,
+                                            const int32_t *masked_m, int64_t T, int k, int64_t H,
+                                            int G, int64_t M_max, uint8_t *Q, float *S,
+                                            cudaStream_t stream);
+
+/*
+ * Expert rows back to their tokens:
+ *   OUT[t] = bf16( sum_j weights[t][j] * Y[row_of_slot[t][j]] ),
+ * FP32 sums in ascending j; a slot whose row is not in [0, rows) adds nothing (Y is not read
+ * for it), and a token without rows gets zeros.  A null `weights` stands for ones: that is the
+ * gradient of dg_moe_dispatch_quantize's gather with respect to X.
+ *
+ * Y_bf16 : [rows][H] BF16 (either layout), 16-byte aligned.  weights : [T][k] FP32 or null.
+ * row_of_slot : int32 [T][k].  OUT_bf16 : [T][H] BF16 out, 16-byte aligned.
+ * H % 16 == 0, 0 <= rows < 2^31.  T == 0 or H == 0 is a no-op.
+ */
+dg_status_t dg_moe_combine(const void *Y_bf16, const float *weights, const int32_t *row_of_slot,
+                           int64_t T, int k, int64_t H, int64_t rows, void *OUT_bf16,
+                           cudaStream_t stream);
+
+/*
+ * Gradient of dg_moe_combine with respect to the weights:
+ *   dweights[t][j] = sum_h dOUT[t][h] * Y[row_of_slot[t][j]][h]   (FP32; 0 for a dropped slot).
+ * The gradient with respect to Y is dg_moe_dispatch_quantize of dOUT with the weights.
+ *
+ * dOUT_bf16 : [T][H] BF16.  Y_bf16 : [rows][H] BF16.  dweights : [T][k] FP32 out.
+ * T == 0 is a no-op.
+ */
+dg_status_t dg_moe_combine_backward(const void *dOUT_bf16, const void *Y_bf16,
+                                    const int32_t *row_of_slot, int64_t T, int k, int64_t H,
+                                    int64_t rows, float *dweights, cudaStream_t stream);
+
+/*
+ * SwiGLU and quantization, a = g * sigma(g) * u in FP32 from H = [g | u]; codes and scales as
+ * dg_quantize_blockwise's definition on the FP32 values a (they are not rounded to BF16).
+ * With H8 and sH_t it also keeps H in 8 bits for the backward pass: the codes and scales of
+ * dg_quantize_1x128 on H, bit for bit.
+ *
+ * H_bf16 : [M][2F] BF16, 16-byte aligned, g in the first F columns, u in the others.
+ * group_offsets : int32 [G+1], or null for all M rows; rows at or past group_offsets[G]
+ *          (taken to lie in [0, M]) are neither read nor written.  G is ignored when null.
+ * Q : [M][F] E4M3 out.      S : [ceil(M/128)][F/128] FP32 out.
+ * H8 : [M][2F] E4M3 out.    sH_t : [2F/128][M] FP32 out.  Both null, or neither.
+ * F % 128 == 0; with group_offsets M % 128 == 0.  M == 0 or F == 0 is a no-op.
+ */
+dg_status_t dg_swiglu_quantize(const void *H_bf16, const int32_t *group_offsets, int G, int64_t M,
+                               int64_t F, uint8_t *Q, float *S, uint8_t *H8, float *sH_t,
+                               cudaStream_t stream);
+
+/*
+ * The same for the masked layout (no checkpoint): the first masked_m[g] rows of slab g.
+ * H_bf16 : [G][M_max][2F].  Q : [G][M_max][F].  S : [G][ceil(M_max/128)][F/128].
+ */
+dg_status_t dg_swiglu_quantize_masked(const void *H_bf16, const int32_t *masked_m, int G,
+                                      int64_t M_max, int64_t F, uint8_t *Q, float *S,
+                                      cudaStream_t stream);
+
+/*
+ * Backward pass of SwiGLU from the 8-bit checkpoint: with g, u the values that H8 and sH_t
+ * stand for,
+ *   dg = dA * u * sigma(g) * (1 + g * (1 - sigma(g))),   du = dA * g * sigma(g)   (FP32),
+ * and Q, S = dg_quantize_blockwise's definition on [dg | du].
+ *
+ * H8, sH_t : as dg_swiglu_quantize wrote them.  dA_bf16 : [M][F] BF16, 16-byte aligned.
+ * Q : [M][2F] E4M3 out.  S : [ceil(M/128)][2F/128] FP32 out.
+ * group_offsets, shapes and no-ops as in dg_swiglu_quantize.
+ */
+dg_status_t dg_swiglu_quantize_backward(const uint8_t *H8, const float *sH_t, const void *dA_bf16,
+                                        const int32_t *group_offsets, int G, int64_t M, int64_t F,
+                                        uint8_t *Q, float *S, cudaStream_t stream);
+
+/*
+ * Input gradient of the dense product C = X * W^T, from dC's codes (dY) and the weights' codes
+ * as the forward product reads them:
+ *   dX[m][k] = bf16( sum_nb sdY[m/128][nb] * sW[nb][k/128] *
+ *                    sum_{n in block nb} dY[m][n] * W[n][k] )
+ *
+ * dY : [M][N] E4M3, sdY : [ceil(M/128)][ceil(N/128)].  W : [N][K], sW : [ceil(N/128)][ceil(K/128)].
+ * dX : [M][K] BF16 out.  Matrices 16-byte aligned.  N > 0, N % 16 == 0, K % 16 == 0.
+ * M == 0 or K == 0 is a no-op.
+ */
+dg_status_t dg_fp8_dgrad_blockscaled(const uint8_t *dY, const float *sdY, const uint8_t *W,
+                                     const float *sW, void *dX_bf16, int64_t M, int64_t N,
+                                     int64_t K, cudaStream_t stream);
+
+/*
+ * Weight gradient of the dense product, from the codes of dC and of the forward input:
+ *   dW[n][k] (+)= sum_mb sdY[mb][n/128] * sX[mb][k/128] *
+ *                 sum_{m in block mb} dY[m][n] * X[m][k]
+ *
+ * dY : [M][N] E4M3, sdY : [ceil(M/128)][ceil(N/128)].  X : [M][K], sX : [ceil(M/128)][ceil(K/128)].
+ * dW : [N][K] out, FP32 when out_fp32 is not 0, else BF16; 16-byte aligned.
+ * accumulate not 0 (FP32 only, else DG_ERR_INVALID_ARG): the gradient is added to dW.
+ * N % 16 == 0, K % 16 == 0.  N == 0 or K == 0 is a no-op; M == 0 gives zeros (accumulate:
+ * leaves dW).
+ */
+dg_status_t dg_fp8_wgrad_blockscaled(const uint8_t *dY, const float *sdY, const uint8_t *X,
+                                     const float *sX, void *dW, int out_fp32, int accumulate,
+                                     int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+
+/*
+ * dg_fp8_dgrad_blockscaled expert by expert: rows [off[g], off[g+1]) of dY with W[g].
+ * dY : [M_total_capacity][N].  W : [G][N][K], sW : [G][N/128][ceil(K/128)].
+ * dX : [M_total_capacity][K] BF16 out; rows at or past off[G] are not written.
+ * group_offsets and its checks as in dg_fp8_grouped_gemm_contiguous.  N % 128 == 0, N > 0,
+ * K % 16 == 0.  M_total_capacity == 0 or K == 0 is a no-op.
+ */
+dg_status_t dg_fp8_grouped_dgrad_contiguous(const uint8_t *dY, const float *sdY, const uint8_t *W,
+                                            const float *sW, void *dX_bf16,
+                                            const int32_t *group_offsets, int64_t M_total_capacity,
+                                            int G, int64_t N, int64_t K, cudaStream_t stream);
+
+/*
+ * dg_fp8_wgrad_blockscaled expert by expert: dW[g] from rows [off[g], off[g+1]) of dY and X,
+ * whose padding rows must be zero codes (as the quantizers here leave them).  An expert
+ * without rows gets zeros (accumulate: its dW is left as it was).
+ * dY : [M_total_capacity][N].  X : [M_total_capacity][K].  dW : [G][N][K].
+ * group_offsets and its checks as in dg_fp8_grouped_gemm_contiguous.  N % 128 == 0,
+ * K % 16 == 0.
+ */
+dg_status_t dg_fp8_grouped_wgrad_contiguous(const uint8_t *dY, const float *sdY, const uint8_t *X,
+                                            const float *sX, void *dW, int out_fp32, int accumulate,
+                                            const int32_t *group_offsets, int64_t M_total_capacity,
+                                            int G, int64_t N, int64_t K, cudaStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *dg_status_string(dg_status_t status);
 
@@ -298,7 +506,8 @@ dg_status_t dg_get_last_device_status(cudaStream_t stream);
  * added dg_fp8_gemm_blockscaled_bf16a_select and DG_KERNEL_SKINNY_FUSED; 1.04 added
  * dg_quantize_blockwise_masked; 1.05: dg_quantize_blockwise_masked quantizes each
  * expert's tokens as a matrix of their own (rows past the count no longer enter the
- * last token block's amax).  Every 1.00 call is unchanged. */
+ * last token block's amax).  The expert-layer and gradient calls came later without a new
+ * number: they only add symbols.  Every 1.00 call is unchanged. */
 int dg_version(void);
 
 /*

@@ -1,0 +1,291 @@
+"""GPU tests of the sort by expert, the quantizing gather and the combination with its
+gradient, against plain float64 forms and (codes, integers) bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from fp8_block_scaled_scales_b200 import binding, inputs
+
+import plain_train as plain
+
+pytestmark = pytest.mark.gpu
+
+
+def route(T, k, G, seed, drop=0.0, dtype=torch.int64, skew=1.0):
+    rng = np.random.default_rng(seed)
+    p = np.arange(1, G + 1, dtype=np.float64) ** -skew
+    ids = rng.choice(G, size=(T, k), p=p / p.sum())  # a token may name an expert twice
+    if drop:
+        bad = rng.random((T, k)) < drop
+        ids[bad] = rng.choice([-1, -7, G, G + 5], size=int(bad.sum()))
+    return torch.from_numpy(ids).to(dtype)
+
+
+SORTS = [
+    (1, 1, 1), (1, 8, 64), (3, 2, 5), (37, 2, 8), (0, 4, 16), (129, 1, 128), (1000, 6, 33), (512, 8, 1024),
+    (513, 8, 256),            # just past one CTA's share
+    (5000, 7, 257), (20000, 8, 64), (32768, 1, 2),
+]
+
+
+@pytest.mark.parametrize("T,k,G", SORTS)
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("drop", [0.0, 0.3])
+def test_sort(T, k, G, dtype, drop):
+    ids = route(T, k, G, seed=T + k + G, drop=drop, dtype=dtype)
+    cap = binding.moe_capacity(T, k, G) + 256  # a caller's larger row map
+    want = plain.sort_plain(ids.numpy(), G, cap)
+    slot = torch.full((cap,), 7, dtype=torch.int32, device="cuda")
+    got = binding.moe_sort(ids.cuda(), G, slot_of_row=slot)
+    for a, b, what in zip(got, want, ("offsets", "row_of_slot", "slot_of_row")):
+        assert np.array_equal(a.cpu().numpy(), b), what
+
+
+@pytest.mark.parametrize("T,k,G", SORTS)
+@pytest.mark.parametrize("m_max", [1, 100, 384])
+def test_sort_masked(T, k, G, m_max):
+    ids = route(T, k, G, seed=T + k + G + 1, drop=0.1, dtype=torch.int32)
+    want = plain.sort_masked_plain(ids.numpy(), G, m_max)
+    got = binding.moe_sort_masked(ids.cuda(), G, m_max)
+    for a, b, what in zip(got, want, ("masked_m", "row_of_slot", "slot_of_row")):
+        assert np.array_equal(a.cpu().numpy(), b), what
+
+
+def test_sort_ids_past_32_bits_are_dropped():
+    ids = torch.tensor([[0, 1 << 32], [(1 << 32) + 1, 1], [-(1 << 40), 1 << 62]], dtype=torch.int64)
+    off, row, slot = binding.moe_sort(ids.cuda(), 2)
+    assert off.tolist() == [0, 128, 256] and row.tolist() == [[0, -1], [-1, 128], [-1, -1]]
+
+
+@pytest.mark.parametrize("m_max,G", [(0, 4)])
+def test_sort_masked_without_rows_drops_everything(m_max, G):
+    m, row, slot = binding.moe_sort_masked(route(9, 2, G, 1).cuda(), G, m_max)
+    assert m.tolist() == [0] * G and bool((row == -1).all()) and slot.numel() == 0
+
+
+def test_sort_two_streams_and_graph():
+    """Two calls at once on their own streams, and a captured call replayed on new ids."""
+    G, a, b = 64, route(20000, 8, 64, 5).cuda(), route(100, 8, 64, 6).cuda()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        r1 = binding.moe_sort(a, G, stream=s1)
+        r2 = binding.moe_sort(b, G, stream=s2)
+    torch.cuda.synchronize()
+    for ids, got in ((a, r1), (b, r2)):
+        for x, y in zip(got, plain.sort_plain(ids.cpu().numpy(), G, binding.moe_capacity(*ids.shape, G))):
+            assert np.array_equal(x.cpu().numpy(), y)
+    ids = a.clone()
+    outs = binding.moe_sort(ids, G)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.moe_sort(ids, G, *outs)
+    ids.copy_(route(20000, 8, 64, 7).cuda())
+    graph.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(outs, plain.sort_plain(ids.cpu().numpy(), G, outs[2].numel())):
+        assert np.array_equal(x.cpu().numpy(), y)
+
+
+def tokens(T, H, seed, scale=1.0):
+    x = torch.randn((T, H), generator=torch.Generator().manual_seed(seed)) * scale
+    if T:
+        x[:: max(1, T // 3)] *= 40
+        x[T // 2] = 0
+    return x.to(torch.bfloat16)
+
+
+def gathered(x, slot, k, weights=None):
+    """float32 rows of the sorted layout."""
+    ok = torch.from_numpy(slot >= 0)
+    s = torch.from_numpy(np.maximum(slot, 0))
+    v = x.float()[s // k]
+    if weights is not None:
+        v = v * weights.reshape(-1)[s][:, None]
+    return torch.where(ok[:, None], v, torch.zeros(()))
+
+
+@pytest.mark.parametrize("T,k,G,H", [(1, 1, 1, 16), (1, 8, 16, 4096), (5, 2, 3, 144), (37, 2, 8, 528), (300, 4, 5, 1040),
+                                     (257, 8, 64, 256)])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_dispatch_is_the_block_quantizer_on_the_gathered_rows(T, k, G, H, weighted):
+    ids = route(T, k, G, seed=T * 7 + H, drop=0.2)
+    cap = plain.cap_of(T, k, G) + 128
+    off, row, slot = plain.sort_plain(ids.numpy(), G, cap)
+    x = tokens(T, H, T + H, 3e-3 if weighted else 1.0)
+    w = (torch.rand((T, k), generator=torch.Generator().manual_seed(3)) + 0.01) if weighted else None
+    v = gathered(x, slot, k, w)
+    used = int(off[-1])
+    q = torch.full((cap, H), 0xA5, dtype=torch.uint8, device="cuda")
+    s = torch.full((cap // 128, -(-H // 128)), -7.0, device="cuda")
+    binding.moe_dispatch_quantize(x.cuda(), torch.from_numpy(slot).int().cuda(), torch.from_numpy(off).int().cuda(), k,
+                                  weights=None if w is None else w.cuda(), q=q, s=s)
+    q, s = q.cpu(), s.cpu()
+    if used:
+        wq, ws = plain.quantize_f32(v[:used])
+        assert torch.equal(q[:used], wq)
+        assert torch.equal(s[:used // 128].view(torch.int32), ws.view(torch.int32))
+        if not weighted:  # and the CPU oracle's quantizer on the BF16 rows
+            oq, os_ = oracle.quantize_blockwise(inputs.bf16_bits(v[:used].to(torch.bfloat16)))
+            assert np.array_equal(q[:used].numpy(), oq) and np.array_equal(s[:used // 128].numpy(), os_)
+    assert bool((q[used:] == 0xA5).all()) and bool((s[used // 128:] == -7).all()), "rows past the last expert"
+
+
+@pytest.mark.parametrize("T,k,G,H,m_max", [(1, 8, 64, 4096, 128), (37, 2, 8, 144, 40), (600, 4, 3, 272, 500), (300, 1, 1, 128, 300)])
+def test_dispatch_masked(T, k, G, H, m_max):
+    ids = route(T, k, G, seed=T + H)
+    m, row, slot = plain.sort_masked_plain(ids.numpy(), G, m_max)
+    x = tokens(T, H, T)
+    v = gathered(x, slot, k).view(G, m_max, H)
+    q = torch.full((G, m_max, H), 0xA5, dtype=torch.uint8, device="cuda")
+    s = torch.full((G, -(-m_max // 128), -(-H // 128)), -7.0, device="cuda")
+    binding.moe_dispatch_quantize_masked(x.cuda(), torch.from_numpy(slot).int().cuda(),
+                                         torch.from_numpy(m).int().cuda(), k, q=q, s=s)
+    q, s = q.cpu(), s.cpu()
+    for g in range(G):
+        c = int(m[g])
+        nb = -(-c // 128)
+        if c:
+            wq, ws = plain.quantize_f32(v[g, :c])
+            assert torch.equal(q[g, :c], wq) and torch.equal(s[g, :nb], ws)
+        assert bool((q[g, c:] == 0xA5).all()) and bool((s[g, nb:] == -7).all())
+
+
+def test_dispatch_never_reads_tokens_without_a_slot():
+    """Infinities and NaN in tokens that no row holds, and in weights of dropped slots, leave no trace;
+    slots outside the table are rows without a slot."""
+    T, k, G, H = 40, 2, 4, 256
+    ids = route(T, k, G, 11)
+    ids[::3] = -1
+    cap = plain.cap_of(T, k, G)
+    off, row, slot = plain.sort_plain(ids.numpy(), G, cap)
+    x, w = tokens(T, H, 1), torch.rand((T, k))
+    want = plain.quantize_f32(gathered(x, slot, k, w)[:int(off[-1])])
+    x[::3], w[::3] = float("nan"), float("inf")
+    slot[slot < 0] = np.resize([-1, T * k, 1 << 30, -(1 << 31)], (slot < 0).sum())
+    q, s = binding.moe_dispatch_quantize(x.cuda(), torch.from_numpy(slot).int().cuda(),
+                                         torch.from_numpy(off).int().cuda(), k, weights=w.cuda())
+    assert torch.equal(q[:int(off[-1])].cpu(), want[0]) and torch.equal(s[:int(off[-1]) // 128].cpu(), want[1])
+
+
+def test_dispatch_weights_so_small_that_the_scale_would_vanish():
+    """amax / 448 rounds to zero in FP32: the scale is 1 and every code is a zero."""
+    x = torch.full((1, 128), 2.0 ** -100, dtype=torch.bfloat16)
+    q, s = binding.moe_dispatch_quantize(x.cuda(), torch.tensor([0] + [-1] * 127, dtype=torch.int32).cuda(),
+                                         torch.tensor([0, 128], dtype=torch.int32).cuda(), 1,
+                                         weights=torch.full((1, 1), 2.0 ** -46).cuda())
+    assert s.item() == 1.0 and not bool((q & 0x7F).any())
+
+
+COMBINES = [(1, 1, 16), (1, 8, 7168), (5, 8, 1040), (37, 2, 4096), (300, 6, 528), (64, 11, 144), (1030, 4, 2048)]
+
+
+def combine_case(T, k, H, seed):
+    G, g = 7, torch.Generator().manual_seed(seed)
+    ids = route(T, k, G, seed, drop=0.25)
+    ids[T // 2] = -1  # a token without any row
+    cap = plain.cap_of(T, k, G)
+    off, row, slot = plain.sort_plain(ids.numpy(), G, cap)
+    y = torch.randn((cap, H), generator=g).to(torch.bfloat16)
+    w = torch.randn((T, k), generator=g)
+    return row, y, w, g
+
+
+@pytest.mark.parametrize("T,k,H", COMBINES)
+@pytest.mark.parametrize("weighted", [False, True])
+def test_combine(T, k, H, weighted):
+    row, y, w, _ = combine_case(T, k, H, T + k + H)
+    r = torch.from_numpy(row)
+    wt = torch.where(r >= 0, w.double() if weighted else torch.ones(T, k, dtype=torch.float64), torch.zeros((), dtype=torch.float64))
+    terms = y.double()[r.clamp_min(0)] * wt[:, :, None]
+    ref, mag = terms.sum(1), terms.abs().sum(1)
+    y[torch.from_numpy(np.setdiff1d(np.arange(y.shape[0]), row))] = float("nan")  # rows no slot names
+    got = binding.moe_combine(y.cuda(), r.int().cuda(), w.cuda() if weighted else None).cpu().double()
+    # k FP32 multiply-adds, then one rounding to BF16
+    assert bool(((got - ref).abs() <= k * 2.0 ** -24 * mag * (1 + 2.0 ** -8) + ref.abs() * 2.0 ** -8).all())
+    assert bool((got[T // 2] == 0).all())
+
+
+@pytest.mark.parametrize("T,k,H", COMBINES)
+def test_combine_backward(T, k, H):
+    row, y, w, g = combine_case(T, k, H, T + k + H + 1)
+    dout = torch.randn((T, H), generator=g).to(torch.bfloat16)
+    r = torch.from_numpy(row)
+    terms = y.double()[r.clamp_min(0)] * dout.double()[:, None, :] * (r >= 0)[:, :, None]
+    ref, mag = terms.sum(2), terms.abs().sum(2)
+    y[torch.from_numpy(np.setdiff1d(np.arange(y.shape[0]), row))] = float("nan")
+    got = binding.moe_combine_backward(dout.cuda(), y.cuda(), r.int().cuda()).cpu().double()
+    # a chain of at most H FP32 multiply-adds, whatever its order
+    assert bool(((got - ref).abs() <= H * 2.0 ** -24 * mag).all())
+    assert bool((got[r < 0] == 0).all())
+
+
+def test_combine_gradients_against_differences():
+    """d(sum of out * dout) along a random direction of the weights, and of y, in float64."""
+    T, k, H, G = 20, 3, 256, 4
+    ids = route(T, k, G, 3, drop=0.2)
+    cap = plain.cap_of(T, k, G)
+    off, row, slot = plain.sort_plain(ids.numpy(), G, cap)
+    g = torch.Generator().manual_seed(1)
+    y = torch.randn((cap, H), generator=g).to(torch.bfloat16)
+    w, dw_dir = torch.rand((T, k), generator=g), torch.randn((T, k), generator=g)
+    dout = torch.randn((T, H), generator=g).to(torch.bfloat16)
+    y_dir = torch.randn((cap, H), generator=g).double()
+    r = torch.from_numpy(row)
+
+    def loss(w, y):
+        wt = torch.where(r >= 0, w.double(), torch.zeros((), dtype=torch.float64))
+        return float(((y.double()[r.clamp_min(0)] * wt[:, :, None]).sum(1) * dout.double()).sum())
+
+    e = 1e-3
+    num_w = (loss(w + e * dw_dir.double(), y) - loss(w - e * dw_dir.double(), y)) / (2 * e)
+    num_y = (loss(w, y.double() + e * y_dir) - loss(w, y.double() - e * y_dir)) / (2 * e)
+    dw = binding.moe_combine_backward(dout.cuda(), y.cuda(), r.int().cuda()).cpu().double()
+    # both are linear: the difference is exact up to float64; dw's own error as in the test above
+    assert abs(float((dw * dw_dir).sum()) - num_w) <= 256 * 2.0 ** -24 * float((dw_dir.abs() * 256 * 8).sum()) + 1e-6
+    q, s = binding.moe_dispatch_quantize(dout.cuda(), torch.from_numpy(slot).int().cuda(),
+                                         torch.from_numpy(off).int().cuda(), k, weights=w.cuda())
+    dy = plain.decode(q.cpu(), s.cpu())
+    used = int(off[-1])
+    step = plain.code_error_bound(gathered(dout, slot, k, w)[:used].double(), s[:used // 128].cpu(), 0.0)
+    assert abs(float((dy[:used] * y_dir[:used]).sum()) - num_y) <= float((step * y_dir[:used].abs()).sum())
+
+
+def test_combine_takes_the_masked_layout_and_no_rows():
+    T, k, G, m_max, H = 30, 2, 5, 9, 144
+    ids = route(T, k, G, 8)
+    m, row, slot = plain.sort_masked_plain(ids.numpy(), G, m_max)  # some slots dropped
+    assert (row < 0).any()
+    y = torch.randn((G, m_max, H)).to(torch.bfloat16)
+    r = torch.from_numpy(row)
+    ref = (y.view(-1, H).double()[r.clamp_min(0)] * (r >= 0)[:, :, None]).sum(1)
+    got = binding.moe_combine(y.cuda(), r.int().cuda()).cpu().double()
+    assert bool(((got - ref).abs() <= 2.0 ** -22 * 10 + ref.abs() * 2.0 ** -8).all())
+    none = binding.moe_combine(torch.empty((0, H), dtype=torch.bfloat16, device="cuda"), r.int().cuda())
+    assert not bool(none.any())
+    none = binding.moe_combine_backward(none, torch.empty((0, H), dtype=torch.bfloat16, device="cuda"), r.int().cuda())
+    assert not bool(none.any())
+
+
+def test_binding_refuses_wrong_types_shapes_and_strides():
+    x = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
+    slot = torch.full((128,), -1, dtype=torch.int32, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    row = torch.zeros((8, 2), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        binding.moe_dispatch_quantize(x.float(), slot, off, 2)
+    with pytest.raises(ValueError):
+        binding.moe_dispatch_quantize(x[:, ::2], slot, off, 2)
+    with pytest.raises(ValueError):
+        binding.moe_dispatch_quantize(x, slot.long(), off, 2)
+    with pytest.raises(ValueError):
+        binding.moe_dispatch_quantize(x, slot, off, 2, weights=torch.zeros((8, 3), device="cuda"))
+    with pytest.raises(ValueError):
+        binding.moe_combine(x, row, torch.zeros((8, 2), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        binding.moe_combine_backward(x, x[:, :32].contiguous(), row)
+    with pytest.raises(ValueError):
+        binding.moe_sort(row.float(), 4)
+    with pytest.raises(binding.DGError):
+        binding.moe_sort(row, 4, slot_of_row=slot)  # a row map too small for the worst case

@@ -1,0 +1,147 @@
+"""Refusals of the expert-layer and gradient calls, decided on the host before any CUDA call."""
+import ctypes
+
+import pytest
+import torch
+
+from fp8_block_scaled_scales_b200 import binding
+from fp8_block_scaled_scales_b200 import build as dgbuild
+
+NULL = ctypes.c_void_p(0)
+P = ctypes.c_void_p(0x10000)   # never dereferenced: the refusal comes first
+ODD = ctypes.c_void_p(0x10001)
+OK, ARG, SHAPE, ALIGN = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    dgbuild.build()
+    return binding.lib()
+
+
+def test_sort_refusals(lib):
+    f = lib.dg_moe_sort
+    assert f(P, 0, -1, 2, 4, P, P, P, 1024, NULL) == SHAPE
+    assert f(P, 0, 8, 0, 4, P, P, P, 1024, NULL) == SHAPE              # k == 0
+    assert f(P, 0, 8, 2, 0, P, P, P, 1024, NULL) == SHAPE
+    assert f(P, 0, 8, 2, 1025, P, P, P, 1 << 20, NULL) == SHAPE
+    assert f(P, 0, 8, 2, 4, P, P, P, 1000, NULL) == SHAPE              # capacity % 128
+    # 16 slots over 4 experts may take four blocks of 128
+    assert f(P, 0, 8, 2, 4, P, P, P, 384, NULL) == SHAPE
+    assert f(P, 0, 1 << 30, 2, 4, P, P, P, 1 << 30, NULL) == SHAPE     # T * k > 2^30
+    assert f(NULL, 0, 8, 2, 4, P, P, P, 512, NULL) == ARG
+    assert f(P, 0, 8, 2, 4, NULL, P, P, 512, NULL) == ARG
+    assert f(P, 0, 8, 2, 4, P, P, NULL, 512, NULL) == ARG
+    assert f(ctypes.c_void_p(0x10004), 1, 8, 2, 4, P, P, P, 512, NULL) == ALIGN  # int64 ids at 4 bytes
+    assert f(P, 0, 8, 2, 4, ODD, P, P, 512, NULL) == ALIGN
+    m = lib.dg_moe_sort_masked
+    assert m(P, 0, 8, 2, 4, P, P, P, -1, NULL) == SHAPE
+    assert m(P, 0, 8, 2, 4, P, P, P, 1 << 30, NULL) == SHAPE           # G * M_max >= 2^31
+    assert m(P, 0, 8, 2, 4, NULL, P, P, 64, NULL) == ARG
+    assert m(P, 0, 8, 2, 4, P, P, ODD, 64, NULL) == ALIGN
+
+
+def test_capacity_helper_is_the_least_the_sort_takes(lib):
+    for T, k, G in ((1, 8, 64), (1, 1, 1), (100, 2, 3), (8192, 2, 8), (0, 4, 16)):
+        cap = binding.moe_capacity(T, k, G)
+        if cap:
+            assert lib.dg_moe_sort(P, 0, T, k, G, P, P, P, cap - 128, NULL) == SHAPE
+        assert lib.dg_moe_sort(P, 0, T, k, G, ODD, P, P, cap, NULL) == ALIGN  # capacity accepted
+        # the worst routing fits: every expert one slot, the rest in one, each rounded up
+        S = T * k
+        used = min(G, S)
+        worst = (used - 1) * 128 + -(-(S - used + 1) // 128) * 128 if S else 0
+        assert worst <= cap
+
+
+def test_dispatch_refusals(lib):
+    f = lib.dg_moe_dispatch_quantize
+    assert f(P, NULL, P, P, 8, 2, 24, 128, 4, P, P, NULL) == SHAPE     # H % 16
+    assert f(P, NULL, P, P, 8, 2, 32, 100, 4, P, P, NULL) == SHAPE     # capacity % 128
+    assert f(P, NULL, P, P, 8, 2, 32, 128, 0, P, P, NULL) == SHAPE
+    assert f(P, NULL, P, P, -1, 2, 32, 128, 4, P, P, NULL) == SHAPE
+    assert f(NULL, NULL, NULL, NULL, 8, 2, 32, 0, 4, NULL, NULL, NULL) == OK
+    assert f(NULL, NULL, NULL, NULL, 8, 2, 0, 128, 4, NULL, NULL, NULL) == OK
+    assert f(P, NULL, NULL, P, 8, 2, 32, 128, 4, P, P, NULL) == ARG
+    assert f(NULL, NULL, P, P, 8, 2, 32, 128, 4, P, P, NULL) == ARG
+    assert f(ODD, NULL, P, P, 8, 2, 32, 128, 4, P, P, NULL) == ALIGN
+    assert f(P, ODD, P, P, 8, 2, 32, 128, 4, P, P, NULL) == ALIGN
+    m = lib.dg_moe_dispatch_quantize_masked
+    assert m(P, P, P, 8, 2, 24, 4, 64, P, P, NULL) == SHAPE
+    assert m(P, P, P, 8, 2, 32, 1025, 64, P, P, NULL) == SHAPE
+    assert m(NULL, NULL, NULL, 8, 2, 32, 4, 0, NULL, NULL, NULL) == OK
+    assert m(P, P, NULL, 8, 2, 32, 4, 64, P, P, NULL) == ARG
+    assert m(P, P, P, 8, 2, 32, 4, 64, ODD, P, NULL) == ALIGN
+
+
+def test_combine_refusals(lib):
+    f = lib.dg_moe_combine
+    assert f(P, P, P, 8, 2, 24, 128, P, NULL) == SHAPE
+    assert f(P, P, P, 8, 2, 32, -1, P, NULL) == SHAPE
+    assert f(P, P, P, 8, 0, 32, 128, P, NULL) == SHAPE
+    assert f(NULL, NULL, NULL, 0, 2, 32, 128, NULL, NULL) == OK
+    assert f(NULL, P, P, 8, 2, 32, 128, P, NULL) == ARG
+    assert f(P, P, P, 8, 2, 32, 128, NULL, NULL) == ARG
+    assert f(P, P, P, 8, 2, 32, 128, ODD, NULL) == ALIGN
+    b = lib.dg_moe_combine_backward
+    assert b(P, P, P, 8, 2, 24, 128, P, NULL) == SHAPE
+    assert b(NULL, NULL, NULL, 0, 2, 32, 128, NULL, NULL) == OK
+    assert b(P, P, P, 8, 2, 32, 128, NULL, NULL) == ARG
+    assert b(P, ODD, P, 8, 2, 32, 128, P, NULL) == ALIGN
+
+
+def test_swiglu_refusals(lib):
+    f = lib.dg_swiglu_quantize
+    assert f(P, NULL, 0, 8, 100, P, P, NULL, NULL, NULL) == SHAPE      # F % 128
+    assert f(P, P, 4, 100, 128, P, P, NULL, NULL, NULL) == SHAPE       # grouped: M % 128
+    assert f(P, P, 0, 128, 128, P, P, NULL, NULL, NULL) == SHAPE       # grouped: G
+    assert f(NULL, NULL, 0, 0, 128, NULL, NULL, NULL, NULL, NULL) == OK
+    assert f(P, NULL, 0, 8, 128, P, P, P, NULL, NULL) == ARG           # half a checkpoint
+    assert f(P, NULL, 0, 8, 128, NULL, P, NULL, NULL, NULL) == ARG
+    assert f(ODD, NULL, 0, 8, 128, P, P, NULL, NULL, NULL) == ALIGN
+    m = lib.dg_swiglu_quantize_masked
+    assert m(P, P, 0, 8, 128, P, P, NULL) == SHAPE
+    assert m(P, NULL, 2, 8, 128, P, P, NULL) == ARG
+    assert m(P, ODD, 2, 8, 128, P, P, NULL) == ALIGN
+    b = lib.dg_swiglu_quantize_backward
+    assert b(P, P, P, NULL, 0, 8, 64, P, P, NULL) == SHAPE
+    assert b(P, NULL, P, NULL, 0, 8, 128, P, P, NULL) == ARG
+    assert b(P, P, ODD, NULL, 0, 8, 128, P, P, NULL) == ALIGN
+
+
+def test_gradient_product_refusals(lib):
+    d = lib.dg_fp8_dgrad_blockscaled
+    assert d(P, P, P, P, P, 8, 0, 128, NULL) == SHAPE                  # nothing to sum over
+    assert d(P, P, P, P, P, 8, 24, 128, NULL) == SHAPE
+    assert d(P, P, P, P, P, 8, 128, 24, NULL) == SHAPE
+    assert d(NULL, NULL, NULL, NULL, NULL, 0, 128, 128, NULL) == OK
+    assert d(P, P, P, P, NULL, 8, 128, 128, NULL) == ARG
+    assert d(P, P, ODD, P, P, 8, 128, 128, NULL) == ALIGN
+    w = lib.dg_fp8_wgrad_blockscaled
+    assert w(P, P, P, P, P, 1, 0, 8, 24, 128, NULL) == SHAPE
+    assert w(P, P, P, P, P, 0, 1, 8, 128, 128, NULL) == ARG            # accumulate in BF16
+    assert w(NULL, NULL, NULL, NULL, NULL, 1, 0, 8, 0, 128, NULL) == OK
+    assert w(P, P, P, P, NULL, 1, 0, 8, 128, 128, NULL) == ARG
+    assert w(NULL, NULL, NULL, NULL, NULL, 1, 0, 0, 128, 128, NULL) == ARG  # M == 0 still writes dW
+    assert w(P, P, P, P, ODD, 1, 0, 8, 128, 128, NULL) == ALIGN
+    gd = lib.dg_fp8_grouped_dgrad_contiguous
+    assert gd(P, P, P, P, P, P, 100, 2, 128, 128, NULL) == SHAPE
+    assert gd(P, P, P, P, P, P, 128, 2, 64, 128, NULL) == SHAPE        # N % 128
+    assert gd(P, P, P, P, P, P, 128, 1025, 128, 128, NULL) == SHAPE
+    assert gd(P, P, P, P, P, NULL, 128, 2, 128, 128, NULL) == ARG
+    assert gd(P, P, P, P, P, ODD, 128, 2, 128, 128, NULL) == ALIGN
+    gw = lib.dg_fp8_grouped_wgrad_contiguous
+    assert gw(P, P, P, P, P, 1, 0, P, 128, 2, 64, 128, NULL) == SHAPE
+    assert gw(P, P, P, P, P, 0, 1, P, 128, 2, 128, 128, NULL) == ARG
+    assert gw(P, P, P, P, P, 1, 0, NULL, 128, 2, 128, 128, NULL) == ARG
+    assert gw(P, P, P, P, P, 1, 0, P, 128, 1 << 20, 1 << 20, 128, NULL) == SHAPE
+
+
+def test_binding_refuses_host_tensors():
+    """Types, ranks and devices are checked before the library sees an address."""
+    with pytest.raises(ValueError):
+        binding.moe_sort(torch.zeros((4, 2), dtype=torch.int32), 4)
+    with pytest.raises(ValueError):
+        binding.swiglu_quantize(torch.zeros((4, 256), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        binding.moe_combine(torch.zeros((4, 16), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32))
