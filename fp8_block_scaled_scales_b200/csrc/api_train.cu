@@ -154,7 +154,7 @@ dg_status_t dg_swiglu_quantize_backward(const uint8_t *H8, const float *sH_t, co
     DeviceInfo dev;
     const dg_status_t st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
-    return launch_swiglu_backward(H8, sH_t, dA_bf16, group_offsets, G, M, F, Q, S, stream);
+    return launch_swiglu_backward(H8, sH_t, dA_bf16, group_offsets, G, M, F, Q, S, dev, stream);
 }
 
 static dg_status_t check_grad(const void *dY, const float *sdY, const void *B, const float *sB, const void *C) {

@@ -46,6 +46,37 @@ __device__ __forceinline__ uint2 quantize8_f32(const float2 (&x)[4], const Block
     return out;
 }
 
+// Scale of a block of such values and its reciprocal.
+struct NearScale {
+    float s, r;
+    bool fast_ok;
+};
+
+__device__ __forceinline__ NearScale near_scale(uint32_t amax_bits) {
+    NearScale b;
+    const float q = __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
+    b.s = (q == 0.0f) ? 1.0f : q;
+    b.r = __frcp_rn(b.s);
+    b.fast_ok = isfinite(b.r);
+    return b;
+}
+
+// Eight FP32 values that are themselves rounded results (an activation, a gradient): x / s as
+// the product with the rounded reciprocal, off by two roundings of 2^-24 where the quotient
+// is off by one.  The values carry larger errors already, so the exact quotient that
+// quantize8 pays for would decide nothing.
+__device__ __forceinline__ uint2 quantize8_near(const float2 (&x)[4], const NearScale &b) {
+    float2 y[4];
+    if (__builtin_expect(b.fast_ok, 1)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = __fmul2_rn(x[j], make_float2(b.r, b.r));
+    } else {  // 1/s is not finite
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = make_float2(__fdiv_rn(x[j].x, b.s), __fdiv_rn(x[j].y, b.s));
+    }
+    return make_uint2(e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y), e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y));
+}
+
 // Four E4M3 codes (lowest byte first) as FP32, exact: every E4M3 value is an FP16 value.
 __device__ __forceinline__ void e4m3x4_to_f32(uint32_t q, float2 &lo, float2 &hi) {
     uint32_t a, b;
@@ -70,8 +101,7 @@ __device__ __forceinline__ void bf16x8_to_f32(uint4 v, float2 (&x)[4]) {
 // |x| folded into an FP32 magnitude kept as bits: the order of non-negative FP32 is that of
 // their bits, and a NaN is above infinity, so a NaN in a block reaches its scale.
 __device__ __forceinline__ uint32_t amax_fold_f32(uint32_t m, float2 x) {
-    m = max(m, __float_as_uint(x.x) & 0x7FFFFFFFu);
-    return max(m, __float_as_uint(x.y) & 0x7FFFFFFFu);
+    return max(m, max(__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu));
 }
 
 // The maximum of `v` over the CTA's warps.  red: one word per warp, not in use by an

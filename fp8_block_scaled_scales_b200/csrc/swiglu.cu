@@ -10,7 +10,8 @@
 //             Q, S = the block quantizer's definition on [dg | du], ready for both gradient
 //             products.
 // sigma uses the hardware exponential and reciprocal (relative error of a few 2^-23 where
-// the result is not negligible), far below the E4M3 rounding that follows.
+// the result is not negligible), far below the E4M3 rounding that follows; for the same
+// reason a / s is a product with the rounded 1/s (quantize8_near).
 #include <cuda_bf16.h>
 
 #include "dg_device.cuh"
@@ -23,10 +24,29 @@ constexpr int kGluThreads = 512;  // 16 lanes a row, 32 rows at a time, 4 times
 constexpr int kGluPer = 4;
 constexpr int64_t kGluMaskedRowCtas = 16;
 
-__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// sigma of two values; exp overflows to infinity for x < -88, whose reciprocal is 0
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+    const float2 e = make_float2(__expf(-x.x), __expf(-x.y));
+    return make_float2(__fdividef(1.0f, 1.0f + e.x), __fdividef(1.0f, 1.0f + e.y));
+}
+
+// One row group of 128 columns (16 lanes, 8 values each) as a 1 x 128 block: codes to *q, the
+// scale to *s by the first lane.  All lanes of the warp call it.
+__device__ __forceinline__ void checkpoint_row(uint4 v, bool ok, bool first, uint8_t *q, float *s) {
+    uint32_t bits = amax_bits_of(amax_fold8(0u, v));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
+    const BlockScale bs = block_scale(bits);
+    if (ok) {
+        *reinterpret_cast<uint2 *>(q) = quantize8(v, bs);
+        if (first) *s = bs.s;
+    }
+}
 
 // Rows row0 .. row0 + rows - 1 (at most 128) of h [.][2F], column block bc of both halves.
-// M: rows of the checkpoint's scale array.
+// M: rows of the checkpoint's scale array.  Rows are taken two at a time: with all four
+// loaded first the 64 registers that let two CTAs share an SM spill (386 us against
+// 0.07 ms of traffic on 16384 x 4096), and two rows of both CTAs keep 64 KB in flight.
 template <bool CKPT>
 __device__ __forceinline__ void glu_block(const uint16_t *__restrict__ Hin, int64_t F, int64_t M, int64_t row0,
                                           int rows, int64_t bc, uint8_t *__restrict__ Q, float *__restrict__ Sp,
@@ -34,54 +54,48 @@ __device__ __forceinline__ void glu_block(const uint16_t *__restrict__ Hin, int6
     const int tid = static_cast<int>(threadIdx.x);
     const int64_t col = bc * 128 + (tid & 15) * 8;
     const int sub = tid >> 4;
-    uint4 vg[kGluPer], vu[kGluPer];
-#pragma unroll
-    for (int i = 0; i < kGluPer; ++i) {
-        const int r = sub + 32 * i;
-        const uint16_t *p = Hin + (row0 + r) * 2 * F + col;
-        vg[i] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
-        vu[i] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(p + F)) : make_uint4(0, 0, 0, 0);
-    }
+    const bool first = (tid & 15) == 0;
+    const int64_t at = (row0 + sub) * 2 * F + col, step = 64 * F;  // 32 rows of h
+    const uint16_t *p = Hin + at;
+    uint8_t *p8 = CKPT ? H8 + at : nullptr;
+    float *ps = CKPT ? sH + bc * M + row0 + sub : nullptr;
     float2 a[kGluPer][4];
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kGluPer; ++i) {
-        float2 g[4], u[4];
-        bf16x8_to_f32(vg[i], g);
-        bf16x8_to_f32(vu[i], u);
+    for (int i0 = 0; i0 < kGluPer; i0 += 2) {
+        uint4 vg[2], vu[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            a[i][j].x = g[j].x * sigmoid_f32(g[j].x) * u[j].x;
-            a[i][j].y = g[j].y * sigmoid_f32(g[j].y) * u[j].y;
-            m = amax_fold_f32(m, a[i][j]);
+        for (int i = 0; i < 2; ++i) {
+            const bool ok = sub + 32 * (i0 + i) < rows;
+            vg[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(p + (i0 + i) * step)) : make_uint4(0, 0, 0, 0);
+            vu[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(p + (i0 + i) * step + F)) : make_uint4(0, 0, 0, 0);
         }
-    }
-    if (CKPT) {
 #pragma unroll
-        for (int i = 0; i < kGluPer; ++i) {
-            const int64_t row = row0 + sub + 32 * i;
-            const bool ok = sub + 32 * i < rows;
+        for (int i = 0; i < 2; ++i) {
+            float2 g[4], u[4];
+            bf16x8_to_f32(vg[i], g);
+            bf16x8_to_f32(vu[i], u);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint4 v = half ? vu[i] : vg[i];
-                uint32_t bits = amax_bits_of(amax_fold8(0u, v));
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
-                const BlockScale bs = block_scale(bits);
-                if (ok) {
-                    *reinterpret_cast<uint2 *>(H8 + row * 2 * F + half * F + col) = quantize8(v, bs);
-                    if ((tid & 15) == 0) sH[(half * (F / 128) + bc) * M + row] = bs.s;
-                }
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = __fmul2_rn(__fmul2_rn(g[j], sigmoid2(g[j])), u[j]);
+                m = amax_fold_f32(m, x);
+                a[i0 + i][j] = x;
+            }
+            if (CKPT) {
+                const bool ok = sub + 32 * (i0 + i) < rows;
+                uint8_t *q = p8 + (i0 + i) * step;
+                float *sp = ps + 32 * (i0 + i);
+                checkpoint_row(vg[i], ok, first, q, sp);
+                checkpoint_row(vu[i], ok, first, q + F, sp + (F / 128) * M);
             }
         }
     }
-    const BlockScale bs = block_scale_f32(__uint_as_float(cta_max<kGluThreads / 32>(m, red)));
+    const NearScale bs = near_scale(cta_max<kGluThreads / 32>(m, red));
     if (tid == 0) *Sp = bs.s;
+    uint8_t *q = Q + (row0 + sub) * F + col;
 #pragma unroll
-    for (int i = 0; i < kGluPer; ++i) {
-        const int r = sub + 32 * i;
-        if (r < rows) *reinterpret_cast<uint2 *>(Q + (row0 + r) * F + col) = quantize8_f32(a[i], bs);
-    }
+    for (int i = 0; i < kGluPer; ++i)
+        if (sub + 32 * i < rows) *reinterpret_cast<uint2 *>(q + i * (step >> 1)) = quantize8_near(a[i], bs);
 }
 
 // rows of the layout that hold something: all M, or up to the last expert's end
@@ -121,74 +135,135 @@ __global__ void __launch_bounds__(kGluThreads, 2)
     }
 }
 
-__global__ void __launch_bounds__(kGluThreads)
+// Backward: one persistent CTA per SM.  A block's [dg | du] in FP32 is half the register
+// file, so no second CTA fits beside it; instead every thread copies its own piece of the
+// next block into shared memory (cp.async) before it computes the current one, so loads
+// run under the arithmetic.
+struct GluBackSmem {
+    uint2 cg[kGluPer][kGluThreads];
+    uint2 cu[kGluPer][kGluThreads];
+    uint4 da[kGluPer][kGluThreads];
+    float scale[2][128];  // the block's row scales, gate then up
+};
+
+__device__ __forceinline__ void cp_async(void *dst, const void *src, int bytes_8_or_16) {
+    if (bytes_8_or_16 == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+__global__ void __launch_bounds__(kGluThreads, 1)
     swiglu_backward_kernel(const uint8_t *__restrict__ H8, const float *__restrict__ sH,
                            const uint16_t *__restrict__ dA, const int32_t *__restrict__ offsets, int G, int64_t M,
                            int64_t F, uint8_t *__restrict__ Q, float *__restrict__ S) {
-    __shared__ uint32_t red[2][kGluThreads / 32];
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    GluBackSmem *stage = reinterpret_cast<GluBackSmem *>(smem_raw);
+    __shared__ uint32_t red[2][2][kGluThreads / 32];
     grid_dep_launch_dependents();
     grid_dep_wait();
     const int tid = static_cast<int>(threadIdx.x);
-    const int64_t Fb = F / 128, blk = blockIdx.x;
-    const int64_t lb = blk / Fb, bc = blk - lb * Fb;
-    const int64_t left = used_rows(offsets, G, M) - lb * 128;
-    if (left <= 0) return;
-    const int rows = static_cast<int>(min(left, int64_t(128)));
-    const int64_t col = bc * 128 + (tid & 15) * 8;
-    const int sub = tid >> 4;
-    uint2 cg[kGluPer], cu[kGluPer];
-    uint4 va[kGluPer];
-    float sg[kGluPer], su[kGluPer];
+    const int lane16 = tid & 15, sub = tid >> 4;
+    const int64_t Fb = F / 128;
+    const int64_t used = used_rows(offsets, G, M);
+    const int64_t blocks = (used + 127) / 128 * Fb;
+
+    auto prefetch = [&](int64_t blk, GluBackSmem &st) {
+        if (blk < blocks) {
+            const int64_t lb = blk / Fb, bc = blk - lb * Fb;
+            const int rows = static_cast<int>(min(used - lb * 128, int64_t(128)));
+            const int64_t row = lb * 128 + sub, col = bc * 128 + lane16 * 8;
+            const uint8_t *p = H8 + row * 2 * F + col;
+            const uint16_t *pa = dA + row * F + col;
 #pragma unroll
-    for (int i = 0; i < kGluPer; ++i) {
-        const int r = sub + 32 * i;
-        const int64_t row = lb * 128 + r;
-        const bool ok = r < rows;
-        const uint8_t *p = H8 + row * 2 * F + col;
-        cg[i] = ok ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0, 0);
-        cu[i] = ok ? __ldg(reinterpret_cast<const uint2 *>(p + F)) : make_uint2(0, 0);
-        va[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(dA + row * F + col)) : make_uint4(0, 0, 0, 0);
-        sg[i] = ok ? __ldg(sH + bc * M + row) : 0.0f;
-        su[i] = ok ? __ldg(sH + (Fb + bc) * M + row) : 0.0f;
-    }
-    float2 dg[kGluPer][4], du[kGluPer][4];
-    uint32_t mg = 0, mu = 0;
+            for (int i = 0; i < kGluPer; ++i) {
+                if (sub + 32 * i < rows) {
+                    cp_async(&st.cg[i][tid], p + i * 64 * F, 8);
+                    cp_async(&st.cu[i][tid], p + i * 64 * F + F, 8);
+                    cp_async(&st.da[i][tid], pa + i * 32 * F, 16);
+                }
+            }
+            if (tid < 256) {
+                const int r = tid & 127, half = tid >> 7;
+                if (r < rows) cp_async4(&st.scale[half][r], sH + (half * Fb + bc) * M + lb * 128 + r);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    int par = 0;
+    prefetch(blockIdx.x, stage[0]);
+    for (int64_t blk = blockIdx.x; blk < blocks; blk += gridDim.x, par ^= 1) {
+        prefetch(blk + gridDim.x, stage[par ^ 1]);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();  // the scales come from other threads' copies
+        const GluBackSmem &st = stage[par];
+        const int64_t lb = blk / Fb, bc = blk - lb * Fb;
+        const int rows = static_cast<int>(min(used - lb * 128, int64_t(128)));
+        float2 dg[kGluPer][4], du[kGluPer][4];
+        uint32_t mg = 0, mu = 0;
 #pragma unroll
-    for (int i = 0; i < kGluPer; ++i) {
-        float2 g[4], u[4], d[4];
-        e4m3x4_to_f32(cg[i].x, g[0], g[1]);
-        e4m3x4_to_f32(cg[i].y, g[2], g[3]);
-        e4m3x4_to_f32(cu[i].x, u[0], u[1]);
-        e4m3x4_to_f32(cu[i].y, u[2], u[3]);
-        bf16x8_to_f32(va[i], d);
+        for (int i = 0; i < kGluPer; ++i) {
+            const int r = sub + 32 * i;
+            const bool ok = r < rows;
+            const uint2 cg = ok ? st.cg[i][tid] : make_uint2(0, 0), cu = ok ? st.cu[i][tid] : make_uint2(0, 0);
+            const uint4 va = ok ? st.da[i][tid] : make_uint4(0, 0, 0, 0);
+            const float sg = ok ? st.scale[0][r] : 0.0f, su = ok ? st.scale[1][r] : 0.0f;
+            float2 g[4], u[4], d[4];
+            e4m3x4_to_f32(cg.x, g[0], g[1]);
+            e4m3x4_to_f32(cg.y, g[2], g[3]);
+            e4m3x4_to_f32(cu.x, u[0], u[1]);
+            e4m3x4_to_f32(cu.y, u[2], u[3]);
+            bf16x8_to_f32(va, d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float gx = g[j].x * sg[i], gy = g[j].y * sg[i];
-            const float ux = u[j].x * su[i], uy = u[j].y * su[i];
-            const float px = sigmoid_f32(gx), py = sigmoid_f32(gy);
-            dg[i][j] = make_float2(d[j].x * ux * px * (1.0f + gx * (1.0f - px)),
-                                   d[j].y * uy * py * (1.0f + gy * (1.0f - py)));
-            du[i][j] = make_float2(d[j].x * gx * px, d[j].y * gy * py);
-            mg = amax_fold_f32(mg, dg[i][j]);
-            mu = amax_fold_f32(mu, du[i][j]);
+            for (int j = 0; j < 4; ++j) {
+                const float2 gs = __fmul2_rn(g[j], make_float2(sg, sg)), us = __fmul2_rn(u[j], make_float2(su, su));
+                const float2 p = sigmoid2(gs);
+                const float2 t = __fmul2_rn(d[j], p);
+                const float2 np = make_float2(1.0f - p.x, 1.0f - p.y);
+                du[i][j] = __fmul2_rn(t, gs);
+                dg[i][j] = __fmul2_rn(__fmul2_rn(t, us), __ffma2_rn(gs, np, make_float2(1.0f, 1.0f)));
+                mg = amax_fold_f32(mg, dg[i][j]);
+                mu = amax_fold_f32(mu, du[i][j]);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            mg = max(mg, __shfl_xor_sync(0xFFFFFFFFu, mg, o));
+            mu = max(mu, __shfl_xor_sync(0xFFFFFFFFu, mu, o));
+        }
+        if ((tid & 31) == 0) {
+            red[par][0][tid >> 5] = mg;
+            red[par][1][tid >> 5] = mu;
+        }
+        __syncthreads();
+        mg = red[par][0][lane16];
+        mu = red[par][1][lane16];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            mg = max(mg, __shfl_xor_sync(0xFFFFFFFFu, mg, o));
+            mu = max(mu, __shfl_xor_sync(0xFFFFFFFFu, mu, o));
+        }
+        const NearScale bg = near_scale(mg), bu = near_scale(mu);
+        if (tid == 0) {
+            S[lb * 2 * Fb + bc] = bg.s;
+            S[lb * 2 * Fb + Fb + bc] = bu.s;
+        }
+        uint8_t *q = Q + (lb * 128 + sub) * 2 * F + bc * 128 + lane16 * 8;
+#pragma unroll
+        for (int i = 0; i < kGluPer; ++i) {
+            if (sub + 32 * i < rows) {
+                *reinterpret_cast<uint2 *>(q + i * 64 * F) = quantize8_near(dg[i], bg);
+                *reinterpret_cast<uint2 *>(q + i * 64 * F + F) = quantize8_near(du[i], bu);
+            }
         }
     }
-    const BlockScale bg = block_scale_f32(__uint_as_float(cta_max<kGluThreads / 32>(mg, red[0])));
-    const BlockScale bu = block_scale_f32(__uint_as_float(cta_max<kGluThreads / 32>(mu, red[1])));
-    if (tid == 0) {
-        S[lb * 2 * Fb + bc] = bg.s;
-        S[lb * 2 * Fb + Fb + bc] = bu.s;
-    }
-#pragma unroll
-    for (int i = 0; i < kGluPer; ++i) {
-        const int r = sub + 32 * i;
-        if (r < rows) {
-            uint8_t *q = Q + (lb * 128 + r) * 2 * F + col;
-            *reinterpret_cast<uint2 *>(q) = quantize8_f32(dg[i], bg);
-            *reinterpret_cast<uint2 *>(q + F) = quantize8_f32(du[i], bu);
-        }
-    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
+static_assert(kGluThreads / 32 == 16, "the reduction over warps uses 16 lanes");
 
 dg_status_t launch_swiglu(const void *H, const int32_t *offsets, const int32_t *masked_m, int G, int64_t M,
                           int64_t F, uint8_t *Q, float *S, uint8_t *H8, float *sH, cudaStream_t stream) {
@@ -207,10 +282,21 @@ dg_status_t launch_swiglu(const void *H, const int32_t *offsets, const int32_t *
 }
 
 dg_status_t launch_swiglu_backward(const uint8_t *H8, const float *sH, const void *dA, const int32_t *offsets,
-                                   int G, int64_t M, int64_t F, uint8_t *Q, float *S, cudaStream_t stream) {
-    const int64_t n = (M + 127) / 128 * (F / 128);
-    if (n > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
-    return launch_pdl(swiglu_backward_kernel, static_cast<int>(n), kGluThreads, 0, stream, H8, sH,
+                                   int G, int64_t M, int64_t F, uint8_t *Q, float *S, const DeviceInfo &dev,
+                                   cudaStream_t stream) {
+    const int64_t blocks = (M + 127) / 128 * (F / 128);
+    const size_t smem = 2 * sizeof(GluBackSmem);
+    static thread_local int configured_device = -1;
+    int device = 0;
+    cudaGetDevice(&device);
+    if (configured_device != device) {
+        if (cudaFuncSetAttribute(swiglu_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(smem)) != cudaSuccess)
+            return DG_ERR_CUDA;
+        configured_device = device;
+    }
+    const int n = static_cast<int>(blocks < dev.num_sms ? blocks : dev.num_sms);
+    return launch_pdl(swiglu_backward_kernel, n, kGluThreads, smem, stream, H8, sH,
                       static_cast<const uint16_t *>(dA), offsets, G, M, F, Q, S);
 }
 
