@@ -11,6 +11,7 @@ namespace {
 
 constexpr int64_t kInt32Max = 0x7FFFFFFFLL;
 constexpr int64_t kMaxSlots = 1LL << 30;
+constexpr int64_t kMaxWidth = 1LL << 24;  // SwiGLU: a block's rows are addressed with 32 bits
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -116,7 +117,7 @@ dg_status_t dg_moe_combine_backward(const void *dOUT_bf16, const void *Y_bf16, c
 
 dg_status_t dg_swiglu_quantize(const void *H_bf16, const int32_t *group_offsets, int G, int64_t M, int64_t F,
                                uint8_t *Q, float *S, uint8_t *H8, float *sH_t, cudaStream_t stream) {
-    if (M < 0 || M > kInt32Max || F < 0 || F % 128 != 0) return DG_ERR_SHAPE;
+    if (M < 0 || M > kInt32Max || F < 0 || F > kMaxWidth || F % 128 != 0) return DG_ERR_SHAPE;
     if (group_offsets && (G < 1 || G > 1024 || M % 128 != 0)) return DG_ERR_SHAPE;
     if (M == 0 || F == 0) return DG_OK;
     if (!H_bf16 || !Q || !S || (H8 == nullptr) != (sH_t == nullptr)) return DG_ERR_INVALID_ARG;
@@ -126,25 +127,25 @@ dg_status_t dg_swiglu_quantize(const void *H_bf16, const int32_t *group_offsets,
     DeviceInfo dev;
     const dg_status_t st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
-    return launch_swiglu(H_bf16, group_offsets, nullptr, G, M, F, Q, S, H8, sH_t, stream);
+    return launch_swiglu(H_bf16, group_offsets, nullptr, G, M, F, Q, S, H8, sH_t, dev, stream);
 }
 
 dg_status_t dg_swiglu_quantize_masked(const void *H_bf16, const int32_t *masked_m, int G, int64_t M_max, int64_t F,
                                       uint8_t *Q, float *S, cudaStream_t stream) {
-    if (G < 1 || G > 1024 || M_max < 0 || M_max > kInt32Max / G || F < 0 || F % 128 != 0) return DG_ERR_SHAPE;
+    if (G < 1 || G > 1024 || M_max < 0 || M_max > kInt32Max / G || F < 0 || F > kMaxWidth || F % 128 != 0) return DG_ERR_SHAPE;
     if (M_max == 0 || F == 0) return DG_OK;
     if (!H_bf16 || !masked_m || !Q || !S) return DG_ERR_INVALID_ARG;
     if (!aligned(H_bf16, 16) || !aligned(Q, 16) || !aligned(S, 4) || !aligned(masked_m, 4)) return DG_ERR_ALIGNMENT;
     DeviceInfo dev;
     const dg_status_t st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
-    return launch_swiglu(H_bf16, nullptr, masked_m, G, M_max, F, Q, S, nullptr, nullptr, stream);
+    return launch_swiglu(H_bf16, nullptr, masked_m, G, M_max, F, Q, S, nullptr, nullptr, dev, stream);
 }
 
 dg_status_t dg_swiglu_quantize_backward(const uint8_t *H8, const float *sH_t, const void *dA_bf16,
                                         const int32_t *group_offsets, int G, int64_t M, int64_t F, uint8_t *Q,
                                         float *S, cudaStream_t stream) {
-    if (M < 0 || M > kInt32Max || F < 0 || F % 128 != 0) return DG_ERR_SHAPE;
+    if (M < 0 || M > kInt32Max || F < 0 || F > kMaxWidth || F % 128 != 0) return DG_ERR_SHAPE;
     if (group_offsets && (G < 1 || G > 1024 || M % 128 != 0)) return DG_ERR_SHAPE;
     if (M == 0 || F == 0) return DG_OK;
     if (!H8 || !sH_t || !dA_bf16 || !Q || !S) return DG_ERR_INVALID_ARG;

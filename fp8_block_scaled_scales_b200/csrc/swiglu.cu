@@ -20,198 +20,287 @@
 
 namespace dg {
 
-constexpr int kGluThreads = 512;  // 16 lanes a row, 32 rows at a time, 4 times
+constexpr int kGluThreads = 512;      // forward: 16 lanes a row, 32 rows at a time, 4 times
 constexpr int kGluPer = 4;
-constexpr int64_t kGluMaskedRowCtas = 16;
+constexpr int kGluBackThreads = 512;   // backward: 32 rows at a time, four times
+constexpr int kGluBackPer = 4;
 
-// sigma of two values; exp overflows to infinity for x < -88, whose reciprocal is 0
+// sigma of two values, one exponential and one reciprocal instruction each.  exp2 overflows to
+// infinity for x < -88, whose reciprocal is 0; 1 + e is never subnormal.
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
-    const float2 e = make_float2(__expf(-x.x), __expf(-x.y));
-    return make_float2(__fdividef(1.0f, 1.0f + e.x), __fdividef(1.0f, 1.0f + e.y));
+    const float2 t = __fmul2_rn(x, make_float2(-1.44269504f, -1.44269504f));  // -log2 e
+    float2 e, p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(e.y));
+    return p;
 }
 
-// One row group of 128 columns (16 lanes, 8 values each) as a 1 x 128 block: codes to *q, the
-// scale to *s by the first lane.  All lanes of the warp call it.
-__device__ __forceinline__ void checkpoint_row(uint4 v, bool ok, bool first, uint8_t *q, float *s) {
-    uint32_t bits = amax_bits_of(amax_fold8(0u, v));
+// Two rows of h, 128 columns of the gate and of the up half each, as four 1 x 128 blocks
+// (16 lanes a row, 8 values each).  The four maxima are found together (gate and up packed
+// in one word), lane j of a row divides for block j only, and scales and reciprocals are
+// passed round: a division per lane and block made up a sixth of all instructions.  All lanes of
+// the warp call it; ok[i]: row i exists.  q + in_q, s + in_s: the first
+// row's gate codes and scale; the up half lies q_up codes and s_up scales on, the second
+// row q_row codes and 32 scales on.
+__device__ __forceinline__ void checkpoint_rows(const uint4 (&vg)[2], const uint4 (&vu)[2], const bool (&ok)[2],
+                                                uint8_t *q, uint32_t in_q, int64_t q_up, int64_t q_row, float *s,
+                                                int in_s, int64_t s_up) {
+    uint32_t pk[2];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
-    const BlockScale bs = block_scale(bits);
-    if (ok) {
-        *reinterpret_cast<uint2 *>(q) = quantize8(v, bs);
-        if (first) *s = bs.s;
+    for (int i = 0; i < 2; ++i)
+        pk[i] = amax_bits_of(amax_pair8(vg[i])) | amax_bits_of(amax_pair8(vu[i])) << 16;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) pk[i] = __vmaxu2(pk[i], __shfl_xor_sync(0xFFFFFFFFu, pk[i], o));
     }
-}
-
-// Rows row0 .. row0 + rows - 1 (at most 128) of h [.][2F], column block bc of both halves.
-// M: rows of the checkpoint's scale array.  Rows are taken two at a time: with all four
-// loaded first the 64 registers that let two CTAs share an SM spill (386 us against
-// 0.07 ms of traffic on 16384 x 4096), and two rows of both CTAs keep 64 KB in flight.
-template <bool CKPT>
-__device__ __forceinline__ void glu_block(const uint16_t *__restrict__ Hin, int64_t F, int64_t M, int64_t row0,
-                                          int rows, int64_t bc, uint8_t *__restrict__ Q, float *__restrict__ Sp,
-                                          uint8_t *__restrict__ H8, float *__restrict__ sH, uint32_t *red) {
-    const int tid = static_cast<int>(threadIdx.x);
-    const int64_t col = bc * 128 + (tid & 15) * 8;
-    const int sub = tid >> 4;
-    const bool first = (tid & 15) == 0;
-    const int64_t at = (row0 + sub) * 2 * F + col, step = 64 * F;  // 32 rows of h
-    const uint16_t *p = Hin + at;
-    uint8_t *p8 = CKPT ? H8 + at : nullptr;
-    float *ps = CKPT ? sH + bc * M + row0 + sub : nullptr;
-    float2 a[kGluPer][4];
-    uint32_t m = 0;
+    const int lane = lane_id(), j = lane & 3;
+    const uint32_t two = (j & 2) ? pk[1] : pk[0];
+    const float amax = __uint_as_float((j & 1) ? (two & 0xFFFF0000u) : (two << 16));
+    const float scale = (amax == 0.0f) ? 1.0f : __fdiv_rn(amax, 448.0f);
+    const float r = __frcp_rn(scale);
+    if ((lane & 15) < 4 && ok[j >> 1]) s[in_s + (j >> 1) * 32 + (j & 1) * s_up] = scale;
 #pragma unroll
-    for (int i0 = 0; i0 < kGluPer; i0 += 2) {
-        uint4 vg[2], vu[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool ok = sub + 32 * (i0 + i) < rows;
-            vg[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(p + (i0 + i) * step)) : make_uint4(0, 0, 0, 0);
-            vu[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(p + (i0 + i) * step + F)) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float2 g[4], u[4];
-            bf16x8_to_f32(vg[i], g);
-            bf16x8_to_f32(vu[i], u);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 x = __fmul2_rn(__fmul2_rn(g[j], sigmoid2(g[j])), u[j]);
-                m = amax_fold_f32(m, x);
-                a[i0 + i][j] = x;
-            }
-            if (CKPT) {
-                const bool ok = sub + 32 * (i0 + i) < rows;
-                uint8_t *q = p8 + (i0 + i) * step;
-                float *sp = ps + 32 * (i0 + i);
-                checkpoint_row(vg[i], ok, first, q, sp);
-                checkpoint_row(vu[i], ok, first, q + F, sp + (F / 128) * M);
-            }
+    for (int i = 0; i < 2; ++i) {
+        const int from = (lane & 16) + 2 * i;
+        const float sg = __shfl_sync(0xFFFFFFFFu, scale, from), rg = __shfl_sync(0xFFFFFFFFu, r, from);
+        const float su = __shfl_sync(0xFFFFFFFFu, scale, from + 1), ru = __shfl_sync(0xFFFFFFFFu, r, from + 1);
+        if (ok[i]) {
+            *reinterpret_cast<uint2 *>(q + i * q_row + in_q) = quantize8_corrected(vg[i], sg, rg);
+            *reinterpret_cast<uint2 *>(q + i * q_row + q_up + in_q) = quantize8_corrected(vu[i], su, ru);
         }
     }
-    const NearScale bs = near_scale(cta_max<kGluThreads / 32>(m, red));
-    if (tid == 0) *Sp = bs.s;
-    uint8_t *q = Q + (row0 + sub) * F + col;
-#pragma unroll
-    for (int i = 0; i < kGluPer; ++i)
-        if (sub + 32 * i < rows) *reinterpret_cast<uint2 *>(q + i * (step >> 1)) = quantize8_near(a[i], bs);
 }
 
-// rows of the layout that hold something: all M, or up to the last expert's end
-__device__ __forceinline__ int64_t used_rows(const int32_t *offsets, int G, int64_t M) {
-    return offsets ? min(max(static_cast<int64_t>(__ldg(offsets + G)), int64_t(0)), M) : M;
+// 16- and 8-byte copies to shared memory that the thread waits for later.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-
-template <bool CKPT>
-__global__ void __launch_bounds__(kGluThreads, 2)
-    swiglu_kernel(const uint16_t *__restrict__ Hin, const int32_t *__restrict__ offsets, int G, int64_t M, int64_t F,
-                  uint8_t *__restrict__ Q, float *__restrict__ S, uint8_t *__restrict__ H8, float *__restrict__ sH) {
-    __shared__ uint32_t red[kGluThreads / 32];
-    grid_dep_launch_dependents();
-    grid_dep_wait();
-    const int64_t Fb = F / 128, blk = blockIdx.x;
-    const int64_t lb = blk / Fb, bc = blk - lb * Fb;
-    const int64_t left = used_rows(offsets, G, M) - lb * 128;
-    if (left <= 0) return;
-    glu_block<CKPT>(Hin, F, M, lb * 128, static_cast<int>(min(left, int64_t(128))), bc, Q, S + blk, H8, sH, red);
-}
-
-__global__ void __launch_bounds__(kGluThreads, 2)
-    swiglu_masked_kernel(const uint16_t *__restrict__ Hin, const int32_t *__restrict__ masked_m, int64_t M, int64_t F,
-                         int64_t Rb, int64_t Ry, uint8_t *__restrict__ Q, float *__restrict__ S) {
-    __shared__ uint32_t red[2][kGluThreads / 32];
-    grid_dep_launch_dependents();
-    grid_dep_wait();
-    const int64_t Fb = F / 128, blk = blockIdx.x;
-    const int64_t gy = blk / Fb, bc = blk - gy * Fb;
-    const int64_t g = gy / Ry, y = gy - g * Ry;
-    const int64_t rows = min(max(static_cast<int64_t>(__ldg(masked_m + g)), int64_t(0)), M);
-    int par = 0;
-    for (int64_t lb = y; lb * 128 < rows; lb += Ry) {
-        glu_block<false>(Hin, F, M, g * M + lb * 128, static_cast<int>(min(rows - lb * 128, int64_t(128))), bc, Q,
-                         S + (g * Rb + lb) * Fb + bc, nullptr, nullptr, red[par]);
-        par ^= 1;
-    }
-}
-
-// Backward: one persistent CTA per SM.  A block's [dg | du] in FP32 is half the register
-// file, so no second CTA fits beside it; instead every thread copies its own piece of the
-// next block into shared memory (cp.async) before it computes the current one, so loads
-// run under the arithmetic.
-struct GluBackSmem {
-    uint2 cg[kGluPer][kGluThreads];
-    uint2 cu[kGluPer][kGluThreads];
-    uint4 da[kGluPer][kGluThreads];
-    float scale[2][128];  // the block's row scales, gate then up
-};
-
-__device__ __forceinline__ void cp_async(void *dst, const void *src, int bytes_8_or_16) {
-    if (bytes_8_or_16 == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async8(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-__global__ void __launch_bounds__(kGluThreads, 1)
-    swiglu_backward_kernel(const uint8_t *__restrict__ H8, const float *__restrict__ sH,
-                           const uint16_t *__restrict__ dA, const int32_t *__restrict__ offsets, int G, int64_t M,
-                           int64_t F, uint8_t *__restrict__ Q, float *__restrict__ S) {
+// The row blocks of a layout: G slabs of M rows (dense and contiguous: one), of which the
+// first ones hold something: all M, or up to the last expert's end, or the slab's count.
+struct GluRows {
+    const int32_t *offsets, *masked_m;  // at most one
+    int G, M;                           // G * M < 2^31
+    int Rb, Fb;                         // 128-row blocks of a slab, 128-column blocks
+};
+
+// A CTA's walk over the blocks (row block rb of all slabs, column block bc), every gridDim-th
+// one, without a division per step.
+struct GluWalk {
+    int rb, bc, step_rb, step_bc, end_rb;
+    int used;  // dense and contiguous: rows that hold something
+
+    __device__ __forceinline__ void start(const GluRows &l) {
+        const int grid = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
+        rb = first / l.Fb;
+        bc = first - rb * l.Fb;
+        step_rb = grid / l.Fb;
+        step_bc = grid - step_rb * l.Fb;
+        used = l.offsets ? min(max(__ldg(l.offsets + l.G), 0), l.M) : l.M;
+        end_rb = l.masked_m ? l.G * l.Rb : (used >> 7) + ((used & 127) != 0);
+    }
+    __device__ __forceinline__ void advance(const GluRows &l) {
+        rb += step_rb;
+        bc += step_bc;
+        if (bc >= l.Fb) {
+            bc -= l.Fb;
+            ++rb;
+        }
+    }
+    // First row of block rb in the whole matrix, and its rows that hold something (0: none).
+    __device__ __forceinline__ int rows(const GluRows &l, int &row0) const {
+        if (!l.masked_m) {
+            row0 = rb * 128;
+            return min(used - row0, 128);
+        }
+        const int g = rb / l.Rb, at = (rb - g * l.Rb) * 128;
+        row0 = g * l.M + at;
+        return min(max(min(__ldg(l.masked_m + g), l.M) - at, 0), 128);
+    }
+    // To the next block, this one included, that holds something; false: there is none.
+    __device__ __forceinline__ bool find(const GluRows &l, int &row0, int &n) {
+        for (; rb < end_rb; advance(l)) {
+            n = rows(l, row0);
+            if (n > 0) return true;
+        }
+        return false;
+    }
+};
+
+// Forward, persistent: two CTAs per SM walk over the blocks.  A thread keeps its 16-byte
+// pieces of a block in shared memory and asks for the same pieces of the next block as soon
+// as it has read them, so loads run under the arithmetic, the block maximum and the stores
+// without costing registers (a CTA per block that loaded into registers: 124 us on 16384 x
+// 4096, and 386 us while it held all four rows at once and spilled).
+struct GluSmem {
+    uint4 g[kGluPer][kGluThreads];
+    uint4 u[kGluPer][kGluThreads];
+};
+
+template <bool CKPT>
+__global__ void __launch_bounds__(kGluThreads, 2)
+    swiglu_kernel(const uint16_t *__restrict__ Hin, const GluRows layout, uint8_t *__restrict__ Q,
+                  float *__restrict__ S, uint8_t *__restrict__ H8, float *__restrict__ sH) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    GluBackSmem *stage = reinterpret_cast<GluBackSmem *>(smem_raw);
-    __shared__ uint32_t red[2][2][kGluThreads / 32];
+    GluSmem &st = *reinterpret_cast<GluSmem *>(smem_raw);
+    __shared__ uint32_t red[2][kGluThreads / 32];
     grid_dep_launch_dependents();
     grid_dep_wait();
     const int tid = static_cast<int>(threadIdx.x);
-    const int lane16 = tid & 15, sub = tid >> 4;
-    const int64_t Fb = F / 128;
-    const int64_t used = used_rows(offsets, G, M);
-    const int64_t blocks = (used + 127) / 128 * Fb;
+    const int sub = tid >> 4;
+    const int64_t F = static_cast<int64_t>(layout.Fb) * 128;
+    const int64_t step = 64 * F;  // 32 rows of h
+    // this thread's place in a block of h and of Q; the block's own address is the same for all
+    const uint32_t in_h = sub * 2 * static_cast<uint32_t>(F) + (tid & 15) * 8;
+    const uint32_t in_q = sub * static_cast<uint32_t>(F) + (tid & 15) * 8;
 
-    auto prefetch = [&](int64_t blk, GluBackSmem &st) {
-        if (blk < blocks) {
-            const int64_t lb = blk / Fb, bc = blk - lb * Fb;
-            const int rows = static_cast<int>(min(used - lb * 128, int64_t(128)));
-            const int64_t row = lb * 128 + sub, col = bc * 128 + lane16 * 8;
-            const uint8_t *p = H8 + row * 2 * F + col;
-            const uint16_t *pa = dA + row * F + col;
-#pragma unroll
-            for (int i = 0; i < kGluPer; ++i) {
-                if (sub + 32 * i < rows) {
-                    cp_async(&st.cg[i][tid], p + i * 64 * F, 8);
-                    cp_async(&st.cu[i][tid], p + i * 64 * F + F, 8);
-                    cp_async(&st.da[i][tid], pa + i * 32 * F, 16);
-                }
-            }
-            if (tid < 256) {
-                const int r = tid & 127, half = tid >> 7;
-                if (r < rows) cp_async4(&st.scale[half][r], sH + (half * Fb + bc) * M + lb * 128 + r);
-            }
+    auto ask = [&](int i, int row0, int rows, int bc) {
+        if (sub + 32 * i < rows) {
+            const uint16_t *p = Hin + static_cast<int64_t>(row0) * 2 * F + bc * 128 + i * step;
+            cp_async16(&st.g[i][tid], p + in_h);
+            cp_async16(&st.u[i][tid], p + F + in_h);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    int par = 0;
-    prefetch(blockIdx.x, stage[0]);
-    for (int64_t blk = blockIdx.x; blk < blocks; blk += gridDim.x, par ^= 1) {
-        prefetch(blk + gridDim.x, stage[par ^ 1]);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();  // the scales come from other threads' copies
-        const GluBackSmem &st = stage[par];
-        const int64_t lb = blk / Fb, bc = blk - lb * Fb;
-        const int rows = static_cast<int>(min(used - lb * 128, int64_t(128)));
-        float2 dg[kGluPer][4], du[kGluPer][4];
-        uint32_t mg = 0, mu = 0;
+    GluWalk walk;
+    walk.start(layout);
+    int row0 = 0, rows = 0;
+    bool have = walk.find(layout, row0, rows);
+    if (have) {
 #pragma unroll
-        for (int i = 0; i < kGluPer; ++i) {
-            const int r = sub + 32 * i;
+        for (int i = 0; i < kGluPer; ++i) ask(i, row0, rows, walk.bc);
+    }
+    int par = 0;
+    while (have) {
+        const int rb = walk.rb, bc = walk.bc;
+        int next_row0 = 0, next_rows = 0;
+        walk.advance(layout);
+        const bool more = walk.find(layout, next_row0, next_rows);
+        if (!more) next_rows = 0;
+        float2 a[kGluPer][4];
+        float m = 0.0f;
+        cp_async_wait();
+#pragma unroll
+        for (int i0 = 0; i0 < kGluPer; i0 += 2) {
+            uint4 vg[2], vu[2];
+            const bool ok[2] = {sub + 32 * i0 < rows, sub + 32 * (i0 + 1) < rows};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                vg[i] = ok[i] ? st.g[i0 + i][tid] : make_uint4(0, 0, 0, 0);
+                vu[i] = ok[i] ? st.u[i0 + i][tid] : make_uint4(0, 0, 0, 0);
+            }
+            if (CKPT)
+                checkpoint_rows(vg, vu, ok, H8 + static_cast<int64_t>(row0) * 2 * F + bc * 128 + i0 * step, in_h, F,
+                                step, sH + static_cast<int64_t>(bc) * layout.M + row0 + 32 * i0, sub,
+                                static_cast<int64_t>(layout.Fb) * layout.M);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float2 g[4], u[4];
+                bf16x8_to_f32(vg[i], g);
+                bf16x8_to_f32(vu[i], u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = __fmul2_rn(__fmul2_rn(g[j], sigmoid2(g[j])), u[j]);
+                    m = amax3(m, x);
+                    a[i0 + i][j] = x;
+                }
+                ask(i0 + i, next_row0, next_rows, walk.bc);
+            }
+        }
+        const NearScale bs = near_scale(cta_max<kGluThreads / 32>(__float_as_uint(m), red[par]));
+        if (tid == 0) S[static_cast<int64_t>(rb) * layout.Fb + bc] = bs.s;
+        uint8_t *q = Q + static_cast<int64_t>(row0) * F + bc * 128;
+#pragma unroll
+        for (int i = 0; i < kGluPer; ++i)
+            if (sub + 32 * i < rows) *reinterpret_cast<uint2 *>(q + i * (step >> 1) + in_q) = quantize8_near(a[i], bs);
+        have = more;
+        row0 = next_row0;
+        rows = next_rows;
+        par ^= 1;
+    }
+}
+
+// Backward, persistent, one CTA per SM: a block's [dg | du] in FP32 is half the register
+// file.  Pieces of the next block are asked for as in the forward kernel; the row scales,
+// which other threads copy, alternate between two buffers.
+struct GluBackSmem {
+    uint4 da[kGluBackPer][kGluBackThreads];
+    uint2 cg[kGluBackPer][kGluBackThreads];
+    uint2 cu[kGluBackPer][kGluBackThreads];
+    float scale[2][2][128];  // [buffer][gate, up][row]
+};
+
+__global__ void __launch_bounds__(kGluBackThreads, 1)
+    swiglu_backward_kernel(const uint8_t *__restrict__ H8, const float *__restrict__ sH,
+                           const uint16_t *__restrict__ dA, const GluRows layout, uint8_t *__restrict__ Q,
+                           float *__restrict__ S) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    GluBackSmem &st = *reinterpret_cast<GluBackSmem *>(smem_raw);
+    __shared__ uint32_t red[2][2][kGluBackThreads / 32];
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    constexpr int kRows = kGluBackThreads / 16;  // rows at a time
+    const int tid = static_cast<int>(threadIdx.x);
+    const int sub = tid >> 4, lane_col = (tid & 15) * 8;
+    const int64_t F = static_cast<int64_t>(layout.Fb) * 128;
+
+    const uint32_t in_h = sub * 2 * static_cast<uint32_t>(F) + lane_col;  // this thread's place in a block
+    const uint32_t in_a = sub * static_cast<uint32_t>(F) + lane_col;
+
+    // one row piece and, with the first, this thread's share of the block's scales
+    auto ask = [&](int i, int row0, int rows, int bc, int buffer) {
+        if (sub + kRows * i < rows) {
+            const int64_t row = row0 + kRows * i;
+            const uint8_t *p = H8 + row * 2 * F + bc * 128;
+            cp_async8(&st.cg[i][tid], p + in_h);
+            cp_async8(&st.cu[i][tid], p + F + in_h);
+            cp_async16(&st.da[i][tid], dA + row * F + bc * 128 + in_a);
+        }
+        if (i == 0 && tid < 256) {
+            const int r = tid & 127, half = tid >> 7;
+            if (r < rows)
+                cp_async4(&st.scale[buffer][half][r],
+                          sH + static_cast<int64_t>(half * layout.Fb + bc) * layout.M + row0 + r);
+        }
+    };
+
+    GluWalk walk;
+    walk.start(layout);
+    int row0 = 0, rows = 0;
+    bool have = walk.find(layout, row0, rows);
+    if (have) {
+#pragma unroll
+        for (int i = 0; i < kGluBackPer; ++i) ask(i, row0, rows, walk.bc, 0);
+    }
+    int par = 0;
+    while (have) {
+        const int rb = walk.rb, bc = walk.bc;
+        int next_row0 = 0, next_rows = 0;
+        walk.advance(layout);
+        const bool more = walk.find(layout, next_row0, next_rows);
+        if (!more) next_rows = 0;
+        cp_async_wait();
+        __syncthreads();  // the scales come from other threads' copies
+        float2 dg[kGluBackPer][4], du[kGluBackPer][4];
+        float ag = 0.0f, au = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kGluBackPer; ++i) {
+            const int r = sub + kRows * i;
             const bool ok = r < rows;
             const uint2 cg = ok ? st.cg[i][tid] : make_uint2(0, 0), cu = ok ? st.cu[i][tid] : make_uint2(0, 0);
             const uint4 va = ok ? st.da[i][tid] : make_uint4(0, 0, 0, 0);
-            const float sg = ok ? st.scale[0][r] : 0.0f, su = ok ? st.scale[1][r] : 0.0f;
+            const float sg = ok ? st.scale[par][0][r] : 0.0f, su = ok ? st.scale[par][1][r] : 0.0f;
             float2 g[4], u[4], d[4];
             e4m3x4_to_f32(cg.x, g[0], g[1]);
             e4m3x4_to_f32(cg.y, g[2], g[3]);
@@ -223,13 +312,15 @@ __global__ void __launch_bounds__(kGluThreads, 1)
                 const float2 gs = __fmul2_rn(g[j], make_float2(sg, sg)), us = __fmul2_rn(u[j], make_float2(su, su));
                 const float2 p = sigmoid2(gs);
                 const float2 t = __fmul2_rn(d[j], p);
-                const float2 np = make_float2(1.0f - p.x, 1.0f - p.y);
+                const float2 np = __ffma2_rn(p, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
                 du[i][j] = __fmul2_rn(t, gs);
                 dg[i][j] = __fmul2_rn(__fmul2_rn(t, us), __ffma2_rn(gs, np, make_float2(1.0f, 1.0f)));
-                mg = amax_fold_f32(mg, dg[i][j]);
-                mu = amax_fold_f32(mu, du[i][j]);
+                ag = amax3(ag, dg[i][j]);
+                au = amax3(au, du[i][j]);
             }
+            ask(i, next_row0, next_rows, walk.bc, par ^ 1);
         }
+        uint32_t mg = __float_as_uint(ag), mu = __float_as_uint(au);  // NaN above infinity
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             mg = max(mg, __shfl_xor_sync(0xFFFFFFFFu, mg, o));
@@ -240,64 +331,82 @@ __global__ void __launch_bounds__(kGluThreads, 1)
             red[par][1][tid >> 5] = mu;
         }
         __syncthreads();
-        mg = red[par][0][lane16];
-        mu = red[par][1][lane16];
+        constexpr int kWarps = kGluBackThreads / 32;
+        mg = red[par][0][tid & (kWarps - 1)];
+        mu = red[par][1][tid & (kWarps - 1)];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
+        for (int o = kWarps / 2; o > 0; o >>= 1) {
             mg = max(mg, __shfl_xor_sync(0xFFFFFFFFu, mg, o));
             mu = max(mu, __shfl_xor_sync(0xFFFFFFFFu, mu, o));
         }
         const NearScale bg = near_scale(mg), bu = near_scale(mu);
         if (tid == 0) {
-            S[lb * 2 * Fb + bc] = bg.s;
-            S[lb * 2 * Fb + Fb + bc] = bu.s;
+            float *sp = S + static_cast<int64_t>(rb) * 2 * layout.Fb + bc;
+            sp[0] = bg.s;
+            sp[layout.Fb] = bu.s;
         }
-        uint8_t *q = Q + (lb * 128 + sub) * 2 * F + bc * 128 + lane16 * 8;
+        uint8_t *q = Q + static_cast<int64_t>(row0) * 2 * F + bc * 128;
 #pragma unroll
-        for (int i = 0; i < kGluPer; ++i) {
-            if (sub + 32 * i < rows) {
-                *reinterpret_cast<uint2 *>(q + i * 64 * F) = quantize8_near(dg[i], bg);
-                *reinterpret_cast<uint2 *>(q + i * 64 * F + F) = quantize8_near(du[i], bu);
+        for (int i = 0; i < kGluBackPer; ++i) {
+            if (sub + kRows * i < rows) {
+                *reinterpret_cast<uint2 *>(q + i * kRows * 2 * F + in_h) = quantize8_near(dg[i], bg);
+                *reinterpret_cast<uint2 *>(q + i * kRows * 2 * F + F + in_h) = quantize8_near(du[i], bu);
             }
         }
+        have = more;
+        row0 = next_row0;
+        rows = next_rows;
+        par ^= 1;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
-static_assert(kGluThreads / 32 == 16, "the reduction over warps uses 16 lanes");
+static_assert(kGluBackThreads == 512 || kGluBackThreads == 1024, "the reduction over warps uses 16 or 32 lanes");
+
+// Dynamic shared memory above the default needs the kernel's consent, once per device and thread.
+template <typename Kernel>
+static dg_status_t allow_smem(Kernel kernel, size_t bytes, int &configured_device) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return DG_ERR_CUDA;
+    if (configured_device == device) return DG_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
+        cudaSuccess)
+        return DG_ERR_CUDA;
+    configured_device = device;
+    return DG_OK;
+}
+
+template <bool CKPT>
+static dg_status_t launch_swiglu_impl(const uint16_t *h, const GluRows &layout, int64_t blocks, uint8_t *Q, float *S,
+                                      uint8_t *H8, float *sH, const DeviceInfo &dev, cudaStream_t stream) {
+    static thread_local int configured_device = -1;
+    const dg_status_t st = allow_smem(swiglu_kernel<CKPT>, sizeof(GluSmem), configured_device);
+    if (st != DG_OK) return st;
+    const int grid = static_cast<int>(blocks < 2 * dev.num_sms ? blocks : 2 * dev.num_sms);
+    return launch_pdl(swiglu_kernel<CKPT>, grid, kGluThreads, sizeof(GluSmem), stream, h, layout, Q, S, H8, sH);
+}
 
 dg_status_t launch_swiglu(const void *H, const int32_t *offsets, const int32_t *masked_m, int G, int64_t M,
-                          int64_t F, uint8_t *Q, float *S, uint8_t *H8, float *sH, cudaStream_t stream) {
-    const int64_t Rb = (M + 127) / 128, Fb = F / 128;
+                          int64_t F, uint8_t *Q, float *S, uint8_t *H8, float *sH, const DeviceInfo &dev,
+                          cudaStream_t stream) {
+    const int64_t Rb = (M + 127) / 128, Fb = F / 128, blocks = (masked_m ? G : 1) * Rb * Fb;
+    if (blocks > 0x3FFFFFFFLL) return DG_ERR_SHAPE;
+    const GluRows layout = {offsets, masked_m, G, static_cast<int>(M), static_cast<int>(Rb), static_cast<int>(Fb)};
     const uint16_t *h = static_cast<const uint16_t *>(H);
-    if (masked_m) {
-        const int64_t Ry = Rb < kGluMaskedRowCtas ? Rb : kGluMaskedRowCtas;
-        if (G * Ry * Fb > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
-        return launch_pdl(swiglu_masked_kernel, static_cast<int>(G * Ry * Fb), kGluThreads, 0, stream, h, masked_m, M,
-                          F, Rb, Ry, Q, S);
-    }
-    if (Rb * Fb > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
-    const int n = static_cast<int>(Rb * Fb);
-    if (H8) return launch_pdl(swiglu_kernel<true>, n, kGluThreads, 0, stream, h, offsets, G, M, F, Q, S, H8, sH);
-    return launch_pdl(swiglu_kernel<false>, n, kGluThreads, 0, stream, h, offsets, G, M, F, Q, S, H8, sH);
+    return H8 ? launch_swiglu_impl<true>(h, layout, blocks, Q, S, H8, sH, dev, stream)
+              : launch_swiglu_impl<false>(h, layout, blocks, Q, S, H8, sH, dev, stream);
 }
 
 dg_status_t launch_swiglu_backward(const uint8_t *H8, const float *sH, const void *dA, const int32_t *offsets,
                                    int G, int64_t M, int64_t F, uint8_t *Q, float *S, const DeviceInfo &dev,
                                    cudaStream_t stream) {
-    const int64_t blocks = (M + 127) / 128 * (F / 128);
-    const size_t smem = 2 * sizeof(GluBackSmem);
+    const int64_t Rb = (M + 127) / 128, Fb = F / 128, blocks = Rb * Fb;
+    if (blocks > 0x3FFFFFFFLL) return DG_ERR_SHAPE;
+    const GluRows layout = {offsets, nullptr, G, static_cast<int>(M), static_cast<int>(Rb), static_cast<int>(Fb)};
     static thread_local int configured_device = -1;
-    int device = 0;
-    cudaGetDevice(&device);
-    if (configured_device != device) {
-        if (cudaFuncSetAttribute(swiglu_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem)) != cudaSuccess)
-            return DG_ERR_CUDA;
-        configured_device = device;
-    }
-    const int n = static_cast<int>(blocks < dev.num_sms ? blocks : dev.num_sms);
-    return launch_pdl(swiglu_backward_kernel, n, kGluThreads, smem, stream, H8, sH,
-                      static_cast<const uint16_t *>(dA), offsets, G, M, F, Q, S);
+    const dg_status_t st = allow_smem(swiglu_backward_kernel, sizeof(GluBackSmem), configured_device);
+    if (st != DG_OK) return st;
+    const int grid = static_cast<int>(blocks < dev.num_sms ? blocks : dev.num_sms);
+    return launch_pdl(swiglu_backward_kernel, grid, kGluBackThreads, sizeof(GluBackSmem), stream, H8, sH,
+                      static_cast<const uint16_t *>(dA), layout, Q, S);
 }
 
 }  // namespace dg

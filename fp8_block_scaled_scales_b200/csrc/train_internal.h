@@ -26,7 +26,8 @@ dg_status_t launch_combine_backward(const void *dout, const void *Y, const int32
 
 // swiglu.cu.  offsets may be null (all M rows); masked_m selects the masked layout (G slabs of M rows).
 dg_status_t launch_swiglu(const void *H, const int32_t *offsets, const int32_t *masked_m, int G, int64_t M,
-                          int64_t F, uint8_t *Q, float *S, uint8_t *H8, float *sH, cudaStream_t stream);
+                          int64_t F, uint8_t *Q, float *S, uint8_t *H8, float *sH, const DeviceInfo &dev,
+                          cudaStream_t stream);
 dg_status_t launch_swiglu_backward(const uint8_t *H8, const float *sH, const void *dA, const int32_t *offsets,
                                    int G, int64_t M, int64_t F, uint8_t *Q, float *S, const DeviceInfo &dev,
                                    cudaStream_t stream);

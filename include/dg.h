@@ -406,7 +406,7 @@ dg_status_t dg_moe_combine_backward(const void *dOUT_bf16, const void *Y_bf16,
  *          (taken to lie in [0, M]) are neither read nor written.  G is ignored when null.
  * Q : [M][F] E4M3 out.      S : [ceil(M/128)][F/128] FP32 out.
  * H8 : [M][2F] E4M3 out.    sH_t : [2F/128][M] FP32 out.  Both null, or neither.
- * F % 128 == 0; with group_offsets M % 128 == 0.  M == 0 or F == 0 is a no-op.
+ * F % 128 == 0, F <= 2^24; with group_offsets M % 128 == 0.  M == 0 or F == 0 is a no-op.
  */
 dg_status_t dg_swiglu_quantize(const void *H_bf16, const int32_t *group_offsets, int G, int64_t M,
                                int64_t F, uint8_t *Q, float *S, uint8_t *H8, float *sH_t,
