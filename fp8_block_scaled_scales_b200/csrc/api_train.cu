@@ -70,7 +70,7 @@ dg_status_t dg_moe_dispatch_quantize(const void *X_bf16, const float *weights, c
     const dg_status_t st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
     return launch_dispatch_quantize(X_bf16, weights, slot_of_row, group_offsets, T * k, k, H, M_total_capacity, G, Q, S,
-                                    stream);
+                                    dev, stream);
 }
 
 dg_status_t dg_moe_dispatch_quantize_masked(const void *X_bf16, const int32_t *slot_of_row, const int32_t *masked_m,
@@ -85,7 +85,7 @@ dg_status_t dg_moe_dispatch_quantize_masked(const void *X_bf16, const int32_t *s
     DeviceInfo dev;
     const dg_status_t st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
-    return launch_dispatch_quantize_masked(X_bf16, slot_of_row, masked_m, T * k, k, H, G, M_max, Q, S, stream);
+    return launch_dispatch_quantize_masked(X_bf16, slot_of_row, masked_m, T * k, k, H, G, M_max, Q, S, dev, stream);
 }
 
 dg_status_t dg_moe_combine(const void *Y_bf16, const float *weights, const int32_t *row_of_slot, int64_t T, int k,

@@ -19,109 +19,147 @@
 namespace dg {
 
 constexpr int kRowThreads = 256;
-constexpr int64_t kDispatchMaskedRowCtas = 16;  // CTAs per slab and column block, as in the masked quantizer
 
-// One 128x128 block: rows row0 .. of the sorted layout (`rows` of them in the block, at most
-// 128), column block bc.  tok / wgt: the block's tokens (-1: no slot) and weights.
+// A CTA's share of the gather: one row block of 128 rows (masked: of a slab, every Ry-th) and
+// a run of column blocks.  The tokens are looked up once; then, column block by column block,
+// a thread reads its eight 16-byte pieces from shared memory, asks for the next column
+// block's (cp.async), and reduces and converts the current ones, so that the gather runs under
+// the conversion.  All CTAs walk the columns at the same pace, so the k copies of a token's
+// piece are read close together: once from memory, then from L2.  (A CTA per block, rows
+// first: 137 us on 32768 slots x 7168 with 28 % L2 hits, against 46 us of traffic.)
+struct DispatchSmem {
+    uint4 piece[8][kRowThreads];
+    int tok[128];
+    float wgt[128];
+    alignas(16) uint32_t red[2][kRowThreads / 32];
+};
+
 template <bool WEIGHTS>
-__device__ __forceinline__ void dispatch_block(const uint16_t *__restrict__ X, const float *__restrict__ weights,
-                                               const int32_t *__restrict__ slot_of_row, int slots, int k, int64_t H,
-                                               int64_t row0, int rows, int64_t bc, uint8_t *__restrict__ Q,
-                                               float *__restrict__ Sp, int *tok, float *wgt, uint32_t *red) {
+__device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, const float *__restrict__ weights,
+                                              const int32_t *__restrict__ slot_of_row, int slots, int k, int64_t H,
+                                              int64_t row0, int rows, int bc0, int bc1, uint8_t *__restrict__ Q,
+                                              float *__restrict__ S, DispatchSmem &sm) {
     const int tid = static_cast<int>(threadIdx.x);
+    const int sub = tid >> 4, lane_col = (tid & 15) * 8;
+    __syncthreads();  // an earlier row block's tokens are no longer read
     if (tid < 128) {
         const int slot = tid < rows ? __ldg(slot_of_row + row0 + tid) : -1;
         const bool ok = slot >= 0 && slot < slots;  // anything else is a row without a slot
-        tok[tid] = ok ? slot / k : -1;
-        if (WEIGHTS) wgt[tid] = ok ? __ldg(weights + slot) : 0.0f;
+        sm.tok[tid] = ok ? slot / k : -1;
+        if (WEIGHTS) sm.wgt[tid] = ok ? __ldg(weights + slot) : 0.0f;
     }
     __syncthreads();
-    const int chunk = tid & 15, sub = tid >> 4;
-    const int64_t col = bc * 128 + chunk * 8;
-    const bool col_ok = col < H;  // H % 16 == 0: an 8-column piece is whole or absent
-    uint4 v[8];
+    // a row without a token: its pieces stay zero
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int t = tok[sub + 16 * i];
-        v[i] = (t >= 0 && col_ok) ? __ldg(reinterpret_cast<const uint4 *>(X + static_cast<int64_t>(t) * H + col))
-                                  : make_uint4(0, 0, 0, 0);
-    }
-    float w[8];
-    uint32_t m = 0;
-    if (WEIGHTS) {
+    for (int i = 0; i < 8; ++i)
+        if (sm.tok[sub + 16 * i] < 0) sm.piece[i][tid] = make_uint4(0, 0, 0, 0);
+
+    auto ask = [&](int bc) {
+        const int64_t col = static_cast<int64_t>(bc) * 128 + lane_col;
+        if (col < H) {  // H % 16 == 0: an 8-column piece is whole or absent
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[i] = wgt[sub + 16 * i];
-            float2 x[4];
-            bf16x8_to_f32(v[i], x);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m = amax_fold_f32(m, __fmul2_rn(x[j], make_float2(w[i], w[i])));
-        }
-    } else {
-        uint32_t m2 = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m2 = amax_fold8(m2, v[i]);
-        m = amax_bits_of(m2);
-    }
-    m = cta_max<kRowThreads / 32>(m, red);
-    const BlockScale bs = WEIGHTS ? block_scale_f32(__uint_as_float(m)) : block_scale(m);
-    if (tid == 0) *Sp = bs.s;
-    uint8_t *qp = Q + (row0 + sub) * H + col;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (!col_ok || sub + 16 * i >= rows) break;
-        uint2 q;
-        if (WEIGHTS) {
-            float2 x[4];
-            bf16x8_to_f32(v[i], x);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], make_float2(w[i], w[i]));
-            q = quantize8_f32(x, bs);
+            for (int i = 0; i < 8; ++i) {
+                const int t = sm.tok[sub + 16 * i];
+                if (t >= 0) {
+                    const uint16_t *p = X + static_cast<int64_t>(t) * H + col;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.piece[i][tid])), "l"(p)
+                                 : "memory");
+                }
+            }
         } else {
-            q = quantize8(v[i], bs);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sm.piece[i][tid] = make_uint4(0, 0, 0, 0);
         }
-        *reinterpret_cast<uint2 *>(qp + static_cast<int64_t>(16 * i) * H) = q;
+    };
+
+    ask(bc0);
+    uint8_t *qp = Q + (row0 + sub) * H + static_cast<int64_t>(bc0) * 128 + lane_col;
+    const int64_t step = 16 * H;
+    for (int bc = bc0; bc < bc1; ++bc, qp += 128) {
+        const bool col_ok = static_cast<int64_t>(bc) * 128 + lane_col < H;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = sm.piece[i][tid];
+        if (bc + 1 < bc1) ask(bc + 1);
+        uint32_t m;
+        if (WEIGHTS) {
+            float f = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float w = sm.wgt[sub + 16 * i];
+                float2 x[4];
+                bf16x8_to_f32(v[i], x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f = amax3(f, __fmul2_rn(x[j], make_float2(w, w)));
+            }
+            m = __float_as_uint(f);
+        } else {
+            uint32_t m2 = amax_pair8(v[0]);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, amax_pair8(v[i]));
+            m = amax_bits_of(m2) << 16;  // the maximum's FP32 bits
+        }
+        m = cta_max<kRowThreads / 32>(m, sm.red[bc & 1]);
+        const FastScale bs = fast_scale(__uint_as_float(m));
+        if (tid == 0) S[bc] = bs.s;
+        if (col_ok) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (sub + 16 * i >= rows) break;
+                uint2 q;
+                if (WEIGHTS) {
+                    const float w = sm.wgt[sub + 16 * i];
+                    float2 x[4];
+                    bf16x8_to_f32(v[i], x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], make_float2(w, w));
+                    q = quantize8_f32(x, bs);
+                } else {
+                    q = quantize8_corrected(v[i], bs);
+                }
+                *reinterpret_cast<uint2 *>(qp + i * step) = q;
+            }
+        }
     }
 }
 
-// Contiguous layout: one CTA per block of the row capacity; those past the last expert's
-// rows leave at once and write nothing.
+// How the column blocks are cut: CTA (chunk, row block), row block fastest, takes column
+// blocks [chunk * cols, ...).
 template <bool WEIGHTS>
 __global__ void __launch_bounds__(kRowThreads, 4)
     dispatch_kernel(const uint16_t *__restrict__ X, const float *__restrict__ weights,
                     const int32_t *__restrict__ slot_of_row, const int32_t *__restrict__ offsets, int G, int slots,
-                    int k, int64_t H, int64_t Cb, uint8_t *__restrict__ Q, float *__restrict__ S) {
-    __shared__ int tok[128];
-    __shared__ float wgt[128];
-    __shared__ uint32_t red[kRowThreads / 32];
+                    int k, int64_t H, int Cb, int cols, int Rb, uint8_t *__restrict__ Q, float *__restrict__ S) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    DispatchSmem &sm = *reinterpret_cast<DispatchSmem *>(smem_raw);
     grid_dep_launch_dependents();
     grid_dep_wait();
-    const int64_t blk = blockIdx.x;
-    const int64_t lb = blk / Cb, bc = blk - lb * Cb;
-    if (lb * 128 >= __ldg(offsets + G)) return;
-    dispatch_block<WEIGHTS>(X, weights, slot_of_row, slots, k, H, lb * 128, 128, bc, Q, S + blk, tok, wgt, red);
+    const int chunk = static_cast<int>(blockIdx.x) / Rb, lb = static_cast<int>(blockIdx.x) - chunk * Rb;
+    if (static_cast<int64_t>(lb) * 128 >= __ldg(offsets + G)) return;  // past the last expert's rows
+    const int bc0 = chunk * cols;
+    dispatch_rows<WEIGHTS>(X, weights, slot_of_row, slots, k, H, static_cast<int64_t>(lb) * 128, 128, bc0,
+                           min(bc0 + cols, Cb), Q, S + static_cast<int64_t>(lb) * Cb, sm);
 }
 
-// Masked layout: CTA (g, y, bc) takes the slab's row blocks y, y + Ry, ... that hold tokens;
-// rows past the count are neither read nor written.
+// Masked layout: CTA (chunk, g, y) takes the slab's row blocks y, y + Ry, ... that hold
+// tokens; rows past the count are neither read nor written.
 __global__ void __launch_bounds__(kRowThreads, 4)
     dispatch_masked_kernel(const uint16_t *__restrict__ X, const int32_t *__restrict__ slot_of_row,
-                           const int32_t *__restrict__ masked_m, int slots, int k, int64_t H, int64_t Cb,
-                           int64_t m_max, int64_t Rb, int64_t Ry, uint8_t *__restrict__ Q, float *__restrict__ S) {
-    __shared__ int tok[128];
-    __shared__ uint32_t red[kRowThreads / 32];
+                           const int32_t *__restrict__ masked_m, int slots, int k, int64_t H, int Cb, int cols, int G,
+                           int m_max, int Rb, int Ry, uint8_t *__restrict__ Q, float *__restrict__ S) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    DispatchSmem &sm = *reinterpret_cast<DispatchSmem *>(smem_raw);
     grid_dep_launch_dependents();
     grid_dep_wait();
-    const int64_t blk = blockIdx.x;
-    const int64_t gy = blk / Cb, bc = blk - gy * Cb;
-    const int64_t g = gy / Ry, y = gy - g * Ry;
-    const int64_t rows = min(max(static_cast<int64_t>(__ldg(masked_m + g)), int64_t(0)), m_max);
-    for (int64_t lb = y; lb * 128 < rows; lb += Ry) {
-        if (lb != y) __syncthreads();  // tok and red of the previous block are no longer read
-        dispatch_block<false>(X, nullptr, slot_of_row, slots, k, H, g * m_max + lb * 128,
-                              static_cast<int>(min(rows - lb * 128, int64_t(128))), bc, Q, S + (g * Rb + lb) * Cb + bc,
-                              tok, nullptr, red);
-    }
+    const int chunk = static_cast<int>(blockIdx.x) / (G * Ry), gy = static_cast<int>(blockIdx.x) - chunk * (G * Ry);
+    const int g = gy / Ry, y = gy - g * Ry;
+    const int rows = min(max(__ldg(masked_m + g), 0), m_max);
+    const int bc0 = chunk * cols;
+    for (int lb = y; lb * 128 < rows; lb += Ry)
+        dispatch_rows<false>(X, nullptr, slot_of_row, slots, k, H, static_cast<int64_t>(g) * m_max + lb * 128,
+                             min(rows - lb * 128, 128), bc0, min(bc0 + cols, Cb), Q,
+                             S + (static_cast<int64_t>(g) * Rb + lb) * Cb, sm);
 }
 
 // One CTA per token and 1024 columns, eight columns a thread; the rows of up to four slots
@@ -208,29 +246,70 @@ __global__ void __launch_bounds__(kRowThreads)
     if (lane == 0) dweights[slot] = sum;
 }
 
+template <typename Kernel>
+static dg_status_t allow_smem(Kernel kernel, size_t bytes, int &configured_device) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return DG_ERR_CUDA;
+    if (configured_device == device) return DG_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
+        cudaSuccess)
+        return DG_ERR_CUDA;
+    configured_device = device;
+    return DG_OK;
+}
+
+// Column blocks per CTA: runs as long as possible (the token lookup and the first, uncovered
+// gather are paid once a run) that still give the SMs about kDispatchWaves CTAs for each of
+// their four places.
+constexpr int64_t kDispatchWaves = 2;
+static int dispatch_cols(int64_t row_ctas, int64_t Cb, int num_sms) {
+    const int64_t want = (kDispatchWaves * 4 * num_sms + row_ctas - 1) / row_ctas;  // runs per row block
+    const int64_t runs = want < 1 ? 1 : (want > Cb ? Cb : want);
+    return static_cast<int>((Cb + runs - 1) / runs);
+}
+
+template <bool WEIGHTS>
+static dg_status_t launch_dispatch_impl(const void *X, const float *weights, const int32_t *slot_of_row,
+                                        const int32_t *offsets, int64_t slots, int k, int64_t H, int64_t rows, int G,
+                                        uint8_t *Q, float *S, const DeviceInfo &dev, cudaStream_t stream) {
+    static thread_local int configured_device = -1;
+    const dg_status_t st = allow_smem(dispatch_kernel<WEIGHTS>, sizeof(DispatchSmem), configured_device);
+    if (st != DG_OK) return st;
+    const int64_t Cb = (H + 127) / 128, Rb = rows / 128;
+    const int cols = dispatch_cols(Rb, Cb, dev.num_sms);
+    const int64_t n = (Cb + cols - 1) / cols * Rb;
+    if (n > 0x7FFFFFFFLL || Cb > 0x3FFFFFFFLL) return DG_ERR_SHAPE;
+    return launch_pdl(dispatch_kernel<WEIGHTS>, static_cast<int>(n), kRowThreads, sizeof(DispatchSmem), stream,
+                      static_cast<const uint16_t *>(X), weights, slot_of_row, offsets, G, static_cast<int>(slots), k, H,
+                      static_cast<int>(Cb), cols, static_cast<int>(Rb), Q, S);
+}
+
 dg_status_t launch_dispatch_quantize(const void *X, const float *weights, const int32_t *slot_of_row,
                                      const int32_t *offsets, int64_t slots, int k, int64_t H, int64_t rows, int G,
-                                     uint8_t *Q, float *S, cudaStream_t stream) {
-    const int64_t Cb = (H + 127) / 128, blocks = rows / 128 * Cb;
-    if (blocks > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
-    const uint16_t *x = static_cast<const uint16_t *>(X);
-    const int n = static_cast<int>(blocks), s = static_cast<int>(slots);
-    if (weights)
-        return launch_pdl(dispatch_kernel<true>, n, kRowThreads, 0, stream, x, weights, slot_of_row, offsets, G, s, k,
-                          H, Cb, Q, S);
-    return launch_pdl(dispatch_kernel<false>, n, kRowThreads, 0, stream, x, weights, slot_of_row, offsets, G, s, k, H,
-                      Cb, Q, S);
+                                     uint8_t *Q, float *S, const DeviceInfo &dev, cudaStream_t stream) {
+    return weights ? launch_dispatch_impl<true>(X, weights, slot_of_row, offsets, slots, k, H, rows, G, Q, S, dev, stream)
+                   : launch_dispatch_impl<false>(X, weights, slot_of_row, offsets, slots, k, H, rows, G, Q, S, dev,
+                                                 stream);
 }
+
+// Row blocks of a slab taken by different CTAs, as in the masked quantizer.
+constexpr int64_t kDispatchMaskedRowCtas = 16;
 
 dg_status_t launch_dispatch_quantize_masked(const void *X, const int32_t *slot_of_row, const int32_t *masked_m,
                                             int64_t slots, int k, int64_t H, int G, int64_t m_max, uint8_t *Q,
-                                            float *S, cudaStream_t stream) {
+                                            float *S, const DeviceInfo &dev, cudaStream_t stream) {
+    static thread_local int configured_device = -1;
+    const dg_status_t st = allow_smem(dispatch_masked_kernel, sizeof(DispatchSmem), configured_device);
+    if (st != DG_OK) return st;
     const int64_t Rb = (m_max + 127) / 128, Cb = (H + 127) / 128;
     const int64_t Ry = Rb < kDispatchMaskedRowCtas ? Rb : kDispatchMaskedRowCtas;
-    if (G * Ry * Cb > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
-    return launch_pdl(dispatch_masked_kernel, static_cast<int>(G * Ry * Cb), kRowThreads, 0, stream,
-                      static_cast<const uint16_t *>(X), slot_of_row, masked_m, static_cast<int>(slots), k, H, Cb, m_max,
-                      Rb, Ry, Q, S);
+    const int cols = dispatch_cols(G * Ry, Cb, dev.num_sms);
+    const int64_t n = (Cb + cols - 1) / cols * G * Ry;
+    if (n > 0x7FFFFFFFLL || Cb > 0x3FFFFFFFLL) return DG_ERR_SHAPE;
+    return launch_pdl(dispatch_masked_kernel, static_cast<int>(n), kRowThreads, sizeof(DispatchSmem), stream,
+                      static_cast<const uint16_t *>(X), slot_of_row, masked_m, static_cast<int>(slots), k, H,
+                      static_cast<int>(Cb), cols, G, static_cast<int>(m_max), static_cast<int>(Rb),
+                      static_cast<int>(Ry), Q, S);
 }
 
 dg_status_t launch_combine(const void *Y, const float *weights, const int32_t *row_of_slot, int64_t T, int k,

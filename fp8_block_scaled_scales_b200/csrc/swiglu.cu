@@ -39,10 +39,8 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
 }
 
 // Two rows of h, 128 columns of the gate and of the up half each, as four 1 x 128 blocks
-// (16 lanes a row, 8 values each).  The four maxima are found together (gate and up packed
-// in one word), lane j of a row divides for block j only, and scales and reciprocals are
-// passed round: a division per lane and block made up a sixth of all instructions.  All lanes of
-// the warp call it; ok[i]: row i exists.  q + in_q, s + in_s: the first
+// (16 lanes a row, 8 values each); the maxima of gate and up are found together, packed in one
+// word.  All lanes of the warp call it; ok[i]: row i exists.  q + in_q, s + in_s: the first
 // row's gate codes and scale; the up half lies q_up codes and s_up scales on, the second
 // row q_row codes and 32 scales on.
 __device__ __forceinline__ void checkpoint_rows(const uint4 (&vg)[2], const uint4 (&vu)[2], const bool (&ok)[2],
@@ -57,20 +55,16 @@ __device__ __forceinline__ void checkpoint_rows(const uint4 (&vg)[2], const uint
 #pragma unroll
         for (int i = 0; i < 2; ++i) pk[i] = __vmaxu2(pk[i], __shfl_xor_sync(0xFFFFFFFFu, pk[i], o));
     }
-    const int lane = lane_id(), j = lane & 3;
-    const uint32_t two = (j & 2) ? pk[1] : pk[0];
-    const float amax = __uint_as_float((j & 1) ? (two & 0xFFFF0000u) : (two << 16));
-    const float scale = (amax == 0.0f) ? 1.0f : __fdiv_rn(amax, 448.0f);
-    const float r = __frcp_rn(scale);
-    if ((lane & 15) < 4 && ok[j >> 1]) s[in_s + (j >> 1) * 32 + (j & 1) * s_up] = scale;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int from = (lane & 16) + 2 * i;
-        const float sg = __shfl_sync(0xFFFFFFFFu, scale, from), rg = __shfl_sync(0xFFFFFFFFu, r, from);
-        const float su = __shfl_sync(0xFFFFFFFFu, scale, from + 1), ru = __shfl_sync(0xFFFFFFFFu, r, from + 1);
-        if (ok[i]) {
-            *reinterpret_cast<uint2 *>(q + i * q_row + in_q) = quantize8_corrected(vg[i], sg, rg);
-            *reinterpret_cast<uint2 *>(q + i * q_row + q_up + in_q) = quantize8_corrected(vu[i], su, ru);
+        if (!ok[i]) continue;
+        const FastScale g = fast_scale(__uint_as_float(pk[i] << 16));
+        const FastScale u = fast_scale(__uint_as_float(pk[i] & 0xFFFF0000u));
+        *reinterpret_cast<uint2 *>(q + i * q_row + in_q) = quantize8_corrected(vg[i], g);
+        *reinterpret_cast<uint2 *>(q + i * q_row + q_up + in_q) = quantize8_corrected(vu[i], u);
+        if ((threadIdx.x & 15u) == 0) {
+            s[in_s + i * 32] = g.s;
+            s[in_s + i * 32 + s_up] = u.s;
         }
     }
 }
@@ -154,7 +148,7 @@ __global__ void __launch_bounds__(kGluThreads, 2)
                   float *__restrict__ S, uint8_t *__restrict__ H8, float *__restrict__ sH) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     GluSmem &st = *reinterpret_cast<GluSmem *>(smem_raw);
-    __shared__ uint32_t red[2][kGluThreads / 32];
+    __shared__ __align__(16) uint32_t red[2][kGluThreads / 32];
     grid_dep_launch_dependents();
     grid_dep_wait();
     const int tid = static_cast<int>(threadIdx.x);
@@ -218,7 +212,7 @@ __global__ void __launch_bounds__(kGluThreads, 2)
                 ask(i0 + i, next_row0, next_rows, walk.bc);
             }
         }
-        const NearScale bs = near_scale(cta_max<kGluThreads / 32>(__float_as_uint(m), red[par]));
+        const FastScale bs = fast_scale(__uint_as_float(cta_max<kGluThreads / 32>(__float_as_uint(m), red[par])));
         if (tid == 0) S[static_cast<int64_t>(rb) * layout.Fb + bc] = bs.s;
         uint8_t *q = Q + static_cast<int64_t>(row0) * F + bc * 128;
 #pragma unroll
@@ -339,7 +333,7 @@ __global__ void __launch_bounds__(kGluBackThreads, 1)
             mg = max(mg, __shfl_xor_sync(0xFFFFFFFFu, mg, o));
             mu = max(mu, __shfl_xor_sync(0xFFFFFFFFu, mu, o));
         }
-        const NearScale bg = near_scale(mg), bu = near_scale(mu);
+        const FastScale bg = fast_scale(__uint_as_float(mg)), bu = fast_scale(__uint_as_float(mu));
         if (tid == 0) {
             float *sp = S + static_cast<int64_t>(rb) * 2 * layout.Fb + bc;
             sp[0] = bg.s;

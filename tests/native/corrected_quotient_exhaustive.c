@@ -1,13 +1,17 @@
 /*
- * Exhaustive check of the E4M3 conversion by a corrected quotient (test infrastructure;
- * the device arithmetic of quant_f32.cuh restated in C, one IEEE rounding per operation).
+ * Exhaustive checks of the arithmetic by which the expert-layer kernels quantize (test
+ * infrastructure; the device arithmetic of quant_f32.cuh restated in C, one IEEE rounding
+ * per operation).
  *
- * For every block maximum amax among the positive finite BF16 values whose scale
- * s = fl32(amax / 448) lies in the window [2^-100, 2^100], and every BF16 x with
- * |x| <= amax:
- *   r = fl32(1 / s), z = fl32(x * -r), e = fma(z, s, x), q = fma(e, -r, z)
- * must have, but for its sign, the E4M3 code of fl32(x / s): z is the negative of the
- * quotient's first approximation, and with this order of signs a zero keeps its own.
+ * 1. The scale: q = fl32(amax c), c = fl32(1/448), s = fma(fma(-q, 448, amax), c, q) must be
+ *    fl32(amax / 448) for every BF16 amax in the window [2^-90, 2^100], and for every FP32
+ *    mantissa at several exponents of it.
+ * 2. The codes: for every such BF16 amax and every BF16 x with |x| <= amax, with n = -x and r
+ *    = fl32(1 / s),
+ *      y = fl32(n * -r), e = fma(y, s, n), q = fma(e, -r, y)
+ *    must have the E4M3 code of fl32(x / s).  The kernel's r comes from an approximation, so
+ *    r one and two units to either side is tried too, for every eighth exponent of amax (the
+ *    arithmetic does not change with a power of two).
  * Prints the number of mismatches.
  */
 #include <math.h>
@@ -40,33 +44,63 @@ static float bf16(uint32_t h)
     return f;
 }
 
+static float step_by(float v, int units)
+{
+    uint32_t u;
+    memcpy(&u, &v, 4);
+    u += (uint32_t)units;  /* positive, far from the ends */
+    memcpy(&v, &u, 4);
+    return v;
+}
+
+static float scale_of(float amax)
+{
+    const float c = 1.0f / 448.0f, q = amax * c;
+    return fmaf(fmaf(-q, 448.0f, amax), c, q);
+}
+
 int main(void)
 {
-    long long bad = 0, pairs = 0;
+    long long bad = 0, pairs = 0, scales = 0;
+    for (int ex = -90; ex < 100; ex += 27) {
+#pragma omp parallel for reduction(+ : bad, scales)
+        for (uint32_t m = 0; m < (1u << 23); ++m) {
+            const uint32_t u = ((uint32_t)(127 + ex) << 23) | m;
+            float amax;
+            memcpy(&amax, &u, 4);
+            ++scales;
+            if (scale_of(amax) != amax / 448.0f) ++bad;
+        }
+    }
 #pragma omp parallel for schedule(dynamic, 64) reduction(+ : bad, pairs)
     for (uint32_t ah = 1; ah < 0x7F80u; ++ah) {
-        const float s = bf16(ah) / 448.0f;
-        if (!(s >= 0x1p-100f && s <= 0x1p100f)) continue;
-        const float r = 1.0f / s;
-        for (uint32_t xm = 0; xm <= ah; ++xm) {
-            for (uint32_t sg = 0; sg < 2; ++sg) {
-                const float x = bf16(xm | (sg << 15));
-                const float z = x * -r;
-                const float e = fmaf(z, s, x);
-                const uint8_t got = e4m3(fmaf(e, -r, z)) ^ 0x80, want = e4m3(x / s);
-                ++pairs;
-                if (got != want) {
-                    ++bad;
-                    if (bad <= 5) {
+        const float amax = bf16(ah);
+        if (!(amax >= 0x1p-90f && amax <= 0x1p100f)) continue;
+        const float s = scale_of(amax);
+        if (s != amax / 448.0f) ++bad;
+        const int wide = ((ah >> 7) & 7u) == 0;
+        for (int d = wide ? -2 : 0; d <= (wide ? 2 : 0); ++d) {
+            const float r = step_by(1.0f / s, d);
+            for (uint32_t xm = 0; xm <= ah; ++xm) {
+                for (uint32_t sg = 0; sg < 2; ++sg) {
+                    const float x = bf16(xm | (sg << 15)), n = -x;
+                    const float y = n * -r;
+                    const float e = fmaf(y, s, n);
+                    const uint8_t got = e4m3(fmaf(e, -r, y)), want = e4m3(x / s);
+                    ++pairs;
+                    if (got != want) {
+                        ++bad;
+                        if (bad <= 5) {
 #pragma omp critical
-                        printf("mismatch amax 0x%04x x 0x%04x: got 0x%02x want 0x%02x\n", ah, xm | (sg << 15), got,
-                               want);
+                            printf("mismatch amax 0x%04x x 0x%04x r %+d: got 0x%02x want 0x%02x\n", ah,
+                                   xm | (sg << 15), d, got, want);
+                        }
                     }
                 }
             }
         }
     }
-    printf("pairs %lld\n", pairs);
+    printf("scales %lld pairs %lld\n", scales, pairs);
     printf("mismatches %lld\n", bad);
     return bad != 0;
 }

@@ -1,8 +1,8 @@
-"""The E4M3 conversion of the activation checkpoint, restated in C and checked for every
-pair it can meet (tests/native/corrected_quotient_exhaustive.c): every BF16 group maximum
-whose scale s = fl32(amax / 448) lies in [2^-100, 2^100] against every BF16 x with
-|x| <= amax, about 8.9e8 pairs.  The corrected quotient's code must equal
-E4M3(fl32(x / s)) in every case."""
+"""The quantizing arithmetic of the expert-layer kernels, restated in C and checked
+exhaustively (tests/native/corrected_quotient_exhaustive.c): the scale amax / 448 by a
+corrected product for every BF16 amax in the window and every FP32 mantissa at several
+exponents, and the E4M3 code of fl32(x / s) by a corrected quotient for every such amax
+against every BF16 x with |x| <= amax, the reciprocal up to two units off."""
 import os
 import shutil
 import subprocess
