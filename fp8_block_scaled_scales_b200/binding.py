@@ -30,7 +30,7 @@ EXPORTS = ("dg_quantize_blockwise", "dg_quantize_blockwise_masked", "dg_fp8_gemm
            "dg_fp8_gemm_1x128", "dg_fp8_gemm_1x128_select",
            "dg_fp8_gemm_blockscaled_select", "dg_status_string", "dg_get_last_device_status",
            "dg_version", "dg_test_set_kernel_control",
-           "dg_moe_sort", "dg_moe_sort_masked", "dg_moe_dispatch_quantize", "dg_moe_dispatch_quantize_masked",
+           "dg_moe_sort", "dg_moe_sort_masked", "dg_moe_sort_workspace", "dg_moe_dispatch_quantize", "dg_moe_dispatch_quantize_masked",
            "dg_moe_combine", "dg_moe_combine_backward", "dg_swiglu_quantize", "dg_swiglu_quantize_masked",
            "dg_swiglu_quantize_backward", "dg_fp8_dgrad_blockscaled", "dg_fp8_wgrad_blockscaled",
            "dg_fp8_grouped_dgrad_contiguous", "dg_fp8_grouped_wgrad_contiguous")
@@ -72,8 +72,9 @@ def lib() -> ctypes.CDLL:
               "dg_fp8_grouped_gemm_contiguous", "dg_fp8_grouped_gemm_masked", "dg_get_last_device_status",
               "dg_quantize_1x128", "dg_fp8_gemm_1x128", "dg_fp8_gemm_1x128_select"):
         getattr(L, f).restype = ctypes.c_int
-    L.dg_moe_sort.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, i64, vp]
-    L.dg_moe_sort_masked.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, i64, vp]
+    L.dg_moe_sort.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, i64, vp, i64, vp]
+    L.dg_moe_sort_masked.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, i64, vp, i64, vp]
+    L.dg_moe_sort_workspace.argtypes = [i64, i32, i32]
     L.dg_moe_dispatch_quantize.argtypes = [vp, vp, vp, vp, i64, i32, i64, i64, i32, vp, vp, vp]
     L.dg_moe_dispatch_quantize_masked.argtypes = [vp, vp, vp, i64, i32, i64, i32, i64, vp, vp, vp]
     L.dg_moe_combine.argtypes = [vp, vp, vp, i64, i32, i64, i64, vp, vp]
@@ -88,6 +89,7 @@ def lib() -> ctypes.CDLL:
     for f in EXPORTS:
         if f.startswith(("dg_moe_", "dg_swiglu_")) or "grad" in f:
             getattr(L, f).restype = ctypes.c_int
+    L.dg_moe_sort_workspace.restype = i64
     L.dg_get_last_device_status.argtypes = [vp]
     L.dg_status_string.restype = ctypes.c_char_p
     L.dg_status_string.argtypes = [ctypes.c_int]
@@ -296,6 +298,17 @@ def moe_capacity(T: int, k: int, G: int) -> int:
     return (S + 127 * min(G, S)) // 128 * 128
 
 
+def _sort_workspace(T: int, k: int, G: int, dev: int, stream):
+    """Scratch for one sort: (tensor kept alive by the caller, address, bytes)."""
+    n = lib().dg_moe_sort_workspace(T, k, G)
+    if n == 0:
+        return None, 0, 0
+    w = torch.empty(n // 4, dtype=_I32, device=dev)
+    if stream is not None:
+        w.record_stream(stream)  # freed here, perhaps while that stream still runs the sort
+    return w, w.data_ptr(), n
+
+
 def moe_sort(topk_ids, G: int, offsets=None, row_of_slot=None, slot_of_row=None, stream=None):
     """Slots sorted by expert: topk_ids [T][k] (int32 or int64) -> (group_offsets [G+1],
     row_of_slot [T][k], slot_of_row [capacity]), int32.  Ids outside [0, G) are dropped (row
@@ -308,7 +321,8 @@ def moe_sort(topk_ids, G: int, offsets=None, row_of_slot=None, slot_of_row=None,
     offsets, p_off = _out(offsets, "offsets", _I32, (G + 1,), dev)
     row_of_slot, p_row = _out(row_of_slot, "row_of_slot", _I32, (T, k), dev)
     slot_of_row, p_slot = _out(slot_of_row, "slot_of_row", _I32, (cap,), dev)
-    _check(lib().dg_moe_sort(ids, wide, T, k, G, p_off, p_row, p_slot, cap, _on(stream, dev)), "dg_moe_sort")
+    w, pw, nw = _sort_workspace(T, k, G, dev, stream)
+    _check(lib().dg_moe_sort(ids, wide, T, k, G, p_off, p_row, p_slot, cap, pw, nw, _on(stream, dev)), "dg_moe_sort")
     return offsets, row_of_slot, slot_of_row
 
 
@@ -321,7 +335,8 @@ def moe_sort_masked(topk_ids, G: int, M_max: int, masked_m=None, row_of_slot=Non
     masked_m, p_m = _out(masked_m, "masked_m", _I32, (G,), dev)
     row_of_slot, p_row = _out(row_of_slot, "row_of_slot", _I32, (T, k), dev)
     slot_of_row, p_slot = _out(slot_of_row, "slot_of_row", _I32, (G * M_max,), dev)
-    _check(lib().dg_moe_sort_masked(ids, wide, T, k, G, p_m, p_row, p_slot, M_max, _on(stream, dev)),
+    w, pw, nw = _sort_workspace(T, k, G, dev, stream)
+    _check(lib().dg_moe_sort_masked(ids, wide, T, k, G, p_m, p_row, p_slot, M_max, pw, nw, _on(stream, dev)),
            "dg_moe_sort_masked")
     return masked_m, row_of_slot, slot_of_row
 

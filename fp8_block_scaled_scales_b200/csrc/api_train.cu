@@ -24,35 +24,46 @@ int64_t most_rows(int64_t slots, int G) { return (slots + 127 * (slots < G ? slo
 
 extern "C" {
 
+int64_t dg_moe_sort_workspace(int64_t T, int k, int G) {
+    return bad_slots(T, k) || G < 1 || G > 1024 ? 0 : moe_sort_workspace(T * k, G);
+}
+
 dg_status_t dg_moe_sort(const void *topk_ids, int ids_64bit, int64_t T, int k, int G, int32_t *group_offsets,
-                        int32_t *row_of_slot, int32_t *slot_of_row, int64_t M_total_capacity, cudaStream_t stream) {
+                        int32_t *row_of_slot, int32_t *slot_of_row, int64_t M_total_capacity, void *workspace,
+                        int64_t workspace_bytes, cudaStream_t stream) {
     if (bad_slots(T, k) || G < 1 || G > 1024 || M_total_capacity < 0 || M_total_capacity % 128 != 0 ||
         M_total_capacity > kInt32Max || M_total_capacity < most_rows(T * k, G))
         return DG_ERR_SHAPE;
-    if (!group_offsets || (T > 0 && (!topk_ids || !row_of_slot)) || (M_total_capacity > 0 && !slot_of_row))
+    const int64_t need = moe_sort_workspace(T * k, G);
+    if (!group_offsets || (T > 0 && (!topk_ids || !row_of_slot)) || (M_total_capacity > 0 && !slot_of_row) ||
+        (need > 0 && !workspace) || workspace_bytes < need)
         return DG_ERR_INVALID_ARG;
     if (!aligned(topk_ids, ids_64bit ? 8 : 4) || !aligned(group_offsets, 4) || !aligned(row_of_slot, 4) ||
-        !aligned(slot_of_row, 4))
+        !aligned(slot_of_row, 4) || !aligned(workspace, 16))
         return DG_ERR_ALIGNMENT;
     DeviceInfo dev;
     const dg_status_t st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
     return launch_moe_sort(topk_ids, ids_64bit != 0, T * k, G, false, M_total_capacity, group_offsets, row_of_slot,
-                           slot_of_row, dev, stream);
+                           slot_of_row, static_cast<int32_t *>(workspace), stream);
 }
 
 dg_status_t dg_moe_sort_masked(const void *topk_ids, int ids_64bit, int64_t T, int k, int G, int32_t *masked_m,
-                               int32_t *row_of_slot, int32_t *slot_of_row, int64_t M_max, cudaStream_t stream) {
+                               int32_t *row_of_slot, int32_t *slot_of_row, int64_t M_max, void *workspace,
+                               int64_t workspace_bytes, cudaStream_t stream) {
     if (bad_slots(T, k) || G < 1 || G > 1024 || M_max < 0 || M_max > kInt32Max / G) return DG_ERR_SHAPE;
-    if (!masked_m || (T > 0 && (!topk_ids || !row_of_slot)) || (M_max > 0 && !slot_of_row)) return DG_ERR_INVALID_ARG;
+    const int64_t need = moe_sort_workspace(T * k, G);
+    if (!masked_m || (T > 0 && (!topk_ids || !row_of_slot)) || (M_max > 0 && !slot_of_row) ||
+        (need > 0 && !workspace) || workspace_bytes < need)
+        return DG_ERR_INVALID_ARG;
     if (!aligned(topk_ids, ids_64bit ? 8 : 4) || !aligned(masked_m, 4) || !aligned(row_of_slot, 4) ||
-        !aligned(slot_of_row, 4))
+        !aligned(slot_of_row, 4) || !aligned(workspace, 16))
         return DG_ERR_ALIGNMENT;
     DeviceInfo dev;
     const dg_status_t st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
-    return launch_moe_sort(topk_ids, ids_64bit != 0, T * k, G, true, M_max, masked_m, row_of_slot, slot_of_row, dev,
-                           stream);
+    return launch_moe_sort(topk_ids, ids_64bit != 0, T * k, G, true, M_max, masked_m, row_of_slot, slot_of_row,
+                           static_cast<int32_t *>(workspace), stream);
 }
 
 dg_status_t dg_moe_dispatch_quantize(const void *X_bf16, const float *weights, const int32_t *slot_of_row,

@@ -7,12 +7,16 @@
 //   row(s) = off[e] + rank, off the prefix sum of the experts' counts rounded up to 128
 //            (masked: e * M_max + rank, dropped when rank >= M_max)
 //
-// One launch of one thread-block cluster: the slots are cut into consecutive pieces, one
-// per warp.  Each warp counts its piece per expert (32 slots at a time, equal experts found
-// with match.any, so no atomics and the order is fixed); a scan over the warps and, through
-// distributed shared memory, over the CTAs turns the counts into each warp's first row per
-// expert; a second pass over the piece hands the rows out.  Needs no scratch memory and no
-// second launch.  A few slots (a decode step) take a single CTA, whose cost is latency.
+// Ranks come without atomics, so the order is fixed: a warp takes 32 consecutive slots, finds
+// the lanes with its own expert from one ballot per bit of the id, and its count per expert
+// goes into a table that is summed over the warps in order.  (match.any in place of the
+// ballots was several times slower: 52 us for 131072 slots, 256 experts, with one cluster of
+// 8 CTAs.)
+//
+// Up to kSortOneCta slots one CTA does it all: a decode step's cost is one launch.  Beyond
+// that, two launches over consecutive chunks, one CTA each: the first ranks the slots inside
+// their chunk and writes the chunk's counts; in the second every CTA adds up the counts of
+// all chunks (a few hundred KB from L2) and hands out the rows.
 #include "dg_device.cuh"
 #include "train_internal.h"
 
@@ -20,212 +24,300 @@ namespace dg {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCluster = 8;
 constexpr int kSortMaxG = 1024;  // one thread per expert in the scans
-constexpr int kSortBatch = 8;    // ids a lane loads ahead
-// Up to this many slots one CTA is used.
-constexpr int64_t kSortOneCta = 4096;
-
+constexpr int kSortSteps = 2;    // slots a thread of the one-CTA form holds
+constexpr int64_t kSortOneCta = kSortSteps * kSortThreads;
 static_assert(kSortMaxG <= kSortThreads, "one thread per expert");
 
-__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
+template <typename IdT>
+__device__ __forceinline__ int expert_of(const IdT *ids, int64_t s, bool there, int G) {
+    const IdT v = there ? __ldg(ids + s) : IdT(-1);
+    return (v >= 0 && v < IdT(G)) ? static_cast<int>(v) : -1;
+}
+
+// Lanes of the warp with this lane's expert (0 for a dropped slot).
+__device__ __forceinline__ uint32_t lanes_with(int e, int bits) {
+    uint32_t peers = __ballot_sync(0xFFFFFFFFu, e >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, (e >> b) & 1);
+        peers &= ((e >> b) & 1) ? m : ~m;
+    }
+    return e >= 0 ? peers : 0u;
+}
+
+// Ranks of one step of 1024 slots among the slots of the same expert since `base` was zero:
+// base[e] (shared, one per expert) is advanced by the step's counts.  hist: [active][G] words.
+// Called by all threads; `active` warps hold slots.  Returns the rank (e >= 0).
+__device__ __forceinline__ int rank_step(int e, int G, int bits, int active, int *hist, int *base) {
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < active * G; i += kSortThreads) hist[i] = 0;
+    const uint32_t peers = lanes_with(e, bits);
+    const int in_warp = __popc(peers & ((1u << lane) - 1u));
+    __syncthreads();
+    if (e >= 0 && in_warp == 0) hist[warp * G + e] = __popc(peers);
+    __syncthreads();
+    if (tid < G) {
+        int run = base[tid];
+        for (int w0 = 0; w0 < active; w0 += 8) {  // eight loads at a time: each alone waits for shared memory
+            int c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = w0 + i < active ? hist[(w0 + i) * G + tid] : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (w0 + i < active) hist[(w0 + i) * G + tid] = run;
+                run += c[i];
+            }
+        }
+        base[tid] = run;
+    }
+    __syncthreads();
+    return e >= 0 ? hist[warp * G + e] + in_warp : -1;
+}
+
+// First row of each expert from the counts (one thread per expert, all threads call it):
+// masked: e * rows; contiguous: the prefix sum of the counts rounded up to 128, into off[0..G]
+// as well.  scan: 32 words.
+template <bool MASKED>
+__device__ __forceinline__ void first_rows(int all, int G, int rows, int *first, int *scan) {
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    if (MASKED) {
+        if (tid < G) first[tid] = tid * rows;
+        return;
+    }
+    const int padded = tid < G ? (all + 127) / 128 * 128 : 0;
+    int incl = padded;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += scan[w];
+    if (tid < G) {
+        first[tid] = before + incl - padded;
+        if (tid == G - 1) first[G] = before + incl;
+    }
+}
+
+// The row of rank `rank` of expert e.
+template <bool MASKED>
+__device__ __forceinline__ int row_of(int e, int rank, const int *first, int rows) {
+    if (e < 0 || (MASKED && rank >= rows)) return -1;
+    return first[e] + rank;
+}
+
+// -1 into the rows without a slot (count: slots per expert that have a row), by `ctas` CTAs.
+template <bool MASKED>
+__device__ __forceinline__ void fill_empty_rows(int G, int rows, const int *first, const int *count, int cta, int ctas,
+                                                int32_t *slot_of_row) {
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    if (!MASKED) {
+        for (int e = cta * kSortWarps + warp; e < G; e += ctas * kSortWarps)
+            for (int r = first[e] + count[e] + lane; r < first[e + 1]; r += 32) slot_of_row[r] = -1;
+    }
+    // masked: all slabs; contiguous: past the last expert
+    const int64_t end = MASKED ? static_cast<int64_t>(G) * rows : rows;
+    for (int64_t r = (MASKED ? 0 : first[G]) + static_cast<int64_t>(cta) * kSortThreads + tid; r < end;
+         r += static_cast<int64_t>(ctas) * kSortThreads) {
+        if (MASKED) {
+            const int e = static_cast<int>(r) / rows;
+            if (static_cast<int>(r) - e * rows < count[e]) continue;
+        }
+        slot_of_row[r] = -1;
+    }
+}
+
+// offsets (contiguous: first[0..G]) or counts (masked) out.
+template <bool MASKED>
+__device__ __forceinline__ void write_offsets(int G, const int *first, const int *count, int32_t *offsets) {
+    const int tid = static_cast<int>(threadIdx.x);
+    if (tid < G) offsets[tid] = MASKED ? count[tid] : first[tid];
+    if (!MASKED && tid == 0) offsets[G] = first[G];
 }
 
 template <typename IdT, bool MASKED>
 __global__ void __launch_bounds__(kSortThreads, 1)
-    moe_sort_kernel(const IdT *__restrict__ ids, int slots, int per_warp, int G, int rows,
-                    int32_t *__restrict__ offsets, int32_t *__restrict__ row_of_slot,
-                    int32_t *__restrict__ slot_of_row, int ctas) {
+    moe_sort_kernel(const IdT *__restrict__ ids, int slots, int G, int bits, int rows, int32_t *__restrict__ offsets,
+                    int32_t *__restrict__ row_of_slot, int32_t *__restrict__ slot_of_row) {
     extern __shared__ int sm[];
-    int *hist = sm;                       // [active warps][G]
-    int *total = hist + kSortWarps * G;   // [G] this CTA's slots per expert
-    int *count = total + G;               // [G] all slots per expert
-    int *off = count + G;                 // [G+1] first row of each expert
-    int *scan = off + G + 1;              // [32]
-
+    int *base = sm;               // [G] slots per expert so far
+    int *first = base + G;        // [G+1]
+    int *scan = first + G + 1;    // [32]
+    int *hist = scan + 32;        // [warps with slots][G]
     const int tid = static_cast<int>(threadIdx.x);
-    const int warp = tid >> 5, lane = tid & 31;
-    const int rank = ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int gw = rank * kSortWarps + warp;
-    const uint32_t lower = (1u << lane) - 1u;
-
-    // warps of this CTA that have a piece
-    const int left = slots - rank * kSortWarps * per_warp;
-    const int active = left <= 0 ? 0 : min(kSortWarps, (left + per_warp - 1) / per_warp);
-    for (int i = tid; i < active * G; i += kSortThreads) hist[i] = 0;
+    if (tid < G) base[tid] = 0;
     grid_dep_launch_dependents();
     grid_dep_wait();  // the ids may come from the previous kernel
-    __syncthreads();
-
-    const int begin = static_cast<int>(min(static_cast<int64_t>(gw) * per_warp, static_cast<int64_t>(slots)));
-    const int end = min(begin + per_warp, slots);
-    int *mine = hist + warp * G;
-
-    // visits the piece 32 slots at a time: f(slot, expert or -1, peers)
-    auto visit = [&](auto f) {
-        for (int b = begin; b < end; b += 32 * kSortBatch) {
-            int e[kSortBatch];
+    int e[kSortSteps], rank[kSortSteps];
 #pragma unroll
-            for (int j = 0; j < kSortBatch; ++j) {
-                const int s = b + j * 32 + lane;
-                const IdT v = s < end ? __ldg(ids + s) : IdT(-1);
-                e[j] = (v >= 0 && v < IdT(G)) ? static_cast<int>(v) : -1;
-            }
+    for (int i = 0; i < kSortSteps; ++i)
+        e[i] = expert_of(ids, i * kSortThreads + tid, i * kSortThreads + tid < slots, G);
 #pragma unroll
-            for (int j = 0; j < kSortBatch; ++j) {
-                if (b + j * 32 >= end) break;
-                const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e[j]);
-                f(b + j * 32 + lane, e[j], peers);
-                __syncwarp();
-            }
-        }
-    };
-
-    visit([&](int, int e, uint32_t peers) {
-        if (e >= 0 && (peers & lower) == 0) mine[e] += __popc(peers);
-    });
-    __syncthreads();
-
-    // per expert: exclusive scan over the warps, then over the CTAs
-    int below = 0, all = 0;
-    if (tid < G) {
-        int run = 0;
-        for (int w = 0; w < active; ++w) {
-            const int c = hist[w * G + tid];
-            hist[w * G + tid] = run;
-            run += c;
-        }
-        total[tid] = all = run;
-    }
-    if (ctas > 1) {
-        cluster_sync();
-        if (tid < G) {
-            all = 0;
-            for (int c = 0; c < ctas; ++c) {
-                const int v = ld_cluster_s32(mapa_shared(smem_u32(total + tid), static_cast<uint32_t>(c)));
-                if (c < rank) below += v;
-                all += v;
-            }
-        }
-    }
-    // first row of each expert
-    int first = 0;
-    if (MASKED) {
-        first = tid * rows;
-        if (tid < G) count[tid] = min(all, rows);
-    } else {
-        const int padded = tid < G ? (all + 127) / 128 * 128 : 0;
-        int incl = padded;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) scan[warp] = incl;
+    for (int i = 0; i < kSortSteps; ++i) {
+        const int left = slots - i * kSortThreads;
+        if (left <= 0) break;
         __syncthreads();
-        int before = 0;
-        for (int w = 0; w < warp; ++w) before += scan[w];
-        first = before + incl - padded;
-        if (tid < G) {
-            count[tid] = all;
-            off[tid] = first;
-            if (tid == G - 1) off[G] = first + padded;
-        }
-    }
-    if (tid < G) {
-        // masked: hist keeps ranks inside the expert, so that rank >= M_max can be seen
-        const int base = below + (MASKED ? 0 : first);
-        for (int w = 0; w < active; ++w) hist[w * G + tid] += base;
+        rank[i] = rank_step(e[i], G, bits, min(kSortWarps, (left + 31) / 32), hist, base);
     }
     __syncthreads();
-    if (rank == 0) {
-        if (MASKED) {
-            if (tid < G) offsets[tid] = count[tid];
-        } else {
-            if (tid < G) offsets[tid] = off[tid];
-            if (tid == 0) offsets[G] = off[G];
-        }
-    }
-
-    visit([&](int s, int e, uint32_t peers) {
-        int row = -1;
-        if (e >= 0) {
-            const int at = mine[e];
-            row = at + __popc(peers & lower);
-            if (MASKED) row = row < rows ? e * rows + row : -1;
-            __syncwarp(peers);
-            if ((peers & lower) == 0) mine[e] = at + __popc(peers);
-        }
-        if (s < end) {
+    const int all = tid < G ? base[tid] : 0;
+    first_rows<MASKED>(all, G, rows, first, scan);
+    if (MASKED && tid < G) base[tid] = min(all, rows);
+    __syncthreads();
+    write_offsets<MASKED>(G, first, base, offsets);
+#pragma unroll
+    for (int i = 0; i < kSortSteps; ++i) {
+        const int s = i * kSortThreads + tid;
+        if (s < slots) {
+            const int row = row_of<MASKED>(e[i], rank[i], first, rows);
             row_of_slot[s] = row;
             if (row >= 0) slot_of_row[row] = s;
         }
-    });
-
-    // rows without a slot
-    if (MASKED) {
-        const int n = G * rows;
-        for (int r = rank * kSortThreads + tid; r < n; r += ctas * kSortThreads) {
-            const int e = r / rows;
-            if (r - e * rows >= count[e]) slot_of_row[r] = -1;
-        }
-    } else {
-        for (int e = gw; e < G; e += ctas * kSortWarps)
-            for (int r = off[e] + count[e] + lane; r < off[e + 1]; r += 32) slot_of_row[r] = -1;
-        for (int r = off[G] + rank * kSortThreads + tid; r < rows; r += ctas * kSortThreads) slot_of_row[r] = -1;
     }
-    if (ctas > 1) cluster_sync();  // no CTA leaves while another may read its totals
+    fill_empty_rows<MASKED>(G, rows, first, base, 0, 1, slot_of_row);
+}
+
+// First launch of two: ranks inside the chunk into row_of_slot, counts into counts[chunk][4 Gq]
+// (zeros past G).
+template <typename IdT>
+__global__ void __launch_bounds__(kSortThreads, 1)
+    moe_rank_kernel(const IdT *__restrict__ ids, int64_t slots, int64_t chunk, int G, int bits,
+                    int32_t *__restrict__ row_of_slot, int32_t *__restrict__ counts) {
+    extern __shared__ int sm[];
+    int *base = sm, *hist = sm + G;
+    const int tid = static_cast<int>(threadIdx.x);
+    if (tid < G) base[tid] = 0;
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int64_t begin = blockIdx.x * chunk, end = min(begin + chunk, slots);
+    int next = expert_of(ids, begin + tid, begin + tid < end, G);
+    for (int64_t b = begin; b < end; b += kSortThreads) {
+        const int e = next;
+        next = expert_of(ids, b + kSortThreads + tid, b + kSortThreads + tid < end, G);
+        __syncthreads();
+        const int rank = rank_step(e, G, bits, static_cast<int>(min(int64_t(kSortWarps), (end - b + 31) / 32)), hist, base);
+        if (b + tid < end) row_of_slot[b + tid] = rank;
+    }
+    __syncthreads();
+    const int row = (G + 3) / 4 * 4;
+    if (tid < row) counts[static_cast<int64_t>(blockIdx.x) * row + tid] = tid < G ? base[tid] : 0;
+}
+
+// Second launch: rows from the ranks.  Gq: ceil(G / 4), the table's row in 16-byte pieces.
+template <typename IdT, bool MASKED>
+__global__ void __launch_bounds__(kSortThreads, 1)
+    moe_place_kernel(const IdT *__restrict__ ids, int64_t slots, int64_t chunk, int G, int Gq, int rows,
+                     const int32_t *__restrict__ counts, int32_t *__restrict__ offsets,
+                     int32_t *__restrict__ row_of_slot, int32_t *__restrict__ slot_of_row) {
+    __shared__ int count[kSortMaxG], below[kSortMaxG], first[kSortMaxG + 1], scan[32];
+    const int tid = static_cast<int>(threadIdx.x);
+    count[tid] = below[tid] = 0;
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    __syncthreads();
+    const int me = static_cast<int>(blockIdx.x), chunks = static_cast<int>(gridDim.x);
+    // Each warp adds up every 32nd chunk's row, four experts a lane and four rows in flight:
+    // all CTAs read the same table, and one word a load took 12 us of 19 for 128 chunks.
+    const int4 *table = reinterpret_cast<const int4 *>(counts);
+    for (int q = tid & 31; q < Gq; q += 32) {
+        int4 all = make_int4(0, 0, 0, 0), before = make_int4(0, 0, 0, 0);
+#pragma unroll 4
+        for (int c = tid >> 5; c < chunks; c += kSortWarps) {
+            const int4 v = __ldcg(table + static_cast<int64_t>(c) * Gq + q);
+            all.x += v.x, all.y += v.y, all.z += v.z, all.w += v.w;
+            if (c < me) before.x += v.x, before.y += v.y, before.z += v.z, before.w += v.w;
+        }
+        // integers: the order does not matter
+        atomicAdd(&count[4 * q], all.x), atomicAdd(&below[4 * q], before.x);
+        atomicAdd(&count[4 * q + 1], all.y), atomicAdd(&below[4 * q + 1], before.y);
+        atomicAdd(&count[4 * q + 2], all.z), atomicAdd(&below[4 * q + 2], before.z);
+        atomicAdd(&count[4 * q + 3], all.w), atomicAdd(&below[4 * q + 3], before.w);
+    }
+    __syncthreads();
+    const int all = tid < G ? count[tid] : 0;
+    first_rows<MASKED>(all, G, rows, first, scan);
+    if (MASKED && tid < G) count[tid] = min(all, rows);
+    __syncthreads();
+    if (me == 0) write_offsets<MASKED>(G, first, count, offsets);
+    const int64_t begin = me * chunk, end = min(begin + chunk, slots);
+    for (int64_t s = begin + tid; s < end; s += kSortThreads) {
+        const int e = expert_of(ids, s, true, G);
+        const int row = e >= 0 ? row_of<MASKED>(e, row_of_slot[s] + below[e], first, rows) : -1;
+        row_of_slot[s] = row;
+        if (row >= 0) slot_of_row[row] = static_cast<int32_t>(s);
+    }
+    fill_empty_rows<MASKED>(G, rows, first, count, me, chunks, slot_of_row);
+}
+
+// Slots per CTA of the two-launch form: a step of 1024, or more so that there are at most
+// kSortChunks chunks (each CTA of the second launch reads every chunk's counts).
+constexpr int64_t kSortChunks = 148;
+static int64_t chunk_of(int64_t slots) {
+    const int64_t steps = (slots + kSortThreads - 1) / kSortThreads;
+    return (steps + kSortChunks - 1) / kSortChunks * kSortThreads;
+}
+
+int64_t moe_sort_workspace(int64_t slots, int G) {
+    if (slots <= kSortOneCta) return 0;
+    const int64_t chunk = chunk_of(slots);
+    return (slots + chunk - 1) / chunk * ((G + 3) / 4) * static_cast<int64_t>(sizeof(int4));
+}
+
+template <typename Kernel>
+static dg_status_t allow_smem(Kernel kernel, size_t bytes, int &configured_device) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return DG_ERR_CUDA;
+    if (configured_device == device) return DG_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
+        cudaSuccess)
+        return DG_ERR_CUDA;
+    configured_device = device;
+    return DG_OK;
 }
 
 template <typename IdT, bool MASKED>
-static dg_status_t launch_sort_impl(const void *ids, int64_t slots, int G, int64_t rows, int32_t *offsets,
-                                    int32_t *row_of_slot, int32_t *slot_of_row, cudaStream_t stream) {
-    auto kernel = moe_sort_kernel<IdT, MASKED>;
-    const int ctas = slots <= kSortOneCta ? 1 : kSortCluster;
-    const int64_t pieces = static_cast<int64_t>(ctas) * kSortWarps;
-    const int per_warp = static_cast<int>(((slots + pieces - 1) / pieces + 31) / 32 * 32);
-    const size_t smem = sizeof(int) * (static_cast<size_t>(kSortWarps) * G + 3 * G + 1 + 32);
-    static thread_local int configured_device = -1;
-    int device = 0;
-    cudaGetDevice(&device);
-    if (configured_device != device) {
-        const int most = static_cast<int>(sizeof(int) * ((kSortWarps + 3) * kSortMaxG + 33));
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
-            return DG_ERR_CUDA;
-        configured_device = device;
+static dg_status_t launch_sort_impl(const IdT *ids, int64_t slots, int G, int64_t rows, int32_t *offsets,
+                                    int32_t *row_of_slot, int32_t *slot_of_row, int32_t *workspace,
+                                    cudaStream_t stream) {
+    int bits = 0;
+    while ((1 << bits) < G) ++bits;
+    if (slots <= kSortOneCta) {
+        static thread_local int configured_device = -1;
+        const size_t fixed = sizeof(int) * (2 * static_cast<size_t>(G) + 1 + 32);
+        const size_t warps = slots < kSortThreads ? (slots + 31) / 32 : kSortWarps;
+        const dg_status_t st = allow_smem(moe_sort_kernel<IdT, MASKED>, sizeof(int) * ((kSortWarps + 2) * kSortMaxG + 33),
+                                          configured_device);
+        if (st != DG_OK) return st;
+        return launch_pdl(moe_sort_kernel<IdT, MASKED>, 1, kSortThreads, fixed + sizeof(int) * warps * G, stream, ids,
+                          static_cast<int>(slots), G, bits, static_cast<int>(rows), offsets, row_of_slot, slot_of_row);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-    cfg.blockDim = dim3(kSortThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const IdT *>(ids), static_cast<int>(slots), per_warp, G,
-                              static_cast<int>(rows), offsets, row_of_slot, slot_of_row, ctas) == cudaSuccess
-               ? DG_OK
-               : DG_ERR_CUDA;
+    static thread_local int configured_device = -1;
+    const size_t smem = sizeof(int) * static_cast<size_t>(kSortWarps + 1) * G;
+    dg_status_t st = allow_smem(moe_rank_kernel<IdT>, sizeof(int) * (kSortWarps + 1) * kSortMaxG, configured_device);
+    if (st != DG_OK) return st;
+    const int64_t chunk = chunk_of(slots);
+    const int n = static_cast<int>((slots + chunk - 1) / chunk);
+    st = launch_pdl(moe_rank_kernel<IdT>, n, kSortThreads, smem, stream, ids, slots, chunk, G, bits, row_of_slot,
+                    workspace);
+    if (st != DG_OK) return st;
+    return launch_pdl(moe_place_kernel<IdT, MASKED>, n, kSortThreads, 0, stream, ids, slots, chunk, G, (G + 3) / 4,
+                      static_cast<int>(rows), static_cast<const int32_t *>(workspace), offsets, row_of_slot,
+                      slot_of_row);
 }
 
 dg_status_t launch_moe_sort(const void *ids, bool ids64, int64_t slots, int G, bool masked, int64_t rows,
-                            int32_t *offsets, int32_t *row_of_slot, int32_t *slot_of_row, const DeviceInfo &dev,
+                            int32_t *offsets, int32_t *row_of_slot, int32_t *slot_of_row, int32_t *workspace,
                             cudaStream_t stream) {
-    (void)dev;
-    if (ids64)
-        return masked ? launch_sort_impl<int64_t, true>(ids, slots, G, rows, offsets, row_of_slot, slot_of_row, stream)
-                      : launch_sort_impl<int64_t, false>(ids, slots, G, rows, offsets, row_of_slot, slot_of_row, stream);
-    return masked ? launch_sort_impl<int32_t, true>(ids, slots, G, rows, offsets, row_of_slot, slot_of_row, stream)
-                  : launch_sort_impl<int32_t, false>(ids, slots, G, rows, offsets, row_of_slot, slot_of_row, stream);
+    if (ids64) {
+        const int64_t *p = static_cast<const int64_t *>(ids);
+        return masked ? launch_sort_impl<int64_t, true>(p, slots, G, rows, offsets, row_of_slot, slot_of_row, workspace, stream)
+                      : launch_sort_impl<int64_t, false>(p, slots, G, rows, offsets, row_of_slot, slot_of_row, workspace, stream);
+    }
+    const int32_t *p = static_cast<const int32_t *>(ids);
+    return masked ? launch_sort_impl<int32_t, true>(p, slots, G, rows, offsets, row_of_slot, slot_of_row, workspace, stream)
+                  : launch_sort_impl<int32_t, false>(p, slots, G, rows, offsets, row_of_slot, slot_of_row, workspace, stream);
 }
 
 }  // namespace dg

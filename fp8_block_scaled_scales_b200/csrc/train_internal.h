@@ -7,9 +7,10 @@
 namespace dg {
 
 // moe_sort.cu.  masked: `offsets` receives the counts [G] and `rows` is M_max, else the
-// group offsets [G+1] and the row capacity.
+// group offsets [G+1] and the row capacity.  workspace: moe_sort_workspace bytes.
+int64_t moe_sort_workspace(int64_t slots, int G);
 dg_status_t launch_moe_sort(const void *ids, bool ids64, int64_t slots, int G, bool masked, int64_t rows,
-                            int32_t *offsets, int32_t *row_of_slot, int32_t *slot_of_row, const DeviceInfo &dev,
+                            int32_t *offsets, int32_t *row_of_slot, int32_t *slot_of_row, int32_t *workspace,
                             cudaStream_t stream);
 
 // moe_rows.cu

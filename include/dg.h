@@ -320,10 +320,17 @@ dg_status_t dg_fp8_gemm_1x128_select(const uint8_t *A, const float *sA_t,
  * k >= 1, T * k <= 2^30, 1 <= G <= 1024; M_total_capacity a multiple of 128 that
  * holds the worst case: at least (S + 127 min(G, S)) / 128 * 128 for S = T * k
  * slots.  T == 0 writes empty groups.
+ * workspace     : at least dg_moe_sort_workspace(T, k, G) bytes of device memory, 16-byte
+ *                 aligned, for this call alone while it runs; null where that is 0 (up to
+ *                 2048 slots).  Less gives DG_ERR_INVALID_ARG.
  */
 dg_status_t dg_moe_sort(const void *topk_ids, int ids_64bit, int64_t T, int k, int G,
                         int32_t *group_offsets, int32_t *row_of_slot, int32_t *slot_of_row,
-                        int64_t M_total_capacity, cudaStream_t stream);
+                        int64_t M_total_capacity, void *workspace, int64_t workspace_bytes,
+                        cudaStream_t stream);
+
+/* Bytes of workspace that dg_moe_sort and dg_moe_sort_masked need (0 for sizes they refuse). */
+int64_t dg_moe_sort_workspace(int64_t T, int k, int G);
 
 /*
  * dg_moe_sort into the masked layout: expert g's slots take rows g * M_max, ... in
@@ -335,7 +342,8 @@ dg_status_t dg_moe_sort(const void *topk_ids, int ids_64bit, int64_t T, int k, i
  */
 dg_status_t dg_moe_sort_masked(const void *topk_ids, int ids_64bit, int64_t T, int k, int G,
                                int32_t *masked_m, int32_t *row_of_slot, int32_t *slot_of_row,
-                               int64_t M_max, cudaStream_t stream);
+                               int64_t M_max, void *workspace, int64_t workspace_bytes,
+                               cudaStream_t stream);
 
 /*
  * Gather by expert and quantize: row r of the sorted layout is x[slot_of_row[r] / k],

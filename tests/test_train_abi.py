@@ -21,32 +21,39 @@ def lib():
 
 def test_sort_refusals(lib):
     f = lib.dg_moe_sort
-    assert f(P, 0, -1, 2, 4, P, P, P, 1024, NULL) == SHAPE
-    assert f(P, 0, 8, 0, 4, P, P, P, 1024, NULL) == SHAPE              # k == 0
-    assert f(P, 0, 8, 2, 0, P, P, P, 1024, NULL) == SHAPE
-    assert f(P, 0, 8, 2, 1025, P, P, P, 1 << 20, NULL) == SHAPE
-    assert f(P, 0, 8, 2, 4, P, P, P, 1000, NULL) == SHAPE              # capacity % 128
+    assert f(P, 0, -1, 2, 4, P, P, P, 1024, NULL, 0, NULL) == SHAPE
+    assert f(P, 0, 8, 0, 4, P, P, P, 1024, NULL, 0, NULL) == SHAPE              # k == 0
+    assert f(P, 0, 8, 2, 0, P, P, P, 1024, NULL, 0, NULL) == SHAPE
+    assert f(P, 0, 8, 2, 1025, P, P, P, 1 << 20, NULL, 0, NULL) == SHAPE
+    assert f(P, 0, 8, 2, 4, P, P, P, 1000, NULL, 0, NULL) == SHAPE              # capacity % 128
     # 16 slots over 4 experts may take four blocks of 128
-    assert f(P, 0, 8, 2, 4, P, P, P, 384, NULL) == SHAPE
-    assert f(P, 0, 1 << 30, 2, 4, P, P, P, 1 << 30, NULL) == SHAPE     # T * k > 2^30
-    assert f(NULL, 0, 8, 2, 4, P, P, P, 512, NULL) == ARG
-    assert f(P, 0, 8, 2, 4, NULL, P, P, 512, NULL) == ARG
-    assert f(P, 0, 8, 2, 4, P, P, NULL, 512, NULL) == ARG
-    assert f(ctypes.c_void_p(0x10004), 1, 8, 2, 4, P, P, P, 512, NULL) == ALIGN  # int64 ids at 4 bytes
-    assert f(P, 0, 8, 2, 4, ODD, P, P, 512, NULL) == ALIGN
+    assert f(P, 0, 8, 2, 4, P, P, P, 384, NULL, 0, NULL) == SHAPE
+    assert f(P, 0, 1 << 30, 2, 4, P, P, P, 1 << 30, NULL, 0, NULL) == SHAPE     # T * k > 2^30
+    assert f(NULL, 0, 8, 2, 4, P, P, P, 512, NULL, 0, NULL) == ARG
+    assert f(P, 0, 8, 2, 4, NULL, P, P, 512, NULL, 0, NULL) == ARG
+    assert f(P, 0, 8, 2, 4, P, P, NULL, 512, NULL, 0, NULL) == ARG
+    assert f(ctypes.c_void_p(0x10004), 1, 8, 2, 4, P, P, P, 512, NULL, 0, NULL) == ALIGN  # int64 ids at 4 bytes
+    assert f(P, 0, 8, 2, 4, ODD, P, P, 512, NULL, 0, NULL) == ALIGN
+    # more slots than one CTA takes: a workspace of the size that the library names
+    need = lib.dg_moe_sort_workspace(8192, 2, 64)
+    cap = binding.moe_capacity(8192, 2, 64)
+    assert need > 0 and lib.dg_moe_sort_workspace(8, 2, 4) == 0 and lib.dg_moe_sort_workspace(-1, 2, 4) == 0
+    assert f(P, 0, 8192, 2, 64, P, P, P, cap, NULL, need, NULL) == ARG
+    assert f(P, 0, 8192, 2, 64, P, P, P, cap, P, need - 4, NULL) == ARG
+    assert f(P, 0, 8192, 2, 64, P, P, P, cap, ODD, need, NULL) == ALIGN
     m = lib.dg_moe_sort_masked
-    assert m(P, 0, 8, 2, 4, P, P, P, -1, NULL) == SHAPE
-    assert m(P, 0, 8, 2, 4, P, P, P, 1 << 30, NULL) == SHAPE           # G * M_max >= 2^31
-    assert m(P, 0, 8, 2, 4, NULL, P, P, 64, NULL) == ARG
-    assert m(P, 0, 8, 2, 4, P, P, ODD, 64, NULL) == ALIGN
+    assert m(P, 0, 8, 2, 4, P, P, P, -1, NULL, 0, NULL) == SHAPE
+    assert m(P, 0, 8, 2, 4, P, P, P, 1 << 30, NULL, 0, NULL) == SHAPE           # G * M_max >= 2^31
+    assert m(P, 0, 8, 2, 4, NULL, P, P, 64, NULL, 0, NULL) == ARG
+    assert m(P, 0, 8, 2, 4, P, P, ODD, 64, NULL, 0, NULL) == ALIGN
 
 
 def test_capacity_helper_is_the_least_the_sort_takes(lib):
     for T, k, G in ((1, 8, 64), (1, 1, 1), (100, 2, 3), (8192, 2, 8), (0, 4, 16)):
         cap = binding.moe_capacity(T, k, G)
         if cap:
-            assert lib.dg_moe_sort(P, 0, T, k, G, P, P, P, cap - 128, NULL) == SHAPE
-        assert lib.dg_moe_sort(P, 0, T, k, G, ODD, P, P, cap, NULL) == ALIGN  # capacity accepted
+            assert lib.dg_moe_sort(P, 0, T, k, G, P, P, P, cap - 128, P, 1 << 30, NULL) == SHAPE
+        assert lib.dg_moe_sort(P, 0, T, k, G, ODD, P, P, cap, P, 1 << 30, NULL) == ALIGN  # capacity accepted
         # the worst routing fits: every expert one slot, the rest in one, each rounded up
         S = T * k
         used = min(G, S)
