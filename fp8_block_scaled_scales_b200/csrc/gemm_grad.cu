@@ -51,19 +51,23 @@ constexpr int kGradRegsProducer = 56;  // warpgroup 0
 constexpr int kGradRegsEpilogue = 224; // warpgroups 1, 2
 static_assert(128 * kGradRegsProducer + 256 * kGradRegsEpilogue <= kGradThreads * kGradRegsLaunch,
               "setmaxnreg split exceeds the registers the block is launched with");
-constexpr int kGradStages = 4;
 constexpr int kGradBufs = 2;
+constexpr uint32_t kGradBHalf = 128 * 128;  // one 128-column box of B
 
+// STAGES operand stages in the ring; BOXES output boxes of 4 KB for each epilogue warp.
+template <int STAGES, int BOXES>
 struct GradSmem {
     static constexpr uint32_t kABytes = 128 * 128;
-    static constexpr uint32_t kBHalf = 128 * 128;  // one 128-column box of B
+    static constexpr uint32_t kBHalf = kGradBHalf;
     static constexpr uint32_t kBBytes = 2 * kBHalf;
     static constexpr uint32_t kCBoxBytes = 32 * 128;  // 32 rows x 128 bytes
     static constexpr uint32_t kOffA = 0;
-    static constexpr uint32_t kOffB = kOffA + kGradStages * kABytes;
-    static constexpr uint32_t kOffC = kOffB + kGradStages * kBBytes;
-    static constexpr uint32_t kOffBar = kOffC + 8 * kCBoxBytes;
-    static constexpr uint32_t kNumBars = 2 * kGradStages + 2 * kGradBufs + 2;
+    static constexpr uint32_t kOffB = kOffA + STAGES * kABytes;
+    static constexpr uint32_t kOffC = kOffB + STAGES * kBBytes;
+    static constexpr uint32_t kOffBar = kOffC + 8 * BOXES * kCBoxBytes;
+    static constexpr uint32_t kNumBars = 3 * STAGES + 2 * kGradBufs + 2;
+    // iterations between two uses of a `full` barrier by its MMA thread
+    static constexpr int kPeriod = STAGES % 2 ? 2 * STAGES : STAGES;
     static constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr uint32_t kBytes = kOffMisc + 16;
     static constexpr uint32_t kDynamicBytes = kBytes + 1024;  // slack for 1024-byte alignment
@@ -76,7 +80,7 @@ struct GradSmem {
 __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(GradSmem::kBHalf >> 4) << 16;
+    d |= static_cast<uint64_t>(kGradBHalf >> 4) << 16;
     d |= static_cast<uint64_t>(1024u >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
@@ -196,11 +200,11 @@ __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, int num_m, in
     return u;
 }
 
-template <int MODE, bool F32>
+template <int MODE, bool F32, int STAGES, int BOXES>
 __global__ void __launch_bounds__(kGradThreads, 1)
     grad_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const GradParams p) {
-    using L = GradSmem;
+    using L = GradSmem<STAGES, BOXES>;
     constexpr int kColsPerWarp = 128;
     constexpr uint32_t kTmemCols = tmem_cols_for(kGradBufs * 256);
     constexpr uint32_t kMajor = kIdescBMajorN | (MODE == kWgrad ? kIdescAMajorM : 0u);
@@ -210,8 +214,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
-    uint64_t *empty = full + kGradStages;
-    uint64_t *tfull = empty + kGradStages;
+    uint64_t *empty = full + 2 * STAGES;
+    uint64_t *tfull = empty + STAGES;
     uint64_t *tempty = tfull + kGradBufs;
     uint64_t *mdone = tempty + kGradBufs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
@@ -222,8 +226,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const int lane = lane_id();
 
     if (warp == 0 && lane == 0) {
-        for (int s = 0; s < kGradStages; ++s) {
-            mbar_init(&full[s], 1);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 2);
+            mbar_init(&full[STAGES + s], 2);
             mbar_init(&empty[s], 1);
         }
         for (int q = 0; q < 2; ++q) mbar_init(&mdone[q], 1);
@@ -285,43 +290,57 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         regs_dealloc<kGradRegsProducer>();
         if ((warp == 0 || warp == 3) && lane == 0) {
             // ----------------------------------------------------------- producers
-            const int pr = warp == 0 ? 0 : 1;
-            uint32_t issued = 0, parity_bits = 0;
-            int it = 0;
+            // One thread loads dY, the other B's one or two boxes, for every iteration: both
+            // see every phase of `empty` in order, whatever the number of stages.  A stage
+            // has two `full` barriers, one for each MMA thread, so that each of those is
+            // waited on by one thread alone and in order too.
+            const bool loads_a = warp == 0;
+            uint32_t issued = 0, parity_bits = 0;  // per full barrier: its last phase
+            int it = 0, s = 0, q = 0;
+            uint32_t v = 0, x = 0;  // it / STAGES, it / kPeriod
             bool ok = true;
             for (int w = static_cast<int>(blockIdx.x); w < num_units && ok; w += grid) {
                 const GradUnit u = unit_at(w);
-                const uint32_t bytes = L::kABytes + (u.narrow ? L::kBHalf : L::kBBytes);
                 for (int i = 0; i < u.blocks; ++i, ++it) {
-                    if ((it & 1) != pr) continue;  // the other producer's stage
-                    const int s = it % kGradStages;
-                    const uint32_t v = static_cast<uint32_t>(it / kGradStages);
                     if (!mbar_wait(&empty[s], (v & 1u) ^ 1u, abort_flag, p.timeout_ns)) {
                         record_failure(p.status, kStatusTimeout, 0, it);
                         *abort_flag = 1;
                         ok = false;
                         break;
                     }
-                    if ((p.debug_flags & 1) && it == 0) continue;  // test hook: never fill stage 0
-                    mbar_arrive_expect_tx(&full[s], bytes);
-                    uint8_t *sa = smem + L::kOffA + s * L::kABytes;
-                    uint8_t *sb = smem + L::kOffB + s * L::kBBytes;
-                    if (MODE == kDgrad)
-                        tma_load_2d(sa, &tmA, &full[s], i * 128, u.a_row);
-                    else
-                        tma_load_2d(sa, &tmA, &full[s], u.a_col, u.a_row + i * 128);
-                    tma_load_2d(sb, &tmB, &full[s], u.b_col, u.b_row + i * 128);
-                    if (!u.narrow) tma_load_2d(sb + L::kBHalf, &tmB, &full[s], u.b_col + 128, u.b_row + i * 128);
-                    issued |= 1u << s;
-                    parity_bits = (parity_bits & ~(1u << s)) | ((v & 1u) << s);
+                    const int bar = q * STAGES + s;
+                    if (!((p.debug_flags & 1) && it == 0)) {  // test hook: never fill stage 0
+                        if (loads_a) {
+                            mbar_arrive_expect_tx(&full[bar], L::kABytes);
+                            uint8_t *dst = smem + L::kOffA + s * L::kABytes;
+                            if (MODE == kDgrad)
+                                tma_load_2d(dst, &tmA, &full[bar], i * 128, u.a_row);
+                            else
+                                tma_load_2d(dst, &tmA, &full[bar], u.a_col, u.a_row + i * 128);
+                        } else {
+                            mbar_arrive_expect_tx(&full[bar], u.narrow ? L::kBHalf : L::kBBytes);
+                            uint8_t *dst = smem + L::kOffB + s * L::kBBytes;
+                            tma_load_2d(dst, &tmB, &full[bar], u.b_col, u.b_row + i * 128);
+                            if (!u.narrow)
+                                tma_load_2d(dst + L::kBHalf, &tmB, &full[bar], u.b_col + 128, u.b_row + i * 128);
+                        }
+                        issued |= 1u << bar;
+                        parity_bits = (parity_bits & ~(1u << bar)) | ((x & 1u) << bar);
+                    }
+                    q ^= 1;
+                    if (++s == STAGES) {
+                        s = 0;
+                        ++v;
+                        if (it % L::kPeriod == L::kPeriod - 1) ++x;
+                    }
                 }
             }
             // every load issued must land before the CTA may exit
             const int never = 0;
-            for (int s = 0; s < kGradStages; ++s)
-                if (issued & (1u << s))
-                    if (!mbar_wait(&full[s], (parity_bits >> s) & 1u, &never, p.timeout_ns))
-                        record_failure(p.status, kStatusTimeout, 0, -1 - s);
+            for (int bar = 0; bar < 2 * STAGES; ++bar)
+                if (issued & (1u << bar))
+                    if (!mbar_wait(&full[bar], (parity_bits >> bar) & 1u, &never, p.timeout_ns))
+                        record_failure(p.status, kStatusTimeout, 0, -1 - bar);
         } else if ((warp == 1 || warp == 2) && lane == 0) {
             // ------------------------------------------------------- MMA (two threads)
             const int q = warp - 1;
@@ -334,15 +353,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 const uint32_t idesc = u.narrow ? kIdescNarrow : kIdescWide;
                 for (int i = 0; i < u.blocks; ++i, ++it) {
                     if ((it & 1) != q) continue;
-                    const int s = it % kGradStages;
-                    const uint32_t v = static_cast<uint32_t>(it / kGradStages);
+                    const int s = it % STAGES;
+                    const uint32_t v = static_cast<uint32_t>(it / L::kPeriod);  // phase of this thread's barrier
                     const int buf = it % kGradBufs;
                     const uint32_t x = static_cast<uint32_t>(it / kGradBufs);
                     const uint64_t adesc = MODE == kDgrad ? sdesc_kmajor_sw128(a0 + s * L::kABytes)
                                                           : sdesc_mnmajor_sw128(a0 + s * L::kABytes);
                     const uint64_t bdesc = sdesc_mnmajor_sw128(b0 + s * L::kBBytes);
                     const uint32_t d = tmem_base + static_cast<uint32_t>(buf * 256);
-                    if (!mbar_wait(&full[s], v & 1u, abort_flag, p.timeout_ns) ||
+                    if (!mbar_wait(&full[q * STAGES + s], v & 1u, abort_flag, p.timeout_ns) ||
                         !mbar_wait(&tempty[buf], (x & 1u) ^ 1u, abort_flag, p.timeout_ns)) {
                         record_failure(p.status, kStatusTimeout, 1, it);
                         *abort_flag = 1;
@@ -374,7 +393,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         const int ew = warp - 4;
         const int quarter = warp & 3;
         const int half = ew >> 2;
-        uint8_t *cstage = smem + L::kOffC + ew * L::kCBoxBytes;
+        uint8_t *boxes = smem + L::kOffC + ew * BOXES * L::kCBoxBytes;
         float2 acc[kColsPerWarp / 2];
         int it = 0;
         bool ok = true;
@@ -417,7 +436,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
             for (int j = 0; j < kColsPerWarp / kBoxCols; ++j) {
                 if (j * kBoxCols >= ncols) break;
-                if (lane == 0) bulk_wait_read0();  // the previous store has finished reading cstage
+                uint8_t *cstage = boxes + (j % BOXES) * L::kCBoxBytes;
+                // the store before the last BOXES - 1 has finished reading this box
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(BOXES - 1) : "memory");
                 __syncwarp();
                 uint8_t *rowp = cstage + lane * 128;
 #pragma unroll
@@ -442,8 +463,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                         tma_store_add_2d(&tmC, cstage, col0 + j * kBoxCols, row0);
                     else
                         tma_store_2d(&tmC, cstage, col0 + j * kBoxCols, row0);
-                    bulk_commit();
                 }
+                if (lane == 0) bulk_commit();  // an empty group keeps the count
             }
         }
         if (lane == 0) bulk_wait_all0();
@@ -457,11 +478,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
 }
 
-template <int MODE, bool F32>
+template <int MODE, bool F32, int STAGES, int BOXES>
 static dg_status_t launch_grad_impl(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    using L = GradSmem;
+    using L = GradSmem<STAGES, BOXES>;
     static_assert(L::kDynamicBytes <= 232448, "shared memory budget");
-    static_assert(kGradStages % 2 == 0 && kGradBufs % 2 == 0, "each MMA thread must own its stages and buffers");
+    static_assert(kGradBufs % 2 == 0, "each MMA thread must own its buffers");
     CUtensorMap tmA, tmB, tmC;
     const uint64_t b_rows = MODE == kDgrad ? static_cast<uint64_t>(a.G) * a.N : static_cast<uint64_t>(a.M);
     const uint64_t c_rows = MODE == kDgrad ? static_cast<uint64_t>(a.M) : static_cast<uint64_t>(a.G) * a.N;
@@ -494,7 +515,7 @@ static dg_status_t launch_grad_impl(const GradArgs &a, const DeviceInfo &dev, cu
     p.status = ctl.status;
     p.debug_flags = ctl.debug_flags;
 
-    auto kernel = grad_gemm_kernel<MODE, F32>;
+    auto kernel = grad_gemm_kernel<MODE, F32, STAGES, BOXES>;
     static thread_local int configured_device = -1;
     int device = 0;
     cudaGetDevice(&device);
@@ -516,11 +537,16 @@ static dg_status_t launch_grad_impl(const GradArgs &a, const DeviceInfo &dev, cu
 }
 
 dg_status_t launch_dgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    return launch_grad_impl<kDgrad, false>(a, dev, stream);
+    return launch_grad_impl<kDgrad, false, 4, 1>(a, dev, stream);
 }
 
+// Three operand stages and two output boxes a warp: an output tile is 128 KB (FP32) against a
+// few blocks of contraction, so its stores matter more than a fourth stage (64 experts of N =
+// 2048, K = 7168 over 32768 slots: 960 us against 1000 with four and one, BF16 728 against 755;
+// 8 experts of 4096^2: 340 and 340).
 dg_status_t launch_wgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    return a.fp32 ? launch_grad_impl<kWgrad, true>(a, dev, stream) : launch_grad_impl<kWgrad, false>(a, dev, stream);
+    return a.fp32 ? launch_grad_impl<kWgrad, true, 3, 2>(a, dev, stream)
+                  : launch_grad_impl<kWgrad, false, 3, 2>(a, dev, stream);
 }
 
 }  // namespace dg

@@ -6,7 +6,7 @@
 //   s = fl32(amax / 448) per 128x128 block (1 if 0), q = E4M3_rn_satfinite(fl32(v / s)).
 //   Without weights the codes and scales are those of the block quantizer on the gathered
 //   matrix, bit for bit.  With weights it is the gradient of the combination with respect to
-//   the expert rows.
+//   the expert rows (quantize8_negated says where a code may differ from the definition's).
 // combine:            out[t] = bf16(sum_j weights[t][j] * y[row(t, j)]), FP32, ascending j;
 //   without weights it is the gradient of the dispatch.
 // combine_backward:   dweights[t][j] = sum_h dout[t][h] * y[row(t, j)][h], FP32.
@@ -84,14 +84,13 @@ __device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, co
         if (bc + 1 < bc1) ask(bc + 1);
         uint32_t m;
         if (WEIGHTS) {
+            // the largest |fl32(w x)| of a row's piece is that of its largest |x|
             float f = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float w = sm.wgt[sub + 16 * i];
-                float2 x[4];
-                bf16x8_to_f32(v[i], x);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f = amax3(f, __fmul2_rn(x[j], make_float2(w, w)));
+            for (int i = 0; i < 8; i += 2) {
+                const float a = __uint_as_float(amax_bits_of(amax_pair8(v[i])) << 16);
+                const float b = __uint_as_float(amax_bits_of(amax_pair8(v[i + 1])) << 16);
+                f = amax3(f, make_float2(a * sm.wgt[sub + 16 * i], b * sm.wgt[sub + 16 * (i + 1)]));
             }
             m = __float_as_uint(f);
         } else {
@@ -109,12 +108,12 @@ __device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, co
                 if (sub + 16 * i >= rows) break;
                 uint2 q;
                 if (WEIGHTS) {
-                    const float w = sm.wgt[sub + 16 * i];
+                    const float nw = -sm.wgt[sub + 16 * i];
                     float2 x[4];
                     bf16x8_to_f32(v[i], x);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], make_float2(w, w));
-                    q = quantize8_f32(x, bs);
+                    for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], make_float2(nw, nw));
+                    q = quantize8_negated(x, bs);
                 } else {
                     q = quantize8_corrected(v[i], bs);
                 }

@@ -55,31 +55,6 @@ __device__ __forceinline__ FastScale fast_scale(float amax) {
     return b;
 }
 
-// Eight FP32 values -> codes of fl32(x / s), exactly: the bracket of quantize8 (quant_e4m3.cuh),
-// whose proof takes any FP32 x and has room for r's error (2^-21 against 2^-23 + 2 * 2^-24).
-__device__ __forceinline__ uint2 quantize8_f32(const float2 (&x)[4], const FastScale &b) {
-    const float rlo = __fmul_rn(b.r, 1.0f - 0x1p-21f), rhi = __fmul_rn(b.r, 1.0f + 0x1p-21f);
-    float2 lo[4], hi[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        lo[j] = __fmul2_rn(x[j], make_float2(rlo, rlo));
-        hi[j] = __fmul2_rn(x[j], make_float2(rhi, rhi));
-    }
-    uint2 out;
-    out.x = e4m3x4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
-    out.y = e4m3x4(hi[2].x, hi[2].y, hi[3].x, hi[3].y);
-    const uint32_t lx = e4m3x4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
-    const uint32_t ly = e4m3x4(lo[2].x, lo[2].y, lo[3].x, lo[3].y);
-    if (__builtin_expect(((out.x ^ lx) | (out.y ^ ly)) != 0u || !b.fast, 0)) {
-        float2 y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = make_float2(__fdiv_rn(x[j].x, b.s), __fdiv_rn(x[j].y, b.s));
-        out.x = e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y);
-        out.y = e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y);
-    }
-    return out;
-}
-
 // Eight FP32 values that are themselves rounded results (an activation, a gradient): x / s as
 // the product x r, off by 2^-23 + 2^-24 where the quotient is off by 2^-24.  The values
 // carry larger errors already, so the exact quotient would decide nothing.
@@ -95,36 +70,44 @@ __device__ __forceinline__ uint2 quantize8_near(const float2 (&x)[4], const Fast
     return make_uint2(e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y), e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y));
 }
 
-// Eight BF16 -> codes of fl32(x / s), exactly: the quotient corrected by its remainder.  With
-// n = -x: y = n (-r), e = y s + n (the negative remainder), x/s = e (-r) + y; in this order
-// of signs a zero keeps its own.  Three multiply-adds a pair and one conversion, with no
-// second path for values near a rounding boundary, which a block whose amax is a multiple of
-// 7 meets often.  For every BF16 x and amax in the window, and any r within 2 units of 1/s,
-// the code is that of the IEEE quotient (checked exhaustively on the CPU).
-__device__ __forceinline__ uint2 quantize8_corrected(uint4 v, const FastScale &b) {
+// Four pairs n = -x -> codes of fl32(x / s): the quotient corrected by its remainder, y = n (-r),
+// e = y s + n (the negative remainder), x/s = e (-r) + y; in this order of signs a zero keeps
+// its own.  Three multiply-adds a pair and one conversion, with no second path for values
+// near a rounding boundary, which a block whose amax is a multiple of 7 meets often.
+//   x BF16: for every x and amax in the window, and any r within 2 units of 1/s, the code is
+//     that of the IEEE quotient (checked exhaustively on the CPU).
+//   x any FP32: the quotient is the rounding of a value within 2^-46 of x/s, so the code can
+//     differ only where x/s lies that close to the middle between an E4M3 rounding boundary
+//     and the next FP32 number.
+__device__ __forceinline__ uint2 quantize8_negated(const float2 (&n)[4], const FastScale &b) {
     float2 q[4];
     if (__builtin_expect(b.fast, 1)) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         const float2 s2 = make_float2(b.s, b.s), nr = make_float2(-b.r, -b.r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float2 n;  // x * (-1) + (-0), exact
-            asm("{\n\t.reg .b16 l, h, m;\n\t"
-                "mov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
-                "fma.rn.f32.bf16 %0, l, m, %3;\n\t"
-                "fma.rn.f32.bf16 %1, h, m, %3;\n\t}"
-                : "=f"(n.x), "=f"(n.y)
-                : "r"(w[j]), "f"(-0.0f));
-            const float2 y = __fmul2_rn(n, nr);
-            q[j] = __ffma2_rn(__ffma2_rn(y, s2, n), nr, y);
+            const float2 y = __fmul2_rn(n[j], nr);
+            q[j] = __ffma2_rn(__ffma2_rn(y, s2, n[j]), nr, y);
         }
     } else {
-        float2 x[4];
-        bf16x8_to_f32(v, x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = make_float2(__fdiv_rn(x[j].x, b.s), __fdiv_rn(x[j].y, b.s));
+        for (int j = 0; j < 4; ++j) q[j] = make_float2(__fdiv_rn(-n[j].x, b.s), __fdiv_rn(-n[j].y, b.s));
     }
     return make_uint2(e4m3x4(q[0].x, q[0].y, q[1].x, q[1].y), e4m3x4(q[2].x, q[2].y, q[3].x, q[3].y));
+}
+
+// Eight BF16 -> codes of fl32(x / s), exactly.
+__device__ __forceinline__ uint2 quantize8_corrected(uint4 v, const FastScale &b) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float2 n[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm("{\n\t.reg .b16 l, h, m;\n\t"  // x * (-1) + (-0), exact
+            "mov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
+            "fma.rn.f32.bf16 %0, l, m, %3;\n\t"
+            "fma.rn.f32.bf16 %1, h, m, %3;\n\t}"
+            : "=f"(n[j].x), "=f"(n[j].y)
+            : "r"(w[j]), "f"(-0.0f));
+    return quantize8_negated(n, b);
 }
 
 // The largest |x| of eight BF16 as two magnitudes side by side, a NaN above infinity.
