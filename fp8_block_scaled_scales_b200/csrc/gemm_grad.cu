@@ -52,6 +52,8 @@ constexpr int kGradRegsEpilogue = 224; // warpgroups 1, 2
 static_assert(128 * kGradRegsProducer + 256 * kGradRegsEpilogue <= kGradThreads * kGradRegsLaunch,
               "setmaxnreg split exceeds the registers the block is launched with");
 constexpr int kGradBufs = 2;
+constexpr uint32_t kGradUnitBytes = 24;
+constexpr int kGradUnits = 8;  // units an epilogue warp works out at a time, one a lane
 constexpr uint32_t kGradBHalf = 128 * 128;  // one 128-column box of B
 
 // STAGES operand stages in the ring; BOXES output boxes of 4 KB for each epilogue warp.
@@ -69,7 +71,8 @@ struct GradSmem {
     // iterations between two uses of a `full` barrier by its MMA thread
     static constexpr int kPeriod = STAGES % 2 ? 2 * STAGES : STAGES;
     static constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;
-    static constexpr uint32_t kBytes = kOffMisc + 16;
+    static constexpr uint32_t kOffUnits = kOffMisc + 16;  // a table of units for each epilogue warp
+    static constexpr uint32_t kBytes = kOffUnits + 8 * kGradUnits * kGradUnitBytes;
     static constexpr uint32_t kDynamicBytes = kBytes + 1024;  // slack for 1024-byte alignment
 };
 
@@ -112,14 +115,12 @@ struct StridedScales {
         const int k = base + lane_id();
         return k < end ? __ldg(a + k * sa) * __ldg(b + k * sb) : 0.0f;
     }
-    __device__ __forceinline__ void start(const float *a0, const float *b0, int64_t step_a, int64_t step_b, int n) {
+    __device__ __forceinline__ void set(const float *a0, const float *b0, int64_t step_a, int64_t step_b, int n) {
         a = a0;
         b = b0;
         sa = step_a;
         sb = step_b;
         end = n;
-        cur = load(0);
-        next = load(32);
     }
     __device__ __forceinline__ float scale(int i) {
         if ((i & 31) == 0 && i > 0) {
@@ -130,6 +131,12 @@ struct StridedScales {
     }
 };
 
+// What the epilogue needs of a unit.
+struct UnitEntry {
+    int blocks, c_row, c_col, narrow, sa_at, sb_row;
+};
+static_assert(sizeof(UnitEntry) == kGradUnitBytes, "table size");
+
 // One unit of work: a 128 x 256 output tile or a 128 x 128 half of one.
 struct GradUnit {
     int blocks;    // 128-deep blocks of the contraction
@@ -137,8 +144,8 @@ struct GradUnit {
     int b_row, b_col;              // of B; block i adds 128 * i to the row
     int c_row, c_col;              // of the output
     bool narrow;                   // 128 columns only
-    int sa_at, sa_step;            // scale indices at block 0 and their steps
-    int64_t sb_at;
+    int sa_at;                     // index into dY's scales at block 0 (its step: 1 or Nb)
+    int sb_row;                    // row of B's scales at block 0
 };
 
 template <int MODE>
@@ -168,8 +175,7 @@ __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, int num_m, in
         u.b_row = g * p.N;
         u.c_row = mb * 128;
         u.sa_at = mb * p.Nb;
-        u.sa_step = 1;
-        u.sb_at = static_cast<int64_t>(g) * p.Nb * p.Kc;
+        u.sb_row = g * p.Nb;
     } else {
         constexpr int kRaster = 8;
         const int per = p.num_m * p.num_k;
@@ -189,14 +195,12 @@ __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, int num_m, in
         u.b_row = m0;
         u.c_row = g * p.N + mb * 128;
         u.sa_at = m0 / 128 * p.Nb + mb;
-        u.sa_step = p.Nb;
-        u.sb_at = static_cast<int64_t>(m0 / 128) * p.Kc;
+        u.sb_row = m0 / 128;
     }
     const int col = kt * 256 + (h > 0 ? 128 : 0);
     u.narrow = h >= 0 || col + 128 >= p.K;
     if (col >= p.K) u.blocks = -1;  // the second half of a tile that has none: nothing to do
     u.b_col = u.c_col = col;
-    u.sb_at += col / 128;
     return u;
 }
 
@@ -394,18 +398,46 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         const int quarter = warp & 3;
         const int half = ew >> 2;
         uint8_t *boxes = smem + L::kOffC + ew * BOXES * L::kCBoxBytes;
+        // Working out a unit (divisions, offsets) takes 700 cycles and its first scales as many
+        // again, which a tile of a few blocks would wait for; so lanes work out the next eight
+        // units at once, and a tile's first scales are loaded before the tile before it is stored.
+        UnitEntry *table = reinterpret_cast<UnitEntry *>(smem + L::kOffUnits) + ew * kGradUnits;
+        const int my_units = static_cast<int>(blockIdx.x) < num_units
+                                 ? (num_units - 1 - static_cast<int>(blockIdx.x)) / grid + 1
+                                 : 0;
+        StridedScales scales;
+        float first_scales = 0.0f;
+        auto prepare = [&](int n) {  // unit n of this CTA: its table entry and its first scales
+            if (n >= my_units) return;
+            if (n % kGradUnits == 0) {
+                __syncwarp();
+                if (lane < kGradUnits && n + lane < my_units) {
+                    const GradUnit u = unit_at(static_cast<int>(blockIdx.x) + (n + lane) * grid);
+                    table[lane] = UnitEntry{u.blocks, u.c_row, u.c_col, u.narrow ? 1 : 0, u.sa_at, u.sb_row};
+                }
+                __syncwarp();
+            }
+            const UnitEntry e = table[n % kGradUnits];
+            const int col0 = e.c_col + half * (e.narrow ? kColsPerWarp / 2 : kColsPerWarp);
+            const bool valid = col0 < p.K;
+            scales.set(p.sA + e.sa_at, p.sB + static_cast<int64_t>(e.sb_row) * p.Kc + (valid ? col0 / 128 : 0),
+                       MODE == kDgrad ? 1 : p.Nb, p.Kc, valid ? e.blocks : 0);
+            first_scales = scales.load(0);
+        };
         float2 acc[kColsPerWarp / 2];
         int it = 0;
         bool ok = true;
-        for (int w = static_cast<int>(blockIdx.x); w < num_units && ok; w += grid) {
-            const GradUnit u = unit_at(w);
-            if (u.blocks < 0 || (MODE == kWgrad && u.blocks == 0 && p.accumulate)) continue;
+        prepare(0);
+        for (int n = 0; n < my_units && ok; ++n) {
+            const UnitEntry u = table[n % kGradUnits];
+            if (u.blocks < 0 || (MODE == kWgrad && u.blocks == 0 && p.accumulate)) {
+                prepare(n + 1);
+                continue;
+            }
             const int ncols = u.narrow ? kColsPerWarp / 2 : kColsPerWarp;
             const int col0 = u.c_col + half * ncols;
-            const bool valid = col0 < p.K;
-            StridedScales scales;
-            scales.start(p.sA + u.sa_at, p.sB + u.sb_at + (valid && !u.narrow ? half : 0), u.sa_step, p.Kc,
-                         valid ? u.blocks : 0);
+            scales.cur = first_scales;
+            scales.next = scales.load(32);
 #pragma unroll
             for (int j = 0; j < kColsPerWarp / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
             for (int i = 0; i < u.blocks; ++i, ++it) {
@@ -429,6 +461,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 });
             }
             if (!ok) break;
+            prepare(n + 1);
             // rows c_row + 32 * quarter + lane; one box of 32 rows x 128 bytes at a time
             constexpr int kBoxCols = F32 ? 32 : 64;
             const int row0 = u.c_row + quarter * 32;

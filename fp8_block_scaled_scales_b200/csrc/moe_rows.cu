@@ -41,6 +41,7 @@ __device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, co
                                               float *__restrict__ S, DispatchSmem &sm) {
     const int tid = static_cast<int>(threadIdx.x);
     const int sub = tid >> 4, lane_col = (tid & 15) * 8;
+    const int Hi = static_cast<int>(H);  // a 32 x 32 bit product for each address
     __syncthreads();  // an earlier row block's tokens are no longer read
     if (tid < 128) {
         const int slot = tid < rows ? __ldg(slot_of_row + row0 + tid) : -1;
@@ -61,7 +62,7 @@ __device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, co
             for (int i = 0; i < 8; ++i) {
                 const int t = sm.tok[sub + 16 * i];
                 if (t >= 0) {
-                    const uint16_t *p = X + static_cast<int64_t>(t) * H + col;
+                    const uint16_t *p = X + static_cast<int64_t>(t) * Hi + col;
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.piece[i][tid])), "l"(p)
                                  : "memory");
                 }
@@ -277,7 +278,7 @@ static dg_status_t launch_dispatch_impl(const void *X, const float *weights, con
     const int64_t Cb = (H + 127) / 128, Rb = rows / 128;
     const int cols = dispatch_cols(Rb, Cb, dev.num_sms);
     const int64_t n = (Cb + cols - 1) / cols * Rb;
-    if (n > 0x7FFFFFFFLL || Cb > 0x3FFFFFFFLL) return DG_ERR_SHAPE;
+    if (n > 0x7FFFFFFFLL || H > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
     return launch_pdl(dispatch_kernel<WEIGHTS>, static_cast<int>(n), kRowThreads, sizeof(DispatchSmem), stream,
                       static_cast<const uint16_t *>(X), weights, slot_of_row, offsets, G, static_cast<int>(slots), k, H,
                       static_cast<int>(Cb), cols, static_cast<int>(Rb), Q, S);
@@ -304,7 +305,7 @@ dg_status_t launch_dispatch_quantize_masked(const void *X, const int32_t *slot_o
     const int64_t Ry = Rb < kDispatchMaskedRowCtas ? Rb : kDispatchMaskedRowCtas;
     const int cols = dispatch_cols(G * Ry, Cb, dev.num_sms);
     const int64_t n = (Cb + cols - 1) / cols * G * Ry;
-    if (n > 0x7FFFFFFFLL || Cb > 0x3FFFFFFFLL) return DG_ERR_SHAPE;
+    if (n > 0x7FFFFFFFLL || H > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
     return launch_pdl(dispatch_masked_kernel, static_cast<int>(n), kRowThreads, sizeof(DispatchSmem), stream,
                       static_cast<const uint16_t *>(X), slot_of_row, masked_m, static_cast<int>(slots), k, H,
                       static_cast<int>(Cb), cols, G, static_cast<int>(m_max), static_cast<int>(Rb),
