@@ -1,10 +1,11 @@
-"""Build libdg.so (the sm_100a CUDA kernels and their C ABI) in-tree with nvcc.
+"""Build libdg.so (the sm_100a CUDA kernels and their C ABI) in-tree with nvcc, and
+_dgtorch.so (the expert-layer calls for torch tensors, on top of that C ABI) with g++.
 
     python -m fp8_block_scaled_scales_b200.build [--force] [--verbose]
 
-Output: fp8_block_scaled_scales_b200/libdg.so.  nvcc cross-compiles for sm_100a
-without a GPU.  The CUDA runtime is linked statically; the driver API is reached
-through cudaGetDriverEntryPoint, so the library needs no -lcuda.
+Output: fp8_block_scaled_scales_b200/libdg.so and _dgtorch.so.  nvcc cross-compiles
+for sm_100a without a GPU.  The CUDA runtime is linked statically; the driver API is
+reached through cudaGetDriverEntryPoint, so the library needs no -lcuda.
 """
 from __future__ import annotations
 
@@ -13,11 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdg.so")
+EXT_SRC = os.path.join(CSRC, "torch_binding.cpp")
+EXT = os.path.join(HERE, "_dgtorch.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -41,7 +45,33 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_ext(force: bool) -> None:
+    deps = [EXT_SRC, os.path.join(ROOT, "include", "dg.h")]
+    if not force and os.path.exists(EXT) and all(os.path.getmtime(d) <= os.path.getmtime(EXT) for d in deps):
+        return
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include")]
+    tmp = EXT + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"]]
+    for path in includes:
+        cmd += ["-isystem", path]
+    cmd += [EXT_SRC, "-o", tmp, "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+            "-ltorch_python", "-L", HERE, "-l:libdg.so", "-Wl,-rpath,$ORIGIN"]
+    subprocess.check_call(cmd)
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    _build_lib(force, verbose)
+    _build_ext(force)
+    return LIB
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
     if not force and not _stale():
         return LIB
     nvcc = nvcc_path()
