@@ -218,6 +218,10 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     grid_dep_wait();
     __syncthreads();
     const int me = static_cast<int>(blockIdx.x), chunks = static_cast<int>(gridDim.x);
+    const int64_t begin = me * chunk, end = min(begin + chunk, slots);
+    // this thread's first slot, loaded under the sums
+    int e = expert_of(ids, begin + tid, begin + tid < end, G);
+    int rank = begin + tid < end ? row_of_slot[begin + tid] : -1;
     // Each warp adds up every 32nd chunk's row, four experts a lane and four rows in flight:
     // all CTAs read the same table, and one word a load took 12 us of 19 for 128 chunks.
     const int4 *table = reinterpret_cast<const int4 *>(counts);
@@ -241,12 +245,14 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     if (MASKED && tid < G) count[tid] = min(all, rows);
     __syncthreads();
     if (me == 0) write_offsets<MASKED>(G, first, count, offsets);
-    const int64_t begin = me * chunk, end = min(begin + chunk, slots);
     for (int64_t s = begin + tid; s < end; s += kSortThreads) {
-        const int e = expert_of(ids, s, true, G);
-        const int row = e >= 0 ? row_of<MASKED>(e, row_of_slot[s] + below[e], first, rows) : -1;
+        const int row = e >= 0 ? row_of<MASKED>(e, rank + below[e], first, rows) : -1;
         row_of_slot[s] = row;
         if (row >= 0) slot_of_row[row] = static_cast<int32_t>(s);
+        if (s + kSortThreads < end) {
+            e = expert_of(ids, s + kSortThreads, true, G);
+            rank = row_of_slot[s + kSortThreads];
+        }
     }
     fill_empty_rows<MASKED>(G, rows, first, count, me, chunks, slot_of_row);
 }
