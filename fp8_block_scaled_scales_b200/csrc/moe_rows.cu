@@ -246,18 +246,6 @@ __global__ void __launch_bounds__(kRowThreads)
     if (lane == 0) dweights[slot] = sum;
 }
 
-template <typename Kernel>
-static dg_status_t allow_smem(Kernel kernel, size_t bytes, int &configured_device) {
-    int device = 0;
-    if (cudaGetDevice(&device) != cudaSuccess) return DG_ERR_CUDA;
-    if (configured_device == device) return DG_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
-        cudaSuccess)
-        return DG_ERR_CUDA;
-    configured_device = device;
-    return DG_OK;
-}
-
 // Column blocks per CTA: runs as long as possible (the token lookup and the first, uncovered
 // gather are paid once a run) that still give the SMs about kDispatchWaves CTAs for each of
 // their four places.

@@ -271,18 +271,6 @@ int64_t moe_sort_workspace(int64_t slots, int G) {
     return (slots + chunk - 1) / chunk * ((G + 3) / 4) * static_cast<int64_t>(sizeof(int4));
 }
 
-template <typename Kernel>
-static dg_status_t allow_smem(Kernel kernel, size_t bytes, int &configured_device) {
-    int device = 0;
-    if (cudaGetDevice(&device) != cudaSuccess) return DG_ERR_CUDA;
-    if (configured_device == device) return DG_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
-        cudaSuccess)
-        return DG_ERR_CUDA;
-    configured_device = device;
-    return DG_OK;
-}
-
 template <typename IdT, bool MASKED>
 static dg_status_t launch_sort_impl(const IdT *ids, int64_t slots, int G, int64_t rows, int32_t *offsets,
                                     int32_t *row_of_slot, int32_t *slot_of_row, int32_t *workspace,

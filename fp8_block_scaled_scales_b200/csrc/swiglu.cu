@@ -355,19 +355,6 @@ __global__ void __launch_bounds__(kGluBackThreads, 1)
 }
 static_assert(kGluBackThreads == 512 || kGluBackThreads == 1024, "the reduction over warps uses 16 or 32 lanes");
 
-// Dynamic shared memory above the default needs the kernel's consent, once per device and thread.
-template <typename Kernel>
-static dg_status_t allow_smem(Kernel kernel, size_t bytes, int &configured_device) {
-    int device = 0;
-    if (cudaGetDevice(&device) != cudaSuccess) return DG_ERR_CUDA;
-    if (configured_device == device) return DG_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
-        cudaSuccess)
-        return DG_ERR_CUDA;
-    configured_device = device;
-    return DG_OK;
-}
-
 template <bool CKPT>
 static dg_status_t launch_swiglu_impl(const uint16_t *h, const GluRows &layout, int64_t blocks, uint8_t *Q, float *S,
                                       uint8_t *H8, float *sH, const DeviceInfo &dev, cudaStream_t stream) {

@@ -6,6 +6,20 @@
 
 namespace dg {
 
+// Dynamic shared memory above the default needs the kernel's consent, once per device and
+// thread.  configured_device: the caller's thread_local, -1 at first.
+template <typename Kernel>
+dg_status_t allow_smem(Kernel kernel, size_t bytes, int &configured_device) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return DG_ERR_CUDA;
+    if (configured_device == device) return DG_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
+        cudaSuccess)
+        return DG_ERR_CUDA;
+    configured_device = device;
+    return DG_OK;
+}
+
 // moe_sort.cu.  masked: `offsets` receives the counts [G] and `rows` is M_max, else the
 // group offsets [G+1] and the row capacity.  workspace: moe_sort_workspace bytes.
 int64_t moe_sort_workspace(int64_t slots, int G);

@@ -176,6 +176,35 @@ def test_malformed_offsets_compute_nothing(bad):
     assert binding.last_device_status() == 0 and not bool((dx[:256] == -3).any())
 
 
+def test_outputs_past_32_bit_offsets():
+    """More than 2^32 elements of dW and of dX: the last tiles are the ones looked at."""
+    G, N, K = 33, 8192, 16384
+    off = torch.zeros(G + 1, dtype=torch.int32, device="cuda")
+    off[G] = 256  # all rows belong to the last expert
+    dy, sdy = quantized(256, N, 5)
+    x, sx = quantized(256, K, 6)
+    C = torch.empty((G, N, K), dtype=BF16, device="cuda")
+    C[0, 0, :5] = 7
+    binding.grouped_wgrad_contiguous(dy, sdy, x, sx, off, C=C)
+    n, k = slice(N - 256, N), slice(K - 512, K)
+    p = plain.decode(dy.cpu(), sdy.cpu())[:, n].t()
+    r = plain.decode(x.cpu(), sx.cpu())[:, k]
+    check(C[G - 1, n, k], p @ r, p.abs() @ r.abs(), 2, BF16)
+    assert not bool(C[0, 0].any()) and not bool(C[G - 2, -1].any())
+    del C
+    M = 266_240  # x 16384 columns
+    w, sw = quantized(128, K, 7)
+    dy = torch.zeros((M, 128), dtype=torch.uint8, device="cuda")
+    sdy = torch.ones((M // 128, 1), device="cuda")
+    tail = quantized(128, 128, 8)
+    dy[-128:], sdy[-1:] = tail
+    dx = binding.dgrad_blockscaled(dy, sdy, w, sw)
+    p, r = plain.decode(tail[0].cpu(), tail[1].cpu()), plain.decode(w.cpu(), sw.cpu())
+    check(dx[-128:], p @ r, p.abs() @ r.abs(), 1, BF16)
+    assert not bool(dx[M - 256:M - 128].any())
+    assert binding.last_device_status() == 0
+
+
 def test_no_rows():
     z = torch.empty((0, 128), dtype=torch.uint8, device="cuda")
     s = torch.empty((0, 1), device="cuda")

@@ -169,6 +169,72 @@ def test_dispatch_never_reads_tokens_without_a_slot():
     assert torch.equal(q[:int(off[-1])].cpu(), want[0]) and torch.equal(s[:int(off[-1]) // 128].cpu(), want[1])
 
 
+def test_dispatch_weights_of_both_signs_and_zero():
+    """Negative and zero weights: magnitudes enter the scale, zeros keep the product's sign."""
+    T, k, G, H = 50, 2, 3, 384
+    ids = route(T, k, G, 21)
+    cap = plain.cap_of(T, k, G)
+    off, row, slot = plain.sort_plain(ids.numpy(), G, cap)
+    x = tokens(T, H, 22)
+    x[:, ::5] = 0
+    w = torch.randn((T, k), generator=torch.Generator().manual_seed(23))
+    w[::4, 0], w[1::4, 1] = 0.0, -0.0
+    used = int(off[-1])
+    q, s = binding.moe_dispatch_quantize(x.cuda(), torch.from_numpy(slot).int().cuda(),
+                                         torch.from_numpy(off).int().cuda(), k, weights=w.cuda())
+    wq, ws = plain.quantize_f32(gathered(x, slot, k, w)[:used])
+    assert torch.equal(q[:used].cpu(), wq) and torch.equal(s[:used // 128].cpu(), ws)
+
+
+def test_dispatch_non_finite_values_stay_in_their_block():
+    """A NaN or an infinity in a used token makes its own block's scale non-finite, and no other."""
+    T, H = 300, 384
+    x = tokens(T, H, 31)
+    clean = x.clone()
+    x[5, 10], x[200, 300] = float("nan"), float("inf")
+    ids = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    off, row, slot = binding.moe_sort(ids, 1)
+    q, s = binding.moe_dispatch_quantize(x.cuda(), slot, off, 1)
+    cq, cs = binding.moe_dispatch_quantize(clean.cuda(), slot, off, 1)
+    bad = torch.zeros((3, 3), dtype=torch.bool)
+    bad[0, 0] = bad[1, 2] = True
+    assert torch.equal(~torch.isfinite(s[:3].cpu()), bad)
+    assert torch.equal(s[:3].cpu()[~bad], cs[:3].cpu()[~bad])
+    keep = ~bad.repeat_interleave(128, 0).repeat_interleave(128, 1)
+    assert torch.equal(q[:384].cpu()[keep], cq[:384].cpu()[keep])
+
+
+def test_rows_past_32_bit_offsets():
+    """Matrices of more than 2^32 elements: the last rows and tokens are the ones looked at."""
+    H, rows = 16384, 270_080  # 4.4e9 elements
+    T, k = 4, 2
+    y = torch.empty((rows, H), dtype=torch.bfloat16, device="cuda")
+    r = torch.tensor([[0, rows - 1], [rows - 2, -1], [rows - 3, rows - 4], [131072, rows // 2]], dtype=torch.int32)
+    for v in r.flatten().tolist():
+        if v >= 0:
+            y[v] = torch.randn(H, generator=torch.Generator().manual_seed(v)).to(torch.bfloat16)
+    picked = torch.stack([torch.stack([y[v].cpu() if v >= 0 else torch.zeros(H, dtype=torch.bfloat16) for v in t]) for t in r.tolist()])
+    ref = picked.double().sum(1)
+    got = binding.moe_combine(y, r.cuda()).cpu().double()
+    assert bool(((got - ref).abs() <= ref.abs() * 2.0 ** -8 + 2.0 ** -23 * picked.double().abs().sum(1)).all())
+    dout = torch.randn((T, H), generator=torch.Generator().manual_seed(7)).to(torch.bfloat16)
+    dw = binding.moe_combine_backward(dout.cuda(), y, r.cuda()).cpu().double()
+    terms = picked.double() * dout.double()[:, None, :]
+    assert bool(((dw - terms.sum(2)).abs() <= H * 2.0 ** -24 * terms.abs().sum(2)).all())
+    # as tokens: the last ones gathered into the last rows of codes past 2^32 bytes
+    cap = 270_080
+    slot = torch.full((cap,), -1, dtype=torch.int32, device="cuda")
+    slot[cap - 2], slot[cap - 1] = rows - 1, 0
+    off = torch.tensor([0, cap], dtype=torch.int32, device="cuda")
+    q = torch.empty((cap, H), dtype=torch.uint8, device="cuda")
+    q, s = binding.moe_dispatch_quantize(y, slot, off, 1, q=q)
+    block = torch.zeros((128, H))
+    block[126], block[127] = y[rows - 1].cpu().float(), y[0].cpu().float()
+    wq, ws = plain.quantize_f32(block)
+    assert torch.equal(q[cap - 128:].cpu(), wq) and torch.equal(s[-1:].cpu(), ws)
+    assert not bool(q[: cap - 128: 4096].any())
+
+
 def test_dispatch_weights_so_small_that_the_scale_would_vanish():
     """amax / 448 rounds to zero in FP32: the scale is 1 and every code is a zero."""
     x = torch.full((1, 128), 2.0 ** -100, dtype=torch.bfloat16)

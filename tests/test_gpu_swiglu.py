@@ -147,3 +147,32 @@ def test_swiglu_backward_against_differences():
         got = plain.decode(q, s)[:, half * F:(half + 1) * F]
         bound = plain.code_error_bound(d, s, noise)[:, half * F:(half + 1) * F]
         assert bool(((got - num).abs() <= bound + 1e-6).all())
+
+
+def test_swiglu_past_32_bit_offsets():
+    """More than 2^32 elements of h: the last block equals the same rows alone."""
+    M, F = 132_224, 16384
+    h = torch.empty((M, 2 * F), dtype=torch.bfloat16, device="cuda")
+    h[-256:] = pre_activation(256, F, 3).cuda()
+    h8 = torch.empty((M, 2 * F), dtype=torch.uint8, device="cuda")
+    q, s, h8, sh = binding.swiglu_quantize(h, checkpoint=True, h8=h8)
+    a = binding.swiglu_quantize(h[-256:].contiguous(), checkpoint=True)
+    assert torch.equal(q[-256:], a[0]) and torch.equal(s[-2:], a[1])
+    assert torch.equal(h8[-256:], a[2]) and torch.equal(sh[:, -256:], a[3])
+    da = torch.empty((M, F), dtype=torch.bfloat16, device="cuda")
+    da[-256:] = torch.randn((256, F), device="cuda").to(torch.bfloat16)
+    dq, ds = binding.swiglu_quantize_backward(h8, sh, da)
+    b = binding.swiglu_quantize_backward(a[2], a[3], da[-256:].contiguous())
+    assert torch.equal(dq[-256:], b[0]) and torch.equal(ds[-2:], b[1])
+
+
+def test_swiglu_non_finite_values_stay_in_their_block():
+    M, F = 256, 256
+    h = pre_activation(M, F, 8)
+    clean = h.clone()
+    h[3, 7], h[200, F + 130] = float("nan"), float("inf")   # a gate in block (0, 0), an up in (1, 1)
+    q, s = binding.swiglu_quantize(h.cuda())
+    cq, cs = binding.swiglu_quantize(clean.cuda())
+    assert torch.equal(torch.isfinite(s).cpu(), torch.tensor([[False, True], [True, False]]))
+    assert torch.equal(q[:128, 128:], cq[:128, 128:]) and torch.equal(q[128:, :128], cq[128:, :128])
+    assert s[0, 1] == cs[0, 1] and s[1, 0] == cs[1, 0]
