@@ -149,8 +149,7 @@ __device__ __forceinline__ float amax3(float m, float2 x) {
 template <int WARPS>
 __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t *red) {
     static_assert(WARPS % 4 == 0, "read four words at a time");
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    v = __reduce_max_sync(0xFFFFFFFFu, v);
     if ((threadIdx.x & 31u) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     uint32_t m = 0;

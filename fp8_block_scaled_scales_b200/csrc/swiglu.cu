@@ -315,11 +315,8 @@ __global__ void __launch_bounds__(kGluBackThreads, 1)
             ask(i, next_row0, next_rows, walk.bc, par ^ 1);
         }
         uint32_t mg = __float_as_uint(ag), mu = __float_as_uint(au);  // NaN above infinity
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            mg = max(mg, __shfl_xor_sync(0xFFFFFFFFu, mg, o));
-            mu = max(mu, __shfl_xor_sync(0xFFFFFFFFu, mu, o));
-        }
+        mg = __reduce_max_sync(0xFFFFFFFFu, mg);
+        mu = __reduce_max_sync(0xFFFFFFFFu, mu);
         if ((tid & 31) == 0) {
             red[par][0][tid >> 5] = mg;
             red[par][1][tid >> 5] = mu;
@@ -328,11 +325,8 @@ __global__ void __launch_bounds__(kGluBackThreads, 1)
         constexpr int kWarps = kGluBackThreads / 32;
         mg = red[par][0][tid & (kWarps - 1)];
         mu = red[par][1][tid & (kWarps - 1)];
-#pragma unroll
-        for (int o = kWarps / 2; o > 0; o >>= 1) {
-            mg = max(mg, __shfl_xor_sync(0xFFFFFFFFu, mg, o));
-            mu = max(mu, __shfl_xor_sync(0xFFFFFFFFu, mu, o));
-        }
+        mg = __reduce_max_sync(0xFFFFFFFFu, mg);
+        mu = __reduce_max_sync(0xFFFFFFFFu, mu);
         const FastScale bg = fast_scale(__uint_as_float(mg)), bu = fast_scale(__uint_as_float(mu));
         if (tid == 0) {
             float *sp = S + static_cast<int64_t>(rb) * 2 * layout.Fb + bc;
