@@ -12,6 +12,8 @@
 // combine_backward:   dweights[t][j] = sum_h dout[t][h] * y[row(t, j)][h], FP32.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "dg_device.cuh"
 #include "quant_f32.cuh"
 #include "train_internal.h"
@@ -103,10 +105,10 @@ __device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, co
         m = cta_max<kRowThreads / 32>(m, sm.red[bc & 1]);
         const FastScale bs = fast_scale(__uint_as_float(m));
         if (tid == 0) S[bc] = bs.s;
-        if (col_ok) {
+        auto convert = [&](auto fast) {
+            constexpr bool kFast = decltype(fast)::value;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (sub + 16 * i >= rows) break;
                 uint2 q;
                 if (WEIGHTS) {
                     const float nw = -sm.wgt[sub + 16 * i];
@@ -114,12 +116,18 @@ __device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, co
                     bf16x8_to_f32(v[i], x);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], make_float2(nw, nw));
-                    q = quantize8_negated(x, bs);
+                    q = quantize8_negated<kFast>(x, bs);
                 } else {
-                    q = quantize8_corrected(v[i], bs);
+                    q = quantize8_corrected<kFast>(v[i], bs);
                 }
-                *reinterpret_cast<uint2 *>(qp + i * step) = q;
+                if (sub + 16 * i < rows) *reinterpret_cast<uint2 *>(qp + i * step) = q;
             }
+        };
+        if (col_ok) {
+            if (__builtin_expect(bs.fast, 1))
+                convert(std::true_type{});
+            else
+                convert(std::false_type{});
         }
     }
 }

@@ -39,14 +39,19 @@ struct FastScale {
     bool fast;
 };
 
-__device__ __forceinline__ FastScale fast_scale(float amax) {
+__device__ __forceinline__ bool scale_is_fast(float amax) {
+    return (amax >= 0x1p-90f && amax <= 0x1p100f) || amax == 0.0f;
+}
+
+// FAST: scale_is_fast(amax).
+template <bool FAST>
+__device__ __forceinline__ FastScale scale_of(float amax) {
     FastScale b;
-    const bool inside = amax >= 0x1p-90f && amax <= 0x1p100f;
-    b.fast = inside || amax == 0.0f;
-    if (__builtin_expect(b.fast, 1)) {
+    b.fast = FAST;
+    if (FAST) {
         constexpr float c = 1.0f / 448.0f;
         const float q = __fmul_rn(amax, c);
-        b.s = inside ? __fmaf_rn(__fmaf_rn(-q, 448.0f, amax), c, q) : 1.0f;  // 1 for a block of zeros
+        b.s = amax == 0.0f ? 1.0f : __fmaf_rn(__fmaf_rn(-q, 448.0f, amax), c, q);  // 1 for a block of zeros
     } else {
         const float q = __fdiv_rn(amax, 448.0f);
         b.s = (q == 0.0f) ? 1.0f : q;
@@ -55,12 +60,19 @@ __device__ __forceinline__ FastScale fast_scale(float amax) {
     return b;
 }
 
+__device__ __forceinline__ FastScale fast_scale(float amax) {
+    return __builtin_expect(scale_is_fast(amax), 1) ? scale_of<true>(amax) : scale_of<false>(amax);
+}
+
 // Eight FP32 values that are themselves rounded results (an activation, a gradient): x / s as
 // the product x r, off by 2^-23 + 2^-24 where the quotient is off by 2^-24.  The values
 // carry larger errors already, so the exact quotient would decide nothing.
+// FAST: b.fast, which the caller tests once for all its rows (a branch a row cost a tenth of
+// the instructions and kept the rows' arithmetic apart).
+template <bool FAST>
 __device__ __forceinline__ uint2 quantize8_near(const float2 (&x)[4], const FastScale &b) {
     float2 y[4];
-    if (__builtin_expect(b.fast, 1)) {
+    if (FAST) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = __fmul2_rn(x[j], make_float2(b.r, b.r));
     } else {
@@ -79,9 +91,10 @@ __device__ __forceinline__ uint2 quantize8_near(const float2 (&x)[4], const Fast
 //   x any FP32: the quotient is the rounding of a value within 2^-46 of x/s, so the code can
 //     differ only where x/s lies that close to the middle between an E4M3 rounding boundary
 //     and the next FP32 number.
+template <bool FAST>
 __device__ __forceinline__ uint2 quantize8_negated(const float2 (&n)[4], const FastScale &b) {
     float2 q[4];
-    if (__builtin_expect(b.fast, 1)) {
+    if (FAST) {
         const float2 s2 = make_float2(b.s, b.s), nr = make_float2(-b.r, -b.r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -96,6 +109,7 @@ __device__ __forceinline__ uint2 quantize8_negated(const float2 (&n)[4], const F
 }
 
 // Eight BF16 -> codes of fl32(x / s), exactly.
+template <bool FAST>
 __device__ __forceinline__ uint2 quantize8_corrected(uint4 v, const FastScale &b) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float2 n[4];
@@ -107,7 +121,7 @@ __device__ __forceinline__ uint2 quantize8_corrected(uint4 v, const FastScale &b
             "fma.rn.f32.bf16 %1, h, m, %3;\n\t}"
             : "=f"(n[j].x), "=f"(n[j].y)
             : "r"(w[j]), "f"(-0.0f));
-    return quantize8_negated(n, b);
+    return quantize8_negated<FAST>(n, b);
 }
 
 // The largest |x| of eight BF16 as two magnitudes side by side, a NaN above infinity.

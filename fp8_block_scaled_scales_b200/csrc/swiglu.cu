@@ -14,6 +14,8 @@
 // reason a / s is a product with the rounded 1/s (quantize8_near).
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "dg_device.cuh"
 #include "quant_f32.cuh"
 #include "train_internal.h"
@@ -55,18 +57,34 @@ __device__ __forceinline__ void checkpoint_rows(const uint4 (&vg)[2], const uint
 #pragma unroll
         for (int i = 0; i < 2; ++i) pk[i] = __vmaxu2(pk[i], __shfl_xor_sync(0xFFFFFFFFu, pk[i], o));
     }
+    float amax[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if (!ok[i]) continue;
-        const FastScale g = fast_scale(__uint_as_float(pk[i] << 16));
-        const FastScale u = fast_scale(__uint_as_float(pk[i] & 0xFFFF0000u));
-        *reinterpret_cast<uint2 *>(q + i * q_row + in_q) = quantize8_corrected(vg[i], g);
-        *reinterpret_cast<uint2 *>(q + i * q_row + q_up + in_q) = quantize8_corrected(vu[i], u);
-        if ((threadIdx.x & 15u) == 0) {
-            s[in_s + i * 32] = g.s;
-            s[in_s + i * 32 + s_up] = u.s;
-        }
+        amax[i][0] = __uint_as_float(pk[i] << 16);
+        amax[i][1] = __uint_as_float(pk[i] & 0xFFFF0000u);
     }
+    auto write = [&](auto fast) {
+        constexpr bool kFast = decltype(fast)::value;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const FastScale g = scale_of<kFast>(amax[i][0]), u = scale_of<kFast>(amax[i][1]);
+            const uint2 qg = quantize8_corrected<kFast>(vg[i], g), qu = quantize8_corrected<kFast>(vu[i], u);
+            if (ok[i]) {
+                *reinterpret_cast<uint2 *>(q + i * q_row + in_q) = qg;
+                *reinterpret_cast<uint2 *>(q + i * q_row + q_up + in_q) = qu;
+                if ((threadIdx.x & 15u) == 0) {
+                    s[in_s + i * 32] = g.s;
+                    s[in_s + i * 32 + s_up] = u.s;
+                }
+            }
+        }
+    };
+    if (__builtin_expect(scale_is_fast(amax[0][0]) && scale_is_fast(amax[0][1]) && scale_is_fast(amax[1][0]) &&
+                             scale_is_fast(amax[1][1]),
+                         1))
+        write(std::true_type{});
+    else
+        write(std::false_type{});
 }
 
 // 16- and 8-byte copies to shared memory that the thread waits for later.
@@ -215,9 +233,17 @@ __global__ void __launch_bounds__(kGluThreads, 2)
         const FastScale bs = fast_scale(__uint_as_float(cta_max<kGluThreads / 32>(__float_as_uint(m), red[par])));
         if (tid == 0) S[static_cast<int64_t>(rb) * layout.Fb + bc] = bs.s;
         uint8_t *q = Q + static_cast<int64_t>(row0) * F + bc * 128;
+        auto convert = [&](auto fast) {
 #pragma unroll
-        for (int i = 0; i < kGluPer; ++i)
-            if (sub + 32 * i < rows) *reinterpret_cast<uint2 *>(q + i * (step >> 1) + in_q) = quantize8_near(a[i], bs);
+            for (int i = 0; i < kGluPer; ++i) {
+                const uint2 c = quantize8_near<decltype(fast)::value>(a[i], bs);
+                if (sub + 32 * i < rows) *reinterpret_cast<uint2 *>(q + i * (step >> 1) + in_q) = c;
+            }
+        };
+        if (__builtin_expect(bs.fast, 1))
+            convert(std::true_type{});
+        else
+            convert(std::false_type{});
         have = more;
         row0 = next_row0;
         rows = next_rows;
@@ -334,13 +360,21 @@ __global__ void __launch_bounds__(kGluBackThreads, 1)
             sp[layout.Fb] = bu.s;
         }
         uint8_t *q = Q + static_cast<int64_t>(row0) * 2 * F + bc * 128;
+        auto convert = [&](auto fast) {
+            constexpr bool kFast = decltype(fast)::value;
 #pragma unroll
-        for (int i = 0; i < kGluBackPer; ++i) {
-            if (sub + kRows * i < rows) {
-                *reinterpret_cast<uint2 *>(q + i * kRows * 2 * F + in_h) = quantize8_near(dg[i], bg);
-                *reinterpret_cast<uint2 *>(q + i * kRows * 2 * F + F + in_h) = quantize8_near(du[i], bu);
+            for (int i = 0; i < kGluBackPer; ++i) {
+                const uint2 cg = quantize8_near<kFast>(dg[i], bg), cu = quantize8_near<kFast>(du[i], bu);
+                if (sub + kRows * i < rows) {
+                    *reinterpret_cast<uint2 *>(q + i * kRows * 2 * F + in_h) = cg;
+                    *reinterpret_cast<uint2 *>(q + i * kRows * 2 * F + F + in_h) = cu;
+                }
             }
-        }
+        };
+        if (__builtin_expect(bg.fast && bu.fast, 1))
+            convert(std::true_type{});
+        else
+            convert(std::false_type{});
         have = more;
         row0 = next_row0;
         rows = next_rows;
