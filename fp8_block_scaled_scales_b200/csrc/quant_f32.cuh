@@ -64,24 +64,6 @@ __device__ __forceinline__ FastScale fast_scale(float amax) {
     return __builtin_expect(scale_is_fast(amax), 1) ? scale_of<true>(amax) : scale_of<false>(amax);
 }
 
-// Eight FP32 values that are themselves rounded results (an activation, a gradient): x / s as
-// the product x r, off by 2^-23 + 2^-24 where the quotient is off by 2^-24.  The values
-// carry larger errors already, so the exact quotient would decide nothing.
-// FAST: b.fast, which the caller tests once for all its rows (a branch a row cost a tenth of
-// the instructions and kept the rows' arithmetic apart).
-template <bool FAST>
-__device__ __forceinline__ uint2 quantize8_near(const float2 (&x)[4], const FastScale &b) {
-    float2 y[4];
-    if (FAST) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = __fmul2_rn(x[j], make_float2(b.r, b.r));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = make_float2(__fdiv_rn(x[j].x, b.s), __fdiv_rn(x[j].y, b.s));
-    }
-    return make_uint2(e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y), e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y));
-}
-
 // Four pairs n = -x -> codes of fl32(x / s): the quotient corrected by its remainder, y = n (-r),
 // e = y s + n (the negative remainder), x/s = e (-r) + y; in this order of signs a zero keeps
 // its own.  Three multiply-adds a pair and one conversion, with no second path for values
@@ -91,6 +73,8 @@ __device__ __forceinline__ uint2 quantize8_near(const float2 (&x)[4], const Fast
 //   x any FP32: the quotient is the rounding of a value within 2^-46 of x/s, so the code can
 //     differ only where x/s lies that close to the middle between an E4M3 rounding boundary
 //     and the next FP32 number.
+// FAST: b.fast, which the caller tests once for all its rows (a branch a row cost a tenth of
+// the instructions and kept the rows' arithmetic apart).
 template <bool FAST>
 __device__ __forceinline__ uint2 quantize8_negated(const float2 (&n)[4], const FastScale &b) {
     float2 q[4];

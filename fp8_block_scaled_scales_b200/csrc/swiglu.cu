@@ -9,9 +9,9 @@
 //             dg = dA * u * sigma(g) * (1 + g * (1 - sigma(g))),   du = dA * g * sigma(g);
 //             Q, S = the block quantizer's definition on [dg | du], ready for both gradient
 //             products.
-// sigma uses the hardware exponential and reciprocal (relative error of a few 2^-23 where
-// the result is not negligible), far below the E4M3 rounding that follows; for the same
-// reason a / s is a product with the rounded 1/s (quantize8_near).
+// Every step is within about one FP32 rounding, the exponential within two: a code differs
+// from the exact value's only next to a rounding boundary, and each wrong ulp would show
+// there for a whole block through its scale.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -27,17 +27,28 @@ constexpr int kGluPer = 4;
 constexpr int kGluBackThreads = 512;   // backward: 32 rows at a time, four times
 constexpr int kGluBackPer = 4;
 
-// sigma of two values, one exponential and one reciprocal instruction each.  exp2 overflows to
-// infinity for x < -88, whose reciprocal is 0; 1 + e is never subnormal.
-__device__ __forceinline__ float2 sigmoid2(float2 x) {
-    const float2 t = __fmul2_rn(x, make_float2(-1.44269504f, -1.44269504f));  // -log2 e
-    float2 e, p;
+// d = 1 + exp(-x) and an approximation r of -1/d, one exponential and one reciprocal
+// instruction a value.  x below -88.5 is taken as that: exp(-x) is still finite there and r
+// flushed to 0, so no infinity meets a zero.  (Putting the rounding of exp2's argument
+// back into the result cost 4 % and left the codes' error where it was.)
+__device__ __forceinline__ void one_plus_exp(float2 x, float2 &d, float2 &r) {
+    const float2 t = __fmul2_rn(make_float2(fmaxf(x.x, -88.5f), fmaxf(x.y, -88.5f)),
+                                make_float2(-1.44269504f, -1.44269504f));  // -log2 e
+    float2 e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-    e = __fadd2_rn(e, make_float2(1.0f, 1.0f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(e.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(e.y));
-    return p;
+    d = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(-d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(-d.y));
+}
+
+// -n / d from r = -1/d: the product corrected by its remainder (Markstein, as in
+// quant_f32.cuh).  With the approximate reciprocal alone, and a / s as a product, the kernels
+// are a tenth faster and a third of the inputs tried had half as much error again in the
+// codes as a plain FP32 evaluation; as it stands they have the same.
+__device__ __forceinline__ float2 negated_quotient(float2 n, float2 d, float2 r) {
+    const float2 z = __fmul2_rn(n, r);
+    return __ffma2_rn(__ffma2_rn(z, d, n), r, z);
 }
 
 // Two rows of h, 128 columns of the gate and of the up half each, as four 1 x 128 blocks
@@ -200,7 +211,7 @@ __global__ void __launch_bounds__(kGluThreads, 2)
         walk.advance(layout);
         const bool more = walk.find(layout, next_row0, next_rows);
         if (!more) next_rows = 0;
-        float2 a[kGluPer][4];
+        float2 a[kGluPer][4];  // negated, as the conversion takes them
         float m = 0.0f;
         cp_async_wait();
 #pragma unroll
@@ -223,7 +234,9 @@ __global__ void __launch_bounds__(kGluThreads, 2)
                 bf16x8_to_f32(vu[i], u);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 x = __fmul2_rn(__fmul2_rn(g[j], sigmoid2(g[j])), u[j]);
+                    float2 d, r;
+                    one_plus_exp(g[j], d, r);
+                    const float2 x = __fmul2_rn(negated_quotient(g[j], d, r), u[j]);  // -(g / d) u
                     m = amax3(m, x);
                     a[i0 + i][j] = x;
                 }
@@ -236,7 +249,7 @@ __global__ void __launch_bounds__(kGluThreads, 2)
         auto convert = [&](auto fast) {
 #pragma unroll
             for (int i = 0; i < kGluPer; ++i) {
-                const uint2 c = quantize8_near<decltype(fast)::value>(a[i], bs);
+                const uint2 c = quantize8_negated<decltype(fast)::value>(a[i], bs);
                 if (sub + 32 * i < rows) *reinterpret_cast<uint2 *>(q + i * (step >> 1) + in_q) = c;
             }
         };
@@ -330,11 +343,13 @@ __global__ void __launch_bounds__(kGluBackThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 gs = __fmul2_rn(g[j], make_float2(sg, sg)), us = __fmul2_rn(u[j], make_float2(su, su));
-                const float2 p = sigmoid2(gs);
-                const float2 t = __fmul2_rn(d[j], p);
-                const float2 np = __ffma2_rn(p, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
-                du[i][j] = __fmul2_rn(t, gs);
-                dg[i][j] = __fmul2_rn(__fmul2_rn(t, us), __ffma2_rn(gs, np, make_float2(1.0f, 1.0f)));
+                float2 e, r;
+                one_plus_exp(gs, e, r);
+                const float2 ns = __ffma2_rn(__ffma2_rn(r, e, make_float2(1.0f, 1.0f)), r, r);  // -sigma
+                const float2 t = __fmul2_rn(d[j], ns);
+                const float2 w = __ffma2_rn(gs, __fadd2_rn(ns, make_float2(1.0f, 1.0f)), make_float2(1.0f, 1.0f));
+                du[i][j] = __fmul2_rn(t, gs);  // both negated
+                dg[i][j] = __fmul2_rn(__fmul2_rn(t, us), w);
                 ag = amax3(ag, dg[i][j]);
                 au = amax3(au, du[i][j]);
             }
@@ -364,7 +379,7 @@ __global__ void __launch_bounds__(kGluBackThreads, 1)
             constexpr bool kFast = decltype(fast)::value;
 #pragma unroll
             for (int i = 0; i < kGluBackPer; ++i) {
-                const uint2 cg = quantize8_near<kFast>(dg[i], bg), cu = quantize8_near<kFast>(du[i], bu);
+                const uint2 cg = quantize8_negated<kFast>(dg[i], bg), cu = quantize8_negated<kFast>(du[i], bu);
                 if (sub + kRows * i < rows) {
                     *reinterpret_cast<uint2 *>(q + i * kRows * 2 * F + in_h) = cg;
                     *reinterpret_cast<uint2 *>(q + i * kRows * 2 * F + F + in_h) = cu;
