@@ -148,13 +148,17 @@ struct GradUnit {
     int sb_row;                    // row of B's scales at block 0
 };
 
+// Row tiles of a raster group: as in the forward kernel 32 dense (8192^3: dgrad 450 us against
+// 463 with 8, wgrad 5 % shorter), 8 grouped.
+__device__ __forceinline__ int grad_raster(const GradParams &p) { return p.offsets ? 8 : 32; }
+
 template <int MODE>
 __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, int num_m, int t, int h) {
     GradUnit u;
     int g = 0, mb, kt;
     if (MODE == kDgrad) {
         // m-block fastest inside raster groups, so that a group's tiles of W are read from L2
-        constexpr int kRaster = 8;
+        const int kRaster = grad_raster(p);
         const int group = t / (kRaster * p.num_k);
         const int first = group * kRaster;
         const int gm = min(kRaster, num_m - first);
@@ -177,7 +181,7 @@ __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, int num_m, in
         u.sa_at = mb * p.Nb;
         u.sb_row = g * p.Nb;
     } else {
-        constexpr int kRaster = 8;
+        const int kRaster = grad_raster(p);
         const int per = p.num_m * p.num_k;
         g = t / per;
         t -= g * per;
@@ -573,13 +577,21 @@ dg_status_t launch_dgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t 
     return launch_grad_impl<kDgrad, false, 4, 1>(a, dev, stream);
 }
 
-// Three operand stages and two output boxes a warp: an output tile is 128 KB (FP32) against a
-// few blocks of contraction, so its stores matter more than a fourth stage (64 experts of N =
-// 2048, K = 7168 over 32768 slots: 960 us against 1000 with four and one, BF16 728 against 755;
-// 8 experts of 4096^2: 340 and 340).
+// Operand stages against output boxes.  An output tile is 128 KB (FP32): with few blocks of
+// contraction a tile its stores matter more than a fourth stage, with many the stages do.
+// Measured (three stages and two boxes, four and one): 64 experts of N = 2048, K = 7168 over
+// 32768 slots, 4 blocks a tile on average, 975-1045 and 1090-1120 us; 8 experts of 4096^2, 16
+// blocks, 320 and 320; 4096^3, 32 blocks, 79.8 and 75.7; 8192^3, 64 blocks, 535 and 525.
+constexpr int64_t kWgradLongBlocks = 24;
+
+template <bool F32>
+static dg_status_t launch_wgrad_impl(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
+    return a.M / 128 > kWgradLongBlocks * a.G ? launch_grad_impl<kWgrad, F32, 4, 1>(a, dev, stream)
+                                              : launch_grad_impl<kWgrad, F32, 3, 2>(a, dev, stream);
+}
+
 dg_status_t launch_wgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    return a.fp32 ? launch_grad_impl<kWgrad, true, 3, 2>(a, dev, stream)
-                  : launch_grad_impl<kWgrad, false, 3, 2>(a, dev, stream);
+    return a.fp32 ? launch_wgrad_impl<true>(a, dev, stream) : launch_wgrad_impl<false>(a, dev, stream);
 }
 
 }  // namespace dg

@@ -28,7 +28,7 @@ def check(got, ref, mag, blocks, dtype, what=""):
 
 # one block and less, tails in every size, both tile widths, several rounds of tiles
 DENSE = [(1, 16, 16), (5, 128, 128), (128, 128, 256), (200, 272, 144), (129, 400, 528), (1000, 528, 784),
-         (384, 1280, 640), (2300, 1040, 2064)]
+         (384, 1280, 640), (2300, 1040, 2064), (5000, 272, 400)]  # the last: past the four-stage rule of wgrad
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
