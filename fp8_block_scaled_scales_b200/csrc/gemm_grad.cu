@@ -20,6 +20,13 @@
 // in FP32 registers); what differs is the walk: a wgrad tile's contraction runs over its
 // expert's row blocks, so its length varies from tile to tile and may be zero (an expert
 // without tokens: zeros are stored), and the scales step by a row of the scale arrays.
+//
+// Measured: dgrad of 8 experts, N = K = 4096, 16384 slots 250 us (2200 TFLOP/s; the forward
+// product of that size 255), dense 4096^3 67.6 us, 8192^3 450 us: bound, as the forward
+// kernel, by the round trip of a partial through tensor memory (tensor pipe 59 % active).
+// wgrad of 64 experts, N = 2048, K = 7168, 32768 slots in FP32 957-1045 us: 3.8 GB of output
+// stored by the warps that also scale the partials, 575 us without the stores, 635 us of
+// stores alone.
 #include <cuda_bf16.h>
 
 #include "dg_device.cuh"

@@ -27,8 +27,11 @@ constexpr int kRowThreads = 256;
 // a thread reads its eight 16-byte pieces from shared memory, asks for the next column
 // block's (cp.async), and reduces and converts the current ones, so that the gather runs under
 // the conversion.  All CTAs walk the columns at the same pace, so the k copies of a token's
-// piece are read close together: once from memory, then from L2.  (A CTA per block, rows
-// first: 137 us on 32768 slots x 7168 with 28 % L2 hits, against 46 us of traffic.)
+// piece are read close together: once from memory (ncu: 64 MB of 59), then from L2.  32768
+// slots x 7168: 97 us, 730 MB through L2; without the conversion, the moves and the block
+// maximum alone take 78 us, without the maximum 85.  (A CTA per block, rows first: 137 us with
+// 28 % L2 hits.)  With weights 102 us.  256 threads of eight rows: 512 of four 116 us, 128 of
+// sixteen 99.
 struct DispatchSmem {
     uint4 piece[8][kRowThreads];
     int tok[128];
@@ -171,7 +174,8 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 }
 
 // One CTA per token and 1024 columns, eight columns a thread; the rows of up to four slots
-// are in flight at a time.
+// are in flight at a time.  Bound by memory: 32768 slots x 7168 take 84 us, 6.2 TB/s; 16384
+// slots x 4096 with k = 2 40 us, 5.1 TB/s (two pieces a thread: 39).
 constexpr int kCombineThreads = 128;
 constexpr int kCombineCols = kCombineThreads * 8;
 
@@ -213,7 +217,8 @@ __global__ void __launch_bounds__(kCombineThreads)
 
 // One warp per slot: each lane adds the products of every 32nd group of eight columns, then
 // the lanes are added in a fixed tree.  The slots of a token are neighbours, so its row of
-// dout comes from the cache.
+// dout comes from the cache.  Bound by memory: 16382 slots x 4096 take 34 us in a graph, 201
+// MB, 5.9 TB/s.
 __global__ void __launch_bounds__(kRowThreads)
     combine_backward_kernel(const uint16_t *__restrict__ dout, const uint16_t *__restrict__ Y,
                             const int32_t *__restrict__ row_of_slot, int64_t slots, int k, int64_t H, int rows,

@@ -16,7 +16,8 @@
 // Up to kSortOneCta slots one CTA does it all: a decode step's cost is one launch.  Beyond
 // that, two launches over consecutive chunks, one CTA each: the first ranks the slots inside
 // their chunk and writes the chunk's counts; in the second every CTA adds up the counts of
-// all chunks (a few hundred KB from L2) and hands out the rows.
+// all chunks (a few hundred KB from L2) and hands out the rows.  Bound by latency: in a graph
+// 3.2 us for 8 slots into 64 slabs of 128 rows, 7.9 us for 131072 slots of 256 experts.
 #include "dg_device.cuh"
 #include "train_internal.h"
 

@@ -406,7 +406,8 @@ dg_status_t dg_moe_combine_backward(const void *dOUT_bf16, const void *Y_bf16,
 
 /*
  * SwiGLU and quantization, a = g * sigma(g) * u in FP32 from H = [g | u]; codes and scales as
- * dg_quantize_blockwise's definition on the FP32 values a (they are not rounded to BF16).
+ * dg_quantize_blockwise's definition on the FP32 values a (they are not rounded to BF16; a
+ * sigma below 2^-126 counts as 0).
  * With H8 and sH_t it also keeps H in 8 bits for the backward pass: the codes and scales of
  * dg_quantize_1x128 on H, bit for bit.
  *
