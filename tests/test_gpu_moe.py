@@ -23,9 +23,10 @@ def route(T, k, G, seed, drop=0.0, dtype=torch.int64, skew=1.0):
 
 
 SORTS = [
-    (1, 1, 1), (1, 8, 64), (3, 2, 5), (37, 2, 8), (0, 4, 16), (129, 1, 128), (1000, 6, 33), (512, 8, 1024),
-    (513, 8, 256),            # just past one CTA's share
-    (5000, 7, 257), (20000, 8, 64), (32768, 1, 2),
+    (1, 1, 1), (1, 8, 64), (3, 2, 5), (37, 2, 8), (0, 4, 16), (129, 1, 128), (5, 64, 1024),
+    (256, 8, 1024), (257, 8, 1024),  # the most that one CTA takes, and just past it, with the most experts
+    (512, 8, 1024), (1000, 6, 33), (513, 8, 256), (5000, 7, 257), (20000, 8, 64), (32768, 1, 2),
+    (40000, 4, 3),                   # chunks of more than one step
 ]
 
 

@@ -144,7 +144,7 @@ def test_gradient_product_refusals(lib):
     assert gw(P, P, P, P, P, 1, 0, P, 128, 1 << 20, 1 << 20, 128, NULL) == SHAPE
 
 
-def test_binding_refuses_host_tensors():
+def test_binding_refuses_host_tensors(lib):
     """Types, ranks and devices are checked before the library sees an address."""
     with pytest.raises(ValueError):
         binding.moe_sort(torch.zeros((4, 2), dtype=torch.int32), 4)
