@@ -170,6 +170,29 @@ def test_dispatch_never_reads_tokens_without_a_slot():
     assert torch.equal(q[:int(off[-1])].cpu(), want[0]) and torch.equal(s[:int(off[-1]) // 128].cpu(), want[1])
 
 
+def test_dispatch_every_bf16_pattern_under_a_scale_sweep():
+    """All finite BF16 values under block maxima over the whole range (subnormal to near the largest, powers of
+    two, multiples of 7, arbitrary ones): the codes and scales of the block quantizer, bit for bit."""
+    bits = torch.arange(65536, dtype=torch.int32)
+    finite = bits[(bits & 0x7F80) != 0x7F80]
+    tops = [0x0001, 0x0007, 0x0080, 0x0700, 0x1000, 0x123F, 0x2A5C, 0x3C00, 0x3F80, 0x3FE0, 0x4055, 0x43E0, 0x43E1,
+            0x4B0E, 0x5A5A, 0x6C63, 0x7000, 0x7F7F]
+    rows = []
+    for top in tops:
+        keep = finite[(finite & 0x7FFF) <= top]
+        n = -(-keep.numel() // 16383) * 16383
+        keep = torch.cat([keep, torch.full((n - keep.numel(),), top, dtype=torch.int32)])
+        for block in keep.view(-1, 16383):  # every block holds the maximum
+            rows.append(torch.cat([block, torch.tensor([top], dtype=torch.int32)]).view(128, 128))
+    x = torch.cat(rows).to(torch.int16).view(torch.bfloat16).cuda()
+    T = x.shape[0]
+    off, row, slot = binding.moe_sort(torch.zeros((T, 1), dtype=torch.int32, device="cuda"), 1)
+    q, s = binding.moe_dispatch_quantize(x, slot, off, 1)
+    wq, ws = binding.quantize_blockwise(x)
+    assert torch.equal(s[:T // 128].view(torch.int32), ws.view(torch.int32))
+    assert torch.equal(q[:T], wq)
+
+
 def test_dispatch_weights_of_both_signs_and_zero():
     """Negative and zero weights: magnitudes enter the scale, zeros keep the product's sign."""
     T, k, G, H = 50, 2, 3, 384

@@ -48,6 +48,21 @@ def test_swiglu_quantize(M, F, checkpoint):
         assert torch.equal(out[2], q.cpu()) and torch.equal(out[3], s.cpu())
 
 
+def test_checkpoint_of_arbitrary_finite_bit_patterns():
+    """Rows of finite BF16 values of every exponent, and rows of subnormals: the checkpoint is still
+    dg_quantize_1x128's output, bit for bit."""
+    g = torch.Generator().manual_seed(6)
+    bits = torch.randint(0, 65536, (512, 512), generator=g, dtype=torch.int32)
+    bits[:, ::3] &= 0xBFFF      # half the exponents below 1
+    bits[128:256] &= 0x807F     # zeros and subnormals
+    bits[256:384] = (bits[256:384] & 0x807F) | 0x3F80  # one exponent
+    bits[(bits & 0x7F80) == 0x7F80] = 0
+    h = bits.to(torch.int16).view(torch.bfloat16).cuda()
+    _, _, h8, sh = binding.swiglu_quantize(h, checkpoint=True)
+    q, s = binding.quantize_1x128(h)
+    assert torch.equal(sh.view(torch.int32), s.view(torch.int32)) and torch.equal(h8, q)
+
+
 def test_swiglu_extremes():
     """Gates whose exponential overflows or underflows: the sigmoid is 0 or 1, nothing is NaN."""
     g = torch.tensor([0.0, -0.0, 88.0, -88.0, 89.0, -89.0, 104.0, -104.0, 1e4, -1e4, 3e38, -3e38, 1e-30, -1e-30, 127.0, -127.0])
