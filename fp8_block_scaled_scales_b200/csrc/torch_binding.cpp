@@ -1,7 +1,7 @@
 // The expert-layer and gradient calls for Python: argument checks, output allocation and the
 // call through the C ABI (include/dg.h), in one native function each.  A decode step is a
 // chain of calls whose kernels take a few microseconds; done in Python, the checks, three
-// allocations and the marshalling of a dozen arguments cost 9 to 17 us a call, here 4 to 6.
+// allocations and the marshalling of a dozen arguments cost 9 to 17 us a call, here 4 to 8.
 //
 // Every function takes positional arguments (binding.py has the signatures and their
 // documentation), raises ValueError for a tensor of the wrong type, shape, device or layout,
@@ -275,7 +275,7 @@ const int32_t *groups(PyObject *o, int dev, int64_t &G) {
     G = 0;
     if (o == Py_None) return nullptr;
     G = tensor(o, "offsets").numel() - 1;
-    TORCH_CHECK_VALUE(G <= kIntMax, "offsets is too long");
+    TORCH_CHECK_VALUE(G >= 1 && G <= kIntMax, "offsets must have G + 1 elements, G at least 1");  // an empty one has no address
     return in<int32_t>(o, "offsets", kI32, {G + 1}, dev);
 }
 

@@ -188,3 +188,21 @@ def test_two_steps_on_two_streams():
     for a, b in zip(alone, got):
         for s, t in zip(a, b):
             assert torch.equal(s, t)
+
+
+def test_offsets_without_an_expert_are_refused():
+    """An empty tensor has no address; it must not be taken for "no offsets", which means all rows."""
+    codes = torch.zeros((128, 128), dtype=torch.uint8, device="cuda")
+    one = torch.ones((1, 1), device="cuda")
+    h = torch.zeros((128, 256), dtype=torch.bfloat16, device="cuda")
+    for n in (0, 1):
+        off = torch.zeros(n, dtype=torch.int32, device="cuda")
+        with pytest.raises(ValueError):
+            dg.swiglu_quantize(h, offsets=off)
+        with pytest.raises(ValueError):
+            dg.swiglu_quantize_backward(h.to(torch.float8_e4m3fn), torch.ones((2, 128), device="cuda"),
+                                        h[:, :128].contiguous(), offsets=off)
+        with pytest.raises(ValueError):
+            dg.grouped_dgrad_contiguous(codes, one, codes, one, off)
+        with pytest.raises(ValueError):
+            dg.grouped_wgrad_contiguous(codes, one, codes, one, off)
