@@ -17,6 +17,8 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 bool bad_slots(int64_t T, int k) { return T < 0 || k < 1 || T > kMaxSlots / k; }
 
+bool bad_columns(int64_t H) { return H < 0 || H % 16 != 0 || H > kInt32Max; }
+
 // the most rows the contiguous layout can need: every expert that has a slot pads by at most 127
 int64_t most_rows(int64_t slots, int G) { return (slots + 127 * (slots < G ? slots : G)) / 128 * 128; }
 
@@ -69,7 +71,7 @@ dg_status_t dg_moe_sort_masked(const void *topk_ids, int ids_64bit, int64_t T, i
 dg_status_t dg_moe_dispatch_quantize(const void *X_bf16, const float *weights, const int32_t *slot_of_row,
                                      const int32_t *group_offsets, int64_t T, int k, int64_t H,
                                      int64_t M_total_capacity, int G, uint8_t *Q, float *S, cudaStream_t stream) {
-    if (bad_slots(T, k) || H < 0 || H % 16 != 0 || M_total_capacity < 0 || M_total_capacity % 128 != 0 ||
+    if (bad_slots(T, k) || bad_columns(H) || M_total_capacity < 0 || M_total_capacity % 128 != 0 ||
         M_total_capacity > kInt32Max || G < 1 || G > 1024)
         return DG_ERR_SHAPE;
     if (M_total_capacity == 0 || H == 0) return DG_OK;
@@ -87,7 +89,7 @@ dg_status_t dg_moe_dispatch_quantize(const void *X_bf16, const float *weights, c
 dg_status_t dg_moe_dispatch_quantize_masked(const void *X_bf16, const int32_t *slot_of_row, const int32_t *masked_m,
                                             int64_t T, int k, int64_t H, int G, int64_t M_max, uint8_t *Q, float *S,
                                             cudaStream_t stream) {
-    if (bad_slots(T, k) || H < 0 || H % 16 != 0 || G < 1 || G > 1024 || M_max < 0 || M_max > kInt32Max / G)
+    if (bad_slots(T, k) || bad_columns(H) || G < 1 || G > 1024 || M_max < 0 || M_max > kInt32Max / G)
         return DG_ERR_SHAPE;
     if (M_max == 0 || H == 0) return DG_OK;
     if ((T > 0 && !X_bf16) || !slot_of_row || !masked_m || !Q || !S) return DG_ERR_INVALID_ARG;
@@ -101,7 +103,7 @@ dg_status_t dg_moe_dispatch_quantize_masked(const void *X_bf16, const int32_t *s
 
 dg_status_t dg_moe_combine(const void *Y_bf16, const float *weights, const int32_t *row_of_slot, int64_t T, int k,
                            int64_t H, int64_t rows, void *OUT_bf16, cudaStream_t stream) {
-    if (bad_slots(T, k) || H < 0 || H % 16 != 0 || rows < 0 || rows > kInt32Max) return DG_ERR_SHAPE;
+    if (bad_slots(T, k) || bad_columns(H) || rows < 0 || rows > kInt32Max) return DG_ERR_SHAPE;
     if (T == 0 || H == 0) return DG_OK;
     if ((rows > 0 && !Y_bf16) || !row_of_slot || !OUT_bf16) return DG_ERR_INVALID_ARG;
     if (!aligned(Y_bf16, 16) || !aligned(OUT_bf16, 16) || !aligned(weights, 4) || !aligned(row_of_slot, 4))
@@ -114,7 +116,7 @@ dg_status_t dg_moe_combine(const void *Y_bf16, const float *weights, const int32
 
 dg_status_t dg_moe_combine_backward(const void *dOUT_bf16, const void *Y_bf16, const int32_t *row_of_slot, int64_t T,
                                     int k, int64_t H, int64_t rows, float *dweights, cudaStream_t stream) {
-    if (bad_slots(T, k) || H < 0 || H % 16 != 0 || rows < 0 || rows > kInt32Max) return DG_ERR_SHAPE;
+    if (bad_slots(T, k) || bad_columns(H) || rows < 0 || rows > kInt32Max) return DG_ERR_SHAPE;
     if (T == 0) return DG_OK;
     if ((H > 0 && !dOUT_bf16) || (rows > 0 && H > 0 && !Y_bf16) || !row_of_slot || !dweights)
         return DG_ERR_INVALID_ARG;
@@ -196,7 +198,7 @@ dg_status_t dg_fp8_grouped_dgrad_contiguous(const uint8_t *dY, const float *sdY,
     if (M_total_capacity < 0 || M_total_capacity % 128 != 0 || N <= 0 || N % 128 != 0 || K < 0 || K % 16 != 0 ||
         G < 1 || G > 1024)
         return DG_ERR_SHAPE;
-    if (M_total_capacity > kInt32Max || G * N > kInt32Max || K > kInt32Max) return DG_ERR_SHAPE;
+    if (M_total_capacity > kInt32Max || N > kInt32Max / G || K > kInt32Max) return DG_ERR_SHAPE;
     if (M_total_capacity == 0 || K == 0) return DG_OK;
     if (!group_offsets) return DG_ERR_INVALID_ARG;
     dg_status_t st = check_grad(dY, sdY, W, sW, dX_bf16);
@@ -242,7 +244,7 @@ dg_status_t dg_fp8_grouped_wgrad_contiguous(const uint8_t *dY, const float *sdY,
     if (M_total_capacity < 0 || M_total_capacity % 128 != 0 || N < 0 || N % 128 != 0 || K < 0 || K % 16 != 0 ||
         G < 1 || G > 1024)
         return DG_ERR_SHAPE;
-    if (M_total_capacity > kInt32Max || G * N > kInt32Max || K > kInt32Max) return DG_ERR_SHAPE;
+    if (M_total_capacity > kInt32Max || N > kInt32Max / G || K > kInt32Max) return DG_ERR_SHAPE;
     if (accumulate && !out_fp32) return DG_ERR_INVALID_ARG;
     if (N == 0 || K == 0) return DG_OK;
     if (M_total_capacity > 0 && !group_offsets) return DG_ERR_INVALID_ARG;

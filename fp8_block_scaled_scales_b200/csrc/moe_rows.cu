@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
     const int g = gy / Ry, y = gy - g * Ry;
     const int rows = min(max(__ldg(masked_m + g), 0), m_max);
     const int bc0 = chunk * cols;
-    for (int lb = y; lb * 128 < rows; lb += Ry)
+    for (int lb = y, blocks = (rows >> 7) + ((rows & 127) != 0); lb < blocks; lb += Ry)
         dispatch_rows<false>(X, nullptr, slot_of_row, slots, k, H, static_cast<int64_t>(g) * m_max + lb * 128,
                              min(rows - lb * 128, 128), bc0, min(bc0 + cols, Cb), Q,
                              S + (static_cast<int64_t>(g) * Rb + lb) * Cb, sm);
@@ -279,7 +279,7 @@ static dg_status_t launch_dispatch_impl(const void *X, const float *weights, con
     const int64_t Cb = (H + 127) / 128, Rb = rows / 128;
     const int cols = dispatch_cols(Rb, Cb, dev.num_sms);
     const int64_t n = (Cb + cols - 1) / cols * Rb;
-    if (n > 0x7FFFFFFFLL || H > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
+    if (n > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
     return launch_pdl(dispatch_kernel<WEIGHTS>, static_cast<int>(n), kRowThreads, sizeof(DispatchSmem), stream,
                       static_cast<const uint16_t *>(X), weights, slot_of_row, offsets, G, static_cast<int>(slots), k, H,
                       static_cast<int>(Cb), cols, static_cast<int>(Rb), Q, S);
@@ -306,7 +306,7 @@ dg_status_t launch_dispatch_quantize_masked(const void *X, const int32_t *slot_o
     const int64_t Ry = Rb < kDispatchMaskedRowCtas ? Rb : kDispatchMaskedRowCtas;
     const int cols = dispatch_cols(G * Ry, Cb, dev.num_sms);
     const int64_t n = (Cb + cols - 1) / cols * G * Ry;
-    if (n > 0x7FFFFFFFLL || H > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
+    if (n > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
     return launch_pdl(dispatch_masked_kernel, static_cast<int>(n), kRowThreads, sizeof(DispatchSmem), stream,
                       static_cast<const uint16_t *>(X), slot_of_row, masked_m, static_cast<int>(slots), k, H,
                       static_cast<int>(Cb), cols, G, static_cast<int>(m_max), static_cast<int>(Rb),

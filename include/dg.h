@@ -359,7 +359,7 @@ dg_status_t dg_moe_sort_masked(const void *topk_ids, int ids_64bit, int64_t T, i
  * slot_of_row : int32 [M_total_capacity].   group_offsets : int32 [G+1].
  * Q : [M_total_capacity][H] E4M3 out, 16-byte aligned.
  * S : [M_total_capacity/128][ceil(H/128)] FP32 out.
- * H % 16 == 0, M_total_capacity % 128 == 0.  M_total_capacity == 0 or H == 0 is a no-op.
+ * H % 16 == 0, H < 2^31, M_total_capacity % 128 == 0.  M_total_capacity == 0 or H == 0 is a no-op.
  */
 dg_status_t dg_moe_dispatch_quantize(const void *X_bf16, const float *weights,
                                      const int32_t *slot_of_row, const int32_t *group_offsets,
@@ -386,7 +386,7 @@ dg_status_t dg_moe_dispatch_quantize_masked(const void *X_bf16, const int32_t *s
  *
  * Y_bf16 : [rows][H] BF16 (either layout), 16-byte aligned.  weights : [T][k] FP32 or null.
  * row_of_slot : int32 [T][k].  OUT_bf16 : [T][H] BF16 out, 16-byte aligned.
- * H % 16 == 0, 0 <= rows < 2^31.  T == 0 or H == 0 is a no-op.
+ * H % 16 == 0, H < 2^31, 0 <= rows < 2^31.  T == 0 or H == 0 is a no-op.
  */
 dg_status_t dg_moe_combine(const void *Y_bf16, const float *weights, const int32_t *row_of_slot,
                            int64_t T, int k, int64_t H, int64_t rows, void *OUT_bf16,

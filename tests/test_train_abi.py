@@ -144,6 +144,20 @@ def test_gradient_product_refusals(lib):
     assert gw(P, P, P, P, P, 1, 0, P, 128, 1 << 20, 1 << 20, 128, NULL) == SHAPE
 
 
+def test_sizes_beyond_the_index_ranges_are_refused(lib):
+    """Widths and products of sizes that 32 or 64 bits do not hold: refused before any of them is computed with."""
+    for H in (1 << 31, 1 << 53, (1 << 63) - 16):
+        assert lib.dg_moe_dispatch_quantize(P, NULL, P, P, 8, 2, H, 128, 4, P, P, NULL) == SHAPE
+        assert lib.dg_moe_dispatch_quantize_masked(P, P, P, 8, 2, H, 4, 64, P, P, NULL) == SHAPE
+        assert lib.dg_moe_combine(P, P, P, 1 << 29, 2, H, 128, P, NULL) == SHAPE
+        assert lib.dg_moe_combine_backward(P, P, P, 8, 2, H, 128, P, NULL) == SHAPE
+    for N in (1 << 31, 1 << 54, 1 << 62):  # 1024 * 2^54 is 0 in 64 bits
+        assert lib.dg_fp8_grouped_dgrad_contiguous(P, P, P, P, P, P, 128, 1024, N, 128, NULL) == SHAPE
+        assert lib.dg_fp8_grouped_wgrad_contiguous(P, P, P, P, P, 1, 0, P, 128, 1024, N, 128, NULL) == SHAPE
+        assert lib.dg_fp8_dgrad_blockscaled(P, P, P, P, P, 8, N, 128, NULL) == SHAPE
+        assert lib.dg_swiglu_quantize(P, NULL, 0, 8, N, P, P, NULL, NULL, NULL) == SHAPE
+
+
 def test_binding_refuses_host_tensors(lib):
     """Types, ranks and devices are checked before the library sees an address."""
     with pytest.raises(ValueError):
