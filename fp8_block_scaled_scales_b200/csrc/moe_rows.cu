@@ -48,13 +48,18 @@ __device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, co
     const int sub = tid >> 4, lane_col = (tid & 15) * 8;
     const int Hi = static_cast<int>(H);  // a 32 x 32 bit product for each address
     __syncthreads();  // an earlier row block's tokens are no longer read
+    bool infinite = false;
     if (tid < 128) {
         const int slot = tid < rows ? __ldg(slot_of_row + row0 + tid) : -1;
         const bool ok = slot >= 0 && slot < slots;  // anything else is a row without a slot
         sm.tok[tid] = ok ? slot / k : -1;
-        if (WEIGHTS) sm.wgt[tid] = ok ? __ldg(weights + slot) : 0.0f;
+        if (WEIGHTS) {
+            const float w = ok ? __ldg(weights + slot) : 0.0f;
+            sm.wgt[tid] = w;
+            infinite = isinf(w);
+        }
     }
-    __syncthreads();
+    infinite = __syncthreads_or(infinite);  // some row's weight is
     // a row without a token: its pieces stay zero
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -97,6 +102,12 @@ __device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, co
                 const float a = __uint_as_float(amax_bits_of(amax_pair8(v[i])) << 16);
                 const float b = __uint_as_float(amax_bits_of(amax_pair8(v[i + 1])) << 16);
                 f = amax3(f, make_float2(a * sm.wgt[sub + 16 * i], b * sm.wgt[sub + 16 * (i + 1)]));
+            }
+            if (__builtin_expect(infinite, 0)) {  // then a zero among the row's columns is a NaN
+                f = col_ok ? f : 0.0f;            // and there is none past the last column
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (col_ok && isinf(sm.wgt[sub + 16 * i]) && has_zero8(v[i])) f = __int_as_float(0x7FFFFFFF);
             }
             m = __float_as_uint(f);
         } else {

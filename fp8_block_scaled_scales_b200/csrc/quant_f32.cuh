@@ -122,6 +122,12 @@ __device__ __forceinline__ uint32_t amax_pair8(uint4 v) {
     return __vmaxu2(a, b);
 }
 
+// Whether one of eight BF16 is a zero.
+__device__ __forceinline__ bool has_zero8(uint4 v) {
+    return (__vcmpeq2(v.x & 0x7FFF7FFFu, 0u) | __vcmpeq2(v.y & 0x7FFF7FFFu, 0u) | __vcmpeq2(v.z & 0x7FFF7FFFu, 0u) |
+            __vcmpeq2(v.w & 0x7FFF7FFFu, 0u)) != 0u;
+}
+
 // Four E4M3 codes (lowest byte first) as FP32, exact: every E4M3 value is an FP16 value.
 __device__ __forceinline__ void e4m3x4_to_f32(uint32_t q, float2 &lo, float2 &hi) {
     uint32_t a, b;

@@ -57,7 +57,7 @@ def quantize_f32(v: torch.Tensor):
         for j in range(s.shape[1]):
             b = v[i * B:(i + 1) * B, j * B:(j + 1) * B]
             t = b.abs().max() / torch.tensor(448.0)
-            if t > 0:
+            if t != 0:  # a NaN too
                 s[i, j] = t
             q[i * B:(i + 1) * B, j * B:(j + 1) * B] = (b / s[i, j]).clamp(-448, 448).to(F8).view(U8)
     return q, s

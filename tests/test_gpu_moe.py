@@ -228,6 +228,31 @@ def test_dispatch_non_finite_values_stay_in_their_block():
     assert torch.equal(q[:384].cpu()[keep], cq[:384].cpu()[keep])
 
 
+@pytest.mark.parametrize("T,k,H", [(40, 2, 400), (700, 8, 656)])
+def test_dispatch_infinite_and_nan_weights(T, k, H):
+    """Products with a weight that is not finite follow FP32: infinite (scale infinite, finite rows' codes 0) or,
+    where the row has a zero in the block or the weight is NaN, NaN; other blocks stay as they are."""
+    G = 3
+    ids = route(T, k, G, 41)
+    cap = plain.cap_of(T, k, G)
+    off, row, slot = plain.sort_plain(ids.numpy(), G, cap)
+    x = tokens(T, H, 42)
+    x[x == 0] = 1.0
+    x[3, 130:140] = 0.0  # zeros in one column block, next to values
+    x[4, 256:384] = 0.0  # and a whole piece of them in another
+    w = torch.rand((T, k), generator=torch.Generator().manual_seed(43)) + 0.5
+    w[3, 0], w[4, 1], w[20, 0] = float("inf"), -float("inf"), float("nan")
+    used = int(off[-1])
+    q, s = binding.moe_dispatch_quantize(x.cuda(), torch.from_numpy(slot).int().cuda(),
+                                         torch.from_numpy(off).int().cuda(), k, weights=w.cuda())
+    wq, ws = plain.quantize_f32(gathered(x, slot, k, w)[:used])
+    assert bool(torch.isinf(ws).any()) and bool(torch.isnan(ws).any()) and bool(torch.isfinite(ws).any())
+    assert torch.equal(s[:used // 128].cpu().nan_to_num(nan=-1.0), ws.nan_to_num(nan=-1.0))
+    q, wq = q[:used].cpu(), wq.view(torch.uint8)
+    nan = (wq & 0x7F) == 0x7F
+    assert torch.equal((q & 0x7F) == 0x7F, nan) and torch.equal(q[~nan], wq[~nan])
+
+
 def test_rows_past_32_bit_offsets():
     """Matrices of more than 2^32 elements: the last rows and tokens are the ones looked at."""
     H, rows = 16384, 270_080  # 4.4e9 elements
