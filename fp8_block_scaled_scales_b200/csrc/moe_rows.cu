@@ -6,7 +6,7 @@
 //   s = fl32(amax / 448) per 128x128 block (1 if 0), q = E4M3_rn_satfinite(fl32(v / s)).
 //   Without weights the codes and scales are those of the block quantizer on the gathered
 //   matrix, bit for bit.  With weights it is the gradient of the combination with respect to
-//   the expert rows (quantize8_negated says where a code may differ from the definition's).
+//   the expert rows (quantize8_f32 says where a code may differ from the definition's).
 // combine:            out[t] = bf16(sum_j weights[t][j] * y[row(t, j)]), FP32, ascending j;
 //   without weights it is the gradient of the dispatch.
 // combine_backward:   dweights[t][j] = sum_h dout[t][h] * y[row(t, j)][h], FP32.
@@ -28,9 +28,9 @@ constexpr int kRowThreads = 256;
 // block's (cp.async), and reduces and converts the current ones, so that the gather runs under
 // the conversion.  All CTAs walk the columns at the same pace, so the k copies of a token's
 // piece are read close together: once from memory (ncu: 64 MB of 59), then from L2.  32768
-// slots x 7168: 97 us, 730 MB through L2; without the conversion, the moves and the block
+// slots x 7168: 92 us, 730 MB through L2; without the conversion, the moves and the block
 // maximum alone take 78 us, without the maximum 85.  (A CTA per block, rows first: 137 us with
-// 28 % L2 hits.)  With weights 102 us.  256 threads of eight rows: 512 of four 116 us, 128 of
+// 28 % L2 hits.)  With weights 96 us.  256 threads of eight rows: 512 of four 116 us, 128 of
 // sixteen 99.
 struct DispatchSmem {
     uint4 piece[8][kRowThreads];
@@ -125,14 +125,14 @@ __device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, co
             for (int i = 0; i < 8; ++i) {
                 uint2 q;
                 if (WEIGHTS) {
-                    const float nw = -sm.wgt[sub + 16 * i];
+                    const float w = sm.wgt[sub + 16 * i];
                     float2 x[4];
                     bf16x8_to_f32(v[i], x);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], make_float2(nw, nw));
-                    q = quantize8_negated<kFast>(x, bs);
+                    for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], make_float2(w, w));
+                    q = quantize8_f32<kFast>(x, bs);
                 } else {
-                    q = quantize8_corrected<kFast>(v[i], bs);
+                    q = quantize8_bf16<kFast>(v[i], bs);
                 }
                 if (sub + 16 * i < rows) *reinterpret_cast<uint2 *>(qp + i * step) = q;
             }

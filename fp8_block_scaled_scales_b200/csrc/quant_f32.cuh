@@ -26,21 +26,34 @@ __device__ __forceinline__ void bf16x8_to_f32(uint4 v, float2 (&x)[4]) {
             : "r"(w[j]), "f"(-0.0f));
 }
 
-// A block's scale and an approximate reciprocal.  Inside the window s is a quotient corrected
+// A block's scale and its reciprocal in two parts.  Inside the window s is a quotient corrected
 // by its remainder, two multiply-adds after the product with 1/448 (P. W. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
 // Dev. 34, 1990, on division with a fused multiply-add): equal to fl32(amax / 448) for every
-// FP32 amax there; r is within 1 unit of 1/s (the hardware's approximation).  Outside the
-// window (NaN included) s comes from the division, and values are divided by it.
+// FP32 amax there.  r is the hardware's approximation (within 1 unit of 1/s) lowered by
+// 2^-21, so that it lies below 1/s; r_lo > 0 is the rest: with e = 1 - s r, exact but for
+// its rounding, 1/s = r / (1 - e) = r + r (e + e^2 + ...), together good to 2^-43.
+// Outside the window (NaN included) s comes from the division, and values are divided by it.
 // The IEEE division and reciprocal cost every thread some 60 instructions a block, against
 // 80 for converting one of its rows.
 struct FastScale {
-    float s, r;
+    float s, r, r_lo;
     bool fast;
+
+    // For values that come with their sign flipped.
+    __device__ __forceinline__ FastScale negated() const { return FastScale{-s, -r, -r_lo, fast}; }
 };
 
 __device__ __forceinline__ bool scale_is_fast(float amax) {
     return (amax >= 0x1p-90f && amax <= 0x1p100f) || amax == 0.0f;
+}
+
+__device__ __forceinline__ void split_reciprocal(FastScale &b) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b.s));
+    b.r = __fmul_rn(r, 1.0f - 0x1p-21f);
+    const float e = __fmaf_rn(-b.s, b.r, 1.0f);
+    b.r_lo = __fmul_rn(__fmaf_rn(e, e, e), b.r);
 }
 
 // FAST: scale_is_fast(amax).
@@ -56,7 +69,7 @@ __device__ __forceinline__ FastScale scale_of(float amax) {
         const float q = __fdiv_rn(amax, 448.0f);
         b.s = (q == 0.0f) ? 1.0f : q;
     }
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b.r) : "f"(b.s));
+    split_reciprocal(b);
     return b;
 }
 
@@ -64,48 +77,38 @@ __device__ __forceinline__ FastScale fast_scale(float amax) {
     return __builtin_expect(scale_is_fast(amax), 1) ? scale_of<true>(amax) : scale_of<false>(amax);
 }
 
-// Four pairs n = -x -> codes of fl32(x / s): the quotient corrected by its remainder, y = n (-r),
-// e = y s + n (the negative remainder), x/s = e (-r) + y; in this order of signs a zero keeps
-// its own.  Three multiply-adds a pair and one conversion, with no second path for values
-// near a rounding boundary, which a block whose amax is a multiple of 7 meets often.
-//   x BF16: for every x and amax in the window, and any r within 2 units of 1/s, the code is
-//     that of the IEEE quotient (checked exhaustively on the CPU).
-//   x any FP32: the quotient is the rounding of a value within 2^-46 of x/s, so the code can
+// Four pairs -> codes of fl32(x / s), as the rounding of x r + fl32(x r_lo): two operations a
+// pair and one conversion, with no second path for values near a rounding boundary, which a
+// block whose amax is a multiple of 7 meets often.  r_lo > 0 keeps the sign of a zero.
+//   x BF16: for every x and amax in the window, and any approximation within 2 units of 1/s,
+//     the code is that of the IEEE quotient (checked exhaustively on the CPU).
+//   x any FP32: the quotient is the rounding of a value within 2^-43 of x/s, so the code can
 //     differ only where x/s lies that close to the middle between an E4M3 rounding boundary
 //     and the next FP32 number.
+// (The product with the reciprocal corrected by its remainder, three operations, was as exact;
+// FP32 products bound the gather's conversion.)
 // FAST: b.fast, which the caller tests once for all its rows (a branch a row cost a tenth of
 // the instructions and kept the rows' arithmetic apart).
 template <bool FAST>
-__device__ __forceinline__ uint2 quantize8_negated(const float2 (&n)[4], const FastScale &b) {
+__device__ __forceinline__ uint2 quantize8_f32(const float2 (&x)[4], const FastScale &b) {
     float2 q[4];
     if (FAST) {
-        const float2 s2 = make_float2(b.s, b.s), nr = make_float2(-b.r, -b.r);
+        const float2 r = make_float2(b.r, b.r), r_lo = make_float2(b.r_lo, b.r_lo);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 y = __fmul2_rn(n[j], nr);
-            q[j] = __ffma2_rn(__ffma2_rn(y, s2, n[j]), nr, y);
-        }
+        for (int j = 0; j < 4; ++j) q[j] = __ffma2_rn(x[j], r, __fmul2_rn(x[j], r_lo));
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = make_float2(__fdiv_rn(-n[j].x, b.s), __fdiv_rn(-n[j].y, b.s));
+        for (int j = 0; j < 4; ++j) q[j] = make_float2(__fdiv_rn(x[j].x, b.s), __fdiv_rn(x[j].y, b.s));
     }
     return make_uint2(e4m3x4(q[0].x, q[0].y, q[1].x, q[1].y), e4m3x4(q[2].x, q[2].y, q[3].x, q[3].y));
 }
 
 // Eight BF16 -> codes of fl32(x / s), exactly.
 template <bool FAST>
-__device__ __forceinline__ uint2 quantize8_corrected(uint4 v, const FastScale &b) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float2 n[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        asm("{\n\t.reg .b16 l, h, m;\n\t"  // x * (-1) + (-0), exact
-            "mov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
-            "fma.rn.f32.bf16 %0, l, m, %3;\n\t"
-            "fma.rn.f32.bf16 %1, h, m, %3;\n\t}"
-            : "=f"(n[j].x), "=f"(n[j].y)
-            : "r"(w[j]), "f"(-0.0f));
-    return quantize8_negated<FAST>(n, b);
+__device__ __forceinline__ uint2 quantize8_bf16(uint4 v, const FastScale &b) {
+    float2 x[4];
+    bf16x8_to_f32(v, x);
+    return quantize8_f32<FAST>(x, b);
 }
 
 // The largest |x| of eight BF16 as two magnitudes side by side, a NaN above infinity.

@@ -79,7 +79,7 @@ __device__ __forceinline__ void checkpoint_rows(const uint4 (&vg)[2], const uint
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const FastScale g = scale_of<kFast>(amax[i][0]), u = scale_of<kFast>(amax[i][1]);
-            const uint2 qg = quantize8_corrected<kFast>(vg[i], g), qu = quantize8_corrected<kFast>(vu[i], u);
+            const uint2 qg = quantize8_bf16<kFast>(vg[i], g), qu = quantize8_bf16<kFast>(vu[i], u);
             if (ok[i]) {
                 *reinterpret_cast<uint2 *>(q + i * q_row + in_q) = qg;
                 *reinterpret_cast<uint2 *>(q + i * q_row + q_up + in_q) = qu;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kGluThreads, 2)
         walk.advance(layout);
         const bool more = walk.find(layout, next_row0, next_rows);
         if (!more) next_rows = 0;
-        float2 a[kGluPer][4];  // negated, as the conversion takes them
+        float2 a[kGluPer][4];  // negated, as negated_quotient leaves them
         float m = 0.0f;
         cp_async_wait();
 #pragma unroll
@@ -247,11 +247,12 @@ __global__ void __launch_bounds__(kGluThreads, 2)
         }
         const FastScale bs = fast_scale(__uint_as_float(cta_max<kGluThreads / 32>(__float_as_uint(m), red[par])));
         if (tid == 0) S[static_cast<int64_t>(rb) * layout.Fb + bc] = bs.s;
+        const FastScale nb = bs.negated();
         uint8_t *q = Q + static_cast<int64_t>(row0) * F + bc * 128;
         auto convert = [&](auto fast) {
 #pragma unroll
             for (int i = 0; i < kGluPer; ++i) {
-                const uint2 c = quantize8_negated<decltype(fast)::value>(a[i], bs);
+                const uint2 c = quantize8_f32<decltype(fast)::value>(a[i], nb);
                 if (sub + 32 * i < rows) *reinterpret_cast<uint2 *>(q + i * (step >> 1) + in_q) = c;
             }
         };
@@ -377,12 +378,13 @@ __global__ void __launch_bounds__(kGluBackThreads, 1)
             sp[0] = bg.s;
             sp[layout.Fb] = bu.s;
         }
+        const FastScale ng = bg.negated(), nu = bu.negated();
         uint8_t *q = Q + static_cast<int64_t>(row0) * 2 * F + bc * 128;
         auto convert = [&](auto fast) {
             constexpr bool kFast = decltype(fast)::value;
 #pragma unroll
             for (int i = 0; i < kGluBackPer; ++i) {
-                const uint2 cg = quantize8_negated<kFast>(dg[i], bg), cu = quantize8_negated<kFast>(du[i], bu);
+                const uint2 cg = quantize8_f32<kFast>(dg[i], ng), cu = quantize8_f32<kFast>(du[i], nu);
                 if (sub + kRows * i < rows) {
                     *reinterpret_cast<uint2 *>(q + i * kRows * 2 * F + in_h) = cg;
                     *reinterpret_cast<uint2 *>(q + i * kRows * 2 * F + F + in_h) = cu;

@@ -350,7 +350,7 @@ dg_status_t dg_moe_sort_masked(const void *topk_ids, int ids_64bit, int64_t T, i
  * multiplied in FP32 by weights[slot_of_row[r]] when weights is not null, and zero where
  * slot_of_row[r] is not in [0, T * k).  The codes and scales are dg_quantize_blockwise's
  * definition on that matrix (without weights, bit for bit its output on the gathered BF16
- * rows; with weights a code may be the neighbouring one where the quotient lies within 2^-46
+ * rows; with weights a code may be the neighbouring one where the quotient lies within 2^-43
  * of a rounding midpoint; a block whose amax / 448 rounds to 0 has scale 1).  Rows at or past
  * group_offsets[G] (taken to lie in [0, M_total_capacity]) are not written.
  * With weights this is the gradient of dg_moe_combine with respect to Y, quantized.

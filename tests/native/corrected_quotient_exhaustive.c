@@ -6,12 +6,13 @@
  * 1. The scale: q = fl32(amax c), c = fl32(1/448), s = fma(fma(-q, 448, amax), c, q) must be
  *    fl32(amax / 448) for every BF16 amax in the window [2^-90, 2^100], and for every FP32
  *    mantissa at several exponents of it.
- * 2. The codes: for every such BF16 amax and every BF16 x with |x| <= amax, with n = -x and r
- *    = fl32(1 / s),
- *      y = fl32(n * -r), e = fma(y, s, n), q = fma(e, -r, y)
- *    must have the E4M3 code of fl32(x / s).  The kernel's r comes from an approximation, so
- *    r one and two units to either side is tried too, for every eighth exponent of amax (the
- *    arithmetic does not change with a power of two).
+ * 2. The codes: for every such BF16 amax and every BF16 x with |x| <= amax, with a = fl32(1 / s),
+ *      r = fl32(a (1 - 2^-21)), e = fma(-s, r, 1), r_lo = fl32(fma(e, e, e) r),
+ *      q = fma(x, r, fl32(x r_lo))
+ *    must have the E4M3 code of fl32(x / s), and r_lo must be positive.  The kernel's a is an
+ *    approximation, so a one and two units to either side is tried too, for every eighth
+ *    exponent of amax (the arithmetic does not change with a power of two).  The same for -x
+ *    with s, r and r_lo negated, as the activation kernels have it.
  * Prints the number of mismatches.
  */
 #include <math.h>
@@ -80,13 +81,15 @@ int main(void)
         if (s != amax / 448.0f) ++bad;
         const int wide = ((ah >> 7) & 7u) == 0;
         for (int d = wide ? -2 : 0; d <= (wide ? 2 : 0); ++d) {
-            const float r = step_by(1.0f / s, d);
+            const float r = step_by(1.0f / s, d) * (1.0f - 0x1p-21f);
+            const float e = fmaf(-s, r, 1.0f), r_lo = fmaf(e, e, e) * r;
+            if (!(r_lo > 0.0f)) ++bad;
             for (uint32_t xm = 0; xm <= ah; ++xm) {
                 for (uint32_t sg = 0; sg < 2; ++sg) {
                     const float x = bf16(xm | (sg << 15)), n = -x;
-                    const float y = n * -r;
-                    const float e = fmaf(y, s, n);
-                    const uint8_t got = e4m3(fmaf(e, -r, y)), want = e4m3(x / s);
+                    const float q = fmaf(x, r, x * r_lo), q2 = fmaf(n, -r, n * -r_lo);
+                    if (q != q2 || signbit(q) != signbit(x) || signbit(q2) != signbit(x)) ++bad;
+                    const uint8_t got = e4m3(q), want = e4m3(x / s);
                     ++pairs;
                     if (got != want) {
                         ++bad;

@@ -1,8 +1,8 @@
 """The quantizing arithmetic of the expert-layer kernels, restated in C and checked
 exhaustively (tests/native/corrected_quotient_exhaustive.c): the scale amax / 448 by a
 corrected product for every BF16 amax in the window and every FP32 mantissa at several
-exponents, and the E4M3 code of fl32(x / s) by a corrected quotient for every such amax
-against every BF16 x with |x| <= amax, the reciprocal up to two units off."""
+exponents, and the E4M3 code of fl32(x / s) by a reciprocal in two parts for every such amax
+against every BF16 x with |x| <= amax, the approximation of 1/s up to two units off."""
 import os
 import shutil
 import subprocess
