@@ -30,7 +30,7 @@ EXPORTS = ("dg_quantize_blockwise", "dg_quantize_blockwise_masked", "dg_fp8_gemm
            "dg_fp8_gemm_1x128", "dg_fp8_gemm_1x128_select",
            "dg_fp8_gemm_blockscaled_select", "dg_status_string", "dg_get_last_device_status",
            "dg_version", "dg_test_set_kernel_control",
-           "dg_moe_sort", "dg_moe_sort_masked", "dg_moe_sort_workspace", "dg_moe_dispatch_quantize", "dg_moe_dispatch_quantize_masked",
+           "dg_moe_sort", "dg_moe_sort_masked", "dg_moe_sort_workspace", "dg_moe_dispatch_quantize", "dg_moe_dispatch_workspace", "dg_moe_dispatch_quantize_masked",
            "dg_moe_combine", "dg_moe_combine_backward", "dg_swiglu_quantize", "dg_swiglu_quantize_masked",
            "dg_swiglu_quantize_backward", "dg_fp8_dgrad_blockscaled", "dg_fp8_wgrad_blockscaled",
            "dg_fp8_grouped_dgrad_contiguous", "dg_fp8_grouped_wgrad_contiguous")
@@ -75,7 +75,8 @@ def lib() -> ctypes.CDLL:
     L.dg_moe_sort.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, i64, vp, i64, vp]
     L.dg_moe_sort_masked.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, i64, vp, i64, vp]
     L.dg_moe_sort_workspace.argtypes = [i64, i32, i32]
-    L.dg_moe_dispatch_quantize.argtypes = [vp, vp, vp, vp, i64, i32, i64, i64, i32, vp, vp, vp]
+    L.dg_moe_dispatch_quantize.argtypes = [vp, vp, vp, vp, i64, i32, i64, i64, i32, vp, vp, vp, i64, vp]
+    L.dg_moe_dispatch_workspace.argtypes = [i64, i32, i64, i64]
     L.dg_moe_dispatch_quantize_masked.argtypes = [vp, vp, vp, i64, i32, i64, i32, i64, vp, vp, vp]
     L.dg_moe_combine.argtypes = [vp, vp, vp, i64, i32, i64, i64, vp, vp]
     L.dg_moe_combine_backward.argtypes = [vp, vp, vp, i64, i32, i64, i64, vp, vp]
@@ -89,7 +90,7 @@ def lib() -> ctypes.CDLL:
     for f in EXPORTS:
         if f.startswith(("dg_moe_", "dg_swiglu_")) or "grad" in f:
             getattr(L, f).restype = ctypes.c_int
-    L.dg_moe_sort_workspace.restype = i64
+    L.dg_moe_sort_workspace.restype = L.dg_moe_dispatch_workspace.restype = i64
     L.dg_get_last_device_status.argtypes = [vp]
     L.dg_status_string.restype = ctypes.c_char_p
     L.dg_status_string.argtypes = [ctypes.c_int]

@@ -68,22 +68,32 @@ dg_status_t dg_moe_sort_masked(const void *topk_ids, int ids_64bit, int64_t T, i
                            static_cast<int32_t *>(workspace), stream);
 }
 
+int64_t dg_moe_dispatch_workspace(int64_t T, int k, int64_t H, int64_t M_total_capacity) {
+    return bad_slots(T, k) || bad_columns(H) || M_total_capacity < 0 || M_total_capacity > kInt32Max
+               ? 0
+               : dispatch_workspace(T, k, H, M_total_capacity);
+}
+
 dg_status_t dg_moe_dispatch_quantize(const void *X_bf16, const float *weights, const int32_t *slot_of_row,
                                      const int32_t *group_offsets, int64_t T, int k, int64_t H,
-                                     int64_t M_total_capacity, int G, uint8_t *Q, float *S, cudaStream_t stream) {
+                                     int64_t M_total_capacity, int G, uint8_t *Q, float *S, void *workspace,
+                                     int64_t workspace_bytes, cudaStream_t stream) {
     if (bad_slots(T, k) || bad_columns(H) || M_total_capacity < 0 || M_total_capacity % 128 != 0 ||
         M_total_capacity > kInt32Max || G < 1 || G > 1024)
         return DG_ERR_SHAPE;
     if (M_total_capacity == 0 || H == 0) return DG_OK;
-    if ((T > 0 && !X_bf16) || !slot_of_row || !group_offsets || !Q || !S) return DG_ERR_INVALID_ARG;
+    const int64_t need = dispatch_workspace(T, k, H, M_total_capacity);
+    if ((T > 0 && !X_bf16) || !slot_of_row || !group_offsets || !Q || !S || (need > 0 && !workspace) ||
+        workspace_bytes < need)
+        return DG_ERR_INVALID_ARG;
     if (!aligned(X_bf16, 16) || !aligned(Q, 16) || !aligned(S, 4) || !aligned(weights, 4) ||
-        !aligned(slot_of_row, 4) || !aligned(group_offsets, 4))
+        !aligned(slot_of_row, 4) || !aligned(group_offsets, 4) || !aligned(workspace, 16))
         return DG_ERR_ALIGNMENT;
     DeviceInfo dev;
     const dg_status_t st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
     return launch_dispatch_quantize(X_bf16, weights, slot_of_row, group_offsets, T * k, k, H, M_total_capacity, G, Q, S,
-                                    dev, stream);
+                                    workspace, dev, stream);
 }
 
 dg_status_t dg_moe_dispatch_quantize_masked(const void *X_bf16, const int32_t *slot_of_row, const int32_t *masked_m,

@@ -184,6 +184,217 @@ __global__ void __launch_bounds__(kRowThreads, 4)
                              S + (static_cast<int64_t>(g) * Rb + lb) * Cb, sm);
 }
 
+// The gather token by token, for tokens of several slots: a token's columns are read and
+// unpacked once and converted k times, where the form above reads them from L2 once a slot.
+// The scales must be known first, so it takes three launches:
+//   tops:   the largest magnitude of every token and column block (T x H read once), and no
+//           row for any slot yet;
+//   scales: per row block the maximum of its tokens' tops, the scale; rows without a token
+//           are written; each other row goes to the head of its slot's list (one row, unless
+//           slot_of_row names the slot again);
+//   rows:   a warp per token and 1024 columns writes the token's rows, 512 bytes at a time.
+// Codes and scales are those of the form above.  HBM bounds it: 32768 slots x 7168, k = 8,
+// 77 us against 88 above, 11 of them for the first launch and about 8 for the second; 131072
+// slots 256 us against 362, 1.44 GB, 5.6 TB/s (without the conversions 256).  One segment a
+// warp 82 and 277 us, four 80 and 267; persistent warps that looked two items ahead 81 and 268.
+constexpr int kTokCols = 512;  // a segment: columns of a warp, 16 a lane
+constexpr int kTokRun = 2;     // segments of a warp in the last launch, the second one's loads under the first
+constexpr int kTokWarps = kRowThreads / 32;
+constexpr int kTopsAhead = 8;  // column blocks of a scales CTA: one 16-byte load of tops
+
+struct TokenGather {
+    const uint16_t *X;
+    const float *weights;
+    const int32_t *slot_of_row, *offsets;
+    int G, k;
+    int64_t T, H;
+    int segs, parts;  // 512-column segments of a token, and its warps in the last launch
+    int Cb, Cb8;           // 128-column blocks, and that rounded up to 8
+    int32_t *head;      // [T][k] first row of a slot, -1: none
+    int32_t *next;      // [rows] the slot's next row
+    int32_t *repeated;  // whether a slot has one
+    uint16_t *tops;     // [T][Cb8] BF16 magnitude bits; with weights bit 15: a zero among them
+    uint8_t *Q;
+    float *S;
+};
+
+template <bool WEIGHTS>
+__global__ void __launch_bounds__(kRowThreads) dispatch_tops_kernel(const TokenGather p) {
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
+    for (int64_t i = first; i < p.T * p.k; i += static_cast<int64_t>(gridDim.x) * kRowThreads) p.head[i] = -1;
+    if (first == 0) *p.repeated = 0;
+    const int64_t w = first >> 5, t = w / p.segs;
+    if (t >= p.T) return;
+    const int lane = lane_id(), col = static_cast<int>(w - t * p.segs) * kTokCols + lane * 16;
+    uint32_t m = 0;
+    bool zero = false;
+    if (col < p.H) {
+        const uint4 *x = reinterpret_cast<const uint4 *>(p.X + t * p.H + col);
+        const uint4 a = __ldg(x), b = __ldg(x + 1);
+        m = amax_bits_of(__vmaxu2(amax_pair8(a), amax_pair8(b)));
+        if (WEIGHTS) zero = has_zero8(a) || has_zero8(b);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (WEIGHTS) {
+        const uint32_t zeros = __ballot_sync(0xFFFFFFFFu, zero);
+        if ((zeros >> (lane & ~7)) & 0xFFu) m |= 0x8000u;
+    }
+    if ((lane & 7) == 0 && col < p.H) p.tops[t * p.Cb8 + col / 128] = static_cast<uint16_t>(m);
+}
+
+template <bool WEIGHTS>
+__global__ void __launch_bounds__(128) dispatch_scales_kernel(const TokenGather p) {
+    __shared__ uint32_t red[4][kTopsAhead];
+    __shared__ uint32_t empty[kTopsAhead];  // the code of a row without a token, four times
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int chunks = p.Cb8 / kTopsAhead;
+    const int lb = static_cast<int>(blockIdx.x) / chunks, chunk = static_cast<int>(blockIdx.x) - lb * chunks;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    const int row = lb * 128 + tid;
+    if (lb * 128 >= __ldg(p.offsets + p.G)) return;
+    const int slot = __ldg(p.slot_of_row + row);
+    const bool ok = slot >= 0 && slot < p.T * p.k;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    float w = 0.0f;
+    if (ok) {
+        v = *reinterpret_cast<const uint4 *>(p.tops + static_cast<int64_t>(slot / p.k) * p.Cb8 + chunk * kTopsAhead);
+        if (WEIGHTS) w = __ldg(p.weights + slot);
+        if (chunk == 0) {
+            const int before = atomicExch(p.head + slot, row);  // a list's order changes nothing
+            p.next[row] = before;
+            if (before >= 0) *p.repeated = 1;
+        }
+    }
+    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < kTopsAhead; ++i) {
+        const uint32_t bits = (i & 1) ? words[i / 2] & 0xFFFF0000u : words[i / 2] << 16;
+        uint32_t m = bits;
+        if (WEIGHTS) {
+            float f = fabsf(__uint_as_float(bits & 0x7FFFFFFFu) * w);
+            if (isinf(w) && (bits >> 31)) f = __int_as_float(0x7FFFFFFF);  // infinity times a zero
+            m = __float_as_uint(f);
+        }
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (lane == 0) red[warp][i] = m;
+    }
+    __syncthreads();
+    const int bc = chunk * kTopsAhead + tid;
+    if (tid < kTopsAhead && bc < p.Cb) {
+        const float s = fast_scale(__uint_as_float(max(max(red[0][tid], red[1][tid]), max(red[2][tid], red[3][tid])))).s;
+        p.S[static_cast<int64_t>(lb) * p.Cb + bc] = s;
+        empty[tid] = isnan(s) ? 0x7F7F7F7Fu : 0u;
+    }
+    __syncthreads();
+    for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, !ok); rest; rest &= rest - 1) {
+        const int r = __ffs(rest) - 1;
+        uint8_t *q = p.Q + static_cast<int64_t>(row - lane + r) * p.H;
+#pragma unroll
+        for (int i = 0; i < kTopsAhead / 4; ++i) {
+            const int64_t col = static_cast<int64_t>(chunk) * kTopsAhead * 128 + i * 512 + lane * 16;
+            if (col < p.H) {
+                const uint32_t c = empty[i * 4 + lane / 8];
+                *reinterpret_cast<uint4 *>(q + col) = make_uint4(c, c, c, c);
+            }
+        }
+    }
+}
+
+template <bool WEIGHTS>
+__global__ void __launch_bounds__(kRowThreads, 3) dispatch_rows_kernel(const TokenGather p) {
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5, t = w / p.parts;
+    if (t >= p.T) return;
+    const int seg0 = static_cast<int>(w - t * p.parts) * kTokRun, seg1 = min(seg0 + kTokRun, p.segs);
+    const int lane = lane_id();
+    const uint16_t *x = p.X + t * p.H;
+    auto load = [&](int seg, uint4 (&v)[2]) {
+        const int64_t col = static_cast<int64_t>(seg) * kTokCols + lane * 16;
+        v[0] = v[1] = make_uint4(0, 0, 0, 0);
+        if (seg < seg1 && col < p.H) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(x + col);
+            v[0] = __ldg(src), v[1] = __ldg(src + 1);
+        }
+    };
+    // Eight slots at a time; lane 4 i + b looks up slot i's row and its scale of column block b.
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        const int j = j0 + (lane >> 2);
+        const int64_t slot = t * p.k + j;
+        int row = j < p.k ? __ldg(p.head + slot) : -1;
+        const float wgt = WEIGHTS && row >= 0 ? __ldg(p.weights + slot) : 0.0f;
+        const bool again = __ldg(p.repeated) != 0;
+        do {
+            uint4 v[2];
+            load(seg0, v);
+            const float *scales = p.S + static_cast<int64_t>(row >> 7) * p.Cb;
+            auto scale = [&](int seg) {
+                const int bc = seg * 4 + (lane & 3);
+                return row >= 0 && seg < seg1 && bc < p.Cb ? __ldg(scales + bc) : 1.0f;
+            };
+            float s = scale(seg0);
+            int r[8];
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                r[i] = __shfl_sync(0xFFFFFFFFu, row, 4 * i);
+                if (WEIGHTS) f[i] = __shfl_sync(0xFFFFFFFFu, wgt, 4 * i);
+            }
+            for (int seg = seg0; seg < seg1; ++seg) {
+                float2 n[2][4];
+                bf16x8_to_f32(v[0], n[0]), bf16x8_to_f32(v[1], n[1]);
+                FastScale mine;
+                mine.s = s;
+                split_reciprocal(mine);
+                const bool fast = s >= 0x1p-90f / 448.0f && s <= 0x1p100f / 448.0f;  // scale_is_fast of its maximum
+                load(seg + 1, v);
+                s = scale(seg + 1);
+                const int64_t col = static_cast<int64_t>(seg) * kTokCols + lane * 16;
+                uint8_t *q = p.Q + col;
+                auto convert = [&](auto fast) {
+                    constexpr bool kFast = decltype(fast)::value;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (r[i] < 0) continue;  // the same for the whole warp
+                        FastScale bs;
+                        if (kFast) {
+                            bs.r = __shfl_sync(0xFFFFFFFFu, mine.r, 4 * i + lane / 8);
+                            bs.r_lo = __shfl_sync(0xFFFFFFFFu, mine.r_lo, 4 * i + lane / 8);
+                        } else {
+                            bs.s = __shfl_sync(0xFFFFFFFFu, mine.s, 4 * i + lane / 8);
+                        }
+                        uint2 c[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (WEIGHTS) {
+                                float2 y[4];
+#pragma unroll
+                                for (int d = 0; d < 4; ++d) y[d] = __fmul2_rn(n[h][d], make_float2(f[i], f[i]));
+                                c[h] = quantize8_f32<kFast>(y, bs);
+                            } else {
+                                c[h] = quantize8_f32<kFast>(n[h], bs);
+                            }
+                        }
+                        if (col < p.H)
+                            *reinterpret_cast<uint4 *>(q + static_cast<int64_t>(r[i]) * p.H) =
+                                make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+                    }
+                };
+                if (__all_sync(0xFFFFFFFFu, fast))
+                    convert(std::true_type{});
+                else
+                    convert(std::false_type{});
+            }
+            if (!again) break;
+            row = row >= 0 ? __ldg(p.next + row) : -1;
+        } while (__any_sync(0xFFFFFFFFu, row >= 0));
+    }
+}
+
 // One CTA per token and 1024 columns, eight columns a thread; the rows of up to four slots
 // are in flight at a time.  Bound by memory: 32768 slots x 7168 take 84 us, 6.2 TB/s; 16384
 // slots x 4096 with k = 2 40 us, 5.1 TB/s (two pieces a thread: 39).
@@ -274,10 +485,36 @@ __global__ void __launch_bounds__(kRowThreads)
 // gather are paid once a run) that still give the SMs about kDispatchWaves CTAs for each of
 // their four places.
 constexpr int64_t kDispatchWaves = 2;
+
 static int dispatch_cols(int64_t row_ctas, int64_t Cb, int num_sms) {
     const int64_t want = (kDispatchWaves * 4 * num_sms + row_ctas - 1) / row_ctas;  // runs per row block
     const int64_t runs = want < 1 ? 1 : (want > Cb ? Cb : want);
     return static_cast<int>((Cb + runs - 1) / runs);
+}
+
+// Bytes of the token form's workspace, 0 where the other form is used: few slots per token
+// (it reads the tokens twice more, the other one k times from L2), or so little work that its
+// two further launches cost more than they save.  Measured, this form against the other: k = 8,
+// H = 7168: 16384 tokens 256 and 362 us, 4096 77 and 88, 1024 32 and 36, 64 29 and 23; H = 2048:
+// 4096 tokens 28 and 28, 1024 19 and 13.  4096 tokens of 7168, k = 4: 62 and 54.
+constexpr int kTokenFormSlots = 8;
+constexpr int64_t kTokenFormWork = (1LL << 26) + 1;  // codes
+int64_t dispatch_workspace(int64_t T, int k, int64_t H, int64_t rows) {
+    const int64_t segs = (H + kTokCols - 1) / kTokCols, Cb8 = (H + 1023) / 1024 * 8;
+    if (k < kTokenFormSlots || T * k * H < kTokenFormWork) return 0;
+    if (T * segs > 0x7FFFFFFFLL || rows / 128 * Cb8 > 0x7FFFFFFFLL) return 0;  // grids
+    return (T * k * 4 + 15) / 16 * 16 + rows * 4 + 16 + T * Cb8 * 2;
+}
+
+template <bool WEIGHTS>
+static dg_status_t launch_token_form(const TokenGather &p, int64_t rows, cudaStream_t stream) {
+    const int n = static_cast<int>((p.T * p.segs + kTokWarps - 1) / kTokWarps);
+    dg_status_t st = launch_pdl(dispatch_tops_kernel<WEIGHTS>, n, kRowThreads, 0, stream, p);
+    if (st != DG_OK) return st;
+    st = launch_pdl(dispatch_scales_kernel<WEIGHTS>, static_cast<int>(rows / 128 * (p.Cb8 / kTopsAhead)), 128, 0, stream, p);
+    if (st != DG_OK) return st;
+    const int m = static_cast<int>((p.T * p.parts + kTokWarps - 1) / kTokWarps);
+    return launch_pdl(dispatch_rows_kernel<WEIGHTS>, m, kRowThreads, 0, stream, p);
 }
 
 template <bool WEIGHTS>
@@ -298,7 +535,18 @@ static dg_status_t launch_dispatch_impl(const void *X, const float *weights, con
 
 dg_status_t launch_dispatch_quantize(const void *X, const float *weights, const int32_t *slot_of_row,
                                      const int32_t *offsets, int64_t slots, int k, int64_t H, int64_t rows, int G,
-                                     uint8_t *Q, float *S, const DeviceInfo &dev, cudaStream_t stream) {
+                                     uint8_t *Q, float *S, void *workspace, const DeviceInfo &dev, cudaStream_t stream) {
+    const int64_t T = slots / k;
+    if (dispatch_workspace(T, k, H, rows) > 0) {
+        const int64_t Cb8 = (H + 1023) / 1024 * 8;
+        const int segs = static_cast<int>((H + kTokCols - 1) / kTokCols);
+        int32_t *head = static_cast<int32_t *>(workspace), *next = head + (slots + 3) / 4 * 4;
+        const TokenGather p = {static_cast<const uint16_t *>(X), weights, slot_of_row, offsets, G, k, T, H,
+                               segs, (segs + kTokRun - 1) / kTokRun, static_cast<int>((H + 127) / 128),
+                               static_cast<int>(Cb8), head, next, next + rows, reinterpret_cast<uint16_t *>(next + rows + 4), Q, S};
+        return weights ? launch_token_form<true>(p, rows, stream)
+                       : launch_token_form<false>(p, rows, stream);
+    }
     return weights ? launch_dispatch_impl<true>(X, weights, slot_of_row, offsets, slots, k, H, rows, G, Q, S, dev, stream)
                    : launch_dispatch_impl<false>(X, weights, slot_of_row, offsets, slots, k, H, rows, G, Q, S, dev,
                                                  stream);

@@ -127,13 +127,12 @@ PyObject *wrap_all(const Ts &...ts) {
 
 constexpr int64_t kIntMax = 0x7FFFFFFF;
 
-// Scratch for one sort: an empty tensor where none is needed.  `stream`: not None when the
-// sort runs on another stream than the one the allocation belongs to.
-Tensor sort_workspace(int64_t T, int64_t k, int64_t G, int dev, PyObject *stream, cudaStream_t handle) {
-    const int64_t bytes = dg_moe_sort_workspace(T, static_cast<int>(k), static_cast<int>(G));
+// Scratch for one call: an empty tensor where none is needed.  `stream`: not None when the
+// call runs on another stream than the one the allocation belongs to.
+Tensor scratch(int64_t bytes, int dev, PyObject *stream, cudaStream_t handle) {
     if (bytes == 0) return Tensor();
     Tensor w = make(kU8, {bytes}, dev);
-    if (stream != Py_None)  // freed at the end of the call, perhaps while that stream still runs the sort
+    if (stream != Py_None)  // freed at the end of the call, perhaps while that stream still runs it
         w.record_stream(c10::cuda::getStreamFromExternal(handle, static_cast<c10::DeviceIndex>(dev)).unwrap());
     return w;
 }
@@ -152,7 +151,7 @@ PyObject *moe_sort(PyObject *, PyObject *const *a, Py_ssize_t) {
     const Tensor row = out(a[3], "row_of_slot", kI32, {T, k}, dev);
     const Tensor slot = out(a[4], "slot_of_row", kI32, {cap}, dev);
     const cudaStream_t st = stream_of(a[5], dev);
-    const Tensor w = sort_workspace(T, k, G, dev, a[5], st);
+    const Tensor w = scratch(dg_moe_sort_workspace(T, static_cast<int>(k), static_cast<int>(G)), dev, a[5], st);
     status(dg_moe_sort(pi, wide, T, static_cast<int>(k), static_cast<int>(G), ptr<int32_t>(offsets), ptr<int32_t>(row),
                        ptr<int32_t>(slot), cap, w.defined() ? w.data_ptr() : nullptr, w.defined() ? w.numel() : 0, st),
            "dg_moe_sort");
@@ -174,7 +173,7 @@ PyObject *moe_sort_masked(PyObject *, PyObject *const *a, Py_ssize_t) {
     const Tensor row = out(a[4], "row_of_slot", kI32, {T, k}, dev);
     const Tensor slot = out(a[5], "slot_of_row", kI32, {G * M_max}, dev);
     const cudaStream_t st = stream_of(a[6], dev);
-    const Tensor w = sort_workspace(T, k, G, dev, a[6], st);
+    const Tensor w = scratch(dg_moe_sort_workspace(T, static_cast<int>(k), static_cast<int>(G)), dev, a[6], st);
     status(dg_moe_sort_masked(pi, wide, T, static_cast<int>(k), static_cast<int>(G), ptr<int32_t>(m), ptr<int32_t>(row),
                               ptr<int32_t>(slot), M_max, w.defined() ? w.data_ptr() : nullptr,
                               w.defined() ? w.numel() : 0, st),
@@ -197,8 +196,11 @@ PyObject *moe_dispatch_quantize(PyObject *, PyObject *const *a, Py_ssize_t) {
     const auto *w = in_or_null<float>(a[4], "weights", kF32, {T, k}, dev);
     const Tensor q = out(a[5], "q", kU8, {cap, H}, dev);
     const Tensor s = out(a[6], "s", kF32, {blocks(cap), blocks(H)}, dev);
+    const cudaStream_t st = stream_of(a[7], dev);
+    const Tensor ws = scratch(dg_moe_dispatch_workspace(T, static_cast<int>(k), H, cap), dev, a[7], st);
     status(dg_moe_dispatch_quantize(px, w, slot, off, T, static_cast<int>(k), H, cap, static_cast<int>(G),
-                                    ptr<uint8_t>(q), ptr<float>(s), stream_of(a[7], dev)),
+                                    ptr<uint8_t>(q), ptr<float>(s), ws.defined() ? ws.data_ptr() : nullptr,
+                                    ws.defined() ? ws.numel() : 0, st),
            "dg_moe_dispatch_quantize");
     return wrap_all(q, s);
     END_HANDLE_TH_ERRORS

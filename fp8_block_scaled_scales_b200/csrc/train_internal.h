@@ -27,10 +27,12 @@ dg_status_t launch_moe_sort(const void *ids, bool ids64, int64_t slots, int G, b
                             int32_t *offsets, int32_t *row_of_slot, int32_t *slot_of_row, int32_t *workspace,
                             cudaStream_t stream);
 
-// moe_rows.cu
+// moe_rows.cu.  workspace: dispatch_workspace bytes.
+int64_t dispatch_workspace(int64_t T, int k, int64_t H, int64_t rows);
 dg_status_t launch_dispatch_quantize(const void *X, const float *weights, const int32_t *slot_of_row,
                                      const int32_t *offsets, int64_t slots, int k, int64_t H, int64_t rows, int G,
-                                     uint8_t *Q, float *S, const DeviceInfo &dev, cudaStream_t stream);
+                                     uint8_t *Q, float *S, void *workspace, const DeviceInfo &dev,
+                                     cudaStream_t stream);
 dg_status_t launch_dispatch_quantize_masked(const void *X, const int32_t *slot_of_row, const int32_t *masked_m,
                                             int64_t slots, int k, int64_t H, int G, int64_t m_max, uint8_t *Q,
                                             float *S, const DeviceInfo &dev, cudaStream_t stream);

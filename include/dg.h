@@ -360,11 +360,15 @@ dg_status_t dg_moe_sort_masked(const void *topk_ids, int ids_64bit, int64_t T, i
  * Q : [M_total_capacity][H] E4M3 out, 16-byte aligned.
  * S : [M_total_capacity/128][ceil(H/128)] FP32 out.
  * H % 16 == 0, H < 2^31, M_total_capacity % 128 == 0.  M_total_capacity == 0 or H == 0 is a no-op.
+ * workspace : device scratch of at least dg_moe_dispatch_workspace bytes, 16-byte aligned; may be null when
+ *             that is 0 (small calls, few slots per token).  Not shared with a call that may run at the same time.
  */
 dg_status_t dg_moe_dispatch_quantize(const void *X_bf16, const float *weights,
                                      const int32_t *slot_of_row, const int32_t *group_offsets,
                                      int64_t T, int k, int64_t H, int64_t M_total_capacity, int G,
-                                     uint8_t *Q, float *S, cudaStream_t stream);
+                                     uint8_t *Q, float *S, void *workspace, int64_t workspace_bytes,
+                                     cudaStream_t stream);
+int64_t dg_moe_dispatch_workspace(int64_t T, int k, int64_t H, int64_t M_total_capacity);
 
 /*
  * The same into the masked layout, as dg_quantize_blockwise_masked quantizes each slab: only

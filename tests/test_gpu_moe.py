@@ -193,6 +193,121 @@ def test_dispatch_every_bf16_pattern_under_a_scale_sweep():
     assert torch.equal(q[:T], wq)
 
 
+def dispatch_slot_by_slot(x, slot, off, k, weights=None):
+    """The same gather with every slot a token of its own: k = 1, the form that reads rows once a slot."""
+    w = None if weights is None else weights.reshape(-1, 1)
+    return binding.moe_dispatch_quantize(x.repeat_interleave(k, 0), slot, off, 1, weights=w)
+
+
+def assert_same_codes(got, want, off):
+    used = int(off[-1])
+    (q, s), (wq, ws) = got, want
+    assert torch.equal(s[:used // 128].nan_to_num(nan=-1.0), ws[:used // 128].nan_to_num(nan=-1.0))
+    assert torch.equal(q[:used], wq[:used])
+
+
+# more than 2^26 codes and eight slots a token or more: gathered token by token
+TOKEN_FORM = [(2100, 8, 64, 4112), (1030, 9, 5, 7440), (600, 20, 300, 8192), (65, 70, 128, 16400)]
+
+
+@pytest.mark.parametrize("T,k,G,H", TOKEN_FORM)
+@pytest.mark.parametrize("weighted", [False, True])
+def test_dispatch_token_by_token(T, k, G, H, weighted):
+    """Odd columns, dropped slots, experts without tokens, more slots than the eight of one step; blocks of zeros,
+    of very small and of very large values; rows past the last expert stay as they were."""
+    assert binding.lib().dg_moe_dispatch_workspace(T, k, H, plain.cap_of(T, k, G)) > 0
+    assert binding.lib().dg_moe_dispatch_workspace(T * k, 1, H, plain.cap_of(T, k, G)) == 0
+    g = torch.Generator().manual_seed(T)
+    ids = torch.stack([torch.randperm(G, generator=g)[:k] if k <= G else torch.randint(0, G, (k,), generator=g)
+                       for _ in range(T)]).int()
+    ids[::7, 1] = -1
+    ids[ids == 3] = 4 % G  # expert 3 stays without tokens
+    x = tokens(T, H, T + 1)
+    x[:, 256:384] = 0
+    x[:, 128:256] *= 1e-36
+    x[: T // 2, 384:512] *= 1e36
+    x = x.cuda()
+    w = torch.randn((T, k), generator=g).cuda() if weighted else None
+    if weighted:
+        w[::5, 0], w[1::5, 1] = 0.0, 1e-30
+    off, row, slot = binding.moe_sort(ids.cuda(), G)
+    cap = slot.numel()
+    assert int(off[-1]) < cap
+    q = torch.full((cap, H), 0xA5, dtype=torch.uint8, device="cuda")
+    s = torch.full((cap // 128, -(-H // 128)), -3.0, device="cuda")
+    binding.moe_dispatch_quantize(x, slot, off, k, weights=w, q=q, s=s)
+    assert_same_codes((q, s), dispatch_slot_by_slot(x, slot, off, k, w), off)
+    used = int(off[-1])
+    assert bool((q[used:] == 0xA5).all()) and bool((s[used // 128:] == -3.0).all())
+    # against the definition, in a few row blocks
+    slots = slot.cpu().numpy()
+    for b in {0, used // 256, used // 128 - 1}:
+        v = gathered(x.cpu(), slots[b * 128:(b + 1) * 128], k, None if w is None else w.cpu())
+        wq, ws = plain.quantize_f32(v)
+        assert torch.equal(s[b].cpu(), ws[0]) and torch.equal(q[b * 128:(b + 1) * 128].cpu(), wq)
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_dispatch_token_by_token_non_finite(weighted):
+    """Blocks with NaN or infinite values or weights, the rows without a token in them included."""
+    T, k, G, H = 1100, 8, 11, 7696
+    x = tokens(T, H, 51).cuda()
+    x[5, 10], x[200, 300], x[700, 7690] = float("nan"), float("inf"), -float("inf")
+    w = torch.randn((T, k), generator=torch.Generator().manual_seed(52)).cuda() if weighted else None
+    if weighted:
+        w[3, 0], w[4, 1], w[20, 0] = float("inf"), -float("inf"), float("nan")
+        x[3, 130:140], x[4, 256:384] = 0.0, 0.0
+    off, row, slot = binding.moe_sort(route(T, k, G, 53).cuda(), G)
+    got, want = binding.moe_dispatch_quantize(x, slot, off, k, weights=w), dispatch_slot_by_slot(x, slot, off, k, w)
+    used = int(off[-1])
+    bad = ~torch.isfinite(got[1][:used // 128])
+    assert bool(bad.any()) and not bool(bad.all())
+    assert_same_codes(got, want, off)
+
+
+def test_dispatch_token_by_token_with_repeated_slots():
+    """A row map of a caller's own, where slots stand in several rows, in none, or out of range."""
+    T, k, H, cap = 1100, 8, 8208, 8960
+    x = tokens(T, H, 61).cuda()
+    g = torch.Generator().manual_seed(62)
+    slot = torch.randint(-5, T * k + 5, (cap,), generator=g).int()
+    slot[1000:1200] = 17
+    slot[-128:] = -1
+    slot, off = slot.cuda(), torch.tensor([0, 128, cap], dtype=torch.int32, device="cuda")
+    w = torch.randn((T, k), generator=g).cuda()
+    for weights in (None, w):
+        assert_same_codes(binding.moe_dispatch_quantize(x, slot, off, k, weights=weights),
+                          dispatch_slot_by_slot(x, slot, off, k, weights), off)
+
+
+def test_dispatch_token_by_token_streams_and_graph():
+    """Two calls at once on their own streams, and a captured call replayed on new tokens and routes."""
+    T, k, G, H = 1100, 8, 16, 7696
+    sets = []
+    for i in range(3):
+        x = tokens(T, H, 71 + i).cuda()
+        sets.append((x, *binding.moe_sort(route(T, k, G, 81 + i).cuda(), G)))
+    want = [dispatch_slot_by_slot(x, slot, off, k) for x, off, row, slot in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [binding.moe_dispatch_quantize(x, slot, off, k, stream=st) for st, (x, off, row, slot) in zip(streams, sets)]
+    torch.cuda.synchronize()
+    for a, b, (x, off, row, slot) in zip(got, want, sets):
+        assert_same_codes(a, b, off)
+    x, off, slot = (t.clone() for t in (sets[0][0], sets[0][1], sets[0][3]))
+    q, s = binding.moe_dispatch_quantize(x, slot, off, k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.moe_dispatch_quantize(x, slot, off, k, q=q, s=s)
+    for i in (2, 1):
+        for dst, src in zip((x, off, slot), (sets[i][0], sets[i][1], sets[i][3])):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_same_codes((q, s), want[i], off)
+
+
 def test_dispatch_weights_of_both_signs_and_zero():
     """Negative and zero weights: magnitudes enter the scale, zeros keep the product's sign."""
     T, k, G, H = 50, 2, 3, 384

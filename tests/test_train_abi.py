@@ -63,16 +63,24 @@ def test_capacity_helper_is_the_least_the_sort_takes(lib):
 
 def test_dispatch_refusals(lib):
     f = lib.dg_moe_dispatch_quantize
-    assert f(P, NULL, P, P, 8, 2, 24, 128, 4, P, P, NULL) == SHAPE     # H % 16
-    assert f(P, NULL, P, P, 8, 2, 32, 100, 4, P, P, NULL) == SHAPE     # capacity % 128
-    assert f(P, NULL, P, P, 8, 2, 32, 128, 0, P, P, NULL) == SHAPE
-    assert f(P, NULL, P, P, -1, 2, 32, 128, 4, P, P, NULL) == SHAPE
-    assert f(NULL, NULL, NULL, NULL, 8, 2, 32, 0, 4, NULL, NULL, NULL) == OK
-    assert f(NULL, NULL, NULL, NULL, 8, 2, 0, 128, 4, NULL, NULL, NULL) == OK
-    assert f(P, NULL, NULL, P, 8, 2, 32, 128, 4, P, P, NULL) == ARG
-    assert f(NULL, NULL, P, P, 8, 2, 32, 128, 4, P, P, NULL) == ARG
-    assert f(ODD, NULL, P, P, 8, 2, 32, 128, 4, P, P, NULL) == ALIGN
-    assert f(P, ODD, P, P, 8, 2, 32, 128, 4, P, P, NULL) == ALIGN
+    assert f(P, NULL, P, P, 8, 2, 24, 128, 4, P, P, NULL, 0, NULL) == SHAPE     # H % 16
+    assert f(P, NULL, P, P, 8, 2, 32, 100, 4, P, P, NULL, 0, NULL) == SHAPE     # capacity % 128
+    assert f(P, NULL, P, P, 8, 2, 32, 128, 0, P, P, NULL, 0, NULL) == SHAPE
+    assert f(P, NULL, P, P, -1, 2, 32, 128, 4, P, P, NULL, 0, NULL) == SHAPE
+    assert f(NULL, NULL, NULL, NULL, 8, 2, 32, 0, 4, NULL, NULL, NULL, 0, NULL) == OK
+    assert f(NULL, NULL, NULL, NULL, 8, 2, 0, 128, 4, NULL, NULL, NULL, 0, NULL) == OK
+    assert f(P, NULL, NULL, P, 8, 2, 32, 128, 4, P, P, NULL, 0, NULL) == ARG
+    assert f(NULL, NULL, P, P, 8, 2, 32, 128, 4, P, P, NULL, 0, NULL) == ARG
+    assert f(ODD, NULL, P, P, 8, 2, 32, 128, 4, P, P, NULL, 0, NULL) == ALIGN
+    assert f(P, ODD, P, P, 8, 2, 32, 128, 4, P, P, NULL, 0, NULL) == ALIGN
+    # many slots a token: a workspace of the size that the library names
+    cap = binding.moe_capacity(4096, 8, 64)
+    need = lib.dg_moe_dispatch_workspace(4096, 8, 7168, cap)
+    assert need >= 4096 * 8 * 4 + cap * 4 + 4096 * 56 * 2 and lib.dg_moe_dispatch_workspace(64, 2, 7168, cap) == 0
+    assert lib.dg_moe_dispatch_workspace(-1, 8, 7168, cap) == lib.dg_moe_dispatch_workspace(4096, 8, 7160, cap) == 0
+    assert f(P, NULL, P, P, 4096, 8, 7168, cap, 64, P, P, NULL, need, NULL) == ARG
+    assert f(P, NULL, P, P, 4096, 8, 7168, cap, 64, P, P, P, need - 1, NULL) == ARG
+    assert f(P, NULL, P, P, 4096, 8, 7168, cap, 64, P, P, ODD, need, NULL) == ALIGN
     m = lib.dg_moe_dispatch_quantize_masked
     assert m(P, P, P, 8, 2, 24, 4, 64, P, P, NULL) == SHAPE
     assert m(P, P, P, 8, 2, 32, 1025, 64, P, P, NULL) == SHAPE
@@ -147,7 +155,7 @@ def test_gradient_product_refusals(lib):
 def test_sizes_beyond_the_index_ranges_are_refused(lib):
     """Widths and products of sizes that 32 or 64 bits do not hold: refused before any of them is computed with."""
     for H in (1 << 31, 1 << 53, (1 << 63) - 16):
-        assert lib.dg_moe_dispatch_quantize(P, NULL, P, P, 8, 2, H, 128, 4, P, P, NULL) == SHAPE
+        assert lib.dg_moe_dispatch_quantize(P, NULL, P, P, 8, 2, H, 128, 4, P, P, NULL, 0, NULL) == SHAPE
         assert lib.dg_moe_dispatch_quantize_masked(P, P, P, 8, 2, H, 4, 64, P, P, NULL) == SHAPE
         assert lib.dg_moe_combine(P, P, P, 1 << 29, 2, H, 128, P, NULL) == SHAPE
         assert lib.dg_moe_combine_backward(P, P, P, 8, 2, H, 128, P, NULL) == SHAPE
