@@ -36,6 +36,7 @@ struct DispatchSmem {
     uint4 piece[8][kRowThreads];
     int tok[128];
     float wgt[128];
+    int groups[4];  // per 32 rows: groups of 16 rows, counted from row 0, up to the last with a token
     alignas(16) uint32_t red[2][kRowThreads / 32];
 };
 
@@ -58,92 +59,114 @@ __device__ __forceinline__ void dispatch_rows(const uint16_t *__restrict__ X, co
             sm.wgt[tid] = w;
             infinite = isinf(w);
         }
+        const uint32_t used = __ballot_sync(0xFFFFFFFFu, ok);
+        if ((tid & 31) == 0) sm.groups[tid >> 5] = used ? (tid + 31 - __clz(used)) / 16 + 1 : 0;
     }
     infinite = __syncthreads_or(infinite);  // some row's weight is
-    // a row without a token: its pieces stay zero
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (sm.tok[sub + 16 * i] < 0) sm.piece[i][tid] = make_uint4(0, 0, 0, 0);
-
-    auto ask = [&](int bc) {
-        const int64_t col = static_cast<int64_t>(bc) * 128 + lane_col;
-        if (col < H) {  // H % 16 == 0: an 8-column piece is whole or absent
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int t = sm.tok[sub + 16 * i];
-                if (t >= 0) {
-                    const uint16_t *p = X + static_cast<int64_t>(t) * Hi + col;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.piece[i][tid])), "l"(p)
-                                 : "memory");
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sm.piece[i][tid] = make_uint4(0, 0, 0, 0);
-        }
-    };
-
-    ask(bc0);
-    uint8_t *qp = Q + (row0 + sub) * H + static_cast<int64_t>(bc0) * 128 + lane_col;
+    const int groups = max(max(sm.groups[0], sm.groups[1]), max(sm.groups[2], sm.groups[3]));
+    uint8_t *const q0 = Q + (row0 + sub) * H + lane_col;
     const int64_t step = 16 * H;
-    for (int bc = bc0; bc < bc1; ++bc, qp += 128) {
-        const bool col_ok = static_cast<int64_t>(bc) * 128 + lane_col < H;
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        uint4 v[8];
+
+    // ALL: every group of rows has a token.  Otherwise the groups past the last one are
+    // neither read nor converted (a decode step's blocks are mostly empty).
+    auto walk = [&](auto all) {
+        constexpr bool kAll = decltype(all)::value;
+        // a row without a token: its pieces stay zero
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = sm.piece[i][tid];
-        if (bc + 1 < bc1) ask(bc + 1);
-        uint32_t m;
-        if (WEIGHTS) {
-            // the largest |fl32(w x)| of a row's piece is that of its largest |x|
-            float f = 0.0f;
+        for (int i = 0; i < 8; ++i)
+            if (sm.tok[sub + 16 * i] < 0) sm.piece[i][tid] = make_uint4(0, 0, 0, 0);
+
+        auto ask = [&](int bc) {
+            const int64_t col = static_cast<int64_t>(bc) * 128 + lane_col;
+            if (col < H) {  // H % 16 == 0: an 8-column piece is whole or absent
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float a = __uint_as_float(amax_bits_of(amax_pair8(v[i])) << 16);
-                const float b = __uint_as_float(amax_bits_of(amax_pair8(v[i + 1])) << 16);
-                f = amax3(f, make_float2(a * sm.wgt[sub + 16 * i], b * sm.wgt[sub + 16 * (i + 1)]));
-            }
-            if (__builtin_expect(infinite, 0)) {  // then a zero among the row's columns is a NaN
-                f = col_ok ? f : 0.0f;            // and there is none past the last column
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (col_ok && isinf(sm.wgt[sub + 16 * i]) && has_zero8(v[i])) f = __int_as_float(0x7FFFFFFF);
-            }
-            m = __float_as_uint(f);
-        } else {
-            uint32_t m2 = amax_pair8(v[0]);
-#pragma unroll
-            for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, amax_pair8(v[i]));
-            m = amax_bits_of(m2) << 16;  // the maximum's FP32 bits
-        }
-        m = cta_max<kRowThreads / 32>(m, sm.red[bc & 1]);
-        const FastScale bs = fast_scale(__uint_as_float(m));
-        if (tid == 0) S[bc] = bs.s;
-        auto convert = [&](auto fast) {
-            constexpr bool kFast = decltype(fast)::value;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint2 q;
-                if (WEIGHTS) {
-                    const float w = sm.wgt[sub + 16 * i];
-                    float2 x[4];
-                    bf16x8_to_f32(v[i], x);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], make_float2(w, w));
-                    q = quantize8_f32<kFast>(x, bs);
-                } else {
-                    q = quantize8_bf16<kFast>(v[i], bs);
+                for (int i = 0; i < 8; ++i) {
+                    if (!kAll && i >= groups) break;
+                    const int t = sm.tok[sub + 16 * i];
+                    if (t >= 0) {
+                        const uint16_t *p = X + static_cast<int64_t>(t) * Hi + col;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.piece[i][tid])), "l"(p)
+                                     : "memory");
+                    }
                 }
-                if (sub + 16 * i < rows) *reinterpret_cast<uint2 *>(qp + i * step) = q;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sm.piece[i][tid] = make_uint4(0, 0, 0, 0);
             }
         };
-        if (col_ok) {
-            if (__builtin_expect(bs.fast, 1))
-                convert(std::true_type{});
-            else
-                convert(std::false_type{});
+
+        ask(bc0);
+        uint8_t *qp = q0 + static_cast<int64_t>(bc0) * 128;
+        for (int bc = bc0; bc < bc1; ++bc, qp += 128) {
+            const bool col_ok = static_cast<int64_t>(bc) * 128 + lane_col < H;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = kAll || i < groups ? sm.piece[i][tid] : make_uint4(0, 0, 0, 0);
+            if (bc + 1 < bc1) ask(bc + 1);
+            uint32_t m;
+            if (WEIGHTS) {
+                // the largest |fl32(w x)| of a row's piece is that of its largest |x|
+                float f = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    if (!kAll && i >= groups) break;
+                    const float a = __uint_as_float(amax_bits_of(amax_pair8(v[i])) << 16);
+                    const float b = __uint_as_float(amax_bits_of(amax_pair8(v[i + 1])) << 16);
+                    f = amax3(f, make_float2(a * sm.wgt[sub + 16 * i], b * sm.wgt[sub + 16 * (i + 1)]));
+                }
+                if (__builtin_expect(infinite, 0)) {  // then a zero among the row's columns is a NaN
+                    f = col_ok ? f : 0.0f;            // and there is none past the last column
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (col_ok && isinf(sm.wgt[sub + 16 * i]) && has_zero8(v[i])) f = __int_as_float(0x7FFFFFFF);
+                }
+                m = __float_as_uint(f);
+            } else {
+                uint32_t m2 = amax_pair8(v[0]);
+#pragma unroll
+                for (int i = 1; i < 8; ++i) {
+                    if (!kAll && i >= groups) break;
+                    m2 = __vmaxu2(m2, amax_pair8(v[i]));
+                }
+                m = amax_bits_of(m2) << 16;  // the maximum's FP32 bits
+            }
+            m = cta_max<kRowThreads / 32>(m, sm.red[bc & 1]);
+            const FastScale bs = fast_scale(__uint_as_float(m));
+            if (tid == 0) S[bc] = bs.s;
+            const uint32_t none = isnan(bs.s) ? 0x7F7F7F7Fu : 0u;  // four codes of a row without a token
+            auto convert = [&](auto fast) {
+                constexpr bool kFast = decltype(fast)::value;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint2 q = make_uint2(none, none);
+                    if (kAll || i < groups) {
+                        if (WEIGHTS) {
+                            const float w = sm.wgt[sub + 16 * i];
+                            float2 x[4];
+                            bf16x8_to_f32(v[i], x);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], make_float2(w, w));
+                            q = quantize8_f32<kFast>(x, bs);
+                        } else {
+                            q = quantize8_bf16<kFast>(v[i], bs);
+                        }
+                    }
+                    if (sub + 16 * i < rows) *reinterpret_cast<uint2 *>(qp + i * step) = q;
+                }
+            };
+            if (col_ok) {
+                if (__builtin_expect(bs.fast, 1))
+                    convert(std::true_type{});
+                else
+                    convert(std::false_type{});
+            }
         }
-    }
+    };
+    if (groups == 8)
+        walk(std::true_type{});
+    else
+        walk(std::false_type{});
 }
 
 // How the column blocks are cut: CTA (chunk, row block), row block fastest, takes column
@@ -485,9 +508,10 @@ __global__ void __launch_bounds__(kRowThreads)
 // gather are paid once a run) that still give the SMs about kDispatchWaves CTAs for each of
 // their four places.
 constexpr int64_t kDispatchWaves = 2;
+constexpr int64_t kDispatchMaskedWaves = 2;
 
-static int dispatch_cols(int64_t row_ctas, int64_t Cb, int num_sms) {
-    const int64_t want = (kDispatchWaves * 4 * num_sms + row_ctas - 1) / row_ctas;  // runs per row block
+static int dispatch_cols(int64_t row_ctas, int64_t Cb, int num_sms, int64_t waves) {
+    const int64_t want = (waves * 4 * num_sms + row_ctas - 1) / row_ctas;  // runs per row block
     const int64_t runs = want < 1 ? 1 : (want > Cb ? Cb : want);
     return static_cast<int>((Cb + runs - 1) / runs);
 }
@@ -525,7 +549,7 @@ static dg_status_t launch_dispatch_impl(const void *X, const float *weights, con
     const dg_status_t st = allow_smem(dispatch_kernel<WEIGHTS>, sizeof(DispatchSmem), configured_device);
     if (st != DG_OK) return st;
     const int64_t Cb = (H + 127) / 128, Rb = rows / 128;
-    const int cols = dispatch_cols(Rb, Cb, dev.num_sms);
+    const int cols = dispatch_cols(Rb, Cb, dev.num_sms, kDispatchWaves);
     const int64_t n = (Cb + cols - 1) / cols * Rb;
     if (n > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
     return launch_pdl(dispatch_kernel<WEIGHTS>, static_cast<int>(n), kRowThreads, sizeof(DispatchSmem), stream,
@@ -563,7 +587,7 @@ dg_status_t launch_dispatch_quantize_masked(const void *X, const int32_t *slot_o
     if (st != DG_OK) return st;
     const int64_t Rb = (m_max + 127) / 128, Cb = (H + 127) / 128;
     const int64_t Ry = Rb < kDispatchMaskedRowCtas ? Rb : kDispatchMaskedRowCtas;
-    const int cols = dispatch_cols(G * Ry, Cb, dev.num_sms);
+    const int cols = dispatch_cols(G * Ry, Cb, dev.num_sms, kDispatchMaskedWaves);
     const int64_t n = (Cb + cols - 1) / cols * G * Ry;
     if (n > 0x7FFFFFFFLL) return DG_ERR_SHAPE;
     return launch_pdl(dispatch_masked_kernel, static_cast<int>(n), kRowThreads, sizeof(DispatchSmem), stream,
