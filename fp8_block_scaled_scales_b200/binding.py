@@ -32,7 +32,8 @@ EXPORTS = ("dg_quantize_blockwise", "dg_quantize_blockwise_masked", "dg_fp8_gemm
            "dg_version", "dg_test_set_kernel_control",
            "dg_moe_sort", "dg_moe_sort_masked", "dg_moe_sort_workspace", "dg_moe_dispatch_quantize", "dg_moe_dispatch_workspace", "dg_moe_dispatch_quantize_masked",
            "dg_moe_combine", "dg_moe_combine_backward", "dg_swiglu_quantize", "dg_swiglu_quantize_masked",
-           "dg_swiglu_quantize_backward", "dg_fp8_dgrad_blockscaled", "dg_fp8_wgrad_blockscaled",
+           "dg_swiglu_quantize_backward", "dg_fp8_dgrad_blockscaled", "dg_fp8_dgrad_workspace", "dg_fp8_wgrad_blockscaled",
+           "dg_fp8_wgrad_workspace",
            "dg_fp8_grouped_dgrad_contiguous", "dg_fp8_grouped_wgrad_contiguous")
 
 
@@ -83,14 +84,16 @@ def lib() -> ctypes.CDLL:
     L.dg_swiglu_quantize.argtypes = [vp, vp, i32, i64, i64, vp, vp, vp, vp, vp]
     L.dg_swiglu_quantize_masked.argtypes = [vp, vp, i32, i64, i64, vp, vp, vp]
     L.dg_swiglu_quantize_backward.argtypes = [vp, vp, vp, vp, i32, i64, i64, vp, vp, vp]
-    L.dg_fp8_dgrad_blockscaled.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp]
-    L.dg_fp8_wgrad_blockscaled.argtypes = [vp, vp, vp, vp, vp, i32, i32, i64, i64, i64, vp]
+    L.dg_fp8_dgrad_blockscaled.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+    L.dg_fp8_wgrad_blockscaled.argtypes = [vp, vp, vp, vp, vp, i32, i32, i64, i64, i64, vp, i64, vp]
+    L.dg_fp8_dgrad_workspace.argtypes = L.dg_fp8_wgrad_workspace.argtypes = [i64, i64, i64]
     L.dg_fp8_grouped_dgrad_contiguous.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, vp]
     L.dg_fp8_grouped_wgrad_contiguous.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, i64, i32, i64, i64, vp]
     for f in EXPORTS:
         if f.startswith(("dg_moe_", "dg_swiglu_")) or "grad" in f:
             getattr(L, f).restype = ctypes.c_int
-    L.dg_moe_sort_workspace.restype = L.dg_moe_dispatch_workspace.restype = i64
+    for f in (L.dg_moe_sort_workspace, L.dg_moe_dispatch_workspace, L.dg_fp8_dgrad_workspace, L.dg_fp8_wgrad_workspace):
+        f.restype = i64
     L.dg_get_last_device_status.argtypes = [vp]
     L.dg_status_string.restype = ctypes.c_char_p
     L.dg_status_string.argtypes = [ctypes.c_int]

@@ -188,17 +188,35 @@ static dg_status_t check_grad(const void *dY, const float *sdY, const void *B, c
     return DG_OK;
 }
 
+static bool bad_grad_sizes(int64_t M, int64_t N, int64_t K) {
+    return M < 0 || N < 0 || K < 0 || N % 16 != 0 || K % 16 != 0 || M > kInt32Max || N > kInt32Max || K > kInt32Max;
+}
+
+int64_t dg_fp8_dgrad_workspace(int64_t M, int64_t N, int64_t K) {
+    return bad_grad_sizes(M, N, K) || M == 0 || N == 0 || K == 0 ? 0 : grad_workspace(false, M, N, K);
+}
+
+int64_t dg_fp8_wgrad_workspace(int64_t M, int64_t N, int64_t K) {
+    return bad_grad_sizes(M, N, K) || M == 0 || N == 0 || K == 0 ? 0 : grad_workspace(true, M, N, K);
+}
+
+static dg_status_t check_workspace(int64_t need, const void *workspace, int64_t bytes) {
+    if ((need > 0 && !workspace) || bytes < need) return DG_ERR_INVALID_ARG;
+    return aligned(workspace, 16) ? DG_OK : DG_ERR_ALIGNMENT;
+}
+
 dg_status_t dg_fp8_dgrad_blockscaled(const uint8_t *dY, const float *sdY, const uint8_t *W, const float *sW,
-                                     void *dX_bf16, int64_t M, int64_t N, int64_t K, cudaStream_t stream) {
-    if (M < 0 || K < 0 || N <= 0 || N % 16 != 0 || K % 16 != 0) return DG_ERR_SHAPE;
-    if (M > kInt32Max || N > kInt32Max || K > kInt32Max) return DG_ERR_SHAPE;
+                                     void *dX_bf16, int64_t M, int64_t N, int64_t K, void *workspace,
+                                     int64_t workspace_bytes, cudaStream_t stream) {
+    if (bad_grad_sizes(M, N, K) || N == 0) return DG_ERR_SHAPE;
     if (M == 0 || K == 0) return DG_OK;
     dg_status_t st = check_grad(dY, sdY, W, sW, dX_bf16);
+    if (st == DG_OK) st = check_workspace(dg_fp8_dgrad_workspace(M, N, K), workspace, workspace_bytes);
     if (st != DG_OK) return st;
     DeviceInfo dev;
     st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
-    const GradArgs a = {dY, sdY, W, sW, dX_bf16, nullptr, M, N, K, 1, false, false};
+    const GradArgs a = {dY, sdY, W, sW, dX_bf16, nullptr, M, N, K, 1, false, false, workspace};
     return launch_dgrad(a, dev, stream);
 }
 
@@ -217,7 +235,7 @@ dg_status_t dg_fp8_grouped_dgrad_contiguous(const uint8_t *dY, const float *sdY,
     DeviceInfo dev;
     st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
-    const GradArgs a = {dY, sdY, W, sW, dX_bf16, group_offsets, M_total_capacity, N, K, G, false, false};
+    const GradArgs a = {dY, sdY, W, sW, dX_bf16, group_offsets, M_total_capacity, N, K, G, false, false, nullptr};
     return launch_dgrad(a, dev, stream);
 }
 
@@ -230,20 +248,20 @@ static dg_status_t wgrad_of_nothing(void *dW, int64_t elements, int out_fp32, in
 }
 
 dg_status_t dg_fp8_wgrad_blockscaled(const uint8_t *dY, const float *sdY, const uint8_t *X, const float *sX, void *dW,
-                                     int out_fp32, int accumulate, int64_t M, int64_t N, int64_t K,
-                                     cudaStream_t stream) {
-    if (M < 0 || N < 0 || K < 0 || N % 16 != 0 || K % 16 != 0) return DG_ERR_SHAPE;
-    if (M > kInt32Max || N > kInt32Max || K > kInt32Max) return DG_ERR_SHAPE;
+                                     int out_fp32, int accumulate, int64_t M, int64_t N, int64_t K, void *workspace,
+                                     int64_t workspace_bytes, cudaStream_t stream) {
+    if (bad_grad_sizes(M, N, K)) return DG_ERR_SHAPE;
     if (accumulate && !out_fp32) return DG_ERR_INVALID_ARG;
     if (N == 0 || K == 0) return DG_OK;
     dg_status_t st = M == 0 ? (dW ? (aligned(dW, 16) ? DG_OK : DG_ERR_ALIGNMENT) : DG_ERR_INVALID_ARG)
                             : check_grad(dY, sdY, X, sX, dW);
+    if (st == DG_OK) st = check_workspace(dg_fp8_wgrad_workspace(M, N, K), workspace, workspace_bytes);
     if (st != DG_OK) return st;
     DeviceInfo dev;
     st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
     if (M == 0) return wgrad_of_nothing(dW, N * K, out_fp32, accumulate, stream);
-    const GradArgs a = {dY, sdY, X, sX, dW, nullptr, M, N, K, 1, out_fp32 != 0, accumulate != 0};
+    const GradArgs a = {dY, sdY, X, sX, dW, nullptr, M, N, K, 1, out_fp32 != 0, accumulate != 0, workspace};
     return launch_wgrad(a, dev, stream);
 }
 
@@ -266,7 +284,7 @@ dg_status_t dg_fp8_grouped_wgrad_contiguous(const uint8_t *dY, const float *sdY,
     st = current_device(&dev, nullptr);
     if (st != DG_OK) return st;
     if (M_total_capacity == 0) return wgrad_of_nothing(dW, G * N * K, out_fp32, accumulate, stream);
-    const GradArgs a = {dY, sdY, X, sX, dW, group_offsets, M_total_capacity, N, K, G, out_fp32 != 0, accumulate != 0};
+    const GradArgs a = {dY, sdY, X, sX, dW, group_offsets, M_total_capacity, N, K, G, out_fp32 != 0, accumulate != 0, nullptr};
     return launch_wgrad(a, dev, stream);
 }
 

@@ -46,6 +46,9 @@ struct GradParams {
     int Nb, Kc;    // ceil(N/128), ceil(K/128)
     int num_m;     // dgrad: m-blocks of the allocation; wgrad: row tiles of one expert's dW
     int num_k;     // 256-column tiles of the output
+    int splits;    // parts of the contraction, each with an output of its own
+    int c_rows;    // output rows from one part (wgrad: and expert) to the next
+    int c_end;     // rows of the output in all
     int accumulate;
     uint64_t timeout_ns;
     int *status;
@@ -147,7 +150,7 @@ static_assert(sizeof(UnitEntry) == kGradUnitBytes, "table size");
 // One unit of work: a 128 x 256 output tile or a 128 x 128 half of one.
 struct GradUnit {
     int blocks;    // 128-deep blocks of the contraction
-    int a_row, a_col, a_step_row;  // TMA coordinates of dY at block 0; block i adds 128 * i to the row or the column
+    int a_row, a_col;  // TMA coordinates of dY at block 0; block i adds 128 * i to the row or the column
     int b_row, b_col;              // of B; block i adds 128 * i to the row
     int c_row, c_col;              // of the output
     bool narrow;                   // 128 columns only
@@ -164,6 +167,9 @@ __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, int num_m, in
     GradUnit u;
     int g = 0, mb, kt;
     if (MODE == kDgrad) {
+        const int per = num_m * p.num_k, part = t / per;
+        t -= part * per;
+        const int b0 = p.Nb * part / p.splits;
         // m-block fastest inside raster groups, so that a group's tiles of W are read from L2
         const int kRaster = grad_raster(p);
         const int group = t / (kRaster * p.num_k);
@@ -180,18 +186,20 @@ __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, int num_m, in
             }
             g = lo;
         }
-        u.blocks = p.Nb;
+        u.blocks = p.Nb * (part + 1) / p.splits - b0;
         u.a_row = mb * 128;
-        u.a_col = 0;
-        u.b_row = g * p.N;
-        u.c_row = mb * 128;
-        u.sa_at = mb * p.Nb;
-        u.sb_row = g * p.Nb;
+        u.a_col = b0 * 128;
+        u.b_row = g * p.N + b0 * 128;
+        u.c_row = part * p.c_rows + mb * 128;
+        u.sa_at = mb * p.Nb + b0;
+        u.sb_row = g * p.Nb + b0;
     } else {
         const int kRaster = grad_raster(p);
         const int per = p.num_m * p.num_k;
-        g = t / per;
-        t -= g * per;
+        const int slice = t / per;  // part of an expert's rows
+        t -= slice * per;
+        g = slice / p.splits;
+        const int part = slice - g * p.splits;
         const int group = t / (kRaster * p.num_k);
         const int first = group * kRaster;
         const int gm = min(kRaster, p.num_m - first);
@@ -200,13 +208,14 @@ __device__ __forceinline__ GradUnit grad_unit(const GradParams &p, int num_m, in
         kt = local / gm;
         const int m0 = p.offsets ? __ldg(p.offsets + g) : 0;
         const int m1 = p.offsets ? __ldg(p.offsets + g + 1) : p.cap;
-        u.blocks = (m1 - m0 + 127) / 128;
-        u.a_row = m0;
+        const int blocks = (m1 - m0 + 127) / 128, b0 = blocks * part / p.splits;
+        u.blocks = blocks * (part + 1) / p.splits - b0;
+        u.a_row = m0 + b0 * 128;
         u.a_col = mb * 128;
-        u.b_row = m0;
-        u.c_row = g * p.N + mb * 128;
-        u.sa_at = m0 / 128 * p.Nb + mb;
-        u.sb_row = m0 / 128;
+        u.b_row = u.a_row;
+        u.c_row = slice * p.c_rows + mb * 128;
+        u.sa_at = (m0 / 128 + b0) * p.Nb + mb;
+        u.sb_row = m0 / 128 + b0;
     }
     const int col = kt * 256 + (h > 0 ? 128 : 0);
     u.narrow = h >= 0 || col + 128 >= p.K;
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
 
     const int num_m = MODE == kDgrad && p.offsets ? __ldg(p.offsets + p.G) / 128 : p.num_m;
-    const int num_tiles = *groups_bad ? 0 : (MODE == kWgrad ? p.G : 1) * num_m * p.num_k;
+    const int num_tiles = *groups_bad ? 0 : (MODE == kWgrad ? p.G : 1) * p.splits * num_m * p.num_k;
     // a last round that would keep at most half the CTAs busy runs as half tiles
     const int grid = static_cast<int>(gridDim.x);
     int tiles_wide = num_tiles, num_units = num_tiles;
@@ -329,7 +338,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                             mbar_arrive_expect_tx(&full[bar], L::kABytes);
                             uint8_t *dst = smem + L::kOffA + s * L::kABytes;
                             if (MODE == kDgrad)
-                                tma_load_2d(dst, &tmA, &full[bar], i * 128, u.a_row);
+                                tma_load_2d(dst, &tmA, &full[bar], u.a_col + i * 128, u.a_row);
                             else
                                 tma_load_2d(dst, &tmA, &full[bar], u.a_col, u.a_row + i * 128);
                         } else {
@@ -476,7 +485,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             // rows c_row + 32 * quarter + lane; one box of 32 rows x 128 bytes at a time
             constexpr int kBoxCols = F32 ? 32 : 64;
             const int row0 = u.c_row + quarter * 32;
-            const int rows_end = MODE == kDgrad ? p.cap : (p.offsets ? p.G * p.N : p.N);
 #pragma unroll
             for (int j = 0; j < kColsPerWarp / kBoxCols; ++j) {
                 if (j * kBoxCols >= ncols) break;
@@ -502,7 +510,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 fence_async_smem();
                 __syncwarp();
                 // a box that starts past the matrix edge is skipped, not clipped
-                if (lane == 0 && col0 + j * kBoxCols < p.K && row0 < rows_end) {
+                if (lane == 0 && col0 + j * kBoxCols < p.K && row0 < p.c_end) {
                     if (F32 && p.accumulate)
                         tma_store_add_2d(&tmC, cstage, col0 + j * kBoxCols, row0);
                     else
@@ -522,14 +530,63 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
 }
 
+// The parts of a split product added up in order: out = sum_s parts[s] (+ out), four columns a
+// thread; a part is `stride` floats.
+template <bool F32>
+__global__ void __launch_bounds__(256)
+    grad_join_kernel(const float *__restrict__ parts, int splits, int64_t stride, int64_t quads, int accumulate,
+                     void *__restrict__ out) {
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= quads) return;
+    const float4 *p = reinterpret_cast<const float4 *>(parts) + i;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (F32 && accumulate) sum = reinterpret_cast<const float4 *>(out)[i];
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) {
+        const float4 v = __ldcg(p + s * (stride / 4));
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+    if (F32)
+        reinterpret_cast<float4 *>(out)[i] = sum;
+    else
+        reinterpret_cast<uint2 *>(out)[i] = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+}
+
+// Parts that a dense product's contraction of `blocks` 128-deep blocks is cut into: as many
+// as leave no half tile without an SM, of four blocks at least.  A block takes 0.4 us on the
+// way through a tile, the sums' launch 2 us, so short contractions stay whole.  wgrad (whole and
+// split): 256 x 256 from 4096 rows 16.0 and 8.3 us, 512 x 512 from 8192 27 and 12, from 2048
+// 10.4 and 8.5, 528 x 784 from 1000 (8 blocks) 7.8 and 8.8; dgrad of 16 rows, N = K = 4096, 13.8
+// and 11.4.  Parts of two or six blocks were no faster.
+constexpr int kSplitBlocks = 4, kSplitMost = 16, kSplitFrom = 12;
+constexpr int64_t kSplitSms = 148;
+static int grad_splits(int64_t rows, int64_t cols, int64_t blocks) {
+    const int64_t tiles = ((rows + 127) / 128) * ((cols + 255) / 256);
+    if (blocks < kSplitFrom) return 1;
+    int64_t n = kSplitSms / (2 * tiles);
+    if (n > blocks / kSplitBlocks) n = blocks / kSplitBlocks;
+    if (n > kSplitMost) n = kSplitMost;
+    return n < 2 ? 1 : static_cast<int>(n);
+}
+
+int64_t grad_workspace(bool wgrad, int64_t M, int64_t N, int64_t K) {
+    const int64_t rows = wgrad ? N : M, n = grad_splits(rows, K, ((wgrad ? M : N) + 127) / 128);
+    return n > 1 ? n * ((rows + 127) / 128 * 128) * K * 4 : 0;
+}
+
 template <int MODE, bool F32, int STAGES, int BOXES>
-static dg_status_t launch_grad_impl(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
+static dg_status_t launch_grad_impl(const GradArgs &a, int splits, const DeviceInfo &dev, cudaStream_t stream) {
     using L = GradSmem<STAGES, BOXES>;
     static_assert(L::kDynamicBytes <= 232448, "shared memory budget");
     static_assert(kGradBufs % 2 == 0, "each MMA thread must own its buffers");
     CUtensorMap tmA, tmB, tmC;
     const uint64_t b_rows = MODE == kDgrad ? static_cast<uint64_t>(a.G) * a.N : static_cast<uint64_t>(a.M);
-    const uint64_t c_rows = MODE == kDgrad ? static_cast<uint64_t>(a.M) : static_cast<uint64_t>(a.G) * a.N;
+    // rows of one output; a split product's parts are padded to whole tiles
+    const int64_t out_rows = MODE == kDgrad ? a.M : a.N;
+    const int64_t part_rows = splits > 1 ? (out_rows + 127) / 128 * 128 : out_rows;
+    const uint64_t c_rows = static_cast<uint64_t>(part_rows) * splits * (MODE == kWgrad ? a.G : 1);
     dg_status_t st = make_tmap_2d(&tmA, a.dY, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.M, a.N, 128, 128,
                                   CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != DG_OK) return st;
@@ -554,6 +611,9 @@ static dg_status_t launch_grad_impl(const GradArgs &a, const DeviceInfo &dev, cu
     p.Kc = static_cast<int>((a.K + 127) / 128);
     p.num_m = MODE == kDgrad ? static_cast<int>((a.M + 127) / 128) : p.Nb;
     p.num_k = static_cast<int>((a.K + 255) / 256);
+    p.splits = splits;
+    p.c_rows = static_cast<int>(part_rows);
+    p.c_end = static_cast<int>(c_rows);
     p.accumulate = a.accumulate ? 1 : 0;
     p.timeout_ns = ctl.timeout_ns;
     p.status = ctl.status;
@@ -573,15 +633,32 @@ static dg_status_t launch_grad_impl(const GradArgs &a, const DeviceInfo &dev, cu
         if (128 * kGradRegsProducer + 256 * kGradRegsEpilogue > kGradThreads * fa.numRegs) return DG_ERR_CUDA;
         configured_device = device;
     }
-    const int64_t tiles = static_cast<int64_t>(MODE == kWgrad ? a.G : 1) * p.num_m * p.num_k;
+    const int64_t tiles = static_cast<int64_t>(MODE == kWgrad ? a.G : 1) * splits * p.num_m * p.num_k;
     if (tiles > 0x3FFFFFFFLL) return DG_ERR_SHAPE;
     // twice the tiles: a single partial round may run as half tiles
     const int grid = static_cast<int>(2 * tiles < dev.num_sms ? 2 * tiles : dev.num_sms);
     return launch_pdl(kernel, grid, kGradThreads, L::kDynamicBytes, stream, tmA, tmB, tmC, p);
 }
 
+// A split product: parts into the workspace, then their sums.
+template <int MODE>
+static dg_status_t launch_split(const GradArgs &a, int splits, const DeviceInfo &dev, cudaStream_t stream) {
+    GradArgs part = a;
+    part.C = a.workspace;
+    part.accumulate = false;
+    dg_status_t st = launch_grad_impl<MODE, true, 4, 1>(part, splits, dev, stream);
+    if (st != DG_OK) return st;
+    const int64_t rows = MODE == kDgrad ? a.M : a.N, quads = rows * a.K / 4;
+    const int64_t stride = (rows + 127) / 128 * 128 * a.K;
+    return launch_pdl(a.fp32 ? grad_join_kernel<true> : grad_join_kernel<false>, static_cast<int>((quads + 255) / 256), 256,
+                      0, stream, static_cast<const float *>(a.workspace), splits, stride, quads, a.accumulate ? 1 : 0,
+                      a.C);
+}
+
 dg_status_t launch_dgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    return launch_grad_impl<kDgrad, false, 4, 1>(a, dev, stream);
+    const int splits = a.offsets ? 1 : grad_splits(a.M, a.K, (a.N + 127) / 128);
+    return splits > 1 ? launch_split<kDgrad>(a, splits, dev, stream)
+                      : launch_grad_impl<kDgrad, false, 4, 1>(a, 1, dev, stream);
 }
 
 // Operand stages against output boxes.  An output tile is 128 KB (FP32): with few blocks of
@@ -593,11 +670,13 @@ constexpr int64_t kWgradLongBlocks = 24;
 
 template <bool F32>
 static dg_status_t launch_wgrad_impl(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    return a.M / 128 > kWgradLongBlocks * a.G ? launch_grad_impl<kWgrad, F32, 4, 1>(a, dev, stream)
-                                              : launch_grad_impl<kWgrad, F32, 3, 2>(a, dev, stream);
+    return a.M / 128 > kWgradLongBlocks * a.G ? launch_grad_impl<kWgrad, F32, 4, 1>(a, 1, dev, stream)
+                                              : launch_grad_impl<kWgrad, F32, 3, 2>(a, 1, dev, stream);
 }
 
 dg_status_t launch_wgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
+    const int splits = a.offsets ? 1 : grad_splits(a.N, a.K, (a.M + 127) / 128);
+    if (splits > 1) return launch_split<kWgrad>(a, splits, dev, stream);
     return a.fp32 ? launch_wgrad_impl<true>(a, dev, stream) : launch_wgrad_impl<false>(a, dev, stream);
 }
 

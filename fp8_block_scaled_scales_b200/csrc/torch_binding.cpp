@@ -371,8 +371,12 @@ PyObject *dgrad(PyObject *, PyObject *const *a, Py_ssize_t) {
     if (off)
         status(dg_fp8_grouped_dgrad_contiguous(pd, pa, pw, pb, ptr(c), off, M, static_cast<int>(G), N, K, st),
                "dg_fp8_grouped_dgrad_contiguous");
-    else
-        status(dg_fp8_dgrad_blockscaled(pd, pa, pw, pb, ptr(c), M, N, K, st), "dg_fp8_dgrad_blockscaled");
+    else {
+        const Tensor ws = scratch(dg_fp8_dgrad_workspace(M, N, K), dev, a[6], st);
+        status(dg_fp8_dgrad_blockscaled(pd, pa, pw, pb, ptr(c), M, N, K, ws.defined() ? ws.data_ptr() : nullptr,
+                                        ws.defined() ? ws.numel() : 0, st),
+               "dg_fp8_dgrad_blockscaled");
+    }
     return wrap(c);
     END_HANDLE_TH_ERRORS
 }
@@ -404,9 +408,12 @@ PyObject *wgrad(PyObject *, PyObject *const *a, Py_ssize_t) {
         status(dg_fp8_grouped_wgrad_contiguous(pd, pa, px, pb, ptr(c), type == kF32, accumulate, off, M,
                                                static_cast<int>(G), N, K, st),
                "dg_fp8_grouped_wgrad_contiguous");
-    else
-        status(dg_fp8_wgrad_blockscaled(pd, pa, px, pb, ptr(c), type == kF32, accumulate, M, N, K, st),
+    else {
+        const Tensor ws = scratch(dg_fp8_wgrad_workspace(M, N, K), dev, a[8], st);
+        status(dg_fp8_wgrad_blockscaled(pd, pa, px, pb, ptr(c), type == kF32, accumulate, M, N, K,
+                                        ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, st),
                "dg_fp8_wgrad_blockscaled");
+    }
     return wrap(c);
     END_HANDLE_TH_ERRORS
 }

@@ -60,7 +60,9 @@ struct GradArgs {
     int64_t M, N, K;
     int G;
     bool fp32, accumulate;  // wgrad
+    void *workspace;        // dense: grad_workspace bytes
 };
+int64_t grad_workspace(bool wgrad, int64_t M, int64_t N, int64_t K);
 dg_status_t launch_dgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream);
 dg_status_t launch_wgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream);
 

@@ -457,10 +457,16 @@ dg_status_t dg_swiglu_quantize_backward(const uint8_t *H8, const float *sH_t, co
  * dY : [M][N] E4M3, sdY : [ceil(M/128)][ceil(N/128)].  W : [N][K], sW : [ceil(N/128)][ceil(K/128)].
  * dX : [M][K] BF16 out.  Matrices 16-byte aligned.  N > 0, N % 16 == 0, K % 16 == 0.
  * M == 0 or K == 0 is a no-op.
+ * workspace : device scratch of at least dg_fp8_dgrad_workspace(M, N, K) bytes, 16-byte aligned;
+ *             may be null where that is 0.  Small outputs of long sums need it: the sum is cut
+ *             into parts that run side by side and are added up in a fixed order.  It must not
+ *             be shared with a call that may run at the same time.
  */
 dg_status_t dg_fp8_dgrad_blockscaled(const uint8_t *dY, const float *sdY, const uint8_t *W,
                                      const float *sW, void *dX_bf16, int64_t M, int64_t N,
-                                     int64_t K, cudaStream_t stream);
+                                     int64_t K, void *workspace, int64_t workspace_bytes,
+                                     cudaStream_t stream);
+int64_t dg_fp8_dgrad_workspace(int64_t M, int64_t N, int64_t K); /* 0 for sizes it refuses */
 
 /*
  * Weight gradient of the dense product, from the codes of dC and of the forward input:
@@ -471,11 +477,13 @@ dg_status_t dg_fp8_dgrad_blockscaled(const uint8_t *dY, const float *sdY, const 
  * dW : [N][K] out, FP32 when out_fp32 is not 0, else BF16; 16-byte aligned.
  * accumulate not 0 (FP32 only, else DG_ERR_INVALID_ARG): the gradient is added to dW.
  * N % 16 == 0, K % 16 == 0.  N == 0 or K == 0 is a no-op; M == 0 gives zeros (accumulate:
- * leaves dW).
+ * leaves dW).  workspace : as in dg_fp8_dgrad_blockscaled, dg_fp8_wgrad_workspace bytes.
  */
 dg_status_t dg_fp8_wgrad_blockscaled(const uint8_t *dY, const float *sdY, const uint8_t *X,
                                      const float *sX, void *dW, int out_fp32, int accumulate,
-                                     int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+                                     int64_t M, int64_t N, int64_t K, void *workspace,
+                                     int64_t workspace_bytes, cudaStream_t stream);
+int64_t dg_fp8_wgrad_workspace(int64_t M, int64_t N, int64_t K); /* 0 for sizes it refuses */
 
 /*
  * dg_fp8_dgrad_blockscaled expert by expert: rows [off[g], off[g+1]) of dY with W[g].

@@ -78,6 +78,72 @@ def test_products_of_small_integers_are_exact(M, N, K):
     assert torch.equal(binding.dgrad_blockscaled(dy, sdy, w, sw).cpu(), ref)
 
 
+# few tiles, long sums: cut into parts that are added up in order
+LONG_WGRAD = [(1537, 48, 80), (2000, 528, 272), (8191, 16, 16), (4096, 256, 256), (3000, 1040, 528)]
+LONG_DGRAD = [(1, 1552, 48), (37, 2000, 784), (130, 4096, 272), (300, 1536, 528)]
+
+
+@pytest.mark.parametrize("M,N,K", LONG_WGRAD)
+def test_wgrad_of_long_sums(M, N, K):
+    """Both types, added to a gradient, twice the same bits, and no write outside the matrix."""
+    assert binding.lib().dg_fp8_wgrad_workspace(M, N, K) > 0
+    dy, sdy = quantized(M, N, M + N, 1e-3)
+    x, sx = quantized(M, K, M + K)
+    a, b = plain.decode(dy.cpu(), sdy.cpu()).t(), plain.decode(x.cpu(), sx.cpu())
+    ref, mag = a @ b, a.abs() @ b.abs()
+    for dtype in (F32, BF16):
+        C = torch.full((N + 2, K), -3.0, dtype=dtype, device="cuda")
+        binding.wgrad_blockscaled(dy, sdy, x, sx, C=C[1:-1])
+        check(C[1:-1], ref, mag, -(-M // 128), dtype)
+        assert bool((C[0] == -3.0).all()) and bool((C[-1] == -3.0).all())
+        again = binding.wgrad_blockscaled(dy, sdy, x, sx, dtype=dtype)
+        assert torch.equal(again, C[1:-1])
+    base = torch.randn((N, K), generator=torch.Generator().manual_seed(1)).cuda()
+    C = base.clone()
+    binding.wgrad_blockscaled(dy, sdy, x, sx, C=C, accumulate=True)
+    check(C, base.cpu().double() + ref, mag + base.cpu().double().abs(), -(-M // 128) + 1, F32)
+    assert binding.last_device_status() == 0
+
+
+@pytest.mark.parametrize("M,N,K", LONG_DGRAD)
+def test_dgrad_of_long_sums(M, N, K):
+    assert binding.lib().dg_fp8_dgrad_workspace(M, N, K) > 0
+    dy, sdy = quantized(M, N, M + N, 1e-3)
+    w, sw = quantized(N, K, N + K, 0.02)
+    C = torch.full((M + 2, K), -3.0, dtype=BF16, device="cuda")
+    binding.dgrad_blockscaled(dy, sdy, w, sw, C=C[1:-1])
+    a, b = plain.decode(dy.cpu(), sdy.cpu()), plain.decode(w.cpu(), sw.cpu())
+    check(C[1:-1], a @ b, a.abs() @ b.abs(), -(-N // 128), BF16)
+    assert bool((C[0] == -3.0).all()) and bool((C[-1] == -3.0).all())
+    assert torch.equal(binding.dgrad_blockscaled(dy, sdy, w, sw), C[1:-1])
+    assert binding.last_device_status() == 0
+
+
+def test_long_sums_at_once_and_captured():
+    """Calls on two streams, each with parts of its own, and a captured one replayed on other codes."""
+    M, N, K = 2500, 272, 400
+    sets = [(*quantized(M, N, 10 + i, 1e-3), *quantized(M, K, 20 + i)) for i in range(3)]
+    want = [binding.wgrad_blockscaled(*t) for t in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [binding.wgrad_blockscaled(*t, stream=st) for st, t in zip(streams, sets)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    live = [t.clone() for t in sets[0]]
+    C = binding.wgrad_blockscaled(*live)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.wgrad_blockscaled(*live, C=C)
+    for i in (1, 2):
+        for dst, src in zip(live, sets[i]):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(C, want[i])
+
+
 COUNTS = [[128], [0, 0], [0, 384, 0, 128], [130, 0, 1, 700, 257], [1] * 9]
 
 

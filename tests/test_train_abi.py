@@ -126,19 +126,30 @@ def test_swiglu_refusals(lib):
 
 def test_gradient_product_refusals(lib):
     d = lib.dg_fp8_dgrad_blockscaled
-    assert d(P, P, P, P, P, 8, 0, 128, NULL) == SHAPE                  # nothing to sum over
-    assert d(P, P, P, P, P, 8, 24, 128, NULL) == SHAPE
-    assert d(P, P, P, P, P, 8, 128, 24, NULL) == SHAPE
-    assert d(NULL, NULL, NULL, NULL, NULL, 0, 128, 128, NULL) == OK
-    assert d(P, P, P, P, NULL, 8, 128, 128, NULL) == ARG
-    assert d(P, P, ODD, P, P, 8, 128, 128, NULL) == ALIGN
+    assert d(P, P, P, P, P, 8, 0, 128, NULL, 0, NULL) == SHAPE                  # nothing to sum over
+    assert d(P, P, P, P, P, 8, 24, 128, NULL, 0, NULL) == SHAPE
+    assert d(P, P, P, P, P, 8, 128, 24, NULL, 0, NULL) == SHAPE
+    assert d(NULL, NULL, NULL, NULL, NULL, 0, 128, 128, NULL, 0, NULL) == OK
+    assert d(P, P, P, P, NULL, 8, 128, 128, NULL, 0, NULL) == ARG
+    assert d(P, P, ODD, P, P, 8, 128, 128, NULL, 0, NULL) == ALIGN
     w = lib.dg_fp8_wgrad_blockscaled
-    assert w(P, P, P, P, P, 1, 0, 8, 24, 128, NULL) == SHAPE
-    assert w(P, P, P, P, P, 0, 1, 8, 128, 128, NULL) == ARG            # accumulate in BF16
-    assert w(NULL, NULL, NULL, NULL, NULL, 1, 0, 8, 0, 128, NULL) == OK
-    assert w(P, P, P, P, NULL, 1, 0, 8, 128, 128, NULL) == ARG
-    assert w(NULL, NULL, NULL, NULL, NULL, 1, 0, 0, 128, 128, NULL) == ARG  # M == 0 still writes dW
-    assert w(P, P, P, P, ODD, 1, 0, 8, 128, 128, NULL) == ALIGN
+    assert w(P, P, P, P, P, 1, 0, 8, 24, 128, NULL, 0, NULL) == SHAPE
+    assert w(P, P, P, P, P, 0, 1, 8, 128, 128, NULL, 0, NULL) == ARG            # accumulate in BF16
+    assert w(NULL, NULL, NULL, NULL, NULL, 1, 0, 8, 0, 128, NULL, 0, NULL) == OK
+    assert w(P, P, P, P, NULL, 1, 0, 8, 128, 128, NULL, 0, NULL) == ARG
+    assert w(NULL, NULL, NULL, NULL, NULL, 1, 0, 0, 128, 128, NULL, 0, NULL) == ARG  # M == 0 still writes dW
+    assert w(P, P, P, P, ODD, 1, 0, 8, 128, 128, NULL, 0, NULL) == ALIGN
+    # few tiles and long sums: a workspace of the size that the library names
+    need = lib.dg_fp8_wgrad_workspace(4096, 256, 256)
+    assert need >= 2 * 256 * 256 * 4 and lib.dg_fp8_wgrad_workspace(4096, 4096, 4096) == 0
+    assert lib.dg_fp8_wgrad_workspace(4096, 250, 256) == lib.dg_fp8_wgrad_workspace(-1, 256, 256) == 0
+    assert w(P, P, P, P, P, 1, 0, 4096, 256, 256, NULL, need, NULL) == ARG
+    assert w(P, P, P, P, P, 1, 0, 4096, 256, 256, P, need - 1, NULL) == ARG
+    assert w(P, P, P, P, P, 1, 0, 4096, 256, 256, ODD, need, NULL) == ALIGN
+    need = lib.dg_fp8_dgrad_workspace(16, 4096, 4096)
+    assert need >= 2 * 16 * 4096 * 4 and lib.dg_fp8_dgrad_workspace(16, 0, 4096) == 0
+    assert d(P, P, P, P, P, 16, 4096, 4096, NULL, 0, NULL) == ARG
+    assert d(P, P, P, P, P, 16, 4096, 4096, ODD, need, NULL) == ALIGN
     gd = lib.dg_fp8_grouped_dgrad_contiguous
     assert gd(P, P, P, P, P, P, 100, 2, 128, 128, NULL) == SHAPE
     assert gd(P, P, P, P, P, P, 128, 2, 64, 128, NULL) == SHAPE        # N % 128
@@ -162,7 +173,7 @@ def test_sizes_beyond_the_index_ranges_are_refused(lib):
     for N in (1 << 31, 1 << 54, 1 << 62):  # 1024 * 2^54 is 0 in 64 bits
         assert lib.dg_fp8_grouped_dgrad_contiguous(P, P, P, P, P, P, 128, 1024, N, 128, NULL) == SHAPE
         assert lib.dg_fp8_grouped_wgrad_contiguous(P, P, P, P, P, 1, 0, P, 128, 1024, N, 128, NULL) == SHAPE
-        assert lib.dg_fp8_dgrad_blockscaled(P, P, P, P, P, 8, N, 128, NULL) == SHAPE
+        assert lib.dg_fp8_dgrad_blockscaled(P, P, P, P, P, 8, N, 128, NULL, 0, NULL) == SHAPE
         assert lib.dg_swiglu_quantize(P, NULL, 0, 8, N, P, P, NULL, NULL, NULL) == SHAPE
 
 
