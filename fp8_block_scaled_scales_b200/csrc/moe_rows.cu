@@ -1,4 +1,4 @@
-// Rows between tokens and experts: tokens gathered by expert and quantized in one pass, and
+// Rows between tokens and experts: tokens gathered by expert and quantized in one call, and
 // expert rows brought back to their tokens with weights, with the weights' gradient.
 //
 // dispatch_quantize:  v[r] = x[slot / k] (times weights[slot] as an FP32 product), zero for a

@@ -43,8 +43,8 @@ __device__ __forceinline__ void one_plus_exp(float2 x, float2 &d, float2 &r) {
 }
 
 // -n / d from r = -1/d: the product corrected by its remainder (Markstein, as in
-// quant_f32.cuh).  With the approximate reciprocal alone, and a / s as a product, the kernels
-// are a tenth faster and a third of the inputs tried had half as much error again in the
+// quant_f32.cuh).  With the approximate reciprocal alone, and a / s as a product with one, the kernels
+// were a tenth faster and a third of the inputs tried had half as much error again in the
 // codes as a plain FP32 evaluation; as it stands they have the same.
 __device__ __forceinline__ float2 negated_quotient(float2 n, float2 d, float2 r) {
     const float2 z = __fmul2_rn(n, r);
@@ -164,9 +164,9 @@ struct GluWalk {
 // Forward, persistent: two CTAs per SM walk over the blocks.  A thread keeps its 16-byte
 // pieces of a block in shared memory and asks for the same pieces of the next block as soon
 // as it has read them, so loads run under the arithmetic, the block maximum and the stores
-// without costing registers.  16384 x 4096 without checkpoint: 63 us, 336 MB, 5.3 TB/s; with
-// checkpoint 108 us, 470 MB, 4.3 TB/s, bound by instruction issue (72 % of the slots; the
-// conversions of three values for each output).  A CTA per block that loaded into registers
+// without costing registers.  16384 x 4096 in a graph, without checkpoint: 57 us, 336 MB, 5.8
+// TB/s; with checkpoint 99 us, 470 MB, 4.8 TB/s, bound by instruction issue (74 % of the slots;
+// the conversions of three values for each output).  A CTA per block that loaded into registers
 // took 124 us, and 386 us while it held all four rows at once and spilled.
 struct GluSmem {
     uint4 g[kGluPer][kGluThreads];
@@ -275,9 +275,10 @@ __global__ void __launch_bounds__(kGluThreads, 2)
 }
 
 // Backward, persistent, one CTA per SM: a block's [dg | du] in FP32 is half the register
-// file.  16384 x 4096: 93 us, 403 MB, 4.3 TB/s, issue-bound with 16 warps (a CTA per block
-// 168 us; 1024 threads of two rows each 112 against 98 then).  Pieces of the next block are asked for as in the forward kernel; the row scales,
-// which other threads copy, alternate between two buffers.
+// file.  16384 x 4096: 87 us in a graph, 403 MB, 4.6 TB/s, issue-bound with 16 warps (a CTA
+// per block 168 us; 1024 threads of two rows each 112 against 98 then).  Pieces of the next
+// block are asked for as in the forward kernel; the row scales, which other threads copy,
+// alternate between two buffers.
 struct GluBackSmem {
     uint4 da[kGluBackPer][kGluBackThreads];
     uint2 cg[kGluBackPer][kGluBackThreads];
