@@ -420,13 +420,15 @@ __global__ void __launch_bounds__(kRowThreads, 3) dispatch_rows_kernel(const Tok
 }
 
 // One CTA per token and 1024 columns, eight columns a thread; the rows of up to four slots
-// are in flight at a time.  Bound by memory: 32768 slots x 7168 take 84 us, 6.2 TB/s; 16384
-// slots x 4096 with k = 2 40 us, 5.1 TB/s (two pieces a thread: 39).
+// are in flight at a time.  Bound by memory: in a graph 32768 slots x 7168 take 79 us, 6.7
+// TB/s; 16384 slots x 4096 with k = 2 37 us, 5.4 TB/s.  Sixteen CTAs an SM: with the 34 registers
+// that they would otherwise take, 84 and 40 us.  Streaming loads and stores, two pieces a
+// thread: within 2 %.
 constexpr int kCombineThreads = 128;
 constexpr int kCombineCols = kCombineThreads * 8;
 
 template <bool WEIGHTS>
-__global__ void __launch_bounds__(kCombineThreads)
+__global__ void __launch_bounds__(kCombineThreads, 16)
     combine_kernel(const uint16_t *__restrict__ Y, const float *__restrict__ weights,
                    const int32_t *__restrict__ row_of_slot, int k, int64_t H, int rows, int chunks,
                    uint16_t *__restrict__ out) {
