@@ -59,7 +59,7 @@ def _build_ext(force: bool) -> None:
            "-I", sysconfig.get_paths()["include"]]
     for path in includes:
         cmd += ["-isystem", path]
-    cmd += [EXT_SRC, "-o", tmp, "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+    cmd += [EXT_SRC, "-o", tmp, "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda",
             "-ltorch_python", "-L", HERE, "-l:libdg.so", "-Wl,-rpath,$ORIGIN"]
     subprocess.check_call(cmd)
     os.replace(tmp, EXT)

@@ -1,7 +1,7 @@
 // The expert-layer and gradient calls for Python: argument checks, output allocation and the
 // call through the C ABI (include/dg.h), in one native function each.  A decode step is a
 // chain of calls whose kernels take a few microseconds; done in Python, the checks, three
-// allocations and the marshalling of a dozen arguments cost 9 to 17 us a call, here 4 to 8.
+// allocations and the marshalling of a dozen arguments cost 9 to 17 us a call, here 3 to 8.
 //
 // Every function takes positional arguments (binding.py has the signatures and their
 // documentation), raises ValueError for a tensor of the wrong type, shape, device or layout,
@@ -9,7 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -65,7 +65,9 @@ T *in_or_null(PyObject *o, const char *name, at::ScalarType type, Shape shape, i
 }
 
 Tensor make(at::ScalarType type, Shape shape, int dev) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev))));
+    // what at::empty comes to on a GPU, without the way through the dispatcher
+    return Tensor(at::detail::empty_cuda(at::IntArrayRef(shape), type,
+                                         c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt));
 }
 
 // The caller's output, checked, or a new one (not filled).
