@@ -368,6 +368,25 @@ def test_dispatch_infinite_and_nan_weights(T, k, H):
     assert torch.equal((q & 0x7F) == 0x7F, nan) and torch.equal(q[~nan], wq[~nan])
 
 
+@pytest.mark.parametrize("T,value", [(3, float("nan")), (20, float("inf")), (70, float("nan"))])
+def test_dispatch_non_finite_values_in_blocks_of_few_rows(T, value):
+    """The rows without a token take part: zero over a NaN scale is NaN, over an infinite one zero."""
+    k, G, H = 2, 3, 272
+    ids = route(T, k, G, T)
+    cap = plain.cap_of(T, k, G)
+    off, row, slot = plain.sort_plain(ids.numpy(), G, cap)
+    x = tokens(T, H, T)
+    x[1, 5] = value
+    used = int(off[-1])
+    q, s = binding.moe_dispatch_quantize(x.cuda(), torch.from_numpy(slot).int().cuda(),
+                                         torch.from_numpy(off).int().cuda(), k)
+    wq, ws = plain.quantize_f32(gathered(x, slot, k)[:used])
+    assert torch.equal(s[:used // 128].cpu().nan_to_num(nan=-1.0), ws.nan_to_num(nan=-1.0))
+    q, wq = q[:used].cpu(), wq.view(torch.uint8)
+    nan = (wq & 0x7F) == 0x7F
+    assert bool(nan.any()) and torch.equal((q & 0x7F) == 0x7F, nan) and torch.equal(q[~nan], wq[~nan])
+
+
 def test_rows_past_32_bit_offsets():
     """Matrices of more than 2^32 elements: the last rows and tokens are the ones looked at."""
     H, rows = 16384, 270_080  # 4.4e9 elements
