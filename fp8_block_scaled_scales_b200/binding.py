@@ -251,7 +251,9 @@ def grouped_gemm_masked(A, sA, B, sB, masked_m, C=None, stream=None):
 # These calls check their tensors, allocate what the caller did not pass and call the C ABI in
 # native code (csrc/torch_binding.cpp): a chain of short kernels should not wait for Python.
 # Tensors of the wrong type, shape, device or layout raise ValueError, what the library
-# refuses DGError.  New outputs are not filled.
+# refuses DGError.  New outputs are not filled.  With stream= a call runs on that stream, and
+# what it allocates, outputs and workspaces, is allocated there too, as under
+# torch.cuda.stream(stream): the caller orders its other streams around it.
 _ext = None
 
 

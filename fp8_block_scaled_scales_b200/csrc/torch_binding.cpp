@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -83,15 +84,31 @@ T *ptr(const Tensor &t) {
     return static_cast<T *>(t.data_ptr());
 }
 
-cudaStream_t stream_of(PyObject *stream, int dev) {
-    if (stream == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-    PyObject *h = PyObject_GetAttrString(stream, "cuda_stream");
-    if (!h) throw python_error();
-    const unsigned long long v = PyLong_AsUnsignedLongLong(h);
-    Py_DECREF(h);
-    if (PyErr_Occurred()) throw python_error();
-    return reinterpret_cast<cudaStream_t>(v);
-}
+// The stream of a call, made the current one while the call lasts: what the call allocates then
+// comes from that stream's own memory, which no work on another stream can still be using, and
+// scratch that is freed at the end of the call goes back to it.
+class CallStream {
+public:
+    CallStream(PyObject *stream, int dev) {
+        const auto device = static_cast<c10::DeviceIndex>(dev);
+        if (stream == Py_None) {
+            handle_ = c10::cuda::getCurrentCUDAStream(device).stream();
+            return;
+        }
+        PyObject *h = PyObject_GetAttrString(stream, "cuda_stream");
+        if (!h) throw python_error();
+        const unsigned long long v = PyLong_AsUnsignedLongLong(h);
+        Py_DECREF(h);
+        if (PyErr_Occurred()) throw python_error();
+        handle_ = reinterpret_cast<cudaStream_t>(v);
+        guard_.reset_stream(c10::cuda::getStreamFromExternal(handle_, device));
+    }
+    operator cudaStream_t() const { return handle_; }
+
+private:
+    cudaStream_t handle_;
+    c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 
 int64_t integer(PyObject *o, const char *name, int64_t least, int64_t most) {
     const long long v = PyLong_AsLongLong(o);
@@ -129,21 +146,15 @@ PyObject *wrap_all(const Ts &...ts) {
 
 constexpr int64_t kIntMax = 0x7FFFFFFF;
 
-// Scratch for one call: an empty tensor where none is needed.  `stream`: not None when the
-// call runs on another stream than the one the allocation belongs to.
-Tensor scratch(int64_t bytes, int dev, PyObject *stream, cudaStream_t handle) {
-    if (bytes == 0) return Tensor();
-    Tensor w = make(kU8, {bytes}, dev);
-    if (stream != Py_None)  // freed at the end of the call, perhaps while that stream still runs it
-        w.record_stream(c10::cuda::getStreamFromExternal(handle, static_cast<c10::DeviceIndex>(dev)).unwrap());
-    return w;
-}
+// Scratch for one call, from the call's stream: an empty tensor where none is needed.
+Tensor scratch(int64_t bytes, int dev) { return bytes == 0 ? Tensor() : make(kU8, {bytes}, dev); }
 
 // (topk_ids, G, offsets, row_of_slot, slot_of_row, stream)
 PyObject *moe_sort(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &ids = tensor(a[0], "topk_ids");
     const int dev = device_of(ids, "topk_ids", 2);
+    const CallStream st(a[5], dev);
     const int64_t T = ids.size(0), k = ids.size(1), G = integer(a[1], "G", 0, kIntMax);
     TORCH_CHECK_VALUE(k <= kIntMax, "topk_ids is too wide");
     const bool wide = ids.scalar_type() == at::kLong;
@@ -152,8 +163,7 @@ PyObject *moe_sort(PyObject *, PyObject *const *a, Py_ssize_t) {
     const Tensor offsets = out(a[2], "offsets", kI32, {G + 1}, dev);
     const Tensor row = out(a[3], "row_of_slot", kI32, {T, k}, dev);
     const Tensor slot = out(a[4], "slot_of_row", kI32, {cap}, dev);
-    const cudaStream_t st = stream_of(a[5], dev);
-    const Tensor w = scratch(dg_moe_sort_workspace(T, static_cast<int>(k), static_cast<int>(G)), dev, a[5], st);
+    const Tensor w = scratch(dg_moe_sort_workspace(T, static_cast<int>(k), static_cast<int>(G)), dev);
     status(dg_moe_sort(pi, wide, T, static_cast<int>(k), static_cast<int>(G), ptr<int32_t>(offsets), ptr<int32_t>(row),
                        ptr<int32_t>(slot), cap, w.defined() ? w.data_ptr() : nullptr, w.defined() ? w.numel() : 0, st),
            "dg_moe_sort");
@@ -166,6 +176,7 @@ PyObject *moe_sort_masked(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &ids = tensor(a[0], "topk_ids");
     const int dev = device_of(ids, "topk_ids", 2);
+    const CallStream st(a[6], dev);
     const int64_t T = ids.size(0), k = ids.size(1), G = integer(a[1], "G", 0, kIntMax);
     const int64_t M_max = integer(a[2], "M_max", 0, kIntMax);
     TORCH_CHECK_VALUE(k <= kIntMax, "topk_ids is too wide");
@@ -174,8 +185,7 @@ PyObject *moe_sort_masked(PyObject *, PyObject *const *a, Py_ssize_t) {
     const Tensor m = out(a[3], "masked_m", kI32, {G}, dev);
     const Tensor row = out(a[4], "row_of_slot", kI32, {T, k}, dev);
     const Tensor slot = out(a[5], "slot_of_row", kI32, {G * M_max}, dev);
-    const cudaStream_t st = stream_of(a[6], dev);
-    const Tensor w = scratch(dg_moe_sort_workspace(T, static_cast<int>(k), static_cast<int>(G)), dev, a[6], st);
+    const Tensor w = scratch(dg_moe_sort_workspace(T, static_cast<int>(k), static_cast<int>(G)), dev);
     status(dg_moe_sort_masked(pi, wide, T, static_cast<int>(k), static_cast<int>(G), ptr<int32_t>(m), ptr<int32_t>(row),
                               ptr<int32_t>(slot), M_max, w.defined() ? w.data_ptr() : nullptr,
                               w.defined() ? w.numel() : 0, st),
@@ -189,6 +199,7 @@ PyObject *moe_dispatch_quantize(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &x = tensor(a[0], "x");
     const int dev = device_of(x, "x", 2);
+    const CallStream st(a[7], dev);
     const int64_t T = x.size(0), H = x.size(1), k = integer(a[3], "k", 0, kIntMax);
     const void *px = checked(x, "x", kBF16, {T, H}, dev);
     const int64_t cap = tensor(a[1], "slot_of_row").numel(), G = tensor(a[2], "offsets").numel() - 1;
@@ -198,8 +209,7 @@ PyObject *moe_dispatch_quantize(PyObject *, PyObject *const *a, Py_ssize_t) {
     const auto *w = in_or_null<float>(a[4], "weights", kF32, {T, k}, dev);
     const Tensor q = out(a[5], "q", kU8, {cap, H}, dev);
     const Tensor s = out(a[6], "s", kF32, {blocks(cap), blocks(H)}, dev);
-    const cudaStream_t st = stream_of(a[7], dev);
-    const Tensor ws = scratch(dg_moe_dispatch_workspace(T, static_cast<int>(k), H, cap), dev, a[7], st);
+    const Tensor ws = scratch(dg_moe_dispatch_workspace(T, static_cast<int>(k), H, cap), dev);
     status(dg_moe_dispatch_quantize(px, w, slot, off, T, static_cast<int>(k), H, cap, static_cast<int>(G),
                                     ptr<uint8_t>(q), ptr<float>(s), ws.defined() ? ws.data_ptr() : nullptr,
                                     ws.defined() ? ws.numel() : 0, st),
@@ -213,6 +223,7 @@ PyObject *moe_dispatch_quantize_masked(PyObject *, PyObject *const *a, Py_ssize_
     HANDLE_TH_ERRORS
     const Tensor &x = tensor(a[0], "x");
     const int dev = device_of(x, "x", 2);
+    const CallStream st(a[6], dev);
     const int64_t T = x.size(0), H = x.size(1), k = integer(a[3], "k", 0, kIntMax);
     const void *px = checked(x, "x", kBF16, {T, H}, dev);
     const int64_t G = tensor(a[2], "masked_m").numel(), rows = tensor(a[1], "slot_of_row").numel();
@@ -224,7 +235,7 @@ PyObject *moe_dispatch_quantize_masked(PyObject *, PyObject *const *a, Py_ssize_
     const Tensor q = out(a[4], "q", kU8, {G, M_max, H}, dev);
     const Tensor s = out(a[5], "s", kF32, {G, blocks(M_max), blocks(H)}, dev);
     status(dg_moe_dispatch_quantize_masked(px, slot, m, T, static_cast<int>(k), H, static_cast<int>(G), M_max,
-                                           ptr<uint8_t>(q), ptr<float>(s), stream_of(a[6], dev)),
+                                           ptr<uint8_t>(q), ptr<float>(s), st),
            "dg_moe_dispatch_quantize_masked");
     return wrap_all(q, s);
     END_HANDLE_TH_ERRORS
@@ -243,6 +254,7 @@ PyObject *moe_combine(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &y = tensor(a[0], "y"), &row = tensor(a[1], "row_of_slot");
     const int dev = device_of(row, "row_of_slot", 2);
+    const CallStream st(a[4], dev);
     const int64_t T = row.size(0), k = row.size(1), H = y.dim() ? y.size(-1) : 0;
     TORCH_CHECK_VALUE(k <= kIntMax, "row_of_slot is too wide");
     int64_t rows;
@@ -250,7 +262,7 @@ PyObject *moe_combine(PyObject *, PyObject *const *a, Py_ssize_t) {
     const auto *pr = in<int32_t>(a[1], "row_of_slot", kI32, {T, k}, dev);
     const auto *w = in_or_null<float>(a[2], "weights", kF32, {T, k}, dev);
     const Tensor o = out(a[3], "out", kBF16, {T, H}, dev);
-    status(dg_moe_combine(py, w, pr, T, static_cast<int>(k), H, rows, ptr(o), stream_of(a[4], dev)), "dg_moe_combine");
+    status(dg_moe_combine(py, w, pr, T, static_cast<int>(k), H, rows, ptr(o), st), "dg_moe_combine");
     return wrap(o);
     END_HANDLE_TH_ERRORS
 }
@@ -260,6 +272,7 @@ PyObject *moe_combine_backward(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &dout = tensor(a[0], "dout"), &row = tensor(a[2], "row_of_slot");
     const int dev = device_of(dout, "dout", 2);
+    const CallStream st(a[4], dev);
     const int64_t T = dout.size(0), H = dout.size(1);
     TORCH_CHECK_VALUE(row.dim() == 2 && row.size(1) <= kIntMax, "row_of_slot must have 2 dimensions");
     const int64_t k = row.size(1);
@@ -268,7 +281,7 @@ PyObject *moe_combine_backward(PyObject *, PyObject *const *a, Py_ssize_t) {
     const void *py = rows_of(tensor(a[1], "y"), H, dev, rows);
     const auto *pr = in<int32_t>(a[2], "row_of_slot", kI32, {T, k}, dev);
     const Tensor dw = out(a[3], "dweights", kF32, {T, k}, dev);
-    status(dg_moe_combine_backward(pd, py, pr, T, static_cast<int>(k), H, rows, ptr<float>(dw), stream_of(a[4], dev)),
+    status(dg_moe_combine_backward(pd, py, pr, T, static_cast<int>(k), H, rows, ptr<float>(dw), st),
            "dg_moe_combine_backward");
     return wrap(dw);
     END_HANDLE_TH_ERRORS
@@ -288,6 +301,7 @@ PyObject *swiglu_quantize(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &h = tensor(a[0], "h");
     const int dev = device_of(h, "h", 2);
+    const CallStream st(a[7], dev);
     const int64_t M = h.size(0), F = h.size(1) / 2;
     const bool checkpoint = truth(a[2]);
     TORCH_CHECK_VALUE(checkpoint || (a[5] == Py_None && a[6] == Py_None), "h8 and sh are outputs of checkpoint=True");
@@ -296,7 +310,6 @@ PyObject *swiglu_quantize(PyObject *, PyObject *const *a, Py_ssize_t) {
     const int32_t *off = groups(a[1], dev, G);
     const Tensor q = out(a[3], "q", kU8, {M, F}, dev);
     const Tensor s = out(a[4], "s", kF32, {blocks(M), blocks(F)}, dev);
-    const cudaStream_t st = stream_of(a[7], dev);
     if (!checkpoint) {
         status(dg_swiglu_quantize(ph, off, static_cast<int>(G), M, F, ptr<uint8_t>(q), ptr<float>(s), nullptr, nullptr, st),
                "dg_swiglu_quantize");
@@ -316,14 +329,14 @@ PyObject *swiglu_quantize_masked(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &h = tensor(a[0], "h");
     const int dev = device_of(h, "h", 3);
+    const CallStream st(a[4], dev);
     const int64_t G = h.size(0), M = h.size(1), F = h.size(2) / 2;
     TORCH_CHECK_VALUE(G <= kIntMax, "h has too many experts");
     const void *ph = checked(h, "h", kBF16, {G, M, 2 * F}, dev);
     const auto *m = in<int32_t>(a[1], "masked_m", kI32, {G}, dev);
     const Tensor q = out(a[2], "q", kU8, {G, M, F}, dev);
     const Tensor s = out(a[3], "s", kF32, {G, blocks(M), blocks(F)}, dev);
-    status(dg_swiglu_quantize_masked(ph, m, static_cast<int>(G), M, F, ptr<uint8_t>(q), ptr<float>(s),
-                                     stream_of(a[4], dev)),
+    status(dg_swiglu_quantize_masked(ph, m, static_cast<int>(G), M, F, ptr<uint8_t>(q), ptr<float>(s), st),
            "dg_swiglu_quantize_masked");
     return wrap_all(q, s);
     END_HANDLE_TH_ERRORS
@@ -334,6 +347,7 @@ PyObject *swiglu_quantize_backward(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &da = tensor(a[2], "da");
     const int dev = device_of(da, "da", 2);
+    const CallStream st(a[6], dev);
     const int64_t M = da.size(0), F = da.size(1);
     const auto *h8 = in<uint8_t>(a[0], "h8", kU8, {M, 2 * F}, dev);
     const auto *sh = in<float>(a[1], "sh", kF32, {2 * F / 128, M}, dev);
@@ -342,8 +356,7 @@ PyObject *swiglu_quantize_backward(PyObject *, PyObject *const *a, Py_ssize_t) {
     const int32_t *off = groups(a[3], dev, G);
     const Tensor q = out(a[4], "q", kU8, {M, 2 * F}, dev);
     const Tensor s = out(a[5], "s", kF32, {blocks(M), blocks(2 * F)}, dev);
-    status(dg_swiglu_quantize_backward(h8, sh, pa, off, static_cast<int>(G), M, F, ptr<uint8_t>(q), ptr<float>(s),
-                                       stream_of(a[6], dev)),
+    status(dg_swiglu_quantize_backward(h8, sh, pa, off, static_cast<int>(G), M, F, ptr<uint8_t>(q), ptr<float>(s), st),
            "dg_swiglu_quantize_backward");
     return wrap_all(q, s);
     END_HANDLE_TH_ERRORS
@@ -354,6 +367,7 @@ PyObject *dgrad(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &dy = tensor(a[0], "dY"), &w = tensor(a[2], "W");
     const int dev = device_of(dy, "dY", 2);
+    const CallStream st(a[6], dev);
     const int64_t M = dy.size(0), N = dy.size(1), K = w.dim() ? w.size(-1) : 0;
     const auto *pd = in<uint8_t>(a[0], "dY", kU8, {M, N}, dev);
     const auto *pa = in<float>(a[1], "sdY", kF32, {blocks(M), blocks(N)}, dev);
@@ -369,12 +383,11 @@ PyObject *dgrad(PyObject *, PyObject *const *a, Py_ssize_t) {
         pb = in<float>(a[3], "sW", kF32, {blocks(N), blocks(K)}, dev);
     }
     const Tensor c = out(a[5], "C", kBF16, {M, K}, dev);
-    const cudaStream_t st = stream_of(a[6], dev);
     if (off)
         status(dg_fp8_grouped_dgrad_contiguous(pd, pa, pw, pb, ptr(c), off, M, static_cast<int>(G), N, K, st),
                "dg_fp8_grouped_dgrad_contiguous");
     else {
-        const Tensor ws = scratch(dg_fp8_dgrad_workspace(M, N, K), dev, a[6], st);
+        const Tensor ws = scratch(dg_fp8_dgrad_workspace(M, N, K), dev);
         status(dg_fp8_dgrad_blockscaled(pd, pa, pw, pb, ptr(c), M, N, K, ws.defined() ? ws.data_ptr() : nullptr,
                                         ws.defined() ? ws.numel() : 0, st),
                "dg_fp8_dgrad_blockscaled");
@@ -388,6 +401,7 @@ PyObject *wgrad(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &dy = tensor(a[0], "dY"), &x = tensor(a[2], "X");
     const int dev = device_of(dy, "dY", 2);
+    const CallStream st(a[8], dev);
     const int64_t M = dy.size(0), N = dy.size(1), K = x.dim() ? x.size(-1) : 0;
     const auto *pd = in<uint8_t>(a[0], "dY", kU8, {M, N}, dev);
     const auto *pa = in<float>(a[1], "sdY", kF32, {blocks(M), blocks(N)}, dev);
@@ -405,13 +419,12 @@ PyObject *wgrad(PyObject *, PyObject *const *a, Py_ssize_t) {
         TORCH_CHECK_VALUE(type == kF32 || type == kBF16, "a weight gradient is float32 or bfloat16");
     }
     const Tensor c = off ? out(a[5], "C", type, {G, N, K}, dev) : out(a[5], "C", type, {N, K}, dev);
-    const cudaStream_t st = stream_of(a[8], dev);
     if (off)
         status(dg_fp8_grouped_wgrad_contiguous(pd, pa, px, pb, ptr(c), type == kF32, accumulate, off, M,
                                                static_cast<int>(G), N, K, st),
                "dg_fp8_grouped_wgrad_contiguous");
     else {
-        const Tensor ws = scratch(dg_fp8_wgrad_workspace(M, N, K), dev, a[8], st);
+        const Tensor ws = scratch(dg_fp8_wgrad_workspace(M, N, K), dev);
         status(dg_fp8_wgrad_blockscaled(pd, pa, px, pb, ptr(c), type == kF32, accumulate, M, N, K,
                                         ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, st),
                "dg_fp8_wgrad_blockscaled");
