@@ -130,6 +130,18 @@ def _u8(t: torch.Tensor) -> torch.Tensor:
     return t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t
 
 
+def _new(shape, dtype, device, stream, filled: bool = False) -> torch.Tensor:
+    """An output, allocated (and zero-filled) on the stream of the call: on the current one, the memory
+    could still be in use there, and the fill would not come before the call's kernel."""
+    make = torch.zeros if filled else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def quantize_blockwise(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tensor | None = None,
                        stream=None):
     """BF16 [R][C] -> (E4M3 codes uint8 [R][C], FP32 scales [ceil(R/128)][ceil(C/128)])."""
@@ -137,9 +149,9 @@ def quantize_blockwise(x: torch.Tensor, q: torch.Tensor | None = None, s: torch.
         raise ValueError("x must be a 2-D bfloat16 tensor")
     R, C = x.shape
     if q is None:
-        q = torch.empty((R, C), dtype=torch.uint8, device=x.device)
+        q = _new((R, C), torch.uint8, x.device, stream)
     if s is None:
-        s = torch.empty(((R + 127) // 128, (C + 127) // 128), dtype=torch.float32, device=x.device)
+        s = _new(((R + 127) // 128, (C + 127) // 128), torch.float32, x.device, stream)
     _check(lib().dg_quantize_blockwise(_p(x), R, C, _p(_u8(q)), _p(s), _stream(stream)),
            "dg_quantize_blockwise")
     return q, s
@@ -152,9 +164,9 @@ def quantize_blockwise_masked(x, masked_m, q=None, s=None, stream=None):
     neither read nor written."""
     G, M_max, K = x.shape
     if q is None:
-        q = torch.zeros((G, M_max, K), dtype=torch.uint8, device=x.device)
+        q = _new((G, M_max, K), torch.uint8, x.device, stream, filled=True)
     if s is None:
-        s = torch.zeros((G, (M_max + 127) // 128, (K + 127) // 128), dtype=torch.float32, device=x.device)
+        s = _new((G, (M_max + 127) // 128, (K + 127) // 128), torch.float32, x.device, stream, filled=True)
     _check(lib().dg_quantize_blockwise_masked(_p(x), G, M_max, K, _p(masked_m), _p(_u8(q)), _p(s), _stream(stream)),
            "dg_quantize_blockwise_masked")
     return q, s
@@ -166,7 +178,7 @@ def gemm_blockscaled(A, sA, B, sB, C=None, kernel: str = "auto", stream=None):
     M, K = A.shape
     N = B.shape[0]
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        C = _new((M, N), torch.bfloat16, A.device, stream)
     _check(lib().dg_fp8_gemm_blockscaled_select(_p(A), _p(sA), _p(B), _p(sB), _p(C), M, N, K,
                                                 KERNELS[kernel], _stream(stream)),
            "dg_fp8_gemm_blockscaled")
@@ -183,11 +195,11 @@ def gemm_blockscaled_bf16a(A, B, sB, C=None, QA=None, sA=None, kernel: str = "au
     N = B.shape[0]
     dev = A.device
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        C = _new((M, N), torch.bfloat16, dev, stream)
     if QA is None:
-        QA = torch.empty((M, K), dtype=torch.uint8, device=dev)
+        QA = _new((M, K), torch.uint8, dev, stream)
     if sA is None:
-        sA = torch.empty(((M + 127) // 128, (K + 127) // 128), dtype=torch.float32, device=dev)
+        sA = _new(((M + 127) // 128, (K + 127) // 128), torch.float32, dev, stream)
     _check(lib().dg_fp8_gemm_blockscaled_bf16a_select(_p(A), _p(B), _p(sB), _p(C), _p(_u8(QA)), _p(sA), M, N, K,
                                                       KERNELS[kernel], _stream(stream)),
            "dg_fp8_gemm_blockscaled_bf16a")
@@ -200,7 +212,7 @@ def grouped_gemm_contiguous(A, sA, B, sB, offsets, C=None, stream=None):
     Mcap, K = A.shape
     G, N, _ = B.shape
     if C is None:
-        C = torch.empty((Mcap, N), dtype=torch.bfloat16, device=A.device)
+        C = _new((Mcap, N), torch.bfloat16, A.device, stream)
     _check(lib().dg_fp8_grouped_gemm_contiguous(_p(A), _p(sA), _p(B), _p(sB), _p(C), _p(offsets), Mcap, G,
                                                 N, K, _stream(stream)),
            "dg_fp8_grouped_gemm_contiguous")
@@ -212,9 +224,9 @@ def quantize_1x128(x: torch.Tensor, q: torch.Tensor | None = None, s_t: torch.Te
     """BF16 [R][C] -> (E4M3 codes [R][C], FP32 scales [ceil(C/128)][R]), one per row and group."""
     R, C = x.shape
     if q is None:
-        q = torch.empty((R, C), dtype=torch.uint8, device=x.device)
+        q = _new((R, C), torch.uint8, x.device, stream)
     if s_t is None:
-        s_t = torch.empty(((C + 127) // 128, R), dtype=torch.float32, device=x.device)
+        s_t = _new(((C + 127) // 128, R), torch.float32, x.device, stream)
     _check(lib().dg_quantize_1x128(_p(x), R, C, _p(_u8(q)), _p(s_t), _stream(stream)), "dg_quantize_1x128")
     return q, s_t
 
@@ -225,7 +237,7 @@ def gemm_1x128(A, sA_t, B, sB, C=None, kernel: str = "auto", stream=None):
     M, K = A.shape
     N = B.shape[0]
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        C = _new((M, N), torch.bfloat16, A.device, stream)
     _check(lib().dg_fp8_gemm_1x128_select(_p(A), _p(sA_t), _p(B), _p(sB), _p(C), M, N, K, KERNELS[kernel],
                                           _stream(stream)),
            "dg_fp8_gemm_1x128")
@@ -240,7 +252,7 @@ def grouped_gemm_masked(A, sA, B, sB, masked_m, C=None, stream=None):
     G, Mmax, K = A.shape
     N = B.shape[1]
     if C is None:
-        C = torch.zeros((G, Mmax, N), dtype=torch.bfloat16, device=A.device)
+        C = _new((G, Mmax, N), torch.bfloat16, A.device, stream, filled=True)
     _check(lib().dg_fp8_grouped_gemm_masked(_p(A), _p(sA), _p(B), _p(sB), _p(C), _p(masked_m), G, Mmax, N, K,
                                             _stream(stream)),
            "dg_fp8_grouped_gemm_masked")

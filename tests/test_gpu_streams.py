@@ -184,3 +184,60 @@ def test_the_current_stream_is_restored_after_a_refusal():
     with pytest.raises(AttributeError):
         binding.moe_sort(route(4, 2, 3, 1), 3, stream=object())
     assert torch.cuda.current_stream() == here
+
+
+def product_and_quantizer_calls():
+    """The forward products and the quantizers on a small problem: name -> call(stream)."""
+    x, xs = torch.randn((40, 256)).to(BF16).cuda(), torch.randn((3, 40, 256)).to(BF16).cuda()
+    m = torch.tensor([40, 0, 7], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 128, 128, 384], dtype=torch.int32, device="cuda")
+    a, b, a1 = quantized(40, 256, 1), quantized(128, 256, 2), binding.quantize_1x128(x)
+    rows, masked = quantized(384, 256, 3), binding.quantize_blockwise_masked(xs, m)
+    wg = torch.zeros((3, 128, 256), dtype=torch.uint8, device="cuda"), torch.ones((3, 1, 2), device="cuda")
+    return {
+        "quantize_blockwise": lambda st: binding.quantize_blockwise(x, stream=st),
+        "quantize_blockwise_masked": lambda st: binding.quantize_blockwise_masked(xs, m, stream=st),
+        "quantize_1x128": lambda st: binding.quantize_1x128(x, stream=st),
+        "gemm_blockscaled": lambda st: binding.gemm_blockscaled(*a, *b, stream=st),
+        "gemm_blockscaled_bf16a": lambda st: binding.gemm_blockscaled_bf16a(x, *b, stream=st),
+        "gemm_1x128": lambda st: binding.gemm_1x128(*a1, *b, stream=st),
+        "grouped_gemm_contiguous": lambda st: binding.grouped_gemm_contiguous(*rows, *wg, off, stream=st),
+        "grouped_gemm_masked": lambda st: binding.grouped_gemm_masked(*masked, *wg, m, stream=st),
+    }
+
+
+def test_new_outputs_of_products_and_quantizers_belong_to_the_calls_stream():
+    calls = product_and_quantizer_calls()
+    side, here = fresh_stream(), torch.cuda.current_stream()
+    for name, call in calls.items():
+        assert_on(call(side), side)
+        assert_on(call(None), here)
+        assert torch.cuda.current_stream() == here, name
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", ["quantize_blockwise_masked", "grouped_gemm_masked"])
+def test_zero_fill_comes_before_the_kernel(name):
+    """The masked calls fill a new output before their kernel writes the tokens' rows, also while the current
+    stream is busy."""
+    call = product_and_quantizer_calls()[name]
+    want = call(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # about 10 ms of work queued on the current stream
+    got = call(side)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want) if isinstance(want, tuple) else ((got, want),):
+        assert torch.equal(a, b)
+
+
+def test_a_stream_of_another_library():
+    """Anything with a cuda_stream handle is a stream."""
+    class Handle:
+        cuda_stream = torch.cuda.Stream().cuda_stream
+    x = torch.randn((40, 256)).to(BF16).cuda()
+    want = binding.quantize_blockwise(x)
+    torch.cuda.synchronize()
+    got = binding.quantize_blockwise(x, stream=Handle())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
