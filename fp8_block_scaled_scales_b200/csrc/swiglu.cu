@@ -45,7 +45,7 @@ __device__ __forceinline__ void one_plus_exp(float2 x, float2 &d, float2 &r) {
 // -n / d from r = -1/d: the product corrected by its remainder (Markstein, as in
 // quant_f32.cuh).  With the approximate reciprocal alone, and a / s as a product with one, the kernels
 // were a tenth faster and a third of the inputs tried had half as much error again in the
-// codes as a plain FP32 evaluation; as it stands they have the same.
+// codes as a plain FP32 evaluation; as it stands they have the same.  An infinite n gives NaN.
 __device__ __forceinline__ float2 negated_quotient(float2 n, float2 d, float2 r) {
     const float2 z = __fmul2_rn(n, r);
     return __ffma2_rn(__ffma2_rn(z, d, n), r, z);
@@ -174,9 +174,9 @@ struct GluSmem {
 };
 
 // FEW (the masked layout): a block's rows past its last one are left out in steps of 32, since a
-// decode step's slabs hold a few.  64 slabs of 8 rows, F = 2048: 13.9 us without, 9.1 with it; 8
-// full slabs of 512, F = 4096: 21.6 and 23.3, as the steps keep the rows' arithmetic apart.  (Both
-// ways in one kernel spilled.)
+// decode step's slabs hold a few.  In a graph of ten calls on the same input (which stays in L2): 64
+// slabs of 8 rows, F = 2048, 14.7 us without, 9.8 with it; 8 full slabs of 512, F = 4096, 16.1 and
+// 17.2, as the steps keep the rows' arithmetic apart.  (Both ways in one kernel spilled.)
 template <bool CKPT, bool FEW>
 __global__ void __launch_bounds__(kGluThreads, 2)
     swiglu_kernel(const uint16_t *__restrict__ Hin, const GluRows layout, uint8_t *__restrict__ Q,
@@ -251,7 +251,31 @@ __global__ void __launch_bounds__(kGluThreads, 2)
                 ask(i0 + i, next_row0, next_rows, walk.bc);
             }
         }
-        const FastScale bs = fast_scale(__uint_as_float(cta_max<kGluThreads / 32>(__float_as_uint(m), red[par])));
+        uint32_t top = cta_max<kGluThreads / 32>(__float_as_uint(m), red[par]);
+        if (__builtin_expect(top > 0x7F800000u, 0)) {
+            // A NaN, perhaps an infinite gate's: that counts as the gate itself times u (and keeps the
+            // code of a NaN, which is infinity over infinity).  The block is read once more, so that
+            // blocks of numbers do without the test, and in a loop, whose code they do not load.
+            const uint16_t *p = Hin + static_cast<int64_t>(row0) * 2 * F + bc * 128 + in_h;
+            m = 0.0f;
+#pragma unroll 1
+            for (int r = sub; r < rows; r += 32, p += step) {
+                float2 g[4], u[4];
+                bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p)), g);
+                bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(p + F)), u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float2 d, n;
+                    one_plus_exp(g[j], d, n);
+                    n = negated_quotient(g[j], d, n);
+                    n = make_float2(g[j].x == INFINITY ? g[j].x : n.x, g[j].y == INFINITY ? g[j].y : n.y);
+                    m = amax3(m, __fmul2_rn(n, u[j]));
+                }
+            }
+            __syncthreads();  // red[par] has been read
+            top = cta_max<kGluThreads / 32>(__float_as_uint(m), red[par]);
+        }
+        const FastScale bs = fast_scale(__uint_as_float(top));
         if (tid == 0) S[static_cast<int64_t>(rb) * layout.Fb + bc] = bs.s;
         const FastScale nb = bs.negated();
         uint8_t *q = Q + static_cast<int64_t>(row0) * F + bc * 128;

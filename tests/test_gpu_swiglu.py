@@ -191,3 +191,57 @@ def test_swiglu_non_finite_values_stay_in_their_block():
     assert torch.equal(torch.isfinite(s).cpu(), torch.tensor([[False, True], [True, False]]))
     assert torch.equal(q[:128, 128:], cq[:128, 128:]) and torch.equal(q[128:, :128], cq[128:, :128])
     assert s[0, 1] == cs[0, 1] and s[1, 0] == cs[1, 0]
+
+
+def non_finite_input():
+    """(h, F, blocks): row block and column block of each value that is not finite."""
+    M, F, inf, nan = 300, 640, float("inf"), float("nan")
+    h = pre_activation(M, F, 12)
+    h[h == 0] = 0.5
+    put = {(0, 0): [(3, 7, inf, 1.5), (90, 100, inf, -2.0)],  # gates of +infinity: infinite of both signs
+           (0, 1): [(17, 130, inf, 0.0)],                     # times zero: NaN
+           (0, 2): [(5, 300, 0.0, inf)], (0, 3): [(5, 400, 1.0, -inf)],
+           (1, 0): [(130, 0, -inf, 1.0)], (1, 1): [(255, 255, nan, 1.0)], (1, 2): [(200, 256, 1.0, nan)],
+           (2, 3): [(299, 511, inf, inf)], (2, 4): [(260, 513, inf, 2.0), (261, 514, -inf, 1.0)]}
+    for places in put.values():
+        for r, c, g, u in places:
+            h[r, c], h[r, F + c] = g, u
+    return h, F, put
+
+
+@pytest.mark.parametrize("form", ["plain", "checkpoint", "masked"])
+def test_swiglu_of_infinite_and_nan_gates(form):
+    """g * sigma(g) * u of an infinite gate is infinite (NaN for u = 0 and for -infinity): the block's scale and
+    codes are the quantizer's definition on that, and blocks of numbers stay as they are."""
+    h, F, put = non_finite_input()
+    clean = torch.where(torch.isfinite(h), h, torch.ones((), dtype=h.dtype))
+    if form == "masked":
+        def call(x):
+            q, s = binding.swiglu_quantize_masked(x.cuda()[None], torch.tensor([len(x)], dtype=torch.int32, device="cuda"))
+            return q[0].cpu(), s[0].cpu()
+    else:
+        def call(x):
+            return [t.cpu() for t in binding.swiglu_quantize(x.cuda(), checkpoint=form == "checkpoint")[:2]]
+    (q, s), (cq, cs) = call(h), call(clean)
+    g, u = h[:, :F].float(), h[:, F:].float()
+    wq, ws = plain.quantize_f32(g / (1 + torch.exp(-g)) * u)
+    for i in range(s.shape[0]):
+        for j in range(s.shape[1]):
+            sl = (slice(i * 128, min(len(h), i * 128 + 128)), slice(j * 128, j * 128 + 128))
+            if (i, j) not in put:
+                assert s[i, j] == cs[i, j] and torch.equal(q[sl], cq[sl]), (i, j)
+                continue
+            assert not torch.isfinite(ws[i, j])
+            assert torch.equal(s[i, j].nan_to_num(nan=-1.0), ws[i, j].nan_to_num(nan=-1.0)), (i, j)
+            nan = (wq[sl] & 0x7F) == 0x7F
+            assert bool(nan.any()) and torch.equal((q[sl] & 0x7F) == 0x7F, nan), (i, j)
+            assert torch.equal(q[sl][~nan], wq[sl][~nan]), (i, j)
+
+
+def test_checkpoint_of_non_finite_values():
+    """The checkpoint is dg_quantize_1x128's output where rows hold infinities and NaN, too."""
+    h = non_finite_input()[0].cuda()
+    _, _, h8, sh = binding.swiglu_quantize(h, checkpoint=True)
+    q, s = binding.quantize_1x128(h)
+    assert torch.equal(sh.nan_to_num(nan=-1.0), s.nan_to_num(nan=-1.0)) and torch.equal(h8, q)
+    assert not bool(torch.isfinite(sh).all())
