@@ -261,7 +261,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             mbar_init(&tempty[b], 8);
         }
         *abort_flag = 0;
-        *groups_bad = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
@@ -273,18 +272,19 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     grid_dep_wait();  // inputs and outputs are touched only from here on
     grid_dep_launch_dependents();
-    if (p.offsets && warp == 3) {
-        // the contract of group_offsets, as in the forward product: a violation computes nothing
+    if (warp == 3) {
+        // the contract of group_offsets, as in the forward product: a violation computes nothing.
+        // This warp alone writes the flag, so that no other thread's first value can follow it.
         bool bad = false;
-        for (int g = lane; g <= p.G; g += 32) {
+        for (int g = lane; p.offsets && g <= p.G; g += 32) {
             const int o = __ldg(p.offsets + g);
             const int prev = g > 0 ? __ldg(p.offsets + g - 1) : 0;
             bad |= (o & 127) != 0 || o < prev || o > p.cap || (g == 0 && o != 0);
         }
         bad = __any_sync(0xFFFFFFFFu, bad);
-        if (lane == 0 && bad) {
-            *groups_bad = 1;
-            if (blockIdx.x == 0) record_failure(p.status, kStatusBadGroups, 3, -1);
+        if (lane == 0) {
+            *groups_bad = bad ? 1 : 0;
+            if (bad && blockIdx.x == 0) record_failure(p.status, kStatusBadGroups, 3, -1);
         }
     }
     tc_fence_before();

@@ -224,7 +224,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(&tempty[b], 8);
         }
         *abort_flag = 0;
-        *groups_bad = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
@@ -240,7 +239,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (GMODE == kContiguous && warp == 3) {
         // group_offsets must start at 0, not decrease, hold multiples of 128 and end
         // within the rows allocated; otherwise nothing is computed and the status
-        // word says why (memory stays safe either way: TMA clips every box)
+        // word says why.  This warp alone writes the flag, so that no other thread's
+        // first value can follow it.
         const int cap = p.num_m_cap * 128;
         bool bad = false;
         for (int g = lane; g <= p.G; g += 32) {
@@ -249,9 +249,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             bad |= (o & 127) != 0 || o < prev || o > cap || (g == 0 && o != 0);
         }
         bad = __any_sync(0xFFFFFFFFu, bad);
-        if (lane == 0 && bad) {
-            *groups_bad = 1;
-            if (blockIdx.x == 0) record_failure(p.status, kStatusBadGroups, 3, -1);
+        if (lane == 0) {
+            *groups_bad = bad ? 1 : 0;
+            if (bad && blockIdx.x == 0) record_failure(p.status, kStatusBadGroups, 3, -1);
         }
     }
     if (GMODE == kMasked && warp == 3) {
