@@ -146,6 +146,12 @@ PyObject *wrap_all(const Ts &...ts) {
 
 constexpr int64_t kIntMax = 0x7FFFFFFF;
 
+// The sorts' outputs follow G and M_max, which no tensor bounds: the library's limits on them
+// are looked at before anything is allocated.
+void sort_sizes(int64_t G, int64_t M_max, const char *what) {
+    if (G < 1 || G > 1024 || M_max > kIntMax / G) status(DG_ERR_SHAPE, what);
+}
+
 // Scratch for one call, from the call's stream: an empty tensor where none is needed.
 Tensor scratch(int64_t bytes, int dev) { return bytes == 0 ? Tensor() : make(kU8, {bytes}, dev); }
 
@@ -159,6 +165,7 @@ PyObject *moe_sort(PyObject *, PyObject *const *a, Py_ssize_t) {
     TORCH_CHECK_VALUE(k <= kIntMax, "topk_ids is too wide");
     const bool wide = ids.scalar_type() == at::kLong;
     void *pi = checked(ids, "topk_ids", wide ? at::kLong : kI32, {T, k}, dev);
+    sort_sizes(G, 0, "dg_moe_sort");
     const int64_t S = T * k, cap = a[4] == Py_None ? (S + 127 * std::min(G, S)) / 128 * 128 : tensor(a[4], "slot_of_row").numel();
     const Tensor offsets = out(a[2], "offsets", kI32, {G + 1}, dev);
     const Tensor row = out(a[3], "row_of_slot", kI32, {T, k}, dev);
@@ -182,6 +189,7 @@ PyObject *moe_sort_masked(PyObject *, PyObject *const *a, Py_ssize_t) {
     TORCH_CHECK_VALUE(k <= kIntMax, "topk_ids is too wide");
     const bool wide = ids.scalar_type() == at::kLong;
     void *pi = checked(ids, "topk_ids", wide ? at::kLong : kI32, {T, k}, dev);
+    sort_sizes(G, M_max, "dg_moe_sort_masked");
     const Tensor m = out(a[3], "masked_m", kI32, {G}, dev);
     const Tensor row = out(a[4], "row_of_slot", kI32, {T, k}, dev);
     const Tensor slot = out(a[5], "slot_of_row", kI32, {G * M_max}, dev);

@@ -538,3 +538,17 @@ def test_binding_refuses_wrong_types_shapes_and_strides():
         binding.moe_sort(row.float(), 4)
     with pytest.raises(binding.DGError):
         binding.moe_sort(row, 4, slot_of_row=slot)  # a row map too small for the worst case
+
+
+@pytest.mark.parametrize("G,m_max", [(0, 1), (1025, 1), (2**31 - 1, 1), (1024, 2**21), (2**31 - 1, 2**31 - 1), (3, 2**31 - 1)])
+def test_sorts_refuse_sizes_before_they_allocate(G, m_max):
+    """G and M_max that the library refuses are refused as such, whatever their outputs would take."""
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    held = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    with pytest.raises(binding.DGError):
+        binding.moe_sort_masked(ids, G, m_max)
+    if not 1 <= G <= 1024:
+        with pytest.raises(binding.DGError):
+            binding.moe_sort(ids, G)
+    assert torch.cuda.max_memory_allocated() == held
