@@ -22,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdg.so")
 EXT_SRC = os.path.join(CSRC, "torch_binding.cpp")
 EXT = os.path.join(HERE, "_dgtorch.so")
+EXT_FOR = os.path.join(HERE, "_build", "_dgtorch.for")  # the torch and Python that EXT was built against
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -45,11 +46,21 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _ext_stale(built_for: str) -> bool:
+    """Whether EXT is missing, older than its sources, or built against another torch or Python."""
+    if not (os.path.exists(EXT) and os.path.exists(EXT_FOR)):
+        return True
+    with open(EXT_FOR) as f:
+        if f.read() != built_for:
+            return True
+    return any(os.path.getmtime(d) > os.path.getmtime(EXT) for d in (EXT_SRC, os.path.join(ROOT, "include", "dg.h")))
+
+
 def _build_ext(force: bool) -> None:
-    deps = [EXT_SRC, os.path.join(ROOT, "include", "dg.h")]
-    if not force and os.path.exists(EXT) and all(os.path.getmtime(d) <= os.path.getmtime(EXT) for d in deps):
-        return
     import torch
+    built_for = f"torch {torch.__version__} in {os.path.dirname(torch.__file__)}, {sys.implementation.cache_tag}\n"
+    if not force and not _ext_stale(built_for):
+        return
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
     includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
@@ -63,6 +74,9 @@ def _build_ext(force: bool) -> None:
             "-ltorch_python", "-L", HERE, "-l:libdg.so", "-Wl,-rpath,$ORIGIN"]
     subprocess.check_call(cmd)
     os.replace(tmp, EXT)
+    os.makedirs(os.path.dirname(EXT_FOR), exist_ok=True)
+    with open(EXT_FOR, "w") as f:
+        f.write(built_for)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
