@@ -315,3 +315,46 @@ def test_bounded_wait_reports_timeout_and_context_survives():
     assert torch.equal(binding.wgrad_blockscaled(dy, sdy, x, sx), want[0])
     assert torch.equal(binding.dgrad_blockscaled(dy, sdy, w, sw), want[1])
     assert binding.last_device_status() == 0
+
+
+# many rows and too many tiles to cut the sum into parts: whole sums of the four-stage form
+WHOLE_LONG = [(3300, 1296, 1040), (3201, 2064, 784)]
+
+
+@pytest.mark.parametrize("M,N,K", WHOLE_LONG)
+@pytest.mark.parametrize("dtype,accumulate", [(F32, False), (F32, True), (BF16, False)])
+def test_wgrad_of_long_sums_in_whole(M, N, K, dtype, accumulate):
+    assert binding.lib().dg_fp8_wgrad_workspace(M, N, K) == 0 and M // 128 > 24
+    dy, sdy = quantized(M, N, M + N, 1e-3)
+    x, sx = quantized(M, K, M + K)
+    a, b = plain.decode(dy.cpu(), sdy.cpu()).t(), plain.decode(x.cpu(), sx.cpu())
+    base = torch.zeros((N, K))
+    if accumulate:
+        base = torch.randn((N, K), generator=torch.Generator().manual_seed(1)) * 1e-2
+    C = torch.full((N + 2, K), -3.0, dtype=dtype, device="cuda")
+    C[1:-1] = base.cuda() if accumulate else float("nan")
+    binding.wgrad_blockscaled(dy, sdy, x, sx, C=C[1:-1], accumulate=accumulate)
+    # the addition to C rounds once more
+    check(C[1:-1], base.double() + a @ b, base.double().abs() + a.abs() @ b.abs(), -(-M // 128) + 1, dtype)
+    assert bool((C[0] == -3.0).all()) and bool((C[-1] == -3.0).all())
+    assert binding.last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,accumulate", [(F32, False), (F32, True), (BF16, False)])
+def test_grouped_wgrad_of_long_sums(dtype, accumulate):
+    """More than 24 row blocks an expert on average, one expert without rows and one with a few."""
+    counts, N, K = [6500, 0, 130, 7000], 256, 528
+    off, cap, dy, x, w, off_d = grouped(counts, N, K, 9)
+    assert cap // 128 > 24 * len(counts)
+    before = torch.randn((4, N, K), generator=torch.Generator().manual_seed(2)) * 1e-2 if accumulate else torch.zeros((4, N, K))
+    C = before.to(dtype).cuda() if accumulate else torch.full((4, N, K), float("nan"), dtype=dtype, device="cuda")
+    binding.grouped_wgrad_contiguous(*dy, *x, off_d, C=C, accumulate=accumulate)
+    for g in range(4):
+        a, b = int(off[g]), int(off[g + 1])
+        if a == b:
+            assert torch.equal(C[g].cpu(), before[g].to(dtype))
+            continue
+        p = plain.decode(dy[0][a:b].cpu(), dy[1][a // 128:b // 128].cpu()).t()
+        r = plain.decode(x[0][a:b].cpu(), x[1][a // 128:b // 128].cpu())
+        check(C[g], p @ r + before[g].double(), p.abs() @ r.abs() + before[g].double().abs(), (b - a) // 128 + 1, dtype, f"expert {g}")
+    assert binding.last_device_status() == 0

@@ -552,3 +552,30 @@ def test_sorts_refuse_sizes_before_they_allocate(G, m_max):
         with pytest.raises(binding.DGError):
             binding.moe_sort(ids, G)
     assert torch.cuda.max_memory_allocated() == held
+
+
+@pytest.mark.parametrize("T,k,G,m_max", [(0, 2, 8, 6912), (1, 8, 64, 4096), (128, 2, 8, 6912), (1024, 2, 8, 6912),
+                                         (1025, 2, 8, 6912), (20000, 2, 8, 6912), (100, 8, 1024, 3001)])
+def test_sort_masked_into_deep_slabs(T, k, G, m_max):
+    """Slabs far deeper than an expert's tokens, by one CTA and in two launches; slabs that overflow."""
+    ids = route(T, k, G, seed=T + G, drop=0.1, dtype=torch.int32)
+    want = plain.sort_masked_plain(ids.numpy(), G, m_max)
+    slot = torch.full((G * m_max,), 7, dtype=torch.int32, device="cuda")
+    got = binding.moe_sort_masked(ids.cuda(), G, m_max, slot_of_row=slot)
+    for a, b, what in zip(got, want, ("masked_m", "row_of_slot", "slot_of_row")):
+        assert np.array_equal(a.cpu().numpy(), b), what
+
+
+@pytest.mark.parametrize("T,k,H", [(300, 1, 400), (1100, 8, 7696)])
+def test_dispatch_of_non_finite_tokens_is_the_block_quantizer(T, k, H):
+    """Codes bit for bit (a NaN's too) and scales of dg_quantize_blockwise on the gathered rows, in both forms."""
+    x = tokens(T, H, 91).cuda()
+    x[5, 10], x[200, 300], x[7, 200], x[250, H - 1] = float("nan"), float("inf"), -float("inf"), -float("nan")
+    x[:, 128:256] = -x[:, 128:256].abs()
+    off, row, slot = binding.moe_sort(route(T, k, 5, 92).cuda(), 5)
+    used, s_of_row = int(off[-1]), slot.clamp_min(0).long()
+    rows = torch.where((slot >= 0)[:, None], x[s_of_row // k], torch.zeros((), dtype=x.dtype, device="cuda"))[:used]
+    q, s = binding.moe_dispatch_quantize(x, slot, off, k)
+    wq, ws = binding.quantize_blockwise(rows.contiguous())
+    assert torch.equal(q[:used], wq)
+    assert torch.equal(s[:used // 128].nan_to_num(nan=-1.0), ws.nan_to_num(nan=-1.0)) and not bool(torch.isfinite(ws).all())
