@@ -21,12 +21,15 @@
 // expert's row blocks, so its length varies from tile to tile and may be zero (an expert
 // without tokens: zeros are stored), and the scales step by a row of the scale arrays.
 //
-// Measured: dgrad of 8 experts, N = K = 4096, 16384 slots 250 us (2200 TFLOP/s; the forward
-// product of that size 255), dense 4096^3 67.6 us, 8192^3 450 us: bound, as the forward
-// kernel, by the round trip of a partial through tensor memory (tensor pipe 59 % active).
-// wgrad of 64 experts, N = 2048, K = 7168, 32768 slots in FP32 957-1045 us: 3.8 GB of output
-// stored by the warps that also scale the partials, 575 us without the stores, 635 us of
-// stores alone.
+// Measured one call at a time, in brackets twenty in a graph, where the power cap tells: dgrad of 8
+// experts, N = K = 4096, 16384 rows in equal parts 241 us (2280 TFLOP/s; the forward product of that
+// size 241), 16384 slots in unequal parts 264 (276); dense 4096^3 70 (65), 8192^3 479 (511), forward
+// 64 (61) and 444 (460): bound, as the forward kernel, by the round trip of a partial through tensor
+// memory (tensor pipe 59 % active).  wgrad dense 4096^3 77 (72), 8192^3 510 (525); in BF16 70 (66) and
+// 486 (518): as dgrad but for the wider output's stores.  wgrad of 64 experts, N = 2048, K = 7168, 32768
+// slots in FP32 1056 (1138), accumulating, which reads the output too, 1717 (1720), in BF16 735 (846):
+// 3.8 GB of FP32 output stored by the warps that also scale the partials, 575 us without the stores,
+// 635 us of stores alone.
 #include <cuda_bf16.h>
 
 #include "dg_device.cuh"
@@ -158,8 +161,8 @@ struct GradUnit {
     int sb_row;                    // row of B's scales at block 0
 };
 
-// Row tiles of a raster group: as in the forward kernel 32 dense (8192^3: dgrad 450 us against
-// 463 with 8, wgrad 5 % shorter), 8 grouped.
+// Row tiles of a raster group: as in the forward kernel 32 dense (8192^3, side by side: dgrad 450 us
+// against 463 with 8, wgrad 5 % shorter), 8 grouped.
 __device__ __forceinline__ int grad_raster(const GradParams &p) { return p.offsets ? 8 : 32; }
 
 template <int MODE>
@@ -663,7 +666,7 @@ dg_status_t launch_dgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t 
 
 // Operand stages against output boxes.  An output tile is 128 KB (FP32): with few blocks of
 // contraction a tile its stores matter more than a fourth stage, with many the stages do.
-// Measured (three stages and two boxes, four and one): 64 experts of N = 2048, K = 7168 over
+// Measured side by side, back to back (three stages and two boxes, four and one): 64 experts of N = 2048, K = 7168 over
 // 32768 slots, 4 blocks a tile on average, 975-1045 and 1090-1120 us; 8 experts of 4096^2, 16
 // blocks, 320 and 320; 4096^3, 32 blocks, 79.8 and 75.7; 8192^3, 64 blocks, 535 and 525.
 constexpr int64_t kWgradLongBlocks = 24;

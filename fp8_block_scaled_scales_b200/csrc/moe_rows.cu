@@ -525,7 +525,9 @@ static int dispatch_cols(int64_t row_ctas, int64_t Cb, int num_sms, int64_t wave
 // (it reads the tokens twice more, the other one k times from L2), or so little work that its
 // two further launches cost more than they save.  Measured, this form against the other: k = 8,
 // H = 7168: 16384 tokens 256 and 362 us, 4096 77 and 88, 1024 32 and 36, 64 29 and 23; H = 2048:
-// 4096 tokens 28 and 28, 1024 19 and 13.  4096 tokens of 7168, k = 4: 62 and 54.
+// 4096 tokens 28 and 28, 1024 19 and 13.  4096 tokens of 7168, k = 4: 62 and 54.  The bound on the
+// codes lies just above the tie, and gives away the 4 us of 1024 tokens of 7168, which have fewer;
+// k of 5 to 7 and weights were not measured on both sides.
 constexpr int kTokenFormSlots = 8;
 constexpr int64_t kTokenFormWork = (1LL << 26) + 1;  // codes
 int64_t dispatch_workspace(int64_t T, int k, int64_t H, int64_t rows) {

@@ -17,7 +17,11 @@
 // that, two launches over consecutive chunks, one CTA each: the first ranks the slots inside
 // their chunk and writes the chunk's counts; in the second every CTA adds up the counts of
 // all chunks (a few hundred KB from L2) and hands out the rows.  Bound by latency: in a graph
-// 3.2 us for 8 slots into 64 slabs of 128 rows, 7.9 us for 131072 slots of 256 experts.
+// 3.3 us for 8 slots into 64 slabs of 128 rows, 7.9 us for 131072 slots of 256 experts.
+//
+// The form goes by the slots alone, and the one CTA also writes the row map of all slabs: 8 slots
+// into 64 slabs of 1024 rows take 10.7 us, of 4096 rows 37 us, 2048 slots into 8 slabs of 6912
+// rows 10.7 us; 2050 slots, in two launches, 7.7 us.
 #include "dg_device.cuh"
 #include "train_internal.h"
 

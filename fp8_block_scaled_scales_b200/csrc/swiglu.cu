@@ -9,9 +9,10 @@
 //             dg = dA * u * sigma(g) * (1 + g * (1 - sigma(g))),   du = dA * g * sigma(g);
 //             Q, S = the block quantizer's definition on [dg | du], ready for both gradient
 //             products.
-// Every step is within about one FP32 rounding, the exponential within two: a code differs
-// from the exact value's only next to a rounding boundary, and each wrong ulp would show
-// there for a whole block through its scale.
+// Every step rounds about once in FP32, but the exponential's argument is one rounded product:
+// exp(-g) may be off by 2 + 1.2 |g| units of 2^-23, and sigma with it by that times 1 - sigma, so
+// for negative gates in full.  A code differs from the exact value's only next to a rounding
+// boundary, and each wrong ulp would show there for a whole block through its scale.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -45,7 +46,8 @@ __device__ __forceinline__ void one_plus_exp(float2 x, float2 &d, float2 &r) {
 // -n / d from r = -1/d: the product corrected by its remainder (Markstein, as in
 // quant_f32.cuh).  With the approximate reciprocal alone, and a / s as a product with one, the kernels
 // were a tenth faster and a third of the inputs tried had half as much error again in the
-// codes as a plain FP32 evaluation; as it stands they have the same.  An infinite n gives NaN.
+// codes as a plain FP32 evaluation; as it stands they have the same on the inputs tried.  An
+// infinite n gives NaN.
 __device__ __forceinline__ float2 negated_quotient(float2 n, float2 d, float2 r) {
     const float2 z = __fmul2_rn(n, r);
     return __ffma2_rn(__ffma2_rn(z, d, n), r, z);
