@@ -34,7 +34,11 @@ EXPORTS = ("dg_quantize_blockwise", "dg_quantize_blockwise_masked", "dg_fp8_gemm
            "dg_moe_combine", "dg_moe_combine_backward", "dg_swiglu_quantize", "dg_swiglu_quantize_masked",
            "dg_swiglu_quantize_backward", "dg_fp8_dgrad_blockscaled", "dg_fp8_dgrad_workspace", "dg_fp8_wgrad_blockscaled",
            "dg_fp8_wgrad_workspace",
-           "dg_fp8_grouped_dgrad_contiguous", "dg_fp8_grouped_wgrad_contiguous")
+           "dg_fp8_grouped_dgrad_contiguous", "dg_fp8_grouped_wgrad_contiguous",
+           "dg_moe_route", "dg_moe_route_workspace", "dg_moe_route_backward",
+           "dg_rmsnorm_residual", "dg_rmsnorm_residual_quantize", "dg_rmsnorm_residual_backward",
+           "dg_rmsnorm_residual_backward_workspace",
+           "dg_grad_norm", "dg_grad_norm_workspace", "dg_grad_clip", "dg_grad_norm_clip")
 
 
 class DGError(RuntimeError):
@@ -89,11 +93,20 @@ def lib() -> ctypes.CDLL:
     L.dg_fp8_dgrad_workspace.argtypes = L.dg_fp8_wgrad_workspace.argtypes = [i64, i64, i64]
     L.dg_fp8_grouped_dgrad_contiguous.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, vp]
     L.dg_fp8_grouped_wgrad_contiguous.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, i64, i32, i64, i64, vp]
+    L.dg_moe_route.argtypes = [vp, i32, vp, vp, vp, i64, i32, i32, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.dg_moe_route_workspace.argtypes = [i64, i32]
+    L.dg_moe_route_backward.argtypes = [vp, i32, vp, vp, vp, vp, vp, i64, i32, i32, vp, vp]
+    L.dg_rmsnorm_residual.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp]
+    L.dg_rmsnorm_residual_quantize.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp]
+    L.dg_rmsnorm_residual_backward.argtypes = [vp] * 10 + [i64, i64] + [vp] * 6 + [i64, vp]
+    L.dg_rmsnorm_residual_backward_workspace.argtypes = [i64, i64, i32, i32]
+    L.dg_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, i64, vp]
+    L.dg_grad_norm_workspace.argtypes = [i64]
+    L.dg_grad_clip.argtypes = [vp, vp, vp, i64, vp, vp, vp, vp]
+    L.dg_grad_norm_clip.argtypes = [vp, vp, vp, i64, vp, vp, vp, vp, i64, vp]
     for f in EXPORTS:
-        if f.startswith(("dg_moe_", "dg_swiglu_")) or "grad" in f:
-            getattr(L, f).restype = ctypes.c_int
-    for f in (L.dg_moe_sort_workspace, L.dg_moe_dispatch_workspace, L.dg_fp8_dgrad_workspace, L.dg_fp8_wgrad_workspace):
-        f.restype = i64
+        if f.startswith(("dg_moe_", "dg_swiglu_", "dg_rmsnorm_")) or "grad" in f:
+            getattr(L, f).restype = i64 if f.endswith("_workspace") else ctypes.c_int
     L.dg_get_last_device_status.argtypes = [vp]
     L.dg_status_string.restype = ctypes.c_char_p
     L.dg_status_string.argtypes = [ctypes.c_int]
@@ -388,6 +401,84 @@ def grouped_wgrad_contiguous(dY, sdY, X, sX, offsets, C=None, accumulate: bool =
     """Weight gradients C [G][N][K] expert by expert, from rows [offsets[g], offsets[g+1]) of dY
     [M_cap][N] and X [M_cap][K]; an expert without rows gets zeros (accumulate: keeps its C)."""
     return (_ext or _native()).wgrad(dY, sdY, X, sX, _given(offsets), C, accumulate, _grad_dtype(dtype), stream)
+
+
+# --------------------------------------------------------------- around the expert layer
+_SCORES = {"softmax": False, "sigmoid": True}
+
+
+def _sigmoid(score):
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {', '.join(_SCORES)}, not {score!r}")
+    return _SCORES[score]
+
+
+def moe_route(logits, k: int, score: str = "softmax", bias=None, mask=None, renormalize: bool = True, scale: float = 1.0,
+              balance: bool = False, topk_ids=None, weights=None, counts=None, loss=None, dprob=None, stream=None):
+    """logits [T][G] (float32 or bfloat16) -> the k experts of every token, (topk_ids [T][k]
+    int32, weights [T][k] float32), largest score first, the lowest id among equals.
+
+    score "softmax" (over the experts) or "sigmoid".  bias [G] (float32) is added to the scores
+    for the choice only.  mask [T] (bool or uint8): tokens where it is 0 are left out.  weights: the
+    chosen scores, divided by their sum if renormalize, times scale.  An expert whose logit is
+    -inf or NaN is not chosen; slots without an expert hold id -1 and weight 0 (moe_sort drops
+    them).  balance=True also returns counts [G] (int32, slots per expert), loss (float32, 0-dim)
+    and dprob [G] (float32): loss = G * sum_e (share of the slots) * (mean probability), and
+    its gradient with respect to every token's probability of e."""
+    return (_ext or _native()).moe_route(logits, k, _sigmoid(score), bias, mask, renormalize, scale, balance, topk_ids,
+                                         weights, counts, loss, dprob, stream)
+
+
+def moe_route_backward(logits, topk_ids, dweights=None, dprob=None, dloss=None, score: str = "softmax",
+                       renormalize: bool = True, scale: float = 1.0, dlogits=None, stream=None):
+    """Gradient of moe_route with respect to logits (dlogits, of their type): from dweights [T][k]
+    (float32; moe_combine_backward's) and, for the balance loss, its dprob [G] and dloss (float32,
+    0-dim, the loss's gradient).  score, renormalize and scale as in the forward call."""
+    return (_ext or _native()).moe_route_backward(logits, topk_ids, dweights, dprob, dloss, _sigmoid(score), renormalize,
+                                                  scale, dlogits, stream)
+
+
+def rmsnorm_residual(x, weight, y=None, gate=None, post_weight=None, alpha: float = 1.0, eps: float = 1e-6, n=None, r=None,
+                     rstd=None, rstd_y=None, stream=None):
+    """The norm after a block, its gate, the scaled residual and the norm before the next block:
+    (n, r, rstd, rstd_y) with u = rmsnorm(y) * post_weight (or y), r = alpha * x + gate * u,
+    n = rmsnorm(r) * weight.  x, y, n, r [T][H] bfloat16; weight, gate, post_weight [H], all float32
+    or all bfloat16; rstd, rstd_y [T] float32 (for the backward pass; rstd_y None without
+    post_weight).  Without y (before the first block) r is x.  r=x updates x in place."""
+    return (_ext or _native()).rmsnorm_residual(x, weight, y, gate, post_weight, alpha, eps, n, r, rstd, rstd_y, stream)
+
+
+def rmsnorm_residual_quantize(x, weight, y=None, gate=None, post_weight=None, alpha: float = 1.0, eps: float = 1e-6, q=None,
+                              s=None, r=None, stream=None):
+    """rmsnorm_residual with n quantized for gemm_1x128: (q codes [T][H], s scales
+    [ceil(H/128)][T], r)."""
+    return (_ext or _native()).rmsnorm_residual_quantize(x, weight, y, gate, post_weight, alpha, eps, q, s, r, stream)
+
+
+def rmsnorm_residual_backward(dn, r, rstd, weight, dr=None, y=None, rstd_y=None, gate=None, post_weight=None,
+                              alpha: float = 1.0, dx=None, dy=None, dweight=None, dgate=None, dpost_weight=None, stream=None):
+    """Gradient of rmsnorm_residual, from dn and dr (None: zeros), the gradients of n and r, and the
+    r, rstd and rstd_y that it returned: (dx, dy, dweight, dgate, dpost_weight), dx and dy [T][H]
+    bfloat16, the others [H] float32; None for what the forward call did not have."""
+    return (_ext or _native()).rmsnorm_residual_backward(dn, r, rstd, weight, dr, y, rstd_y, gate, post_weight, alpha, dx, dy,
+                                                         dweight, dgate, dpost_weight, stream)
+
+
+def grad_norm(grads, norm=None, stream=None):
+    """sqrt of the sum of squares over all tensors of grads (a sequence; float32 or bfloat16, contiguous):
+    float32, 0-dim, on the device."""
+    return (_ext or _native()).grad_norm(grads, norm, stream)
+
+
+def grad_clip(grads, norm, max_norm: float, out=None, stream=None) -> None:
+    """grads *= max_norm / norm where norm (float32, 0-dim, on the device) exceeds max_norm, in
+    place, or written to the tensors of out.  A norm that is not finite clips nothing."""
+    return (_ext or _native()).grad_clip(grads, norm, max_norm, out, stream)
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, norm=None, stream=None):
+    """grad_norm, and grad_clip by it; returns the norm before clipping."""
+    return (_ext or _native()).clip_grad_norm(grads, max_norm, out, norm, stream)
 
 
 def last_device_status(stream=None) -> int:

@@ -1,4 +1,4 @@
-// The expert-layer and gradient calls for Python: argument checks, output allocation and the
+// The expert-layer and gradient calls, and those around the expert layer, for Python: argument checks, output allocation and the
 // call through the C ABI (include/dg.h), in one native function each.  A decode step is a
 // chain of calls whose kernels take a few microseconds; done in Python, the checks, three
 // allocations and the marshalling of a dozen arguments cost 9 to 17 us a call, here 3 to 8.
@@ -15,6 +15,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <vector>
 
 #include "../../include/dg.h"
 
@@ -441,6 +443,281 @@ PyObject *wgrad(PyObject *, PyObject *const *a, Py_ssize_t) {
     END_HANDLE_TH_ERRORS
 }
 
+float number(PyObject *o, const char *name) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw python_error();
+    const float f = static_cast<float>(v);
+    TORCH_CHECK_VALUE(f - f == 0.0f, name, " must be finite in float32, not ", v);
+    return f;
+}
+
+// logits [T][G], float32 or bfloat16
+const void *scores(const Tensor &z, const char *name, int dev, bool &bf16) {
+    bf16 = z.scalar_type() == kBF16;
+    return checked(z, name, bf16 ? kBF16 : kF32, {z.size(0), z.size(1)}, dev);
+}
+
+// (logits, k, sigmoid, bias, mask, renormalize, scale, balance, topk_ids, weights, counts, loss, dprob, stream)
+PyObject *moe_route(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const Tensor &z = tensor(a[0], "logits");
+    const int dev = device_of(z, "logits", 2);
+    const CallStream st(a[13], dev);
+    const int64_t T = z.size(0), G = z.size(1), k = integer(a[1], "k", 0, kIntMax);
+    bool bf16;
+    const void *pz = scores(z, "logits", dev, bf16);
+    const auto *bias = in_or_null<float>(a[3], "bias", kF32, {G}, dev);
+    const uint8_t *mask = nullptr;
+    if (a[4] != Py_None) {
+        const Tensor &m = tensor(a[4], "mask");
+        mask = static_cast<const uint8_t *>(checked(m, "mask", m.scalar_type() == kU8 ? kU8 : at::kBool, {T}, dev));
+    }
+    const bool balance = truth(a[7]);
+    const dg_route_options_t options = {truth(a[2]) ? DG_SCORE_SIGMOID : DG_SCORE_SOFTMAX, truth(a[5]), number(a[6], "scale")};
+    TORCH_CHECK_VALUE(balance || (a[10] == Py_None && a[11] == Py_None && a[12] == Py_None),
+                      "counts, loss and dprob are outputs of balance=True");
+    // the outputs follow k, which no tensor bounds
+    if (G < 1 || G > 1024 || k < 1 || k > 32 || k > G) status(DG_ERR_SHAPE, "dg_moe_route");
+    const Tensor ids = out(a[8], "topk_ids", kI32, {T, k}, dev);
+    const Tensor w = out(a[9], "weights", kF32, {T, k}, dev);
+    if (!balance) {
+        status(dg_moe_route(pz, bf16, &options, bias, mask, T, static_cast<int>(G), static_cast<int>(k),
+                            ptr<int32_t>(ids), ptr<float>(w), nullptr, nullptr, nullptr, nullptr, 0, st),
+               "dg_moe_route");
+        return wrap_all(ids, w);
+    }
+    const Tensor counts = out(a[10], "counts", kI32, {G}, dev);
+    const Tensor loss = out(a[11], "loss", kF32, {}, dev);
+    const Tensor dprob = out(a[12], "dprob", kF32, {G}, dev);
+    const Tensor ws = scratch(dg_moe_route_workspace(T, static_cast<int>(G)), dev);
+    status(dg_moe_route(pz, bf16, &options, bias, mask, T, static_cast<int>(G), static_cast<int>(k),
+                        ptr<int32_t>(ids), ptr<float>(w), ptr<int32_t>(counts), ptr<float>(loss), ptr<float>(dprob),
+                        ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, st),
+           "dg_moe_route");
+    return wrap_all(ids, w, counts, loss, dprob);
+    END_HANDLE_TH_ERRORS
+}
+
+// (logits, topk_ids, dweights, dprob, dloss, sigmoid, renormalize, scale, dlogits, stream)
+PyObject *moe_route_backward(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const Tensor &z = tensor(a[0], "logits"), &ids = tensor(a[1], "topk_ids");
+    const int dev = device_of(z, "logits", 2);
+    const CallStream st(a[9], dev);
+    const int64_t T = z.size(0), G = z.size(1);
+    bool bf16;
+    const void *pz = scores(z, "logits", dev, bf16);
+    TORCH_CHECK_VALUE(ids.dim() == 2 && ids.size(1) <= kIntMax && G <= kIntMax, "topk_ids must have 2 dimensions");
+    const int64_t k = ids.size(1);
+    const auto *pi = in<int32_t>(a[1], "topk_ids", kI32, {T, k}, dev);
+    const auto *dw = in_or_null<float>(a[2], "dweights", kF32, {T, k}, dev);
+    const auto *dprob = in_or_null<float>(a[3], "dprob", kF32, {G}, dev);
+    const auto *dloss = in_or_null<float>(a[4], "dloss", kF32, {}, dev);
+    TORCH_CHECK_VALUE((a[3] == Py_None) == (a[4] == Py_None), "dprob and dloss go together");
+    const dg_route_options_t options = {truth(a[5]) ? DG_SCORE_SIGMOID : DG_SCORE_SOFTMAX, truth(a[6]), number(a[7], "scale")};
+    const Tensor dz = out(a[8], "dlogits", bf16 ? kBF16 : kF32, {T, G}, dev);
+    status(dg_moe_route_backward(pz, bf16, &options, pi, dw, dprob, dloss, T, static_cast<int>(G), static_cast<int>(k),
+                                 ptr(dz), st),
+           "dg_moe_route_backward");
+    return wrap(dz);
+    END_HANDLE_TH_ERRORS
+}
+
+// The inputs that the norms' calls share: x, weight, y, gate and post_weight of a row width.
+struct NormInputs {
+    int dev;
+    int64_t T, H;
+    bool bf16;
+    const void *x, *y, *weight, *gate, *post;
+
+    NormInputs(PyObject *x_, const char *name, PyObject *weight_, PyObject *y_, PyObject *gate_, PyObject *post_) {
+        const Tensor &t = tensor(x_, name), &w = tensor(weight_, "weight");
+        dev = device_of(t, name, 2);
+        T = t.size(0), H = t.size(1);
+        x = checked(t, name, kBF16, {T, H}, dev);
+        bf16 = w.scalar_type() == kBF16;  // the vectors are of one type
+        const auto type = bf16 ? kBF16 : kF32;
+        weight = checked(w, "weight", type, {H}, dev);
+        y = in_or_null(y_, "y", kBF16, {T, H}, dev);
+        gate = in_or_null(gate_, "gate", type, {H}, dev);
+        post = in_or_null(post_, "post_weight", type, {H}, dev);
+        TORCH_CHECK_VALUE(y_ != Py_None || (gate_ == Py_None && post_ == Py_None), "gate and post_weight belong to y");
+    }
+};
+
+// A new reference to a tensor, or None.
+PyObject *wrap_or_none(const Tensor &t) {
+    if (t.defined()) return wrap(t);
+    Py_RETURN_NONE;
+}
+
+template <typename... Ts>
+PyObject *wrap_some(const Ts &...ts) {
+    PyObject *tuple = PyTuple_New(sizeof...(ts));
+    if (!tuple) throw python_error();
+    Py_ssize_t i = 0;
+    (PyTuple_SET_ITEM(tuple, i++, wrap_or_none(ts)), ...);
+    return tuple;
+}
+
+// (x, weight, y, gate, post_weight, alpha, eps, n, r, rstd, rstd_y, stream)
+PyObject *rmsnorm_residual(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const NormInputs in(a[0], "x", a[1], a[2], a[3], a[4]);
+    const CallStream st(a[11], in.dev);
+    const dg_norm_options_t options = {number(a[5], "alpha"), number(a[6], "eps"), in.bf16};
+    TORCH_CHECK_VALUE(a[2] != Py_None || a[8] == Py_None, "r is x itself without y");
+    TORCH_CHECK_VALUE(a[4] != Py_None || a[10] == Py_None, "rstd_y belongs to post_weight");
+    const Tensor n = out(a[7], "n", kBF16, {in.T, in.H}, in.dev);
+    const Tensor r = a[2] == Py_None ? Tensor() : out(a[8], "r", kBF16, {in.T, in.H}, in.dev);
+    const Tensor rstd = out(a[9], "rstd", kF32, {in.T}, in.dev);
+    const Tensor rstd_y = a[4] == Py_None ? Tensor() : out(a[10], "rstd_y", kF32, {in.T}, in.dev);
+    status(dg_rmsnorm_residual(in.x, in.y, in.weight, in.post, in.gate, &options, in.T, in.H, ptr(n),
+                               r.defined() ? ptr(r) : nullptr, ptr<float>(rstd),
+                               rstd_y.defined() ? ptr<float>(rstd_y) : nullptr, st),
+           "dg_rmsnorm_residual");
+    return wrap_some(n, r.defined() ? r : tensor(a[0], "x"), rstd, rstd_y);
+    END_HANDLE_TH_ERRORS
+}
+
+// (x, weight, y, gate, post_weight, alpha, eps, q, s, r, stream)
+PyObject *rmsnorm_residual_quantize(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const NormInputs in(a[0], "x", a[1], a[2], a[3], a[4]);
+    const CallStream st(a[10], in.dev);
+    const dg_norm_options_t options = {number(a[5], "alpha"), number(a[6], "eps"), in.bf16};
+    TORCH_CHECK_VALUE(a[2] != Py_None || a[9] == Py_None, "r is x itself without y");
+    const Tensor q = out(a[7], "q", kU8, {in.T, in.H}, in.dev);
+    const Tensor s = out(a[8], "s", kF32, {blocks(in.H), in.T}, in.dev);
+    const Tensor r = a[2] == Py_None ? Tensor() : out(a[9], "r", kBF16, {in.T, in.H}, in.dev);
+    status(dg_rmsnorm_residual_quantize(in.x, in.y, in.weight, in.post, in.gate, &options, in.T, in.H,
+                                        ptr<uint8_t>(q), ptr<float>(s), r.defined() ? ptr(r) : nullptr, st),
+           "dg_rmsnorm_residual_quantize");
+    return wrap_some(q, s, r.defined() ? r : tensor(a[0], "x"));
+    END_HANDLE_TH_ERRORS
+}
+
+// (dn, r, rstd, weight, dr, y, rstd_y, gate, post_weight, alpha, dx, dy, dweight, dgate, dpost_weight, stream)
+PyObject *rmsnorm_residual_backward(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const NormInputs v(a[1], "r", a[3], a[5], a[7], a[8]);
+    const CallStream st(a[15], v.dev);
+    const int dev = v.dev;
+    const int64_t T = v.T, H = v.H;
+    const auto type = kBF16;
+    const void *dn = checked(tensor(a[0], "dn"), "dn", type, {T, H}, dev);
+    const auto *rstd = in<float>(a[2], "rstd", kF32, {T}, dev);
+    const void *dr = in_or_null(a[4], "dr", type, {T, H}, dev);
+    const auto *rstd_y = in_or_null<float>(a[6], "rstd_y", kF32, {T}, dev);
+    const bool has_y = a[5] != Py_None, has_gate = a[7] != Py_None, has_post = a[8] != Py_None;
+    TORCH_CHECK_VALUE(has_post == (a[6] != Py_None), "post_weight and rstd_y go together");
+    TORCH_CHECK_VALUE((has_y || a[11] == Py_None) && (has_gate || a[13] == Py_None) && (has_post || a[14] == Py_None),
+                      "dy, dgate and dpost_weight are outputs where y, gate and post_weight are given");
+    const dg_norm_options_t options = {number(a[9], "alpha"), 0.0f, v.bf16};
+    const Tensor dx = out(a[10], "dx", type, {T, H}, dev);
+    const Tensor dy = has_y ? out(a[11], "dy", type, {T, H}, dev) : Tensor();
+    const Tensor dw = out(a[12], "dweight", kF32, {H}, dev);
+    const Tensor dg = has_gate ? out(a[13], "dgate", kF32, {H}, dev) : Tensor();
+    const Tensor dp = has_post ? out(a[14], "dpost_weight", kF32, {H}, dev) : Tensor();
+    const Tensor ws = scratch(dg_rmsnorm_residual_backward_workspace(T, H, has_post, has_gate), dev);
+    status(dg_rmsnorm_residual_backward(dn, dr, v.x, rstd, v.y, rstd_y, v.weight, v.post, v.gate, &options, T, H,
+                                        ptr(dx), has_y ? ptr(dy) : nullptr, ptr<float>(dw),
+                                        has_post ? ptr<float>(dp) : nullptr, has_gate ? ptr<float>(dg) : nullptr,
+                                        ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, st),
+           "dg_rmsnorm_residual_backward");
+    return wrap_some(dx, dy, dw, dg, dp);
+    END_HANDLE_TH_ERRORS
+}
+
+// A sequence of gradients as the C interface's host arrays; `out` None: in place.
+struct Grads {
+    std::vector<void *> in, out;
+    std::vector<int64_t> sizes;
+    std::vector<uint8_t> bf16;
+    int dev = -1;  // the tensors', which has to be the current one
+    bool in_place = true;
+
+    Grads(PyObject *grads, PyObject *outs) {
+        const Items g(grads, "grads");
+        in.reserve(g.size), sizes.reserve(g.size), bf16.reserve(g.size);
+        for (Py_ssize_t i = 0; i < g.size; ++i) {
+            const Tensor &t = tensor(g.items[i], "a gradient");
+            if (i == 0) dev = device_of(t, "a gradient", t.dim());
+            bf16.push_back(t.scalar_type() == kBF16);
+            in.push_back(checked(t, "a gradient", bf16.back() ? kBF16 : kF32, t.sizes(), dev));
+            sizes.push_back(t.numel());
+        }
+        if (g.size == 0) dev = c10::cuda::current_device();
+        if (outs == Py_None) return;
+        in_place = false;
+        const Items o(outs, "out");
+        TORCH_CHECK_VALUE(o.size == g.size, "out must hold ", g.size, " tensors, not ", o.size);
+        out.reserve(o.size);
+        for (Py_ssize_t i = 0; i < o.size; ++i)
+            out.push_back(checked(tensor(o.items[i], "an output"), "an output", bf16[i] ? kBF16 : kF32,
+                                  tensor(g.items[i], "a gradient").sizes(), dev));
+    }
+
+    int64_t count() const { return static_cast<int64_t>(in.size()); }
+    void *const *outs() const { return in_place ? nullptr : out.data(); }
+
+private:
+    struct Items {  // a list or tuple, held while it is read
+        PyObject *held, **items;
+        Py_ssize_t size;
+        Items(PyObject *o, const char *name) {
+            TORCH_CHECK_TYPE(!THPVariable_Check(o), name, " must be a sequence of tensors");
+            held = PySequence_Fast(o, "expected a sequence of tensors");
+            if (!held) throw python_error();
+            items = PySequence_Fast_ITEMS(held);
+            size = PySequence_Fast_GET_SIZE(held);
+        }
+        ~Items() { Py_DECREF(held); }
+        Items(const Items &) = delete;
+    };
+};
+
+// (grads, norm, stream)
+PyObject *grad_norm(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const Grads g(a[0], Py_None);
+    const CallStream st(a[2], g.dev);
+    const Tensor norm = out(a[1], "norm", kF32, {}, g.dev);
+    const Tensor ws = scratch(dg_grad_norm_workspace(g.count()), g.dev);
+    status(dg_grad_norm(g.in.data(), g.sizes.data(), g.bf16.data(), g.count(), ptr<float>(norm),
+                        ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, st),
+           "dg_grad_norm");
+    return wrap(norm);
+    END_HANDLE_TH_ERRORS
+}
+
+// (grads, norm, max_norm, out, stream)
+PyObject *grad_clip(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const Grads g(a[0], a[3]);
+    const CallStream st(a[4], g.dev);
+    const auto *norm = in<float>(a[1], "norm", kF32, {}, g.dev);
+    const auto limit = number(a[2], "max_norm");
+    status(dg_grad_clip(g.in.data(), g.sizes.data(), g.bf16.data(), g.count(), norm, &limit, g.outs(), st), "dg_grad_clip");
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// (grads, max_norm, out, norm, stream)
+PyObject *clip_grad_norm(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const Grads g(a[0], a[2]);
+    const CallStream st(a[4], g.dev);
+    const auto limit = number(a[1], "max_norm");
+    const Tensor norm = out(a[3], "norm", kF32, {}, g.dev);
+    const Tensor ws = scratch(dg_grad_norm_workspace(g.count()), g.dev);
+    status(dg_grad_norm_clip(g.in.data(), g.sizes.data(), g.bf16.data(), g.count(), &limit, g.outs(), ptr<float>(norm),
+                             ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, st),
+           "dg_grad_norm_clip");
+    return wrap(norm);
+    END_HANDLE_TH_ERRORS
+}
+
 // (exception class): what a status is raised as
 PyObject *set_error(PyObject *, PyObject *cls) {
     Py_INCREF(cls);
@@ -473,6 +750,14 @@ PyMethodDef methods[] = {DG_METHOD(moe_sort, 6),
                          DG_METHOD(swiglu_quantize_backward, 7),
                          DG_METHOD(dgrad, 7),
                          DG_METHOD(wgrad, 9),
+                         DG_METHOD(moe_route, 14),
+                         DG_METHOD(moe_route_backward, 10),
+                         DG_METHOD(rmsnorm_residual, 12),
+                         DG_METHOD(rmsnorm_residual_quantize, 11),
+                         DG_METHOD(rmsnorm_residual_backward, 16),
+                         DG_METHOD(grad_norm, 3),
+                         DG_METHOD(grad_clip, 5),
+                         DG_METHOD(clip_grad_norm, 5),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

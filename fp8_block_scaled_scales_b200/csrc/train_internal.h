@@ -66,4 +66,70 @@ int64_t grad_workspace(bool wgrad, int64_t M, int64_t N, int64_t K);
 dg_status_t launch_dgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream);
 dg_status_t launch_wgrad(const GradArgs &a, const DeviceInfo &dev, cudaStream_t stream);
 
+// moe_route.cu.  counts, loss and dprob: all null, or none (then workspace: route_workspace bytes).
+struct RouteArgs {
+    const void *logits;  // [T][G]
+    bool bf16, sigmoid, renormalize;
+    float scale;
+    const float *bias;    // [G] or null
+    const uint8_t *mask;  // [T] or null
+    int64_t T;
+    int G, k;
+    int32_t *ids;
+    float *weights;
+    int32_t *counts;
+    float *loss, *dprob;
+    void *workspace;
+};
+struct RouteBackwardArgs {
+    const void *logits;
+    bool bf16, sigmoid, renormalize;
+    float scale;
+    const int32_t *ids;
+    const float *dweights, *dprob, *dloss;  // dprob and dloss: both null, or neither
+    int64_t T;
+    int G, k;
+    void *dlogits;
+};
+int64_t route_workspace(int64_t T, int G);
+dg_status_t launch_route(const RouteArgs &a, const DeviceInfo &dev, cudaStream_t stream);
+dg_status_t launch_route_backward(const RouteBackwardArgs &a, const DeviceInfo &dev, cudaStream_t stream);
+
+// rmsnorm.cu.  y, post, gate null where absent; n, or q and s_t; T > 0 and H > 0 (backward: T >= 0).
+struct NormArgs {
+    const void *x, *y, *weight, *post, *gate;
+    bool vec_bf16;
+    float alpha, eps;
+    int64_t T, H;
+    void *n, *r;
+    uint8_t *q;
+    float *s_t, *rstd, *rstd_y;
+};
+struct NormBackwardArgs {
+    const void *dn, *dr, *r, *y, *weight, *post, *gate;
+    const float *rstd, *rstd_y;
+    bool vec_bf16;
+    float alpha;
+    int64_t T, H;
+    void *dx, *dy;
+    float *dweight, *dpost, *dgate;
+    void *workspace;  // rmsnorm_backward_workspace bytes
+};
+int64_t rmsnorm_backward_workspace(int64_t T, int64_t H, bool post, bool gate);
+dg_status_t launch_rmsnorm(const NormArgs &a, const DeviceInfo &dev, cudaStream_t stream);
+dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo &dev, cudaStream_t stream);
+
+// grad_norm.cu.  Host arrays of device addresses; out null: in place.
+struct GradList {
+    const void *const *in;
+    void *const *out;
+    const int64_t *sizes;
+    const uint8_t *bf16;
+    int64_t count;
+};
+int64_t grad_norm_workspace(int64_t count);
+dg_status_t launch_grad_norm(const GradList &g, float *norm, void *workspace, cudaStream_t stream);
+dg_status_t launch_grad_clip(const GradList &g, const float *norm, float max_norm, cudaStream_t stream);
+dg_status_t launch_grad_norm_clip(const GradList &g, float max_norm, float *norm, void *workspace, cudaStream_t stream);
+
 }  // namespace dg

@@ -510,6 +510,179 @@ dg_status_t dg_fp8_grouped_wgrad_contiguous(const uint8_t *dY, const float *sdY,
                                             const int32_t *group_offsets, int64_t M_total_capacity,
                                             int G, int64_t N, int64_t K, cudaStream_t stream);
 
+/*
+ * ---------------------------------------------------------------- around the expert layer
+ * What a training or decode step computes between expert layers: the router's choice with its
+ * balance loss, the norms before and after a block with its gate and the scaled residual, and
+ * the norm of all gradients with clipping.  One step, in calls:
+ *   dg_rmsnorm_residual         x, y of the block before -> r, n
+ *   (router product, n -> logits)
+ *   dg_moe_route                logits -> topk_ids, weights, counts, loss
+ *   dg_moe_sort ... dg_moe_combine
+ *   and back: dg_moe_combine_backward -> dweights; dg_moe_route_backward -> dlogits;
+ *   dg_rmsnorm_residual_backward; at the end of the step dg_grad_norm_clip.
+ */
+
+/* How dg_moe_route turns a token's logits into scores. */
+typedef enum {
+    DG_SCORE_SOFTMAX = 0, /* over all G experts */
+    DG_SCORE_SIGMOID = 1  /* of each expert alone */
+} dg_score_t;
+
+/* Options are HOST structures, read before the call returns. */
+typedef struct {
+    dg_score_t score;
+    int renormalize; /* not 0: weights are divided by their sum */
+    float scale;     /* of the weights; finite */
+} dg_route_options_t;
+
+typedef struct {
+    float alpha;      /* of the residual; finite */
+    float eps;        /* finite, at least 0; not used by the gradient */
+    int vectors_bf16; /* weight, post and gate: 0 FP32, else BF16 */
+} dg_norm_options_t;
+
+/*
+ * Routing.  For token t with logits z, s = softmax(z) or sigmoid(z):
+ *   topk_ids[t] = the k experts with the largest key, largest first, the lowest id among equal
+ *                 keys; the key is z (of which s is a growing function), or s + bias when bias
+ *                 is not null: then the comparison is that of s + bias in FP64;
+ *   weights[t][j] = scale * s[id_j] / sum of the k chosen s   (renormalize not 0),
+ *                 = scale * s[id_j]                           (renormalize 0).
+ * An expert whose logit is -inf or NaN, or whose key is, is not chosen.  Where fewer than k
+ * experts can be chosen, and for tokens that the mask leaves out, the remaining slots hold id -1 and
+ * weight 0: dg_moe_sort drops such slots.
+ * With counts, loss and dprob, for the n tokens that reach at least one expert and p = s
+ * (softmax) or s / sum_e s (sigmoid):
+ *   counts[e] = slots that name expert e;   dprob[e] = G * counts[e] / (k * n^2);
+ *   loss = sum_e dprob[e] * sum_t p[t][e],
+ * that is G * sum_e (share of the n * k slots) * (mean p); 1 when both are even.  dprob is the
+ * gradient of loss with respect to every p[t][e] (counts have none), as
+ * dg_moe_route_backward takes it.
+ *
+ * logits : [T][G] FP32, or BF16 when logits_bf16 is not 0; aligned to its type.
+ * bias   : FP32 [G] or null.        mask : bytes [T] or null; 0 leaves the token out.
+ * topk_ids : int32 [T][k] out.      weights : FP32 [T][k] out.
+ * counts : int32 [G] out, loss : FP32 out, dprob : FP32 [G] out; all null, or none.
+ * 1 <= G <= 1024, 1 <= k <= min(G, 32), T * k <= 2^30.  T == 0 writes counts, dprob and
+ * loss of 0 when they are asked for.
+ * workspace : device scratch of at least dg_moe_route_workspace(T, G) bytes, 16-byte aligned,
+ *             where counts are asked for; else it may be null.  Not shared with a call that
+ *             may run at the same time.
+ */
+dg_status_t dg_moe_route(const void *logits, int logits_bf16, const dg_route_options_t *options,
+                         const float *bias, const uint8_t *mask, int64_t T, int G, int k,
+                         int32_t *topk_ids, float *weights, int32_t *counts, float *loss, float *dprob,
+                         void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+int64_t dg_moe_route_workspace(int64_t T, int G); /* 0 for sizes that dg_moe_route refuses */
+
+/*
+ * Gradient of dg_moe_route with respect to the logits, from the gradients of the weights and
+ * of the loss; topk_ids are constants (and with them counts and the bias):
+ *   dlogits[t] = sum_j dweights[t][j] dweights_j/dz + sum_e dloss * dprob[e] dp[t][e]/dz.
+ * Tokens without an expert get zeros; ids outside [0, G) are slots without one.  The weights'
+ * sum runs over the token's slots, an expert named twice included twice.
+ *
+ * topk_ids : as dg_moe_route wrote them.  dweights : FP32 [T][k], or null for zeros.
+ * dprob : FP32 [G] and dloss : FP32 [1] (device), or both null.
+ * dlogits : [T][G] out, of the logits' type.  Sizes as in dg_moe_route; T == 0 is a no-op.
+ */
+dg_status_t dg_moe_route_backward(const void *logits, int logits_bf16, const dg_route_options_t *options,
+                                  const int32_t *topk_ids, const float *dweights, const float *dprob,
+                                  const float *dloss, int64_t T, int G, int k, void *dlogits,
+                                  cudaStream_t stream);
+
+/*
+ * The norm after a block, its gate, the scaled residual and the norm before the next block:
+ *   u = Y * rstd_y * post,  rstd_y[t] = 1 / sqrt(mean_h Y[t]^2 + eps)   (post null: u = Y)
+ *   r = alpha * X + gate * u                                            (gate null: of ones)
+ *   N = r * rstd * weight,  rstd[t] = 1 / sqrt(mean_h r[t]^2 + eps)
+ * in FP32; R is r rounded to BF16, N is computed from r before that rounding.
+ * Y null (before the first block): r = X; R, post, gate and rstd_y must be null and alpha 1.
+ *
+ * X_bf16, Y_bf16 : [T][H] BF16.   weight, post, gate : [H].   N_bf16 : [T][H] BF16 out.   R_bf16 : [T][H] BF16 out; R may be X.
+ * rstd : FP32 [T] out or null.   rstd_y : FP32 [T] out or null; null without post.
+ * Matrices and vectors 16-byte aligned.  H % 16 == 0, H <= 16384, T < 2^31.
+ * T == 0 or H == 0 is a no-op.
+ */
+dg_status_t dg_rmsnorm_residual(const void *X_bf16, const void *Y_bf16, const void *weight,
+                                const void *post, const void *gate, const dg_norm_options_t *options,
+                                int64_t T, int64_t H, void *N_bf16, void *R_bf16, float *rstd,
+                                float *rstd_y, cudaStream_t stream);
+
+/*
+ * The same with N as the input of dg_fp8_gemm_1x128: codes and scales of dg_quantize_1x128's
+ * definition on the FP32 values N (they are not rounded to BF16; a code may be the neighbouring
+ * one where the quotient lies within 2^-43 of a rounding midpoint).
+ * Q : [T][H] E4M3 out, 16-byte aligned.   S_t : [ceil(H/128)][T] FP32 out.
+ */
+dg_status_t dg_rmsnorm_residual_quantize(const void *X_bf16, const void *Y_bf16, const void *weight,
+                                         const void *post, const void *gate,
+                                         const dg_norm_options_t *options, int64_t T, int64_t H,
+                                         uint8_t *Q, float *S_t, void *R_bf16, cudaStream_t stream);
+
+/*
+ * Gradient of dg_rmsnorm_residual, from the gradients dN and dR of its outputs and the r, rstd
+ * and rstd_y that it wrote:
+ *   g = dR + rstd * (dN * weight - rh * mean_h(dN * weight * rh)),   rh = R * rstd
+ *   dX = alpha * g,  dweight = sum_t dN * rh,  dgate = sum_t g * u
+ *   dpost = sum_t g * gate * yh,  yh = Y * rstd_y
+ *   dY = rstd_y * (g * gate * post - yh * mean_h(g * gate * post * yh))   (post null: g * gate)
+ *
+ * dN_bf16 : [T][H].  dR_bf16 : [T][H], or null for zeros.  R_bf16 : [T][H] (X where Y is null).
+ * Y null : dY, post, gate, rstd_y, dpost and dgate must be null.  post, rstd_y and dpost : all null, or
+ * none; gate and dgate likewise.
+ * dX_bf16, dY_bf16 : [T][H] BF16 out.   dweight, dpost, dgate : FP32 [H] out.
+ * Alignment and sizes as in dg_rmsnorm_residual.  H == 0 is a no-op; T == 0 writes zeros to the
+ * vectors' gradients.
+ * workspace : device scratch of at least dg_rmsnorm_residual_backward_workspace bytes, 16-byte
+ *             aligned, for this call alone while it runs.  Column sums are kept per CTA and
+ *             added up in order.
+ */
+dg_status_t dg_rmsnorm_residual_backward(const void *dN_bf16, const void *dR_bf16, const void *R_bf16,
+                                         const float *rstd, const void *Y_bf16, const float *rstd_y,
+                                         const void *weight, const void *post, const void *gate,
+                                         const dg_norm_options_t *options, int64_t T, int64_t H,
+                                         void *dX_bf16, void *dY_bf16, float *dweight, float *dpost,
+                                         float *dgate, void *workspace, int64_t workspace_bytes,
+                                         cudaStream_t stream);
+/* has_post, has_gate not 0: with those vectors.  0 for sizes that the call refuses. */
+int64_t dg_rmsnorm_residual_backward_workspace(int64_t T, int64_t H, int has_post, int has_gate);
+
+/*
+ * The global norm of a step's gradients, sqrt(sum over all tensors of sum g^2): squares are
+ * taken in FP32 where that loses nothing, else in FP64, and added up in FP64 in a fixed order,
+ * so a finite norm does not overflow on the way.  A NaN or an infinity in a gradient shows in it.
+ *
+ * grads, sizes, bf16 : HOST arrays of `count` device addresses, element counts and types (0 FP32,
+ *             else BF16); read before the call returns.  A tensor is contiguous, aligned to
+ *             its type (16 bytes are faster); one of size 0 is skipped, its address unused.
+ * norm      : FP32 out (device).  0 without any elements.
+ * workspace : device scratch of at least dg_grad_norm_workspace(count) bytes, 16-byte aligned,
+ *             for this call alone while it runs.
+ */
+dg_status_t dg_grad_norm(const void *const *grads, const int64_t *sizes, const uint8_t *bf16,
+                         int64_t count, float *norm, void *workspace, int64_t workspace_bytes,
+                         cudaStream_t stream);
+int64_t dg_grad_norm_workspace(int64_t count);
+
+/*
+ * Clipping by a norm (device): out = grads * (max_norm / norm) where norm > max_norm, else
+ * grads.  A norm that is not finite clips nothing, so that the caller can see it and drop the
+ * step.  out null: in place, and without a write where nothing is clipped.  out[i] is grads[i],
+ * or a tensor of the same type and size that overlaps no other tensor of the call (written in
+ * any case); tensors that are written must not overlap each other (DG_ERR_INVALID_ARG).
+ * max_norm : HOST address of the limit, read before the call returns; finite, at least 0.
+ */
+dg_status_t dg_grad_clip(const void *const *grads, const int64_t *sizes, const uint8_t *bf16,
+                         int64_t count, const float *norm, const float *max_norm, void *const *out,
+                         cudaStream_t stream);
+
+/* dg_grad_norm, then dg_grad_clip by it, in one launch less. */
+dg_status_t dg_grad_norm_clip(const void *const *grads, const int64_t *sizes, const uint8_t *bf16,
+                              int64_t count, const float *max_norm, void *const *out, float *norm,
+                              void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *dg_status_string(dg_status_t status);
 
@@ -528,8 +701,8 @@ dg_status_t dg_get_last_device_status(cudaStream_t stream);
  * added dg_fp8_gemm_blockscaled_bf16a_select and DG_KERNEL_SKINNY_FUSED; 1.04 added
  * dg_quantize_blockwise_masked; 1.05: dg_quantize_blockwise_masked quantizes each
  * expert's tokens as a matrix of their own (rows past the count no longer enter the
- * last token block's amax).  The expert-layer and gradient calls came later without a new
- * number: they only add symbols.  Every 1.00 call is unchanged. */
+ * last token block's amax).  The expert-layer and gradient calls, and those around the
+ * expert layer, came later without a new number: they only add symbols.  Every 1.00 call is unchanged. */
 int dg_version(void);
 
 /*
