@@ -22,8 +22,6 @@
 namespace dg {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr uint32_t kNoKey = 0x007FFFFFu;  // ordered(-inf): a key at or below it is not chosen
-constexpr int kRouteThreads = 512;        // with the balance loss; 128 without
 constexpr int kFinishCtas = 8;
 constexpr int kFinishThreads = 512;
 
@@ -64,24 +62,38 @@ __device__ __forceinline__ T warp_sum(T v) {
     return v;
 }
 
-__device__ __forceinline__ float warp_max(float v) {  // a NaN loses
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+__device__ __forceinline__ float warp_max(float v) {  // a NaN loses against anything, alone it is -inf
+    return from_ordered(__reduce_max_sync(kAll, ordered(fmaxf(v, -CUDART_INF_F) + 0.0f)));
+}
+
+__device__ __forceinline__ float reciprocal(float x) {  // within one unit; 0 for 2^126 and more
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // Rows whose largest score is below this: 1 / (1 + e^-z) is e^z to far below an FP32 rounding,
 // and ratios of sigmoids are those of exponentials, which do not vanish together.
 constexpr float kFarBelow = -60.0f;
 
-__device__ __forceinline__ float sigmoid_of(float z) {
-    const float e = expf(-fabsf(z));
-    return __fdividef(z >= 0.0f ? 1.0f : e, 1.0f + e);
+// e^x, for sums over a row and for keys: the argument's product and the hardware's approximation are
+// off by 2 + 1.2 |x| units of the last place; 0 below 2^-126.
+__device__ __forceinline__ float exp_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504f));  // log2(e)
+    return r;
 }
+
+__device__ __forceinline__ float sigmoid_fast(float z) { return reciprocal(1.0f + exp_fast(-z)); }
 
 // What p is proportional to, for a row whose largest score is `top`.
 __device__ __forceinline__ float unnormalized(float z, float top, bool exponential) {
-    return exponential ? expf(z - top) : sigmoid_of(z);
+    return exponential ? exp_fast(z - top) : sigmoid_fast(z);
+}
+
+__device__ __forceinline__ float sigmoid_of(float z) {
+    const float e = expf(-fabsf(z));
+    return (z >= 0.0f ? 1.0f : e) / (1.0f + e);
 }
 
 // Lane j's share of the chosen scores' sum, in FP32 without common under- or overflow; lanes
@@ -89,51 +101,121 @@ __device__ __forceinline__ float unnormalized(float z, float top, bool exponenti
 __device__ __forceinline__ float share_of_chosen(float z, bool ok, bool sigmoid) {
     const float m = warp_max(ok ? z : -CUDART_INF_F);
     float s = 0.0f;
-    if (ok) {
-        if (!sigmoid || m < kFarBelow) {
-            s = expf(z - m);
-        } else {
-            const float e = expf(-fabsf(z));
-            s = (z >= 0.0f ? 1.0f : e) / (1.0f + e);
-        }
-    }
+    if (ok) s = !sigmoid || m < kFarBelow ? expf(z - m) : sigmoid_of(z);
     return s / warp_sum(s);  // 0 / 0 where no lane holds a slot: the caller's ok is false then
 }
 
-// Among the experts whose keys lie within the FP32 error of the largest one, `near` (bit i: the
-// lane's i-th expert), the one whose key is largest in FP64, the lowest index among equals.
-// Two keys s + b in FP32 come that close for about one token in a hundred.
-__device__ __noinline__ int choose_in_fp64(const void *logits, const float *bias, int64_t row, int G, bool bf16, bool sigmoid,
-                                           uint32_t near, float top) {
-    const int lane = lane_id();
-    double sum = 1.0;
-    if (!sigmoid) {
-        sum = 0.0;
-        for (int e = lane; e < G; e += 32) sum += exp(static_cast<double>(load_score(logits, bf16, row + e)) - top);
-        sum = warp_sum(sum);
-    }
-    uint64_t best = 0;
-    int at = 0x7FFFFFFF;
-    while (near) {
-        const int e = lane + 32 * (__ffs(near) - 1);
-        near &= near - 1;
-        const double z = load_score(logits, bf16, row + e);
-        const double s = sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - top) / sum;
-        const double key = s + __ldg(bias + e) + 0.0;
-        const uint64_t u = static_cast<uint64_t>(__double_as_longlong(key));
-        const uint64_t o = (u >> 63) ? ~u : u | 0x8000000000000000ull;
-        if (o > best) best = o, at = e;  // ascending e: the lowest index stays
-    }
-    const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(best >> 32));
-    bool in = static_cast<uint32_t>(best >> 32) == hi && at != 0x7FFFFFFF;
-    const uint32_t lo = __reduce_max_sync(kAll, in ? static_cast<uint32_t>(best) : 0u);
-    in = in && static_cast<uint32_t>(best) == lo;
-    return __reduce_min_sync(kAll, in ? at : 0x7FFFFFFF);
+// A key in FP64: z itself without a bias (top and sum: of a row's exponentials).
+template <bool BIAS>
+__device__ __forceinline__ double exact_key(float z, const float *bias, int e, bool sigmoid, double top, double sum) {
+    double key = z;
+    if (BIAS) key = (sigmoid ? 1.0 / (1.0 + exp(-key)) : exp(key - top) / sum) + __ldg(bias + e);
+    return key + 0.0;  // -0 is +0
 }
 
+__device__ __forceinline__ void exact_sum(const void *logits, int64_t row, int G, bool bf16, double &top, double &sum) {
+    float m = -CUDART_INF_F;
+    for (int e = lane_id(); e < G; e += 32) m = fmaxf(m, load_score(logits, bf16, row + e));
+    top = warp_max(m);
+    sum = 0.0;
+    for (int e = lane_id(); e < G; e += 32) sum += exp(load_score(logits, bf16, row + e) - top);
+    sum = warp_sum(sum);
+}
+
+// Lanes below n hold the candidates, no other expert comes before any of them: their order by FP64
+// keys, the lowest id among equals.
+template <bool BIAS>
+__device__ __noinline__ int order_exactly(const void *logits, const float *bias, int64_t row, int G, bool bf16, bool sigmoid,
+                                          int id, int n) {
+    const int lane = lane_id();
+    double top = 0.0, sum = 1.0;
+    if (BIAS && !sigmoid) exact_sum(logits, row, G, bf16, top, sum);
+    double key = 0.0;
+    if (lane < n) key = exact_key<BIAS>(load_score(logits, bf16, row + id), bias, id, sigmoid, top, sum);
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const double other = __shfl_sync(kAll, key, i);
+        const int e = __shfl_sync(kAll, id, i);
+        rank += other > key || (other == key && e < id) ? 1 : 0;
+    }
+    int sorted = -1;
+    for (int i = 0; i < n; ++i) {
+        const int r = __shfl_sync(kAll, rank, i), e = __shfl_sync(kAll, id, i);
+        if (r == lane) sorted = e;
+    }
+    return sorted;
+}
+
+// The choice among all experts by FP64 keys, for rows with more near keys than a warp has lanes:
+// lane j returns slot j's expert or -1.
+template <int PER, bool BIAS>
+__device__ __noinline__ int choose_exactly(const void *logits, const float *bias, int64_t row, int G, int k, bool bf16,
+                                           bool sigmoid) {
+    const int lane = lane_id();
+    double top = 0.0, sum = 1.0;
+    if (BIAS && !sigmoid) exact_sum(logits, row, G, bf16, top, sum);
+    uint64_t keys[PER];
+#pragma unroll 1
+    for (int i = 0; i < PER; ++i) {
+        keys[i] = 0;
+        const int e = lane + 32 * i;
+        if (e >= G) continue;
+        const float z = load_score(logits, bf16, row + e);
+        const double key = exact_key<BIAS>(z, bias, e, sigmoid, top, sum);
+        const uint64_t u = static_cast<uint64_t>(__double_as_longlong(key));
+        if (z > -CUDART_INF_F && key > -CUDART_INF) keys[i] = (u >> 63) ? ~u : u | 0x8000000000000000ull;
+    }
+    int id = -1;
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) {
+        uint64_t best = 0;
+        int at = 0x7FFFFFFF;
+#pragma unroll 1
+        for (int i = 0; i < PER; ++i)
+            if (keys[i] > best) best = keys[i], at = i;  // ascending: the lowest id stays
+        const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(best >> 32));
+        if (hi == 0) break;
+        bool in = static_cast<uint32_t>(best >> 32) == hi;
+        const uint32_t lo = __reduce_max_sync(kAll, in ? static_cast<uint32_t>(best) : 0u);
+        in = in && static_cast<uint32_t>(best) == lo;
+        const int e = __reduce_min_sync(kAll, in ? lane + 32 * at : 0x7FFFFFFF);
+        if (in && lane + 32 * at == e) keys[at] = 0;
+        if (lane == j) id = e;
+    }
+    return id;
+}
+
+// Descending order of a lane's keys (odd-even merge sort, K. E. Batcher, "Sorting networks and
+// their applications", 1968): a minimum and a maximum per comparator.
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t a = v[i + j], b = v[i + j + q];
+                        v[i + j] = max(a, b);
+                        v[i + j + q] = min(a, b);
+                    }
+}
+
+// A warp chooses by 32-bit keys whose low bits are the expert's id, inverted: one maximum over the
+// warp gives key and id, the lowest id among equals, and no two keys are the same.  The id takes the place of
+// the key's last 5 to 10 bits, so the choice is settled only where neighbours in the order differ
+// by more than those (and, with a bias, by more than the key's own FP32 error); otherwise (a token
+// in thirty) the candidates are put in order by FP64 keys.  BF16 logits without a bias have the bits to spare.
+// 16384 tokens x 256 experts, k = 8, with bias and balance loss: see launch_route.
+constexpr int route_max_threads(int per) { return per <= 8 ? 1024 : 512; }
+
 template <int PER, bool BIAS, bool BALANCE>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const RouteParams p) {
     extern __shared__ float sums[];  // BALANCE: [warps][G] of p, then [G] counts, then the tokens
+    constexpr uint32_t kIdBits = 32 * PER - 1;
     const int lane = lane_id();
     const int warps = static_cast<int>(blockDim.x) >> 5, warp = static_cast<int>(threadIdx.x) >> 5;
     int *counts = reinterpret_cast<int *>(sums + warps * p.G);
@@ -141,106 +223,151 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
         for (int e = static_cast<int>(threadIdx.x); e <= p.G; e += static_cast<int>(blockDim.x)) counts[e] = 0;
         __syncthreads();
     }
-    float psum[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) psum[i] = 0.0f;
-    int tokens = 0;
     grid_dep_wait();
     grid_dep_launch_dependents();
+    float psum[PER], b[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        psum[i] = 0.0f;
+        b[i] = (BIAS && lane + 32 * i < p.G ? __ldg(p.bias + lane + 32 * i) : 0.0f) + 0.0f;
+    }
+    const bool exact_keys = !BIAS && p.bf16;
+    const int rounds = exact_keys || p.k == p.G ? p.k : p.k + 1;  // the next one too: is the last one settled?
+    int tokens = 0;
 
     const int64_t stride = static_cast<int64_t>(gridDim.x) * warps;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * warps + warp; t < p.T; t += stride) {
-        const bool live = !p.mask || __ldg(p.mask + t) != 0;
-        int id = -1;       // lane j: slot j
-        float z_id = 0.0f;
-        float top = -CUDART_INF_F, sum = 1.0f;
-        if (live) {
+        const int64_t row = t * p.G;
+        int id = -1;  // lane j: slot j
+        float top = 0.0f, sum = 1.0f;
+        if (!p.mask || __ldg(p.mask + t) != 0) {
             float z[PER];
             uint32_t key[PER];
+            if (p.bf16) {
+                const uint16_t *at = static_cast<const uint16_t *>(p.logits) + row + lane;
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                z[i] = lane + 32 * i < p.G ? load_score(p.logits, p.bf16, t * p.G + lane + 32 * i) : -CUDART_INF_F;
+                for (int i = 0; i < PER; ++i)
+                    z[i] = lane + 32 * i < p.G ? __uint_as_float(static_cast<uint32_t>(__ldg(at + 32 * i)) << 16) : -CUDART_INF_F;
+            } else {
+                const float *at = static_cast<const float *>(p.logits) + row + lane;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) top = fmaxf(top, z[i]);
-            top = warp_max(top);
-            if (top > -CUDART_INF_F) {
-                if (BALANCE || BIAS || (!p.renormalize && !p.sigmoid)) {
-                    const bool exponential = !p.sigmoid || (BALANCE && top < kFarBelow);
-                    float q[PER];
+                for (int i = 0; i < PER; ++i) z[i] = lane + 32 * i < p.G ? __ldg(at + 32 * i) : -CUDART_INF_F;
+            }
+            // the id goes under the key's high bits; 0 for an expert that is not chosen
+            auto keyed = [&](float c, bool able, int i) {
+                const uint32_t id_bits = kIdBits - static_cast<uint32_t>(lane + 32 * i);
+                return able ? (ordered(c) & ~kIdBits) | id_bits : 0u;
+            };
+            if (BALANCE || BIAS || (!p.renormalize && !p.sigmoid)) {
+                float q[PER];
+                auto exponentials = [&] {
+                    top = -CUDART_INF_F;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) top = fmaxf(top, z[i]);
+                    top = warp_max(top);
                     sum = 0.0f;
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
-                        q[i] = unnormalized(z[i], top, exponential);
-                        if (lane + 32 * i >= p.G) q[i] = 0.0f;
+                        q[i] = exp_fast(z[i] - top);  // 0 past the last expert; NaN in a row without a score
                         sum += q[i];
                     }
                     sum = warp_sum(sum);
-                    const float r = 1.0f / sum;
-                    if (BALANCE) {
+                };
+                if (p.sigmoid) {
+                    sum = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < PER; ++i) psum[i] += q[i] * r;
+                    for (int i = 0; i < PER; ++i) {
+                        q[i] = sigmoid_fast(z[i]);
+                        sum += q[i];
                     }
                     if (BIAS) {
 #pragma unroll
                         for (int i = 0; i < PER; ++i) {
-                            const float s = p.sigmoid ? (exponential ? sigmoid_of(z[i]) : q[i]) : q[i] * r;
-                            const float c = lane + 32 * i < p.G ? s + __ldg(p.bias + lane + 32 * i) + 0.0f : 0.0f;
-                            key[i] = c == c && z[i] > -CUDART_INF_F ? ordered(c) : 0u;
+                            const float c = q[i] + b[i];  // never -0: b is not
+                            key[i] = keyed(c, z[i] > -CUDART_INF_F && c > -CUDART_INF_F, i);
+                        }
+                    }
+                    if (BALANCE) {
+                        sum = warp_sum(sum);
+                        if (sum < 0x1p-80f) exponentials();  // all far below 0: ratios of exponentials
+                    }
+                } else {
+                    exponentials();
+                    if (BIAS) {
+                        const float r = reciprocal(sum);
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const float c = fmaf(q[i], r, b[i]);
+                            key[i] = keyed(c, z[i] > -CUDART_INF_F && c > -CUDART_INF_F, i);
                         }
                     }
                 }
-                if (!BIAS) {
+                if (BALANCE) {
+                    const float r = reciprocal(sum);
+                    if (top > -CUDART_INF_F) {  // for sigmoids 0, unless no expert has a score
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) key[i] = z[i] == z[i] ? ordered(z[i] + 0.0f) : 0u;
-                }
-                for (int j = 0; j < p.k; ++j) {
-                    uint32_t most = key[0];
-#pragma unroll
-                    for (int i = 1; i < PER; ++i) most = max(most, key[i]);
-                    most = __reduce_max_sync(kAll, most);
-                    if (most <= kNoKey) break;
-                    int at = 0x7FFFFFFF;
-                    if (BIAS) {
-                        const float f = from_ordered(most);
-                        // keys are off by less than 2^-18 max(1, |key|): 2^-22 in s (37 additions
-                        // of softmax's sum among them) and a rounding of s + b
-                        const float least = f - 0x1p-17f * fminf(fmaxf(1.0f, fabsf(f)), 0x1p126f);
-                        const uint32_t u = max(ordered(least + 0.0f), kNoKey + 1u);
-                        uint32_t near = 0;
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) near |= key[i] >= u ? 1u << i : 0u;
-                        const uint32_t lanes = __ballot_sync(kAll, near != 0);
-                        const bool several = (lanes & (lanes - 1)) != 0 || __any_sync(kAll, (near & (near - 1)) != 0);
-                        if (several)
-                            at = choose_in_fp64(p.logits, p.bias, t * p.G, p.G, p.bf16, p.sigmoid, near, top);
-                        else
-                            at = __shfl_sync(kAll, lane + 32 * (__ffs(near) - 1), __ffs(lanes) - 1);
-                    } else {
-#pragma unroll
-                        for (int i = PER - 1; i >= 0; --i)
-                            if (key[i] == most) at = lane + 32 * i;
-                        at = __reduce_min_sync(kAll, at);
+                        for (int i = 0; i < PER; ++i) psum[i] = fmaf(q[i], r, psum[i]);
                     }
-#pragma unroll
-                    for (int i = 0; i < PER; ++i)
-                        if (lane + 32 * i == at) key[i] = 0u;
-                    if (lane == j) id = at;
                 }
+            }
+            if (!BIAS) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) key[i] = keyed(z[i] + 0.0f, z[i] > -CUDART_INF_F, i);
+            }
+            sort_descending(key);
+            uint32_t mine = 0u, prev = 0u, last = 0u;  // lane j: the j-th largest; the last two of them
+            int found = 0;
+            auto next = [&] {
+                prev = last;
+                last = __reduce_max_sync(kAll, key[0]);
+                if (lane == found) mine = last;
+                ++found;
+                if (key[0] == last) {
+#pragma unroll
+                    for (int i = 0; i + 1 < PER; ++i) key[i] = key[i + 1];
+                    key[PER - 1] = 0u;
+                }
+            };
+            // whether b may come before a, its predecessor in the order of the 32-bit keys
+            auto unsettled = [&](uint32_t a, uint32_t b) {
+                if (b == 0u) return false;
+                if (!BIAS) return (a ^ b) <= kIdBits;
+                // keys are off by less than 2^-18 max(1, |key|): 2^-21 in s (37 additions of softmax's
+                // sum among them) and a rounding of s + b
+                const float x = from_ordered(a & ~kIdBits), y = from_ordered(b | kIdBits);
+                return !(x - y > 0x1p-17f * fmaxf(1.0f, fabsf(x)));  // infinite keys too
+            };
+            while (found < rounds) next();
+            if (!exact_keys) {
+                uint32_t below = __shfl_down_sync(kAll, mine, 1);
+                if (lane == p.k - 1) below = p.k == p.G ? 0u : last;
+                if (__any_sync(kAll, lane < p.k && unsettled(mine, below))) {
+                    // more candidates, until the next one certainly comes after them
+                    while (p.k < p.G && found < 32 && unsettled(prev, last)) next();
+                    const int n = p.k == p.G ? p.k : found - 1;
+                    const uint32_t held = __ballot_sync(kAll, lane < n && mine != 0u);
+                    id = static_cast<int>(kIdBits - (mine & kIdBits));
+                    if (p.k == p.G || !unsettled(prev, last))
+                        id = order_exactly<BIAS>(p.logits, p.bias, row, p.G, p.bf16, p.sigmoid, id, __popc(held));
+                    else
+                        id = choose_exactly<PER, BIAS>(p.logits, p.bias, row, p.G, p.k, p.bf16, p.sigmoid);
+                    if (lane >= p.k) id = -1;
+                } else if (lane < p.k && mine != 0u) {
+                    id = static_cast<int>(kIdBits - (mine & kIdBits));
+                }
+            } else if (lane < p.k && mine != 0u) {
+                id = static_cast<int>(kIdBits - (mine & kIdBits));
             }
         }
         const bool ok = id >= 0;
-        if (ok) z_id = load_score(p.logits, p.bf16, t * p.G + id);
         const bool routed = __any_sync(kAll, ok);
         float w = 0.0f;
         if (routed) {
-            if (p.renormalize) {
-                w = share_of_chosen(z_id, ok, p.sigmoid);
-            } else if (p.sigmoid) {
-                const float e = expf(-fabsf(z_id));
-                w = (z_id >= 0.0f ? 1.0f : e) / (1.0f + e);
-            } else {
-                w = expf(z_id - top) / sum;
-            }
+            const float z = ok ? load_score(p.logits, p.bf16, row + id) : 0.0f;
+            if (p.renormalize)
+                w = share_of_chosen(z, ok, p.sigmoid);
+            else
+                w = p.sigmoid ? sigmoid_of(z) : expf(z - top) / sum;
         }
         if (lane < p.k) {
             p.ids[t * p.k + lane] = id;
@@ -268,59 +395,74 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     }
 }
 
-// The CTAs' sums to counts, dprob and the loss: one cluster, each CTA a share of the experts,
-// 16 threads an expert (parts in turn), FP64 sums in a fixed order.
+// The CTAs' sums to counts, dprob and the loss: one cluster; a CTA takes 32 experts at a time, a lane
+// each, and its warps share the parts.  FP64 sums in a fixed order.
 __global__ void __cluster_dims__(kFinishCtas, 1, 1) __launch_bounds__(kFinishThreads)
     route_finish_kernel(const float *__restrict__ part_p, const int32_t *__restrict__ part_count,
                         const int32_t *__restrict__ part_tokens, int parts, int G, int k,
                         int32_t *__restrict__ counts, float *__restrict__ loss, float *__restrict__ dprob) {
-    __shared__ double warp_loss[kFinishThreads / 32], cta_loss;
-    __shared__ int warp_tokens[kFinishThreads / 32];
+    constexpr int kWarps = kFinishThreads / 32;
+    __shared__ double warp_p[kWarps][32], cta_loss;
+    __shared__ int warp_count[kWarps][32], warp_tokens[kWarps];
     grid_dep_wait();
     grid_dep_launch_dependents();
     const int tid = static_cast<int>(threadIdx.x), lane = lane_id(), warp = tid >> 5;
+    const int rank = static_cast<int>(cluster_ctarank());
     int n = 0;
     for (int i = tid; i < parts; i += kFinishThreads) n += __ldg(part_tokens + i);
     n = warp_sum(n);
     if (lane == 0) warp_tokens[warp] = n;
-    __syncthreads();
-    n = 0;
-    for (int i = 0; i < kFinishThreads / 32; ++i) n += warp_tokens[i];
-    const double nd = n > 0 ? static_cast<double>(n) : 1.0;
-    const double unit = static_cast<double>(G) / (static_cast<double>(k) * nd * nd);
 
-    // lane: expert lane % 8 of the warp's eight, parts lane / 8, + 4, ...
-    double mine = 0.0;
-    const int rank = static_cast<int>(cluster_ctarank());
-    for (int e0 = (rank * (kFinishThreads / 32) + warp) * 8; e0 < G; e0 += kFinishCtas * (kFinishThreads / 32) * 8) {
-        const int e = e0 + (lane & 7);
+    double mine = 0.0, unit = 0.0;
+    for (int e0 = rank * 32; e0 < G; e0 += kFinishCtas * 32) {
+        const int e = e0 + lane;
         double s = 0.0;
         int c = 0;
         if (e < G) {
-#pragma unroll 4
-            for (int i = lane >> 3; i < parts; i += 4) {
-                s += static_cast<double>(__ldg(part_p + static_cast<int64_t>(i) * G + e));
-                c += __ldg(part_count + static_cast<int64_t>(i) * G + e);
+            constexpr int kDeep = 10;  // loads in flight: 148 parts over 16 warps
+            for (int i0 = warp; i0 < parts; i0 += kDeep * kWarps) {
+                float v[kDeep];
+                int w[kDeep];
+#pragma unroll
+                for (int j = 0; j < kDeep; ++j) {
+                    const int i = i0 + j * kWarps;
+                    v[j] = i < parts ? __ldg(part_p + static_cast<int64_t>(i) * G + e) : 0.0f;
+                    w[j] = i < parts ? __ldg(part_count + static_cast<int64_t>(i) * G + e) : 0;
+                }
+#pragma unroll
+                for (int j = 0; j < kDeep; ++j) {
+                    s += static_cast<double>(v[j]);
+                    c += w[j];
+                }
             }
         }
-        s += __shfl_xor_sync(kAll, s, 8);
-        s += __shfl_xor_sync(kAll, s, 16);
-        c += __shfl_xor_sync(kAll, c, 8);
-        c += __shfl_xor_sync(kAll, c, 16);
-        if (e < G && lane < 8) {
-            const double d = unit * c;
-            counts[e] = c;
-            dprob[e] = static_cast<float>(d);
-            mine += d * s;
+        warp_p[warp][lane] = s;
+        warp_count[warp][lane] = c;
+        __syncthreads();
+        if (warp == 0) {
+            n = 0;
+            s = 0.0;
+            c = 0;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                n += warp_tokens[i];
+                s += warp_p[i][lane];
+                c += warp_count[i][lane];
+            }
+            const double nd = n > 0 ? static_cast<double>(n) : 1.0;
+            unit = static_cast<double>(G) / (static_cast<double>(k) * nd * nd);
+            if (e < G) {
+                const double d = unit * c;
+                counts[e] = c;
+                dprob[e] = static_cast<float>(d);
+                mine += d * s;
+            }
         }
+        __syncthreads();
     }
-    mine = warp_sum(mine);
-    if (lane == 0) warp_loss[warp] = mine;
-    __syncthreads();
-    if (tid == 0) {
-        double s = 0.0;
-        for (int i = 0; i < kFinishThreads / 32; ++i) s += warp_loss[i];
-        cta_loss = s;
+    if (warp == 0) {
+        mine = warp_sum(mine);
+        if (lane == 0) cta_loss = mine;
     }
     cluster_sync();
     if (rank == 0 && tid == 0) {
@@ -410,8 +552,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteBackward
             } else {
                 float s;
                 if (p.sigmoid) {
-                    const float e = expf(-fabsf(z_id));
-                    s = (z_id >= 0.0f ? 1.0f : e) / (1.0f + e);
+                    s = sigmoid_of(z_id);
                 } else {
                     s = expf(z_id - top) * r;
                 }
@@ -425,7 +566,7 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteBackward
             float v = 0.0f;
             if (ROWS && routed) {
                 v = q[i] * r * (dp[i] - base);
-                if (p.sigmoid) v *= sigmoid_of(-z[i]);
+                if (p.sigmoid) v *= sigmoid_fast(-z[i]);
             }
             if (lane + 32 * i < p.G) store_score(p.dlogits, p.bf16, row + lane + 32 * i, v);
         }
@@ -453,37 +594,55 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteBackward
 }
 
 // --------------------------------------------------------------------------- launchers
-static int route_grid(int64_t T, const DeviceInfo &dev) {
-    const int64_t want = (T + kRouteThreads / 32 - 1) / (kRouteThreads / 32), most = 2 * dev.num_sms;
-    return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+namespace {
+
+constexpr int kSms = 148;  // of a B200: the workspace is sized without asking a device
+
+int per_lane(int G) {
+    int per = 1;
+    while (32 * per < G) per *= 2;
+    return per;
 }
 
-// The partial sums of at most two CTAs per SM; SMs of a B200, since no device is asked here.
+struct RouteShape {
+    int threads, grid;
+};
+
+// A CTA per SM with as many warps as there are tokens for, up to 32: fewer parts to add up.
+RouteShape balance_shape(int64_t T, int G) {
+    const int64_t most = route_max_threads(per_lane(G)) / 32;
+    int64_t warps = (T + kSms - 1) / kSms;
+    warps = warps < 4 ? 4 : warps > most ? most : warps;
+    int64_t grid = (T + warps - 1) / warps;
+    const int64_t limit = kSms * (1024 / 32 / most);
+    grid = grid < 1 ? 1 : grid > limit ? limit : grid;
+    return {static_cast<int>(warps) * 32, static_cast<int>(grid)};
+}
+
+}  // namespace
+
 int64_t route_workspace(int64_t T, int G) {
-    DeviceInfo dev = {};
-    dev.num_sms = 148;
-    return static_cast<int64_t>(route_grid(T, dev)) * (G * 8 + 4);
+    return static_cast<int64_t>(balance_shape(T, G).grid) * (G * 8 + 4);
 }
 
 template <int PER, bool BIAS, bool BALANCE>
-static dg_status_t launch_route_impl(const RouteParams &p, int grid, int threads, cudaStream_t stream) {
+static dg_status_t launch_route_impl(const RouteParams &p, const RouteShape &s, cudaStream_t stream) {
     auto kernel = route_kernel<PER, BIAS, BALANCE>;
-    const size_t smem = BALANCE ? (static_cast<size_t>(threads / 32) * p.G + p.G + 1) * 4 : 0;
+    const size_t smem = BALANCE ? (static_cast<size_t>(s.threads / 32) * p.G + p.G + 1) * 4 : 0;
     if (smem > 48 * 1024) {
         static thread_local int configured_device = -1;
-        const dg_status_t st = allow_smem(kernel, (static_cast<size_t>(kRouteThreads / 32) * 1024 + 1025) * 4, configured_device);
+        const dg_status_t st = allow_smem(kernel, (static_cast<size_t>(route_max_threads(PER) / 32 + 1) * 32 * PER + 1) * 4,
+                                          configured_device);
         if (st != DG_OK) return st;
     }
-    return launch_pdl(kernel, grid, threads, smem, stream, p);
+    return launch_pdl(kernel, s.grid, s.threads, smem, stream, p);
 }
 
 template <int PER>
-static dg_status_t launch_route_per(const RouteParams &p, bool balance, int grid, int threads, cudaStream_t stream) {
+static dg_status_t launch_route_per(const RouteParams &p, bool balance, const RouteShape &s, cudaStream_t stream) {
     if (p.bias)
-        return balance ? launch_route_impl<PER, true, true>(p, grid, threads, stream)
-                       : launch_route_impl<PER, true, false>(p, grid, threads, stream);
-    return balance ? launch_route_impl<PER, false, true>(p, grid, threads, stream)
-                   : launch_route_impl<PER, false, false>(p, grid, threads, stream);
+        return balance ? launch_route_impl<PER, true, true>(p, s, stream) : launch_route_impl<PER, true, false>(p, s, stream);
+    return balance ? launch_route_impl<PER, false, true>(p, s, stream) : launch_route_impl<PER, false, false>(p, s, stream);
 }
 
 dg_status_t launch_route(const RouteArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
@@ -501,30 +660,28 @@ dg_status_t launch_route(const RouteArgs &a, const DeviceInfo &dev, cudaStream_t
     p.scale = a.scale;
     p.ids = a.ids;
     p.weights = a.weights;
-    int grid, threads;
+    RouteShape s;
     if (balance) {
-        DeviceInfo sized = dev;
-        sized.num_sms = 148;  // as route_workspace counts
-        grid = route_grid(a.T, sized);
-        threads = kRouteThreads;
+        s = balance_shape(a.T, a.G);
         p.part_p = static_cast<float *>(a.workspace);
-        p.part_count = reinterpret_cast<int32_t *>(p.part_p + static_cast<int64_t>(grid) * a.G);
-        p.part_tokens = p.part_count + static_cast<int64_t>(grid) * a.G;
+        p.part_count = reinterpret_cast<int32_t *>(p.part_p + static_cast<int64_t>(s.grid) * a.G);
+        p.part_tokens = p.part_count + static_cast<int64_t>(s.grid) * a.G;
     } else {
-        threads = 128;
         const int64_t want = (a.T + 3) / 4, most = 16 * static_cast<int64_t>(dev.num_sms);
-        grid = static_cast<int>(want < most ? want : most);
+        s = {128, static_cast<int>(want < most ? want : most)};
     }
     dg_status_t st;
-    if (a.G <= 32) st = launch_route_per<1>(p, balance, grid, threads, stream);
-    else if (a.G <= 64) st = launch_route_per<2>(p, balance, grid, threads, stream);
-    else if (a.G <= 128) st = launch_route_per<4>(p, balance, grid, threads, stream);
-    else if (a.G <= 256) st = launch_route_per<8>(p, balance, grid, threads, stream);
-    else if (a.G <= 512) st = launch_route_per<16>(p, balance, grid, threads, stream);
-    else st = launch_route_per<32>(p, balance, grid, threads, stream);
+    switch (per_lane(a.G)) {
+    case 1: st = launch_route_per<1>(p, balance, s, stream); break;
+    case 2: st = launch_route_per<2>(p, balance, s, stream); break;
+    case 4: st = launch_route_per<4>(p, balance, s, stream); break;
+    case 8: st = launch_route_per<8>(p, balance, s, stream); break;
+    case 16: st = launch_route_per<16>(p, balance, s, stream); break;
+    default: st = launch_route_per<32>(p, balance, s, stream); break;
+    }
     if (st != DG_OK || !balance) return st;
     return launch_pdl(route_finish_kernel, kFinishCtas, kFinishThreads, 0, stream, static_cast<const float *>(p.part_p),
-                      static_cast<const int32_t *>(p.part_count), static_cast<const int32_t *>(p.part_tokens), grid, a.G,
+                      static_cast<const int32_t *>(p.part_count), static_cast<const int32_t *>(p.part_tokens), s.grid, a.G,
                       a.k, a.counts, a.loss, a.dprob);
 }
 
@@ -540,12 +697,14 @@ dg_status_t launch_route_backward(const RouteBackwardArgs &a, const DeviceInfo &
                              a.bf16, a.sigmoid, a.renormalize, a.scale, a.dlogits};
     const int64_t want = (a.T + 7) / 8, most = 8 * static_cast<int64_t>(dev.num_sms);
     const int grid = static_cast<int>(want < most ? want : most);
-    if (a.G <= 32) return launch_route_backward_per<1>(p, grid, stream);
-    if (a.G <= 64) return launch_route_backward_per<2>(p, grid, stream);
-    if (a.G <= 128) return launch_route_backward_per<4>(p, grid, stream);
-    if (a.G <= 256) return launch_route_backward_per<8>(p, grid, stream);
-    if (a.G <= 512) return launch_route_backward_per<16>(p, grid, stream);
-    return launch_route_backward_per<32>(p, grid, stream);
+    switch (per_lane(a.G)) {
+    case 1: return launch_route_backward_per<1>(p, grid, stream);
+    case 2: return launch_route_backward_per<2>(p, grid, stream);
+    case 4: return launch_route_backward_per<4>(p, grid, stream);
+    case 8: return launch_route_backward_per<8>(p, grid, stream);
+    case 16: return launch_route_backward_per<16>(p, grid, stream);
+    default: return launch_route_backward_per<32>(p, grid, stream);
+    }
 }
 
 }  // namespace dg
