@@ -199,7 +199,7 @@ struct NormBackwardParams {
     float alpha;
     int64_t T;
     int H;
-    int cols;    // columns of a CTA: H, or half of it
+    int cols;    // columns of a CTA: H, or a share of it
     int stages;
     uint4 *dx, *dy;
     float *part;  // [grid / CTAS][sums][H] per-column sums of a CTA's rows
@@ -207,10 +207,11 @@ struct NormBackwardParams {
     int *status;
 };
 
-// Shared memory of the backward kernel: barriers, the reduction's words, the vectors in FP32
-// and a ring of rows (dn, r, dr, y).
-constexpr int kNormHeader = 1024;
-constexpr int kNormMaxStages = 4;
+constexpr int kBackThreads = 512;                      // eight columns a thread: 4096 columns a CTA
+constexpr int kBackCols = kBackThreads * kVec;
+constexpr int kNormMaxStages = 6;
+constexpr int kNormHeader = 3072;  // barriers and flag, then the warps' sums, then the ring of rows (dn, r, y, dr)
+constexpr int kNormSums = 128;     // [2][4][16 warps x 4 CTAs] floats
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
@@ -218,53 +219,69 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+// Four values summed over a warp's lanes: lane l holds the sum of value (l / 8) % 4.  Two exchanges
+// halve what each lane carries, so this takes six shuffles instead of twenty.
+__device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
+    const int lane = lane_id();
+    const bool high = lane & 16, odd = lane & 8;
+    const float keep0 = high ? c : a, keep1 = high ? d : b, give0 = high ? a : c, give1 = high ? b : d;
+    const float x = keep0 + __shfl_xor_sync(0xFFFFFFFFu, give0, 16), y = keep1 + __shfl_xor_sync(0xFFFFFFFFu, give1, 16);
+    float v = (odd ? y : x) + __shfl_xor_sync(0xFFFFFFFFu, odd ? x : y, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 
-// CTAS CTAs (a cluster) walk rows together, each over its columns, NV pieces a thread.  The
-// per-column sums stay in registers until the last row.
-template <int NV, int CTAS, bool Y, bool POST, bool GATE>
-__global__ void __launch_bounds__(512) rmsnorm_backward_kernel(const NormBackwardParams p) {
+// CTAS CTAs (a cluster) walk rows together, each over up to 4096 columns, eight a thread.  The
+// vectors and the per-column sums stay in registers; rows come through a ring of bulk copies.
+// The loop takes a row's sums one iteration before it uses them, so that one barrier a row
+// (the cluster's where there is one) publishes the next row's sums and frees the last row's
+// stage, and the reduction of one row runs under the arithmetic of the other.
+template <int CTAS, bool Y, bool POST, bool GATE>
+__global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const NormBackwardParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 64);
-    float *exchange = reinterpret_cast<float *>(smem + 80);                // [2][3]: the CTA's sums, per row parity
-    float4 *red = reinterpret_cast<float4 *>(smem + 128);                  // [2][16] per row parity and warp
-    float *vec = reinterpret_cast<float *>(smem + kNormHeader);            // weight, post, gate: [cols] each
+    constexpr int kWords = 16 * CTAS;  // warps of the cluster
+    float *red = reinterpret_cast<float *>(smem + kNormSums);  // [2][4][kWords]
+    uint8_t *ring = smem + kNormHeader;
     constexpr int kVectors = 1 + POST + GATE;
-    uint8_t *ring = smem + kNormHeader + kVectors * p.cols * 4;
     const int arrays = 2 + (p.dr != nullptr) + Y;
     const uint32_t row_bytes = static_cast<uint32_t>(p.cols) * 2;
     const uint32_t stage_bytes = row_bytes * arrays;
 
-    const int tid = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x);
-    const int warp = tid >> 5, warps = threads >> 5, lane = lane_id();
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = lane_id();
     const int rank = CTAS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int first = static_cast<int>(blockIdx.x) / CTAS, step = static_cast<int>(gridDim.x) / CTAS;
     const int col0 = rank * p.cols;
     const int cols = min(p.cols, p.H - col0);
     const uint32_t load_bytes = static_cast<uint32_t>(cols) * 2;
+    const bool mine = tid * kVec < cols;  // this thread has columns
 
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
+    for (int i = tid; i < 2 * 4 * kWords; i += static_cast<int>(blockDim.x)) red[i] = 0.0f;  // absent warps add nothing
     grid_dep_wait();
     grid_dep_launch_dependents();
-    for (int c = tid; c < cols; c += threads) {
-        auto one = [&](const void *v) {
-            return p.vec_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(v)[col0 + c])
-                              : static_cast<const float *>(v)[col0 + c];
-        };
-        vec[c] = one(p.weight);
-        if (POST) vec[p.cols + c] = one(p.post);
-        if (GATE) vec[(1 + POST) * p.cols + c] = one(p.gate);
+    const float2 zero = make_float2(0.0f, 0.0f);
+    float2 w[4], po[4], ga[4], acc_w[4], acc_g[4], acc_p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = po[j] = ga[j] = acc_w[j] = acc_g[j] = acc_p[j] = zero;
+    if (mine) {
+        load_vec8(p.weight, p.vec_bf16, col0 + tid * kVec, w);
+        if (POST) load_vec8(p.post, p.vec_bf16, col0 + tid * kVec, po);
+        if (GATE) load_vec8(p.gate, p.vec_bf16, col0 + tid * kVec, ga);
     }
-    __syncthreads();
+    auto everyone = [] {  // all threads that share rows
+        if (CTAS > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+    };
+    everyone();
 
     auto ask = [&](int64_t t, int s) {  // one thread
         uint8_t *dst = ring + s * stage_bytes;
@@ -280,174 +297,145 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(const NormBackwar
         for (; asked < p.stages && first + static_cast<int64_t>(asked) * step < p.T; ++asked)
             ask(first + static_cast<int64_t>(asked) * step, asked);
 
-    float2 acc_w[NV][4], acc_g[GATE ? NV : 1][4], acc_p[POST ? NV : 1][4];
-    const float2 zero = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            acc_w[v][j] = zero;
-            if (GATE) acc_g[v][j] = zero;
-            if (POST) acc_p[v][j] = zero;
-        }
-    const float inv_h = 1.0f / static_cast<float>(p.H);
-
-    int it = 0;
-    for (int64_t t = first; t < p.T; t += step, ++it) {
-        const int s = it % p.stages;
-        const uint8_t *src = ring + s * stage_bytes;
-        const float rstd = __ldg(p.rstd + t), rstd_y = POST ? __ldg(p.rstd_y + t) : 1.0f;
-        if (!mbar_wait(&full[s], static_cast<uint32_t>(it / p.stages) & 1u, abort_flag, p.timeout_ns)) {
+    auto piece = [&](int s, int array, float2(&out)[4]) {
+        bf16x8_to_f32(reinterpret_cast<const uint4 *>(ring + s * stage_bytes + array * row_bytes)[tid], out);
+    };
+    // the warp's share of a row's sums, to every CTA of the cluster
+    auto sum_row = [&](int it, int s, uint32_t parity, float rstd, float rstd_y) {
+        if (!mbar_wait(&full[s], parity, abort_flag, p.timeout_ns)) {
             // no row is asked for any more, and every later wait ends at once
             record_failure(p.status, kStatusTimeout, 20, it);
             *abort_flag = 1;
         }
-        const float2 rstd2 = make_float2(rstd, rstd), rstd_y2 = make_float2(rstd_y, rstd_y);
         float2 s1 = zero, s2 = zero, s3 = zero;
-        auto load = [&](int array, int i, float2(&out)[4]) {
-            bf16x8_to_f32(reinterpret_cast<const uint4 *>(src + array * row_bytes)[i], out);
-        };
-        auto vec8 = [&](int which, int i, float2(&out)[4]) {
-            const float4 *q = reinterpret_cast<const float4 *>(vec + which * p.cols) + 2 * i;
-            const float4 a = q[0], b = q[1];
-            out[0] = make_float2(a.x, a.y);
-            out[1] = make_float2(a.z, a.w);
-            out[2] = make_float2(b.x, b.y);
-            out[3] = make_float2(b.z, b.w);
-        };
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int i = tid + v * threads;
-            if (i * kVec >= cols) break;
-            float2 dn[4], rh[4], w[4];
-            load(0, i, dn);
-            load(1, i, rh);
-            vec8(0, i, w);
+        if (mine) {
+            const float2 rs = make_float2(rstd, rstd), ry = make_float2(rstd_y, rstd_y);
+            float2 g[4], rh[4];
+            piece(s, 0, g);
+            piece(s, 1, rh);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                rh[j] = __fmul2_rn(rh[j], rstd2);
-                dn[j] = __fmul2_rn(dn[j], w[j]);
-                s1 = __ffma2_rn(dn[j], rh[j], s1);
+                rh[j] = __fmul2_rn(rh[j], rs);
+                g[j] = __fmul2_rn(g[j], w[j]);
+                s1 = __ffma2_rn(g[j], rh[j], s1);
             }
             if (POST) {
-                float2 q[4], d[4];
-                load(2, i, q);
-                vec8(1, i, w);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) q[j] = __fmul2_rn(__fmul2_rn(q[j], rstd_y2), w[j]);
-                if (GATE) {
-                    vec8(1 + POST, i, w);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) q[j] = __fmul2_rn(q[j], w[j]);
-                }
-                if (p.dr) {
-                    load(2 + Y, i, d);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) d[j] = zero;
-                }
+                float2 q[4];
+                piece(s, 2, q);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s2 = __ffma2_rn(__ffma2_rn(dn[j], rstd2, d[j]), q[j], s2);
+                    q[j] = __fmul2_rn(__fmul2_rn(q[j], ry), po[j]);
+                    if (GATE) q[j] = __fmul2_rn(q[j], ga[j]);
                     s3 = __ffma2_rn(rh[j], q[j], s3);
+                    g[j] = __fmul2_rn(g[j], rs);
                 }
+                if (p.dr) {
+                    piece(s, 2 + Y, rh);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) g[j] = __fadd2_rn(g[j], rh[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(g[j], q[j], s2);
             }
         }
-        float a = s1.x + s1.y, b = s2.x + s2.y, c = s3.x + s3.y;
+        const float v = warp_sum4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.0f);
+        if ((lane & 7) == 0) {
+            float *word = red + ((it & 1) * 4 + (lane >> 3)) * kWords + rank * 16 + warp;
+            if (CTAS == 1) {
+                *word = v;
+            } else {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-            if (POST) {
-                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-                c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+                for (int c = 0; c < CTAS; ++c)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(word), c)), "f"(v) : "memory");
             }
         }
-        float4 *words = red + (it & 1) * 16;  // the other row's may still be read
-        if (lane == 0) words[warp] = make_float4(a, b, c, 0.0f);
-        __syncthreads();
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int i = 0; i < warps; ++i) {
-            const float4 w = words[i];
-            sum.x += w.x;
-            sum.y += w.y;
-            sum.z += w.z;
-        }
-        if (CTAS > 1) {
-            float *mine = exchange + (it & 1) * 3;
-            if (tid == 0) mine[0] = sum.x, mine[1] = sum.y, mine[2] = sum.z;
-            cluster_sync();
-            const uint32_t at = smem_u32(mine);
-            sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    float c1 = 0.0f, c2 = 0.0f;
+    const float inv_h = 1.0f / static_cast<float>(p.H);
+    auto read_sums = [&](int it, float rstd) {  // after everyone(): in the same order in every warp and CTA
+        const float *words = red + ((it & 1) * 4 + (lane >> 3)) * kWords + (lane & 7) * 2;
+        float v = 0.0f;
 #pragma unroll
-            for (int q = 0; q < CTAS; ++q) {  // the same order in every CTA
-                const uint32_t far = mapa_shared(at, q);
-                sum.x += ld_cluster_f32(far);
-                sum.y += ld_cluster_f32(far + 4);
-                sum.z += ld_cluster_f32(far + 8);
-            }
+        for (int c = 0; c < CTAS; ++c) {
+            const float2 two = *reinterpret_cast<const float2 *>(words + 16 * c);
+            v += two.x + two.y;
         }
-        const float c1 = sum.x * inv_h;
-        const float c2 = (sum.y - rstd * c1 * sum.z) * inv_h;
-        const float2 back = make_float2(-rstd * c1, -rstd * c1), alpha2 = make_float2(p.alpha, p.alpha);
-        const float2 c2n = make_float2(-c2, -c2);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int i = tid + v * threads;
-            if (i * kVec >= cols) break;
-            float2 dn[4], rh[4], w[4], d[4];
-            load(0, i, dn);
-            load(1, i, rh);
-            vec8(0, i, w);
+        for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        c1 = __shfl_sync(0xFFFFFFFFu, v, 0) * inv_h;
+        if (POST) c2 = __shfl_sync(0xFFFFFFFFu, v, 8) * inv_h - rstd * c1 * (__shfl_sync(0xFFFFFFFFu, v, 16) * inv_h);
+    };
+    auto scale_of_row = [&](const float *v, int64_t t) { return t < p.T ? __ldg(v + t) : 0.0f; };
+
+    int64_t t = first;
+    float rstd = scale_of_row(p.rstd, t), rstd_y = POST ? scale_of_row(p.rstd_y, t) : 1.0f;
+    if (t < p.T) sum_row(0, 0, 0u, rstd, rstd_y);
+    everyone();
+    if (t < p.T) read_sums(0, rstd);
+    int s = 0, next_s = 1;  // at least two stages
+    uint32_t next_parity = 0u;
+    float next_rstd = scale_of_row(p.rstd, t + step), next_rstd_y = POST ? scale_of_row(p.rstd_y, t + step) : 1.0f;
+    for (int it = 0; t < p.T; t += step, ++it) {
+        const int64_t next = t + step;
+        const float later_rstd = scale_of_row(p.rstd, next + step);
+        const float later_rstd_y = POST ? scale_of_row(p.rstd_y, next + step) : 1.0f;
+        if (next < p.T) sum_row(it + 1, next_s, next_parity, next_rstd, next_rstd_y);
+        if (mine) {
+            const float2 rs = make_float2(rstd, rstd), ry = make_float2(rstd_y, rstd_y);
+            const float2 back = make_float2(-rstd * c1, -rstd * c1), alpha2 = make_float2(p.alpha, p.alpha);
+            const float2 c2n = make_float2(-c2, -c2);
+            float2 dn[4], rh[4], d[4];
+            piece(s, 0, dn);
+            piece(s, 1, rh);
             if (p.dr) {
-                load(2 + Y, i, d);
+                piece(s, 2 + Y, d);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[j] = zero;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                rh[j] = __fmul2_rn(rh[j], rstd2);
-                acc_w[v][j] = __ffma2_rn(dn[j], rh[j], acc_w[v][j]);
-                d[j] = __ffma2_rn(__fmul2_rn(dn[j], w[j]), rstd2, d[j]);
+                rh[j] = __fmul2_rn(rh[j], rs);
+                acc_w[j] = __ffma2_rn(dn[j], rh[j], acc_w[j]);
+                d[j] = __ffma2_rn(__fmul2_rn(dn[j], w[j]), rs, d[j]);
                 d[j] = __ffma2_rn(back, rh[j], d[j]);  // dR
-                w[j] = __fmul2_rn(d[j], alpha2);
+                dn[j] = __fmul2_rn(d[j], alpha2);
             }
-            const int64_t out = (t * p.H + col0) / kVec + i;
-            p.dx[out] = pack8(w);
+            const int64_t out = (t * p.H + col0) / kVec + tid;
+            p.dx[out] = pack8(dn);
             if (Y) {
-                float2 u[4], g[4], yh[4];
-                load(2, i, u);
-                if (POST) {
-                    vec8(1, i, w);
+                float2 u[4];
+                piece(s, 2, u);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        yh[j] = __fmul2_rn(u[j], rstd_y2);
-                        u[j] = __fmul2_rn(yh[j], w[j]);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 yh = POST ? __fmul2_rn(u[j], ry) : u[j];
+                    if (GATE) {
+                        acc_g[j] = __ffma2_rn(d[j], POST ? __fmul2_rn(yh, po[j]) : yh, acc_g[j]);
+                        d[j] = __fmul2_rn(d[j], ga[j]);
                     }
-                }
-                if (GATE) {
-                    vec8(1 + POST, i, g);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        acc_g[v][j] = __ffma2_rn(d[j], u[j], acc_g[v][j]);
-                        d[j] = __fmul2_rn(d[j], g[j]);
-                    }
-                }
-                if (POST) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        acc_p[v][j] = __ffma2_rn(d[j], yh[j], acc_p[v][j]);
-                        d[j] = __fmul2_rn(__ffma2_rn(c2n, yh[j], __fmul2_rn(d[j], w[j])), rstd_y2);
+                    if (POST) {
+                        acc_p[j] = __ffma2_rn(d[j], yh, acc_p[j]);
+                        d[j] = __fmul2_rn(__ffma2_rn(c2n, yh, __fmul2_rn(d[j], po[j])), ry);
                     }
                 }
                 p.dy[out] = pack8(d);
             }
         }
-        __syncthreads();  // the stage has been read
-        const int64_t next = t + static_cast<int64_t>(p.stages) * step;
-        if (tid == 0 && next < p.T && !*abort_flag) {
-            ask(next, s);
+        everyone();  // the row's stage has been read, and the next row's sums are there
+        const int64_t refill = t + static_cast<int64_t>(p.stages) * step;
+        if (tid == 0 && refill < p.T && !*abort_flag) {
+            ask(refill, s);
             ++asked;
+        }
+        rstd = next_rstd;
+        rstd_y = next_rstd_y;
+        next_rstd = later_rstd;
+        next_rstd_y = later_rstd_y;
+        if (next < p.T) read_sums(it + 1, rstd);
+        s = next_s;
+        if (++next_s == p.stages) {
+            next_s = 0;
+            next_parity ^= 1u;
         }
     }
     if (tid == 0 && *abort_flag) {  // every copy must land before the CTA may exit
@@ -456,42 +444,44 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(const NormBackwar
             if (!mbar_wait(&full[i % p.stages], static_cast<uint32_t>(i / p.stages) & 1u, &never, p.timeout_ns))
                 record_failure(p.status, kStatusTimeout, 20, -1);
     }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int i = tid + v * threads;
-        if (i * kVec >= cols) break;
+    if (mine) {
         auto put = [&](int which, const float2(&a)[4]) {
-            float4 *dst = reinterpret_cast<float4 *>(p.part + (static_cast<int64_t>(first) * kVectors + which) * p.H + col0) + 2 * i;
+            float4 *dst = reinterpret_cast<float4 *>(p.part + (static_cast<int64_t>(first) * kVectors + which) * p.H + col0) + 2 * tid;
             dst[0] = make_float4(a[0].x, a[0].y, a[1].x, a[1].y);
             dst[1] = make_float4(a[2].x, a[2].y, a[3].x, a[3].y);
         };
-        put(0, acc_w[v]);
-        if (POST) put(1, acc_p[v]);
-        if (GATE) put(1 + POST, acc_g[v]);
+        put(0, acc_w);
+        if (POST) put(1, acc_p);
+        if (GATE) put(1 + POST, acc_g);
     }
-    if (CTAS > 1) cluster_sync();  // no CTA leaves while the other reads its sums
 }
 
-// Columns of [parts][columns] added up in order: 32 columns a CTA, eight threads a column.
-__global__ void __launch_bounds__(256) rmsnorm_columns_kernel(const float *__restrict__ part, int parts, int H, int vectors,
+// Columns of [parts][columns] added up in order: 32 columns a CTA, sixteen threads a column.
+__global__ void __launch_bounds__(512) rmsnorm_columns_kernel(const float *__restrict__ part, int parts, int H, int vectors,
                                                               float *__restrict__ out0, float *__restrict__ out1,
                                                               float *__restrict__ out2) {
-    __shared__ float sums[8][33];
+    __shared__ float sums[16][33];
     grid_dep_wait();
     grid_dep_launch_dependents();
     const int lane = lane_id(), w = static_cast<int>(threadIdx.x) >> 5;
     const int64_t width = static_cast<int64_t>(vectors) * H, c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float s = 0.0f;
     if (c < width) {
-#pragma unroll 4
-        for (int i = w; i < parts; i += 8) s += __ldg(part + i * width + c);
+        constexpr int kDeep = 10;  // loads in flight: 148 parts over 16 warps
+        for (int i0 = w; i0 < parts; i0 += kDeep * 16) {
+            float v[kDeep];
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j) v[j] = i0 + 16 * j < parts ? __ldg(part + (i0 + 16 * j) * width + c) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j) s += v[j];
+        }
     }
     sums[w][lane] = s;
     __syncthreads();
     if (w == 0 && c < width) {
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += sums[i][lane];
+        for (int i = 0; i < 16; ++i) s += sums[i][lane];
         const int which = static_cast<int>(c / H);
         (which == 0 ? out0 : which == 1 ? out1 : out2)[c - static_cast<int64_t>(which) * H] = s;
     }
@@ -500,37 +490,33 @@ __global__ void __launch_bounds__(256) rmsnorm_columns_kernel(const float *__res
 namespace {
 
 struct NormShape {
-    int nv, ctas, threads, cols, stages, grid;
+    int ctas, threads, cols, stages, grid;
     size_t smem;
 };
 
 constexpr int kSmemLimit = 232448;
 constexpr int kSms = 148;  // of a B200: the workspace is sized without asking a device
 
-NormShape norm_shape(int64_t T, int64_t H, bool y, bool post, bool gate, bool dr) {
+NormShape norm_shape(int64_t T, int64_t H, bool y, bool dr) {
     NormShape s;
-    s.ctas = H > 8192 ? 2 : 1;
-    s.cols = s.ctas == 1 ? static_cast<int>(H) : static_cast<int>((H / 2 + 15) / 16 * 16);
-    const int pieces = s.cols / kVec;
-    s.nv = pieces <= 512 ? 1 : 2;
-    s.threads = ((pieces + s.nv - 1) / s.nv + 31) / 32 * 32;
-    const int fixed = kNormHeader + (1 + post + gate) * s.cols * 4, stage = (2 + y + dr) * s.cols * 2;
-    s.stages = (kSmemLimit - fixed) / stage;
+    s.ctas = H <= kBackCols ? 1 : H <= 2 * kBackCols ? 2 : 4;
+    s.cols = static_cast<int>((H / s.ctas + 15) / 16 * 16);
+    if (s.ctas == 1) s.cols = static_cast<int>(H);
+    s.threads = (s.cols / kVec + 31) / 32 * 32;
+    const int per_sm = kBackThreads / s.threads;  // 128 registers a thread
+    const int stage = (2 + y + dr) * s.cols * 2;
+    s.stages = (kSmemLimit / per_sm - 1024 - kNormHeader) / stage;
     if (s.stages > kNormMaxStages) s.stages = kNormMaxStages;
-    s.smem = static_cast<size_t>(fixed) + static_cast<size_t>(s.stages) * stage;
-    int per_sm = 512 / s.threads;
-    const int fit = kSmemLimit / static_cast<int>(s.smem + 1024);
-    if (per_sm > fit) per_sm = fit;
-    if (per_sm < 1) per_sm = 1;
+    s.smem = static_cast<size_t>(kNormHeader) + static_cast<size_t>(s.stages) * stage;
     int64_t walkers = static_cast<int64_t>(kSms / s.ctas) * per_sm;
     if (walkers > T) walkers = T;
     s.grid = static_cast<int>(walkers) * s.ctas;
     return s;
 }
 
-template <int NV, int CTAS, bool Y, bool POST, bool GATE>
+template <int CTAS, bool Y, bool POST, bool GATE>
 dg_status_t launch_backward_impl(const NormBackwardParams &p, const NormShape &s, cudaStream_t stream) {
-    auto kernel = rmsnorm_backward_kernel<NV, CTAS, Y, POST, GATE>;
+    auto kernel = rmsnorm_backward_kernel<CTAS, Y, POST, GATE>;
     static thread_local int configured_device = -1;
     const dg_status_t st = allow_smem(kernel, kSmemLimit, configured_device);
     if (st != DG_OK) return st;
@@ -552,23 +538,22 @@ dg_status_t launch_backward_impl(const NormBackwardParams &p, const NormShape &s
 
 template <bool Y, bool POST, bool GATE>
 dg_status_t launch_backward_shape(const NormBackwardParams &p, const NormShape &s, cudaStream_t stream) {
-    if (s.ctas == 2) return launch_backward_impl<2, 2, Y, POST, GATE>(p, s, stream);
-    return s.nv == 1 ? launch_backward_impl<1, 1, Y, POST, GATE>(p, s, stream)
-                     : launch_backward_impl<2, 1, Y, POST, GATE>(p, s, stream);
+    if (s.ctas == 4) return launch_backward_impl<4, Y, POST, GATE>(p, s, stream);
+    return s.ctas == 2 ? launch_backward_impl<2, Y, POST, GATE>(p, s, stream)
+                       : launch_backward_impl<1, Y, POST, GATE>(p, s, stream);
 }
 
 }  // namespace
 
 int64_t rmsnorm_backward_workspace(int64_t T, int64_t H, bool post, bool gate) {
-    // the shape with the most walkers is the one with the smallest stages
-    const NormShape s = norm_shape(T, H, false, post, gate, false);
+    const NormShape s = norm_shape(T, H, false, false);
     return static_cast<int64_t>(s.grid / s.ctas) * (1 + post + gate) * H * 4;
 }
 
 dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
     (void)dev;
     const bool y = a.y != nullptr, post = a.post != nullptr, gate = a.gate != nullptr;
-    const NormShape s = norm_shape(a.T, a.H, y, post, gate, a.dr != nullptr);
+    const NormShape s = norm_shape(a.T, a.H, y, a.dr != nullptr);
     const KernelControl ctl = kernel_control();
     NormBackwardParams p;
     p.dn = static_cast<const uint8_t *>(a.dn);
@@ -603,7 +588,7 @@ dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo 
     const int vectors = 1 + post + gate;
     float *second = post ? a.dpost : a.dgate;
     const int64_t width = vectors * a.H;
-    return launch_pdl(rmsnorm_columns_kernel, static_cast<int>((width + 31) / 32), 256, 0, stream,
+    return launch_pdl(rmsnorm_columns_kernel, static_cast<int>((width + 31) / 32), 512, 0, stream,
                       static_cast<const float *>(p.part), s.grid / s.ctas, p.H, vectors, a.dweight, second, a.dgate);
 }
 
