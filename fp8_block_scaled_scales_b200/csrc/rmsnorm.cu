@@ -9,8 +9,10 @@
 //   dR = dr + rstd (dn w - rh c1),      c1 = mean(dn w rh)
 //   dx = alpha dR,   dw = sum_t dn rh,   dgate = sum_t dR u,   dpost = sum_t dR gate yh
 //   dy = rstd_y (dR gate post - yh c2), c2 = mean(dR gate post yh);  without post: dy = dR gate
-//   c2's sum needs c1's; written out, mean((dr + rstd dn w) q) - rstd c1 mean(rh q) with
-//   q = gate post yh, all three sums come out of one reduction.
+//   c2's sum needs c1's; written out with g = dn w and q = gate post y,
+//     c1 = rstd mean(g r),  c2 = rstd_y (mean(dr q) + rstd mean(g q) - rstd^2 c1 mean(r q)),
+//   all four sums come out of one reduction.  dgate and dpost have one sum in common:
+//     E = sum_t dR yh,  dgate = post E,  dpost = gate E   (yh = y without post).
 #include <cuda_bf16.h>
 
 #include "dg_device.cuh"
@@ -237,7 +239,8 @@ __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
 // The loop takes a row's sums one iteration before it uses them, so that one barrier a row
 // (the cluster's where there is one) publishes the next row's sums and frees the last row's
 // stage, and the reduction of one row runs under the arithmetic of the other.
-template <int CTAS, bool Y, bool POST, bool GATE>
+// VECTOR: y has a post or a gate (POST implies it).
+template <int CTAS, bool Y, bool POST, bool VECTOR>
 __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const NormBackwardParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
     constexpr int kWords = 16 * CTAS;  // warps of the cluster
     float *red = reinterpret_cast<float *>(smem + kNormSums);  // [2][4][kWords]
     uint8_t *ring = smem + kNormHeader;
-    constexpr int kVectors = 1 + POST + GATE;
+    constexpr int kSumsKept = 1 + VECTOR;
     const int arrays = 2 + (p.dr != nullptr) + Y;
     const uint32_t row_bytes = static_cast<uint32_t>(p.cols) * 2;
     const uint32_t stage_bytes = row_bytes * arrays;
@@ -267,13 +270,18 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
     grid_dep_wait();
     grid_dep_launch_dependents();
     const float2 zero = make_float2(0.0f, 0.0f);
-    float2 w[4], po[4], ga[4], acc_w[4], acc_g[4], acc_p[4];
+    float2 w[4], gp[4], acc_w[4], acc_e[4];  // weight, gate * post
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = po[j] = ga[j] = acc_w[j] = acc_g[j] = acc_p[j] = zero;
+    for (int j = 0; j < 4; ++j) w[j] = gp[j] = acc_w[j] = acc_e[j] = zero;
     if (mine) {
         load_vec8(p.weight, p.vec_bf16, col0 + tid * kVec, w);
-        if (POST) load_vec8(p.post, p.vec_bf16, col0 + tid * kVec, po);
-        if (GATE) load_vec8(p.gate, p.vec_bf16, col0 + tid * kVec, ga);
+        if (VECTOR) load_vec8(POST ? p.post : p.gate, p.vec_bf16, col0 + tid * kVec, gp);
+        if (POST && p.gate) {
+            float2 gate[4];
+            load_vec8(p.gate, p.vec_bf16, col0 + tid * kVec, gate);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) gp[j] = __fmul2_rn(gp[j], gate[j]);
+        }
     }
     auto everyone = [] {  // all threads that share rows
         if (CTAS > 1)
@@ -300,45 +308,40 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
     auto piece = [&](int s, int array, float2(&out)[4]) {
         bf16x8_to_f32(reinterpret_cast<const uint4 *>(ring + s * stage_bytes + array * row_bytes)[tid], out);
     };
-    // the warp's share of a row's sums, to every CTA of the cluster
-    auto sum_row = [&](int it, int s, uint32_t parity, float rstd, float rstd_y) {
+    // the warp's share of a row's sums (g r, dr q, g q, r q), to every CTA of the cluster
+    auto sum_row = [&](int it, int s, uint32_t parity) {
         if (!mbar_wait(&full[s], parity, abort_flag, p.timeout_ns)) {
             // no row is asked for any more, and every later wait ends at once
             record_failure(p.status, kStatusTimeout, 20, it);
             *abort_flag = 1;
         }
-        float2 s1 = zero, s2 = zero, s3 = zero;
+        float2 gr = zero, dq = zero, gq = zero, rq = zero;
         if (mine) {
-            const float2 rs = make_float2(rstd, rstd), ry = make_float2(rstd_y, rstd_y);
-            float2 g[4], rh[4];
+            float2 g[4], r[4];
             piece(s, 0, g);
-            piece(s, 1, rh);
+            piece(s, 1, r);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                rh[j] = __fmul2_rn(rh[j], rs);
                 g[j] = __fmul2_rn(g[j], w[j]);
-                s1 = __ffma2_rn(g[j], rh[j], s1);
+                gr = __ffma2_rn(g[j], r[j], gr);
             }
             if (POST) {
                 float2 q[4];
                 piece(s, 2, q);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    q[j] = __fmul2_rn(__fmul2_rn(q[j], ry), po[j]);
-                    if (GATE) q[j] = __fmul2_rn(q[j], ga[j]);
-                    s3 = __ffma2_rn(rh[j], q[j], s3);
-                    g[j] = __fmul2_rn(g[j], rs);
+                    q[j] = __fmul2_rn(q[j], gp[j]);
+                    gq = __ffma2_rn(g[j], q[j], gq);
+                    rq = __ffma2_rn(r[j], q[j], rq);
                 }
                 if (p.dr) {
-                    piece(s, 2 + Y, rh);
+                    piece(s, 2 + Y, r);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) g[j] = __fadd2_rn(g[j], rh[j]);
+                    for (int j = 0; j < 4; ++j) dq = __ffma2_rn(r[j], q[j], dq);
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(g[j], q[j], s2);
             }
         }
-        const float v = warp_sum4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.0f);
+        const float v = warp_sum4(gr.x + gr.y, dq.x + dq.y, gq.x + gq.y, rq.x + rq.y);
         if ((lane & 7) == 0) {
             float *word = red + ((it & 1) * 4 + (lane >> 3)) * kWords + rank * 16 + warp;
             if (CTAS == 1) {
@@ -350,9 +353,9 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
             }
         }
     };
-    float c1 = 0.0f, c2 = 0.0f;
+    float back = 0.0f, back_y = 0.0f;  // -rstd^2 c1 and -rstd_y^2 c2 of the row
     const float inv_h = 1.0f / static_cast<float>(p.H);
-    auto read_sums = [&](int it, float rstd) {  // after everyone(): in the same order in every warp and CTA
+    auto read_sums = [&](int it, float rstd, float rstd_y) {  // after everyone(): in the same order in every warp and CTA
         const float *words = red + ((it & 1) * 4 + (lane >> 3)) * kWords + (lane & 7) * 2;
         float v = 0.0f;
 #pragma unroll
@@ -362,16 +365,20 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        c1 = __shfl_sync(0xFFFFFFFFu, v, 0) * inv_h;
-        if (POST) c2 = __shfl_sync(0xFFFFFFFFu, v, 8) * inv_h - rstd * c1 * (__shfl_sync(0xFFFFFFFFu, v, 16) * inv_h);
+        v *= inv_h;
+        back = -rstd * rstd * rstd * __shfl_sync(0xFFFFFFFFu, v, 0);
+        if (POST) {
+            const float dq = __shfl_sync(0xFFFFFFFFu, v, 8), gq = __shfl_sync(0xFFFFFFFFu, v, 16), rq = __shfl_sync(0xFFFFFFFFu, v, 24);
+            back_y = -rstd_y * rstd_y * rstd_y * fmaf(back, rq, fmaf(rstd, gq, dq));
+        }
     };
     auto scale_of_row = [&](const float *v, int64_t t) { return t < p.T ? __ldg(v + t) : 0.0f; };
 
     int64_t t = first;
     float rstd = scale_of_row(p.rstd, t), rstd_y = POST ? scale_of_row(p.rstd_y, t) : 1.0f;
-    if (t < p.T) sum_row(0, 0, 0u, rstd, rstd_y);
+    if (t < p.T) sum_row(0, 0, 0u);
     everyone();
-    if (t < p.T) read_sums(0, rstd);
+    if (t < p.T) read_sums(0, rstd, rstd_y);
     int s = 0, next_s = 1;  // at least two stages
     uint32_t next_parity = 0u;
     float next_rstd = scale_of_row(p.rstd, t + step), next_rstd_y = POST ? scale_of_row(p.rstd_y, t + step) : 1.0f;
@@ -379,14 +386,13 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
         const int64_t next = t + step;
         const float later_rstd = scale_of_row(p.rstd, next + step);
         const float later_rstd_y = POST ? scale_of_row(p.rstd_y, next + step) : 1.0f;
-        if (next < p.T) sum_row(it + 1, next_s, next_parity, next_rstd, next_rstd_y);
+        if (next < p.T) sum_row(it + 1, next_s, next_parity);
         if (mine) {
-            const float2 rs = make_float2(rstd, rstd), ry = make_float2(rstd_y, rstd_y);
-            const float2 back = make_float2(-rstd * c1, -rstd * c1), alpha2 = make_float2(p.alpha, p.alpha);
-            const float2 c2n = make_float2(-c2, -c2);
-            float2 dn[4], rh[4], d[4];
-            piece(s, 0, dn);
-            piece(s, 1, rh);
+            const float2 rs = make_float2(rstd, rstd), ry = make_float2(rstd_y, rstd_y), alpha2 = make_float2(p.alpha, p.alpha);
+            const float2 back2 = make_float2(back, back), back_y2 = make_float2(back_y, back_y);
+            float2 m[4], r[4], d[4];
+            piece(s, 0, m);
+            piece(s, 1, r);
             if (p.dr) {
                 piece(s, 2 + Y, d);
             } else {
@@ -395,27 +401,23 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                rh[j] = __fmul2_rn(rh[j], rs);
-                acc_w[j] = __ffma2_rn(dn[j], rh[j], acc_w[j]);
-                d[j] = __ffma2_rn(__fmul2_rn(dn[j], w[j]), rs, d[j]);
-                d[j] = __ffma2_rn(back, rh[j], d[j]);  // dR
-                dn[j] = __fmul2_rn(d[j], alpha2);
+                m[j] = __fmul2_rn(m[j], rs);
+                acc_w[j] = __ffma2_rn(m[j], r[j], acc_w[j]);
+                d[j] = __ffma2_rn(m[j], w[j], d[j]);
+                d[j] = __ffma2_rn(r[j], back2, d[j]);  // dR
+                m[j] = __fmul2_rn(d[j], alpha2);
             }
             const int64_t out = (t * p.H + col0) / kVec + tid;
-            p.dx[out] = pack8(dn);
+            p.dx[out] = pack8(m);
             if (Y) {
-                float2 u[4];
-                piece(s, 2, u);
+                if (VECTOR) {
+                    piece(s, 2, r);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 yh = POST ? __fmul2_rn(u[j], ry) : u[j];
-                    if (GATE) {
-                        acc_g[j] = __ffma2_rn(d[j], POST ? __fmul2_rn(yh, po[j]) : yh, acc_g[j]);
-                        d[j] = __fmul2_rn(d[j], ga[j]);
-                    }
-                    if (POST) {
-                        acc_p[j] = __ffma2_rn(d[j], yh, acc_p[j]);
-                        d[j] = __fmul2_rn(__ffma2_rn(c2n, yh, __fmul2_rn(d[j], po[j])), ry);
+                    for (int j = 0; j < 4; ++j) {
+                        if (POST) d[j] = __fmul2_rn(d[j], ry);
+                        acc_e[j] = __ffma2_rn(d[j], r[j], acc_e[j]);
+                        d[j] = __fmul2_rn(d[j], gp[j]);
+                        if (POST) d[j] = __ffma2_rn(r[j], back_y2, d[j]);
                     }
                 }
                 p.dy[out] = pack8(d);
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
         rstd_y = next_rstd_y;
         next_rstd = later_rstd;
         next_rstd_y = later_rstd_y;
-        if (next < p.T) read_sums(it + 1, rstd);
+        if (next < p.T) read_sums(it + 1, rstd, rstd_y);
         s = next_s;
         if (++next_s == p.stages) {
             next_s = 0;
@@ -446,25 +448,26 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
     }
     if (mine) {
         auto put = [&](int which, const float2(&a)[4]) {
-            float4 *dst = reinterpret_cast<float4 *>(p.part + (static_cast<int64_t>(first) * kVectors + which) * p.H + col0) + 2 * tid;
+            float4 *dst = reinterpret_cast<float4 *>(p.part + (static_cast<int64_t>(first) * kSumsKept + which) * p.H + col0) + 2 * tid;
             dst[0] = make_float4(a[0].x, a[0].y, a[1].x, a[1].y);
             dst[1] = make_float4(a[2].x, a[2].y, a[3].x, a[3].y);
         };
         put(0, acc_w);
-        if (POST) put(1, acc_p);
-        if (GATE) put(1 + POST, acc_g);
+        if (VECTOR) put(1, acc_e);
     }
 }
 
-// Columns of [parts][columns] added up in order: 32 columns a CTA, sixteen threads a column.
-__global__ void __launch_bounds__(512) rmsnorm_columns_kernel(const float *__restrict__ part, int parts, int H, int vectors,
-                                                              float *__restrict__ out0, float *__restrict__ out1,
-                                                              float *__restrict__ out2) {
-    __shared__ float sums[16][33];
+// Columns of [parts][sums][H] added up in order: 32 columns a CTA, sixteen threads a column.  The
+// second sum is E, of which dgate and dpost are multiples.
+__global__ void __launch_bounds__(512) rmsnorm_columns_kernel(const float *__restrict__ part, int parts, int H, int sums,
+                                                              const void *post, const void *gate, bool vec_bf16,
+                                                              float *__restrict__ dweight, float *__restrict__ dpost,
+                                                              float *__restrict__ dgate) {
+    __shared__ float shares[16][33];
     grid_dep_wait();
     grid_dep_launch_dependents();
     const int lane = lane_id(), w = static_cast<int>(threadIdx.x) >> 5;
-    const int64_t width = static_cast<int64_t>(vectors) * H, c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const int64_t width = static_cast<int64_t>(sums) * H, c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float s = 0.0f;
     if (c < width) {
         constexpr int kDeep = 10;  // loads in flight: 148 parts over 16 warps
@@ -476,14 +479,23 @@ __global__ void __launch_bounds__(512) rmsnorm_columns_kernel(const float *__res
             for (int j = 0; j < kDeep; ++j) s += v[j];
         }
     }
-    sums[w][lane] = s;
+    shares[w][lane] = s;
     __syncthreads();
     if (w == 0 && c < width) {
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s += sums[i][lane];
-        const int which = static_cast<int>(c / H);
-        (which == 0 ? out0 : which == 1 ? out1 : out2)[c - static_cast<int64_t>(which) * H] = s;
+        for (int i = 0; i < 16; ++i) s += shares[i][lane];
+        if (c < H) {
+            dweight[c] = s;
+        } else {
+            const int64_t h = c - H;
+            auto times = [&](const void *v) {  // one element of a vector, or 1
+                if (!v) return 1.0f;
+                return vec_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(v)[h]) : static_cast<const float *>(v)[h];
+            };
+            if (dgate) dgate[h] = s * times(post);
+            if (dpost) dpost[h] = s * times(gate);
+        }
     }
 }
 
@@ -514,9 +526,9 @@ NormShape norm_shape(int64_t T, int64_t H, bool y, bool dr) {
     return s;
 }
 
-template <int CTAS, bool Y, bool POST, bool GATE>
+template <int CTAS, bool Y, bool POST, bool VECTOR>
 dg_status_t launch_backward_impl(const NormBackwardParams &p, const NormShape &s, cudaStream_t stream) {
-    auto kernel = rmsnorm_backward_kernel<CTAS, Y, POST, GATE>;
+    auto kernel = rmsnorm_backward_kernel<CTAS, Y, POST, VECTOR>;
     static thread_local int configured_device = -1;
     const dg_status_t st = allow_smem(kernel, kSmemLimit, configured_device);
     if (st != DG_OK) return st;
@@ -536,18 +548,18 @@ dg_status_t launch_backward_impl(const NormBackwardParams &p, const NormShape &s
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
-template <bool Y, bool POST, bool GATE>
+template <bool Y, bool POST, bool VECTOR>
 dg_status_t launch_backward_shape(const NormBackwardParams &p, const NormShape &s, cudaStream_t stream) {
-    if (s.ctas == 4) return launch_backward_impl<4, Y, POST, GATE>(p, s, stream);
-    return s.ctas == 2 ? launch_backward_impl<2, Y, POST, GATE>(p, s, stream)
-                       : launch_backward_impl<1, Y, POST, GATE>(p, s, stream);
+    if (s.ctas == 4) return launch_backward_impl<4, Y, POST, VECTOR>(p, s, stream);
+    return s.ctas == 2 ? launch_backward_impl<2, Y, POST, VECTOR>(p, s, stream)
+                       : launch_backward_impl<1, Y, POST, VECTOR>(p, s, stream);
 }
 
 }  // namespace
 
 int64_t rmsnorm_backward_workspace(int64_t T, int64_t H, bool post, bool gate) {
     const NormShape s = norm_shape(T, H, false, false);
-    return static_cast<int64_t>(s.grid / s.ctas) * (1 + post + gate) * H * 4;
+    return static_cast<int64_t>(s.grid / s.ctas) * (1 + (post || gate)) * H * 4;
 }
 
 dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
@@ -579,17 +591,15 @@ dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo 
     if (a.T > 0) {
         dg_status_t st;
         if (!y) st = launch_backward_shape<false, false, false>(p, s, stream);
-        else if (post) st = gate ? launch_backward_shape<true, true, true>(p, s, stream)
-                                 : launch_backward_shape<true, true, false>(p, s, stream);
-        else st = gate ? launch_backward_shape<true, false, true>(p, s, stream)
-                       : launch_backward_shape<true, false, false>(p, s, stream);
+        else if (post) st = launch_backward_shape<true, true, true>(p, s, stream);
+        else if (gate) st = launch_backward_shape<true, false, true>(p, s, stream);
+        else st = launch_backward_shape<true, false, false>(p, s, stream);
         if (st != DG_OK) return st;
     }
-    const int vectors = 1 + post + gate;
-    float *second = post ? a.dpost : a.dgate;
-    const int64_t width = vectors * a.H;
-    return launch_pdl(rmsnorm_columns_kernel, static_cast<int>((width + 31) / 32), 512, 0, stream,
-                      static_cast<const float *>(p.part), s.grid / s.ctas, p.H, vectors, a.dweight, second, a.dgate);
+    const int sums = 1 + (post || gate);
+    return launch_pdl(rmsnorm_columns_kernel, static_cast<int>((sums * a.H + 31) / 32), 512, 0, stream,
+                      static_cast<const float *>(p.part), s.grid / s.ctas, p.H, sums, a.post, a.gate, a.vec_bf16, a.dweight,
+                      a.dpost, a.dgate);
 }
 
 }  // namespace dg
