@@ -237,13 +237,18 @@ __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
 // CTAS CTAs (a cluster) walk rows together, each over up to 4096 columns, eight a thread.  The
 // vectors and the per-column sums stay in registers; rows come through a ring of bulk copies.
 // The loop takes a row's sums one iteration before it uses them, so that one barrier a row
-// (the cluster's where there is one) publishes the next row's sums and frees the last row's
-// stage, and the reduction of one row runs under the arithmetic of the other.
+// publishes the next row's sums and frees the last row's stage, and the reduction of one row
+// runs under the arithmetic of the other.  In a cluster each warp stores its share into every
+// CTA asynchronously, counted by that CTA's barrier of the row's parity: the cluster's own
+// barrier would wait for the row's stores to global memory (8192 x 8192: 232 us with it).  A share of row
+// i + 2 cannot overtake a reader of row i: it is sent after all shares of row i + 1 have come, and a warp
+// sends its share of row i + 1 after it has read row i.
 // VECTOR: y has a post or a gate (POST implies it).
 template <int CTAS, bool Y, bool POST, bool VECTOR>
 __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const NormBackwardParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
+    uint64_t *shared_sums = full + kNormMaxStages;  // [2], in a cluster: a row's shares have come
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 64);
     constexpr int kWords = 16 * CTAS;  // warps of the cluster
     float *red = reinterpret_cast<float *>(smem + kNormSums);  // [2][4][kWords]
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
     const bool mine = tid * kVec < cols;  // this thread has columns
 
     if (tid == 0) {
-        for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+        for (int s = 0; s < kNormMaxStages + 2; ++s) mbar_init(&full[s], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -283,13 +288,11 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
             for (int j = 0; j < 4; ++j) gp[j] = __fmul2_rn(gp[j], gate[j]);
         }
     }
-    auto everyone = [] {  // all threads that share rows
-        if (CTAS > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-    };
-    everyone();
+    if (CTAS > 1)
+        cluster_sync();  // every CTA's barriers are there
+    else
+        __syncthreads();
+    const uint32_t share_bytes = static_cast<uint32_t>(blockDim.x >> 5) * 16 * CTAS;
 
     auto ask = [&](int64_t t, int s) {  // one thread
         uint8_t *dst = ring + s * stage_bytes;
@@ -342,20 +345,25 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
             }
         }
         const float v = warp_sum4(gr.x + gr.y, dq.x + dq.y, gq.x + gq.y, rq.x + rq.y);
-        if ((lane & 7) == 0) {
-            float *word = red + ((it & 1) * 4 + (lane >> 3)) * kWords + rank * 16 + warp;
-            if (CTAS == 1) {
-                *word = v;
-            } else {
-#pragma unroll
-                for (int c = 0; c < CTAS; ++c)
-                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(word), c)), "f"(v) : "memory");
-            }
+        float *word = red + ((it & 1) * 4 + (lane >> 3)) * kWords + rank * 16 + warp;
+        if (CTAS == 1) {
+            if ((lane & 7) == 0) *word = v;
+        } else {
+            if (tid == 0) mbar_arrive_expect_tx(&shared_sums[it & 1], share_bytes);
+            if ((lane & 7) < CTAS)  // one lane for each value and CTA
+                asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                                 mapa_shared(smem_u32(word), lane & 7)),
+                             "r"(__float_as_uint(v)), "r"(mapa_shared(smem_u32(&shared_sums[it & 1]), lane & 7))
+                             : "memory");
         }
     };
     float back = 0.0f, back_y = 0.0f;  // -rstd^2 c1 and -rstd_y^2 c2 of the row
     const float inv_h = 1.0f / static_cast<float>(p.H);
-    auto read_sums = [&](int it, float rstd, float rstd_y) {  // after everyone(): in the same order in every warp and CTA
+    auto read_sums = [&](int it, float rstd, float rstd_y) {  // in the same order in every warp and CTA
+        if (CTAS > 1 && !mbar_wait(&shared_sums[it & 1], static_cast<uint32_t>(it >> 1) & 1u, abort_flag, p.timeout_ns)) {
+            record_failure(p.status, kStatusTimeout, 21, it);
+            *abort_flag = 1;
+        }
         const float *words = red + ((it & 1) * 4 + (lane >> 3)) * kWords + (lane & 7) * 2;
         float v = 0.0f;
 #pragma unroll
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
     int64_t t = first;
     float rstd = scale_of_row(p.rstd, t), rstd_y = POST ? scale_of_row(p.rstd_y, t) : 1.0f;
     if (t < p.T) sum_row(0, 0, 0u);
-    everyone();
+    __syncthreads();
     if (t < p.T) read_sums(0, rstd, rstd_y);
     int s = 0, next_s = 1;  // at least two stages
     uint32_t next_parity = 0u;
@@ -423,7 +431,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
                 p.dy[out] = pack8(d);
             }
         }
-        everyone();  // the row's stage has been read, and the next row's sums are there
+        __syncthreads();  // the row's stage has been read, and the next row's sums are there
         const int64_t refill = t + static_cast<int64_t>(p.stages) * step;
         if (tid == 0 && refill < p.T && !*abort_flag) {
             ask(refill, s);
@@ -446,6 +454,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
             if (!mbar_wait(&full[i % p.stages], static_cast<uint32_t>(i / p.stages) & 1u, &never, p.timeout_ns))
                 record_failure(p.status, kStatusTimeout, 20, -1);
     }
+    if (CTAS > 1) cluster_sync();  // after a failure a CTA could leave while shares are on their way to it
     if (mine) {
         auto put = [&](int which, const float2(&a)[4]) {
             float4 *dst = reinterpret_cast<float4 *>(p.part + (static_cast<int64_t>(first) * kSumsKept + which) * p.H + col0) + 2 * tid;
@@ -520,7 +529,12 @@ NormShape norm_shape(int64_t T, int64_t H, bool y, bool dr) {
     s.stages = (kSmemLimit / per_sm - 1024 - kNormHeader) / stage;
     if (s.stages > kNormMaxStages) s.stages = kNormMaxStages;
     s.smem = static_cast<size_t>(kNormHeader) + static_cast<size_t>(s.stages) * stage;
-    int64_t walkers = static_cast<int64_t>(kSms / s.ctas) * per_sm;
+    // clusters of four lie within a GPC: 33 of them run at once on the 148 SMs, not 37 (4000 x 16384 with
+    // 37: 332 us, in two rounds)
+    int64_t walkers = s.ctas == 4 ? 32 : static_cast<int64_t>(kSms / s.ctas) * per_sm;
+    // two rows each at least, once every SM has a walker: fewer sums to add up (333 x 784: 6.9 -> 6.7 us)
+    const int64_t one_round = kSms / s.ctas;
+    if (walkers > one_round && walkers > T / 2) walkers = T / 2 > one_round ? T / 2 : one_round;
     if (walkers > T) walkers = T;
     s.grid = static_cast<int>(walkers) * s.ctas;
     return s;
