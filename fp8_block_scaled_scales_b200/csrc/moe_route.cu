@@ -613,16 +613,16 @@ RouteShape balance_shape(int64_t T, int G) {
     const int64_t most = route_max_threads(per_lane(G)) / 32;
     int64_t warps = (T + kSms - 1) / kSms;
     warps = warps < 4 ? 4 : warps > most ? most : warps;
-    int64_t grid = (T + warps - 1) / warps;
-    const int64_t limit = kSms * (1024 / 32 / most);
-    grid = grid < 1 ? 1 : grid > limit ? limit : grid;
-    return {static_cast<int>(warps) * 32, static_cast<int>(grid)};
+    const int64_t grid = (T + warps - 1) / warps, limit = kSms * (32 / most);
+    return {static_cast<int>(warps) * 32, static_cast<int>(grid < 1 ? 1 : grid > limit ? limit : grid)};
 }
 
 }  // namespace
 
+// As many parts as any T up to this one gives: a workspace for the largest batch serves smaller ones.
 int64_t route_workspace(int64_t T, int G) {
-    return static_cast<int64_t>(balance_shape(T, G).grid) * (G * 8 + 4);
+    const int64_t most = T < 4 ? 1 : (T + 3) / 4, limit = kSms * (32 * 32 / route_max_threads(per_lane(G)));
+    return (most < limit ? most : limit) * (G * 8 + 4);
 }
 
 template <int PER, bool BIAS, bool BALANCE>

@@ -67,7 +67,24 @@ __device__ __forceinline__ float cta_sum(float v, float *red) {
     return v;
 }
 
-// A CTA per row, NV pieces of eight columns a thread.
+// A thread's eight columns as codes; 16 threads hold a group of 128 columns and share its scale.
+// All lanes call it; those without columns (in == false) bring zeros.
+__device__ __forceinline__ void store_codes(const NormParams &p, const float2 (&n)[4], int64_t t, int col, bool in) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = amax3(m, n[j]);
+    uint32_t bits = __float_as_uint(m);  // a NaN above infinity
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
+    const FastScale s = fast_scale(__uint_as_float(bits));
+    if (in) {
+        const uint2 c = s.fast ? quantize8_f32<true>(n, s) : quantize8_f32<false>(n, s);
+        *reinterpret_cast<uint2 *>(p.q + t * p.H + col) = c;
+        if ((lane_id() & 15) == 0) p.s_t[static_cast<int64_t>(col >> 7) * p.T + t] = s.s;
+    }
+}
+
+// Few rows: a CTA per row, NV pieces of eight columns a thread.
 template <int NV, bool CODES>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p) {
     __shared__ float red[2][32];
@@ -145,22 +162,279 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p) {
         if (!CODES) {
             if (in) p.n[row + i] = pack8(w);
         } else {
-            // 16 threads hold a group of 128 columns
-            float m = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m = amax3(m, w[j]);
-            uint32_t bits = __float_as_uint(m);  // a NaN above infinity
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
-            const FastScale s = fast_scale(__uint_as_float(bits));
-            if (in) {
-                const uint2 c = s.fast ? quantize8_f32<true>(w, s) : quantize8_f32<false>(w, s);
-                *reinterpret_cast<uint2 *>(p.q + t * p.H + i * kVec) = c;
-                if ((tid & 15) == 0) p.s_t[static_cast<int64_t>(i >> 4) * p.T + t] = s.s;
-            }
+            store_codes(p, w, t, i * kVec, in);
         }
     }
 }
+
+// ------------------------------------------------------------------- walking over rows
+constexpr int kWalkThreads = 512;                      // eight columns a thread: 4096 columns a CTA
+constexpr int kWalkCols = kWalkThreads * kVec;
+constexpr int kWalkMaxStages = 6;
+constexpr int kWalkHeader = 3072;  // barriers and flag, then the warps' sums, then the ring of rows
+constexpr int kWalkSums = 128;     // [2][4][16 warps x 4 CTAs] floats
+constexpr int kSmemLimit = 232448;
+constexpr int kSms = 148;  // of a B200: the workspace is sized without asking a device
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// One float to the same place in CTA `rank` of the cluster, counted by that CTA's barrier `bar`.
+__device__ __forceinline__ void store_share(float *word, float v, uint64_t *bar, uint32_t rank) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                     mapa_shared(smem_u32(word), rank)),
+                 "r"(__float_as_uint(v)), "r"(mapa_shared(smem_u32(bar), rank))
+                 : "memory");
+}
+
+struct WalkShape {
+    int ctas, threads, cols, stages, grid;
+    size_t smem;
+};
+
+// For rows of H columns in `arrays` arrays: CTAs that walk a row together, threads of each, and
+// as many walkers as run at once with `warps` warps an SM.
+static WalkShape walk_shape(int64_t T, int64_t H, int arrays, int threads_per_sm) {
+    WalkShape s;
+    s.ctas = H <= kWalkCols ? 1 : H <= 2 * kWalkCols ? 2 : 4;
+    s.cols = s.ctas == 1 ? static_cast<int>(H) : static_cast<int>((H / s.ctas + 15) / 16 * 16);
+    s.threads = (s.cols / kVec + 31) / 32 * 32;
+    const int per_sm = threads_per_sm / s.threads;
+    const int stage = arrays * s.cols * 2;
+    s.stages = (kSmemLimit / per_sm - 1024 - kWalkHeader) / stage;
+    if (s.stages > kWalkMaxStages) s.stages = kWalkMaxStages;
+    s.smem = static_cast<size_t>(kWalkHeader) + static_cast<size_t>(s.stages) * stage;
+    // clusters of four lie within a GPC: 33 of them run at once on 148 SMs, not 37 (the gradient of 4000 x 16384
+    // with 37: 332 us, in two rounds; with 32 198)
+    int64_t walkers = (s.ctas == 4 ? 32 : static_cast<int64_t>(kSms / s.ctas)) * per_sm;
+    // two rows each at least, once every SM has a walker: fewer sums to add up (the gradient of 333 x 784: 6.9 -> 6.7 us)
+    const int64_t one_round = kSms / s.ctas;
+    if (walkers > one_round && walkers > T / 2) walkers = T / 2 > one_round ? T / 2 : one_round;
+    if (walkers > T) walkers = T;
+    s.grid = static_cast<int>(walkers) * s.ctas;
+    return s;
+}
+
+template <typename Kernel, typename Params>
+static dg_status_t launch_walk(Kernel kernel, const Params &p, const WalkShape &s, int &configured_device, cudaStream_t stream) {
+    const dg_status_t st = allow_smem(kernel, kSmemLimit, configured_device);
+    if (st != DG_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(s.grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(s.threads), 1, 1);
+    cfg.dynamicSmemBytes = s.smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(s.ctas);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = s.ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+struct NormWalkParams {
+    NormParams n;
+    int cols, stages;
+    uint64_t timeout_ns;
+    int *status;
+};
+
+// Many rows: CTAS CTAs (a cluster) walk rows together, each over up to 4096 columns.  The vectors
+// stay in registers, rows come through a ring of bulk copies.  An iteration finishes row k, forms r
+// of row k + 1 and squares y of row k + 2, so that a row's two sums take one barrier an
+// iteration and their latency passes under the other rows' arithmetic.  In a cluster the warps'
+// shares go to every CTA as in the gradient's kernel below.  VECTOR: y has a post or a gate.
+template <int CTAS, bool Y, bool POST, bool VECTOR, bool CODES>
+__global__ void __launch_bounds__(kWalkThreads, 2) rmsnorm_walk_kernel(const NormWalkParams wp) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const NormParams &p = wp.n;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem);
+    uint64_t *shared_sums = full + kWalkMaxStages;  // [2], in a cluster: an iteration's shares have come
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 64);
+    constexpr int kWords = 16 * CTAS;
+    float *red = reinterpret_cast<float *>(smem + kWalkSums);  // [2][2][kWords]: y^2 of row k + 2, r^2 of row k + 1
+    uint8_t *ring = smem + kWalkHeader;
+    const uint32_t row_bytes = static_cast<uint32_t>(wp.cols) * 2, stage_bytes = row_bytes * (1 + Y);
+
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = lane_id();
+    const int rank = CTAS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int first = static_cast<int>(blockIdx.x) / CTAS, step = static_cast<int>(gridDim.x) / CTAS;
+    const int col0 = rank * wp.cols;
+    const int cols = min(wp.cols, p.H - col0);
+    const uint32_t load_bytes = static_cast<uint32_t>(cols) * 2;
+    const bool mine = tid * kVec < cols;
+    const int rows = static_cast<int>((p.T - first + step - 1) / step);  // the grid has no more walkers than rows
+
+    if (tid == 0) {
+        for (int s = 0; s < kWalkMaxStages + 2; ++s) mbar_init(&full[s], 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    for (int i = tid; i < 2 * 2 * kWords; i += static_cast<int>(blockDim.x)) red[i] = 0.0f;  // absent warps add nothing
+    grid_dep_wait();
+    grid_dep_launch_dependents();
+    const float2 zero = make_float2(0.0f, 0.0f);
+    float2 w[4], gp[4], r[4];  // weight, gate * post
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = gp[j] = r[j] = zero;
+    if (mine) {
+        load_vec8(p.weight, p.vec_bf16, col0 + tid * kVec, w);
+        if (VECTOR) load_vec8(POST ? p.post : p.gate, p.vec_bf16, col0 + tid * kVec, gp);
+        if (POST && p.gate) {
+            load_vec8(p.gate, p.vec_bf16, col0 + tid * kVec, r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) gp[j] = __fmul2_rn(gp[j], r[j]);
+        }
+    }
+    if (CTAS > 1)
+        cluster_sync();  // every CTA's barriers are there
+    else
+        __syncthreads();
+    const uint32_t share_bytes = static_cast<uint32_t>(blockDim.x >> 5) * 8 * CTAS;
+
+    auto row_of = [&](int i) { return first + static_cast<int64_t>(i) * step; };
+    auto ask = [&](int i, int s) {  // one thread
+        uint8_t *dst = ring + s * stage_bytes;
+        const int64_t at = (row_of(i) * p.H + col0) * 2;
+        mbar_arrive_expect_tx(&full[s], load_bytes * (1 + Y));
+        bulk_load(dst, reinterpret_cast<const uint8_t *>(p.x) + at, load_bytes, &full[s]);
+        if (Y) bulk_load(dst + row_bytes, reinterpret_cast<const uint8_t *>(p.y) + at, load_bytes, &full[s]);
+    };
+    int asked = 0;
+    if (tid == 0)
+        for (; asked < wp.stages && asked < rows; ++asked) ask(asked, asked);
+    auto piece = [&](int s, int array, float2(&out)[4]) {
+        bf16x8_to_f32(reinterpret_cast<const uint4 *>(ring + s * stage_bytes + array * row_bytes)[tid], out);
+    };
+    const float inv_h = 1.0f / static_cast<float>(p.H);
+    const float2 alpha2 = make_float2(p.alpha, p.alpha);
+    constexpr int kAhead = POST ? 2 : 1;  // rows that come in before row k is finished
+    float rstd = 0.0f, rstd_y = 1.0f;     // of rows k and k + 1
+    int s_in = 0, s_r = 0;                // stages of rows k + kAhead and k + 1
+    uint32_t parity = 0u;                 // of the first
+
+    for (int k = -kAhead; k < rows; ++k) {
+        const int it = k + kAhead;
+        float yy = 0.0f, rr = 0.0f;
+        if (it < rows) {
+            if (!mbar_wait(&full[s_in], parity, abort_flag, wp.timeout_ns)) {
+                // no row is asked for any more, and every later wait ends at once
+                record_failure(wp.status, kStatusTimeout, 22, it);
+                *abort_flag = 1;
+            }
+            if (POST && mine) {
+                float2 y[4], sum = zero;
+                piece(s_in, 1, y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum = __ffma2_rn(y[j], y[j], sum);
+                yy = sum.x + sum.y;
+            }
+        }
+        if (k >= 0) {  // n of row k
+            const int64_t t = row_of(k);
+            if (tid == 0 && rank == 0 && p.rstd) p.rstd[t] = rstd;
+            const float2 rs = make_float2(rstd, rstd);
+            float2 n[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) n[j] = __fmul2_rn(__fmul2_rn(r[j], rs), w[j]);
+            if (!CODES) {
+                if (mine) p.n[(t * p.H + col0) / kVec + tid] = pack8(n);
+            } else {
+                store_codes(p, n, t, col0 + tid * kVec, mine);
+            }
+        }
+        if (k + 1 >= 0 && k + 1 < rows) {  // r of row k + 1
+            const int64_t t = row_of(k + 1);
+            if (POST && tid == 0 && rank == 0 && p.rstd_y) p.rstd_y[t] = rstd_y;
+            if (mine) {
+                piece(s_r, 0, r);
+                if (Y) {
+                    const float2 ry = make_float2(rstd_y, rstd_y);
+                    float2 u[4];
+                    piece(s_r, 1, u);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (POST) u[j] = __fmul2_rn(u[j], ry);
+                        if (VECTOR) u[j] = __fmul2_rn(u[j], gp[j]);
+                        r[j] = __ffma2_rn(alpha2, r[j], u[j]);
+                    }
+                    p.r[(t * p.H + col0) / kVec + tid] = pack8(r);
+                }
+                float2 sum = zero;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum = __ffma2_rn(r[j], r[j], sum);
+                rr = sum.x + sum.y;
+            }
+        }
+        {  // lanes 0 to 15 sum y^2, the others r^2
+            const bool high = lane & 16;
+            float v = (high ? rr : yy) + __shfl_xor_sync(0xFFFFFFFFu, high ? yy : rr, 16);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            float *word = red + ((it & 1) * 2 + (lane >> 4)) * kWords + rank * 16 + warp;
+            if (CTAS == 1) {
+                if ((lane & 15) == 0) *word = v;
+            } else {
+                if (tid == 0) mbar_arrive_expect_tx(&shared_sums[it & 1], share_bytes);
+                if ((lane & 15) < CTAS) store_share(word, v, &shared_sums[it & 1], lane & 15);
+            }
+        }
+        __syncthreads();  // row k + 1's stage has been read, and the CTA's sums are there
+        if (tid == 0 && k + 1 >= 0 && k + 1 + wp.stages < rows && !*abort_flag) {
+            ask(k + 1 + wp.stages, s_r);
+            ++asked;
+        }
+        if (CTAS > 1 && !mbar_wait(&shared_sums[it & 1], static_cast<uint32_t>(it >> 1) & 1u, abort_flag, wp.timeout_ns)) {
+            record_failure(wp.status, kStatusTimeout, 23, it);
+            *abort_flag = 1;
+        }
+        float v = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CTAS; ++c) v += red[((it & 1) * 2 + (lane >> 4)) * kWords + c * 16 + (lane & 15)];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        v = __frsqrt_rn(fmaf(v, inv_h, p.eps));
+        if (POST) rstd_y = __shfl_sync(0xFFFFFFFFu, v, 0);
+        rstd = __shfl_sync(0xFFFFFFFFu, v, 16);
+        if (k + 1 >= 0) s_r = s_r + 1 == wp.stages ? 0 : s_r + 1;
+        if (++s_in == wp.stages) {
+            s_in = 0;
+            parity ^= 1u;
+        }
+    }
+    if (tid == 0 && *abort_flag) {  // every copy must land before the CTA may exit
+        const int never = 0;
+        for (int i = asked > wp.stages ? asked - wp.stages : 0; i < asked; ++i)
+            if (!mbar_wait(&full[i % wp.stages], static_cast<uint32_t>(i / wp.stages) & 1u, &never, wp.timeout_ns))
+                record_failure(wp.status, kStatusTimeout, 22, -1);
+    }
+    if (CTAS > 1) cluster_sync();  // after a failure a CTA could leave while shares are on their way to it
+}
+
+template <bool Y, bool POST, bool VECTOR, bool CODES>
+static dg_status_t launch_walk_forward(const NormWalkParams &p, const WalkShape &s, cudaStream_t stream) {
+    static thread_local int one = -1, two = -1, four = -1;
+    if (s.ctas == 1) return launch_walk(rmsnorm_walk_kernel<1, Y, POST, VECTOR, CODES>, p, s, one, stream);
+    if (s.ctas == 2) return launch_walk(rmsnorm_walk_kernel<2, Y, POST, VECTOR, CODES>, p, s, two, stream);
+    return launch_walk(rmsnorm_walk_kernel<4, Y, POST, VECTOR, CODES>, p, s, four, stream);
+}
+
+template <bool CODES>
+static dg_status_t launch_walk_form(const NormWalkParams &p, const WalkShape &s, cudaStream_t stream) {
+    if (!p.n.y) return launch_walk_forward<false, false, false, CODES>(p, s, stream);
+    if (p.n.post) return launch_walk_forward<true, true, true, CODES>(p, s, stream);
+    if (p.n.gate) return launch_walk_forward<true, false, true, CODES>(p, s, stream);
+    return launch_walk_forward<true, false, false, CODES>(p, s, stream);
+}
+
+// Above this many rows they are walked over.
+constexpr int64_t kWalkRows = 600;
 
 dg_status_t launch_rmsnorm(const NormArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
     NormParams p;
@@ -180,10 +454,16 @@ dg_status_t launch_rmsnorm(const NormArgs &a, const DeviceInfo &dev, cudaStream_
     p.s_t = a.s_t;
     p.rstd = a.rstd;
     p.rstd_y = a.rstd_y;
+    const bool codes = a.q != nullptr;
+    if (a.T > kWalkRows) {
+        const WalkShape s = walk_shape(a.T, a.H, 1 + (a.y != nullptr), 2 * kWalkThreads);
+        const KernelControl ctl = kernel_control();
+        const NormWalkParams wp = {p, s.cols, s.stages, ctl.timeout_ns, ctl.status};
+        return codes ? launch_walk_form<true>(wp, s, stream) : launch_walk_form<false>(wp, s, stream);
+    }
     const int pieces = p.H / kVec;
     auto threads_for = [&](int nv) { return (((pieces + nv - 1) / nv) + 31) / 32 * 32; };
     const int grid = static_cast<int>(a.T);
-    const bool codes = a.q != nullptr;
     const bool few = a.T <= 2 * dev.num_sms;  // rows that do not fill the GPU: short rather than many
     if (pieces <= 1024 && (few || pieces <= 128))
         return codes ? launch_pdl(rmsnorm_kernel<1, true>, grid, threads_for(1), 0, stream, p)
@@ -209,18 +489,6 @@ struct NormBackwardParams {
     int *status;
 };
 
-constexpr int kBackThreads = 512;                      // eight columns a thread: 4096 columns a CTA
-constexpr int kBackCols = kBackThreads * kVec;
-constexpr int kNormMaxStages = 6;
-constexpr int kNormHeader = 3072;  // barriers and flag, then the warps' sums, then the ring of rows (dn, r, y, dr)
-constexpr int kNormSums = 128;     // [2][4][16 warps x 4 CTAs] floats
-
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 // Four values summed over a warp's lanes: lane l holds the sum of value (l / 8) % 4.  Two exchanges
 // halve what each lane carries, so this takes six shuffles instead of twenty.
 __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
@@ -245,14 +513,14 @@ __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
 // sends its share of row i + 1 after it has read row i.
 // VECTOR: y has a post or a gate (POST implies it).
 template <int CTAS, bool Y, bool POST, bool VECTOR>
-__global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const NormBackwardParams p) {
+__global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const NormBackwardParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
-    uint64_t *shared_sums = full + kNormMaxStages;  // [2], in a cluster: a row's shares have come
+    uint64_t *shared_sums = full + kWalkMaxStages;  // [2], in a cluster: a row's shares have come
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 64);
     constexpr int kWords = 16 * CTAS;  // warps of the cluster
-    float *red = reinterpret_cast<float *>(smem + kNormSums);  // [2][4][kWords]
-    uint8_t *ring = smem + kNormHeader;
+    float *red = reinterpret_cast<float *>(smem + kWalkSums);  // [2][4][kWords]
+    uint8_t *ring = smem + kWalkHeader;
     constexpr int kSumsKept = 1 + VECTOR;
     const int arrays = 2 + (p.dr != nullptr) + Y;
     const uint32_t row_bytes = static_cast<uint32_t>(p.cols) * 2;
@@ -267,7 +535,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
     const bool mine = tid * kVec < cols;  // this thread has columns
 
     if (tid == 0) {
-        for (int s = 0; s < kNormMaxStages + 2; ++s) mbar_init(&full[s], 1);
+        for (int s = 0; s < kWalkMaxStages + 2; ++s) mbar_init(&full[s], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -351,10 +619,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) rmsnorm_backward_kernel(const
         } else {
             if (tid == 0) mbar_arrive_expect_tx(&shared_sums[it & 1], share_bytes);
             if ((lane & 7) < CTAS)  // one lane for each value and CTA
-                asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
-                                 mapa_shared(smem_u32(word), lane & 7)),
-                             "r"(__float_as_uint(v)), "r"(mapa_shared(smem_u32(&shared_sums[it & 1]), lane & 7))
-                             : "memory");
+                store_share(word, v, &shared_sums[it & 1], lane & 7);
         }
     };
     float back = 0.0f, back_y = 0.0f;  // -rstd^2 c1 and -rstd_y^2 c2 of the row
@@ -508,78 +773,23 @@ __global__ void __launch_bounds__(512) rmsnorm_columns_kernel(const float *__res
     }
 }
 
-namespace {
-
-struct NormShape {
-    int ctas, threads, cols, stages, grid;
-    size_t smem;
-};
-
-constexpr int kSmemLimit = 232448;
-constexpr int kSms = 148;  // of a B200: the workspace is sized without asking a device
-
-NormShape norm_shape(int64_t T, int64_t H, bool y, bool dr) {
-    NormShape s;
-    s.ctas = H <= kBackCols ? 1 : H <= 2 * kBackCols ? 2 : 4;
-    s.cols = static_cast<int>((H / s.ctas + 15) / 16 * 16);
-    if (s.ctas == 1) s.cols = static_cast<int>(H);
-    s.threads = (s.cols / kVec + 31) / 32 * 32;
-    const int per_sm = kBackThreads / s.threads;  // 128 registers a thread
-    const int stage = (2 + y + dr) * s.cols * 2;
-    s.stages = (kSmemLimit / per_sm - 1024 - kNormHeader) / stage;
-    if (s.stages > kNormMaxStages) s.stages = kNormMaxStages;
-    s.smem = static_cast<size_t>(kNormHeader) + static_cast<size_t>(s.stages) * stage;
-    // clusters of four lie within a GPC: 33 of them run at once on the 148 SMs, not 37 (4000 x 16384 with
-    // 37: 332 us, in two rounds)
-    int64_t walkers = s.ctas == 4 ? 32 : static_cast<int64_t>(kSms / s.ctas) * per_sm;
-    // two rows each at least, once every SM has a walker: fewer sums to add up (333 x 784: 6.9 -> 6.7 us)
-    const int64_t one_round = kSms / s.ctas;
-    if (walkers > one_round && walkers > T / 2) walkers = T / 2 > one_round ? T / 2 : one_round;
-    if (walkers > T) walkers = T;
-    s.grid = static_cast<int>(walkers) * s.ctas;
-    return s;
-}
-
-template <int CTAS, bool Y, bool POST, bool VECTOR>
-dg_status_t launch_backward_impl(const NormBackwardParams &p, const NormShape &s, cudaStream_t stream) {
-    auto kernel = rmsnorm_backward_kernel<CTAS, Y, POST, VECTOR>;
-    static thread_local int configured_device = -1;
-    const dg_status_t st = allow_smem(kernel, kSmemLimit, configured_device);
-    if (st != DG_OK) return st;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(s.grid), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(s.threads), 1, 1);
-    cfg.dynamicSmemBytes = s.smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CTAS;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = CTAS > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
-}
-
 template <bool Y, bool POST, bool VECTOR>
-dg_status_t launch_backward_shape(const NormBackwardParams &p, const NormShape &s, cudaStream_t stream) {
-    if (s.ctas == 4) return launch_backward_impl<4, Y, POST, VECTOR>(p, s, stream);
-    return s.ctas == 2 ? launch_backward_impl<2, Y, POST, VECTOR>(p, s, stream)
-                       : launch_backward_impl<1, Y, POST, VECTOR>(p, s, stream);
+static dg_status_t launch_backward_form(const NormBackwardParams &p, const WalkShape &s, cudaStream_t stream) {
+    static thread_local int one = -1, two = -1, four = -1;
+    if (s.ctas == 1) return launch_walk(rmsnorm_backward_kernel<1, Y, POST, VECTOR>, p, s, one, stream);
+    if (s.ctas == 2) return launch_walk(rmsnorm_backward_kernel<2, Y, POST, VECTOR>, p, s, two, stream);
+    return launch_walk(rmsnorm_backward_kernel<4, Y, POST, VECTOR>, p, s, four, stream);
 }
-
-}  // namespace
 
 int64_t rmsnorm_backward_workspace(int64_t T, int64_t H, bool post, bool gate) {
-    const NormShape s = norm_shape(T, H, false, false);
+    const WalkShape s = walk_shape(T, H, 2, kWalkThreads);
     return static_cast<int64_t>(s.grid / s.ctas) * (1 + (post || gate)) * H * 4;
 }
 
 dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
     (void)dev;
     const bool y = a.y != nullptr, post = a.post != nullptr, gate = a.gate != nullptr;
-    const NormShape s = norm_shape(a.T, a.H, y, a.dr != nullptr);
+    const WalkShape s = walk_shape(a.T, a.H, 2 + y + (a.dr != nullptr), kWalkThreads);
     const KernelControl ctl = kernel_control();
     NormBackwardParams p;
     p.dn = static_cast<const uint8_t *>(a.dn);
@@ -604,10 +814,10 @@ dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo 
     p.status = ctl.status;
     if (a.T > 0) {
         dg_status_t st;
-        if (!y) st = launch_backward_shape<false, false, false>(p, s, stream);
-        else if (post) st = launch_backward_shape<true, true, true>(p, s, stream);
-        else if (gate) st = launch_backward_shape<true, false, true>(p, s, stream);
-        else st = launch_backward_shape<true, false, false>(p, s, stream);
+        if (!y) st = launch_backward_form<false, false, false>(p, s, stream);
+        else if (post) st = launch_backward_form<true, true, true>(p, s, stream);
+        else if (gate) st = launch_backward_form<true, false, true>(p, s, stream);
+        else st = launch_backward_form<true, false, false>(p, s, stream);
         if (st != DG_OK) return st;
     }
     const int sums = 1 + (post || gate);
