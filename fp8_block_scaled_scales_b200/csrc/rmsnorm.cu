@@ -197,7 +197,7 @@ struct WalkShape {
 
 // For rows of H columns in `arrays` arrays: CTAs that walk a row together, threads of each, and
 // as many walkers as run at once with `warps` warps an SM.
-static WalkShape walk_shape(int64_t T, int64_t H, int arrays, int threads_per_sm) {
+static WalkShape walk_shape(int64_t T, int64_t H, int arrays, int threads_per_sm, int most_stages) {
     WalkShape s;
     s.ctas = H <= kWalkCols ? 1 : H <= 2 * kWalkCols ? 2 : 4;
     s.cols = s.ctas == 1 ? static_cast<int>(H) : static_cast<int>((H / s.ctas + 15) / 16 * 16);
@@ -205,7 +205,7 @@ static WalkShape walk_shape(int64_t T, int64_t H, int arrays, int threads_per_sm
     const int per_sm = threads_per_sm / s.threads;
     const int stage = arrays * s.cols * 2;
     s.stages = (kSmemLimit / per_sm - 1024 - kWalkHeader) / stage;
-    if (s.stages > kWalkMaxStages) s.stages = kWalkMaxStages;
+    if (s.stages > most_stages) s.stages = most_stages;
     s.smem = static_cast<size_t>(kWalkHeader) + static_cast<size_t>(s.stages) * stage;
     // clusters of four lie within a GPC: 33 of them run at once on 148 SMs, not 37 (the gradient of 4000 x 16384
     // with 37: 332 us, in two rounds; with 32 198)
@@ -456,7 +456,11 @@ dg_status_t launch_rmsnorm(const NormArgs &a, const DeviceInfo &dev, cudaStream_
     p.rstd_y = a.rstd_y;
     const bool codes = a.q != nullptr;
     if (a.T > kWalkRows) {
-        const WalkShape s = walk_shape(a.T, a.H, 1 + (a.y != nullptr), 2 * kWalkThreads);
+        // Reads far ahead of the writes cost bandwidth: 16384 x 4096 with a post and a gate, two CTAs an SM, takes
+        // 87 us with three rows in the ring, 94 with four, 101 with six (one CTA: 104).  With less arithmetic one
+        // CTA and four rows keep up: 86 us without post, against 107 with two CTAs and three rows.
+        const bool heavy = codes || a.post;
+        const WalkShape s = walk_shape(a.T, a.H, 1 + (a.y != nullptr), heavy ? 2 * kWalkThreads : kWalkThreads, heavy ? 3 : 4);
         const KernelControl ctl = kernel_control();
         const NormWalkParams wp = {p, s.cols, s.stages, ctl.timeout_ns, ctl.status};
         return codes ? launch_walk_form<true>(wp, s, stream) : launch_walk_form<false>(wp, s, stream);
@@ -782,14 +786,14 @@ static dg_status_t launch_backward_form(const NormBackwardParams &p, const WalkS
 }
 
 int64_t rmsnorm_backward_workspace(int64_t T, int64_t H, bool post, bool gate) {
-    const WalkShape s = walk_shape(T, H, 2, kWalkThreads);
+    const WalkShape s = walk_shape(T, H, 2, kWalkThreads, kWalkMaxStages);
     return static_cast<int64_t>(s.grid / s.ctas) * (1 + (post || gate)) * H * 4;
 }
 
 dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
     (void)dev;
     const bool y = a.y != nullptr, post = a.post != nullptr, gate = a.gate != nullptr;
-    const WalkShape s = walk_shape(a.T, a.H, 2 + y + (a.dr != nullptr), kWalkThreads);
+    const WalkShape s = walk_shape(a.T, a.H, 2 + y + (a.dr != nullptr), kWalkThreads, kWalkMaxStages);
     const KernelControl ctl = kernel_control();
     NormBackwardParams p;
     p.dn = static_cast<const uint8_t *>(a.dn);
