@@ -69,7 +69,7 @@ __device__ __forceinline__ float cta_sum(float v, float *red) {
 
 // A thread's eight columns as codes; 16 threads hold a group of 128 columns and share its scale.
 // All lanes call it; those without columns (in == false) bring zeros.
-__device__ __forceinline__ void store_codes(const NormParams &p, const float2 (&n)[4], int64_t t, int col, bool in) {
+__device__ __forceinline__ void store_codes(const float2 (&n)[4], uint2 *q, float *scale, bool in) {
     float m = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) m = amax3(m, n[j]);
@@ -78,9 +78,8 @@ __device__ __forceinline__ void store_codes(const NormParams &p, const float2 (&
     for (int o = 8; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
     const FastScale s = fast_scale(__uint_as_float(bits));
     if (in) {
-        const uint2 c = s.fast ? quantize8_f32<true>(n, s) : quantize8_f32<false>(n, s);
-        *reinterpret_cast<uint2 *>(p.q + t * p.H + col) = c;
-        if ((lane_id() & 15) == 0) p.s_t[static_cast<int64_t>(col >> 7) * p.T + t] = s.s;
+        *q = s.fast ? quantize8_f32<true>(n, s) : quantize8_f32<false>(n, s);
+        if ((lane_id() & 15) == 0) *scale = s.s;
     }
 }
 
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p) {
         if (!CODES) {
             if (in) p.n[row + i] = pack8(w);
         } else {
-            store_codes(p, w, t, i * kVec, in);
+            store_codes(w, reinterpret_cast<uint2 *>(p.q) + row + i, p.s_t + static_cast<int64_t>(i >> 4) * p.T + t, in);
         }
     }
 }
@@ -316,6 +315,11 @@ __global__ void __launch_bounds__(kWalkThreads, 2) rmsnorm_walk_kernel(const Nor
     const float2 alpha2 = make_float2(p.alpha, p.alpha);
     constexpr int kAhead = POST ? 2 : 1;  // rows that come in before row k is finished
     float rstd = 0.0f, rstd_y = 1.0f;     // of rows k and k + 1
+    // the thread's piece in row k + 1, and its group's scale in row k (a 64-bit product a row saved)
+    const int64_t row_pieces = static_cast<int64_t>(step) * (p.H / kVec);
+    int64_t at = (row_of(0) * p.H + col0) / kVec + tid;
+    const int col = col0 + tid * kVec;
+    float *scale_at = CODES && mine ? p.s_t + static_cast<int64_t>(col >> 7) * p.T + first : nullptr;
     int s_in = 0, s_r = 0;                // stages of rows k + kAhead and k + 1
     uint32_t parity = 0u;                 // of the first
 
@@ -337,21 +341,20 @@ __global__ void __launch_bounds__(kWalkThreads, 2) rmsnorm_walk_kernel(const Nor
             }
         }
         if (k >= 0) {  // n of row k
-            const int64_t t = row_of(k);
-            if (tid == 0 && rank == 0 && p.rstd) p.rstd[t] = rstd;
+            if (tid == 0 && rank == 0 && p.rstd) p.rstd[row_of(k)] = rstd;
             const float2 rs = make_float2(rstd, rstd);
             float2 n[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) n[j] = __fmul2_rn(__fmul2_rn(r[j], rs), w[j]);
             if (!CODES) {
-                if (mine) p.n[(t * p.H + col0) / kVec + tid] = pack8(n);
+                if (mine) p.n[at - row_pieces] = pack8(n);
             } else {
-                store_codes(p, n, t, col0 + tid * kVec, mine);
+                store_codes(n, reinterpret_cast<uint2 *>(p.q) + (at - row_pieces), scale_at, mine);
+                scale_at += step;
             }
         }
         if (k + 1 >= 0 && k + 1 < rows) {  // r of row k + 1
-            const int64_t t = row_of(k + 1);
-            if (POST && tid == 0 && rank == 0 && p.rstd_y) p.rstd_y[t] = rstd_y;
+            if (POST && tid == 0 && rank == 0 && p.rstd_y) p.rstd_y[row_of(k + 1)] = rstd_y;
             if (mine) {
                 piece(s_r, 0, r);
                 if (Y) {
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) rmsnorm_walk_kernel(const Nor
                         if (VECTOR) u[j] = __fmul2_rn(u[j], gp[j]);
                         r[j] = __ffma2_rn(alpha2, r[j], u[j]);
                     }
-                    p.r[(t * p.H + col0) / kVec + tid] = pack8(r);
+                    p.r[at] = pack8(r);
                 }
                 float2 sum = zero;
 #pragma unroll
@@ -402,7 +405,10 @@ __global__ void __launch_bounds__(kWalkThreads, 2) rmsnorm_walk_kernel(const Nor
         v = __frsqrt_rn(fmaf(v, inv_h, p.eps));
         if (POST) rstd_y = __shfl_sync(0xFFFFFFFFu, v, 0);
         rstd = __shfl_sync(0xFFFFFFFFu, v, 16);
-        if (k + 1 >= 0) s_r = s_r + 1 == wp.stages ? 0 : s_r + 1;
+        if (k + 1 >= 0) {
+            s_r = s_r + 1 == wp.stages ? 0 : s_r + 1;
+            at += row_pieces;
+        }
         if (++s_in == wp.stages) {
             s_in = 0;
             parity ^= 1u;
@@ -659,7 +665,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
     int s = 0, next_s = 1;  // at least two stages
     uint32_t next_parity = 0u;
     float next_rstd = scale_of_row(p.rstd, t + step), next_rstd_y = POST ? scale_of_row(p.rstd_y, t + step) : 1.0f;
-    for (int it = 0; t < p.T; t += step, ++it) {
+    const int64_t row_pieces = static_cast<int64_t>(step) * (p.H / kVec);
+    int64_t out = (t * p.H + col0) / kVec + tid;  // the thread's piece in row t
+    for (int it = 0; t < p.T; t += step, out += row_pieces, ++it) {
         const int64_t next = t + step;
         const float later_rstd = scale_of_row(p.rstd, next + step);
         const float later_rstd_y = POST ? scale_of_row(p.rstd_y, next + step) : 1.0f;
@@ -684,7 +692,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
                 d[j] = __ffma2_rn(r[j], back2, d[j]);  // dR
                 m[j] = __fmul2_rn(d[j], alpha2);
             }
-            const int64_t out = (t * p.H + col0) / kVec + tid;
             p.dx[out] = pack8(m);
             if (Y) {
                 if (VECTOR) {
