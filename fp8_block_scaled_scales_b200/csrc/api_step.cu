@@ -56,27 +56,39 @@ dg_status_t check_grads(const GradList &g) {
     return DG_OK;
 }
 
-// A tensor that is written overlaps no other one: the kernel's CTAs run in no order.
+// A tensor that is written overlaps no other one: the kernel's CTAs run in no order.  What is
+// written is put in order and drawn together into spans with gaps of less than 4 KB; a tensor
+// that is only read seldom meets one, and only then is looked up among the written ones.
 dg_status_t check_overlap(const GradList &g) try {
     struct Range {
         uintptr_t begin, end;
-        bool written;
     };
-    std::vector<Range> ranges;
-    ranges.reserve(static_cast<size_t>(g.count) * 2);
-    for (int64_t i = 0; i < g.count; ++i) {
-        if (g.sizes[i] == 0) continue;
-        const uintptr_t bytes = static_cast<uintptr_t>(g.sizes[i]) * (g.bf16[i] ? 2 : 4);
-        const uintptr_t in = reinterpret_cast<uintptr_t>(g.in[i]), out = g.out ? reinterpret_cast<uintptr_t>(g.out[i]) : in;
-        ranges.push_back({out, out + bytes, true});
-        if (out != in) ranges.push_back({in, in + bytes, false});
+    std::vector<Range> written, spans;
+    written.reserve(static_cast<size_t>(g.count));
+    auto bytes = [&](int64_t i) { return static_cast<uintptr_t>(g.sizes[i]) * (g.bf16[i] ? 2 : 4); };
+    auto target = [&](int64_t i) { return reinterpret_cast<uintptr_t>(g.out ? g.out[i] : g.in[i]); };
+    for (int64_t i = 0; i < g.count; ++i)
+        if (g.sizes[i] != 0) written.push_back({target(i), target(i) + bytes(i)});
+    const auto before = [](const Range &a, const Range &b) { return a.begin < b.begin; };
+    if (!std::is_sorted(written.begin(), written.end(), before)) std::sort(written.begin(), written.end(), before);
+    for (size_t i = 1; i < written.size(); ++i)
+        if (written[i].begin < written[i - 1].end) return DG_ERR_INVALID_ARG;
+    if (!g.out) return DG_OK;
+    for (const Range &r : written) {
+        if (spans.empty() || r.begin - spans.back().end >= 4096)
+            spans.push_back(r);
+        else
+            spans.back().end = r.end;
     }
-    std::sort(ranges.begin(), ranges.end(), [](const Range &a, const Range &b) { return a.begin < b.begin; });
-    uintptr_t any_end = 0, written_end = 0;
-    for (const Range &r : ranges) {
-        if (r.begin < (r.written ? any_end : written_end)) return DG_ERR_INVALID_ARG;
-        any_end = std::max(any_end, r.end);
-        if (r.written) written_end = std::max(written_end, r.end);
+    for (int64_t i = 0; i < g.count; ++i) {
+        const uintptr_t begin = reinterpret_cast<uintptr_t>(g.in[i]), end = begin + bytes(i);
+        if (g.sizes[i] == 0 || begin == target(i)) continue;
+        // the first range that ends past `begin`
+        const auto past = [](uintptr_t at, const Range &r) { return at < r.end; };
+        const auto span = std::upper_bound(spans.begin(), spans.end(), begin, past);
+        if (span == spans.end() || span->begin >= end) continue;
+        const auto one = std::upper_bound(written.begin(), written.end(), begin, past);
+        if (one != written.end() && one->begin < end) return DG_ERR_INVALID_ARG;
     }
     return DG_OK;
 } catch (...) {  // no host memory for the list: no exception may pass the C interface

@@ -219,61 +219,113 @@ __global__ void __launch_bounds__(kNormThreads) grad_clip_kernel(const __grid_co
 
 namespace {
 
-constexpr int kTable = 1024;      // tensors of a launch at most
-constexpr int kSmallTable = 64;   // parameters cost host time: 2 KB for few tensors instead of 29
+// Tensors of a launch at most.  Parameters cost host time: 2 or 9 KB for fewer tensors instead of 27.
+constexpr int kTable = 960, kMiddleTable = 320, kSmallTable = 64;
 
 int64_t chunks_of(int64_t size) { return (size + kChunk - 1) / kChunk; }
 
-// Calls launch(table, grid) for runs of at most kTable tensors that have elements.
-template <int N, typename F>
-dg_status_t walk_tables(const GradList &g, F launch) {
-    // filled from scratch for each run; too large for some threads' stacks twice over
-    GradTable<N> t;
-    t.tensors = t.chunks = 0;
-    for (uint32_t &w : t.kind) w = 0;
-    auto flush = [&] {
-        if (t.tensors == 0) return DG_OK;
-        const dg_status_t st = launch(t, t.chunks < kGradCtas ? t.chunks : kGradCtas);
-        t.tensors = t.chunks = 0;
-        for (uint32_t &w : t.kind) w = 0;
-        return st;
-    };
-    for (int64_t i = 0; i < g.count; ++i) {
-        if (g.sizes[i] == 0) continue;
-        const int64_t chunks = chunks_of(g.sizes[i]);
-        if (t.tensors == N || t.chunks + chunks > 0x3FFFFFFFLL) {
-            const dg_status_t st = flush();
+// The gradients, table after table.  One that holds them all is built once and serves both launches.
+template <int N>
+class Tables {
+public:
+    explicit Tables(const GradList &g) : g_(g) {}
+
+    // launch(table, grid) for each.
+    template <typename F>
+    dg_status_t each(F launch) {
+        if (whole_) return launch(t_, ctas_);
+        int64_t next = 0;
+        while (next < g_.count) {
+            const bool first = next == 0;
+            next = fill(next);
+            if (t_.tensors == 0) break;
+            whole_ = first && next == g_.count;
+            t_.chunks = t_.chunk_end[t_.tensors - 1];
+            ctas_ = t_.chunks < kGradCtas ? t_.chunks : kGradCtas;
+            const dg_status_t st = launch(t_, ctas_);
             if (st != DG_OK) return st;
         }
-        const int at = t.tensors++;
-        t.in[at] = g.in[i];
-        t.out[at] = g.out ? g.out[i] : const_cast<void *>(g.in[i]);
-        t.size[at] = g.sizes[i];
-        t.chunks += static_cast<int>(chunks);
-        t.chunk_end[at] = t.chunks;
-        if (g.bf16[i]) t.kind[at >> 5] |= 1u << (at & 31);
+        return DG_OK;
     }
-    return flush();
+
+private:
+    // Tensors from `next` on, as many as fit; returns the first that is left.
+    int64_t fill(int64_t next) {
+        t_.tensors = 0;
+        for (uint32_t &w : t_.kind) w = 0;
+        int64_t chunks = 0;
+        for (; next < g_.count; ++next) {
+            const int64_t size = g_.sizes[next], n = chunks_of(size);
+            if (size == 0) continue;
+            if (t_.tensors == N || chunks + n > 0x3FFFFFFFLL) break;
+            const int at = t_.tensors++;
+            t_.in[at] = g_.in[next];
+            t_.out[at] = g_.out ? g_.out[next] : const_cast<void *>(g_.in[next]);
+            t_.size[at] = size;
+            t_.chunk_end[at] = static_cast<int32_t>(chunks += n);
+            if (g_.bf16[next]) t_.kind[at >> 5] |= 1u << (at & 31);
+        }
+        while (next < g_.count && g_.sizes[next] == 0) ++next;
+        return next;
+    }
+
+    const GradList &g_;
+    GradTable<N> t_;
+    int ctas_ = 0;
+    bool whole_ = false;
+};
+
+// launch_pdl takes its arguments by value; a table is better not copied once more.
+template <typename Kernel, typename... Args>
+dg_status_t launch_table(Kernel kernel, int grid, cudaStream_t stream, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kNormThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *pointers[] = {const_cast<void *>(static_cast<const void *>(&args))...};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), pointers) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
 template <int N>
-dg_status_t squares(const GradList &g, double *part, int &parts, cudaStream_t stream) {
+dg_status_t squares(Tables<N> &tables, double *part, int &parts, cudaStream_t stream) {
     parts = 0;
-    return walk_tables<N>(g, [&](const GradTable<N> &t, int grid) {
-        const dg_status_t st = launch_pdl(grad_squares_kernel<N>, grid, kNormThreads, 0, stream, t, part + parts);
-        parts += grid;
-        return st;
+    return tables.each([&](const GradTable<N> &t, int ctas) {
+        double *const to = part + parts;
+        parts += ctas;
+        return launch_table(grad_squares_kernel<N>, ctas, stream, t, to);
     });
 }
 
 template <int N>
-dg_status_t clip(const GradList &g, const double *part, int parts, float *norm, float max_norm, cudaStream_t stream) {
+dg_status_t clip(Tables<N> &tables, const double *part, int parts, float *norm, float max_norm, cudaStream_t stream) {
     bool first = true;
-    return walk_tables<N>(g, [&](const GradTable<N> &t, int grid) {
-        const dg_status_t st = launch_pdl(grad_clip_kernel<N>, grid, kNormThreads, 0, stream, t, part, parts, norm, first, max_norm);
+    return tables.each([&](const GradTable<N> &t, int ctas) {
+        const bool write = first;
         first = false;
-        return st;
+        return launch_table(grad_clip_kernel<N>, ctas, stream, t, part, parts, norm, write, max_norm);
     });
+}
+
+template <int N>
+dg_status_t norm_of_list(const GradList &g, float *norm, double *part, cudaStream_t stream) {
+    Tables<N> tables(g);
+    int parts = 0;
+    const dg_status_t st = squares<N>(tables, part, parts, stream);
+    if (st != DG_OK) return st;
+    return launch_pdl(grad_norm_kernel, 1, kNormThreads, 0, stream, static_cast<const double *>(part), parts, norm);
+}
+
+template <int N>
+dg_status_t clip_list(const GradList &g, float max_norm, float *norm, double *part, cudaStream_t stream) {
+    Tables<N> tables(g);
+    int parts = 0;
+    const dg_status_t st = squares<N>(tables, part, parts, stream);
+    return st != DG_OK ? st : clip<N>(tables, part, parts, norm, max_norm, stream);
 }
 
 int64_t with_elements(const GradList &g) {
@@ -284,32 +336,35 @@ int64_t with_elements(const GradList &g) {
 
 }  // namespace
 
+// A table ends early only where its chunks outrun 30 bits: 2^43 elements, more than a GPU holds.
 int64_t grad_norm_workspace(int64_t count) { return (count / kTable + 1) * kGradCtas * 8; }
 
 dg_status_t launch_grad_norm(const GradList &g, float *norm, void *workspace, cudaStream_t stream) {
     double *part = static_cast<double *>(workspace);
-    int parts = 0;
-    const dg_status_t st = with_elements(g) <= kSmallTable ? squares<kSmallTable>(g, part, parts, stream)
-                                                           : squares<kTable>(g, part, parts, stream);
-    if (st != DG_OK) return st;
-    return launch_pdl(grad_norm_kernel, 1, kNormThreads, 0, stream, static_cast<const double *>(part), parts, norm);
+    const int64_t n = with_elements(g);
+    if (n <= kSmallTable) return norm_of_list<kSmallTable>(g, norm, part, stream);
+    return n <= kMiddleTable ? norm_of_list<kMiddleTable>(g, norm, part, stream) : norm_of_list<kTable>(g, norm, part, stream);
+}
+
+template <int N>
+static dg_status_t clip_by(const GradList &g, const float *norm, float max_norm, cudaStream_t stream) {
+    Tables<N> tables(g);
+    return clip<N>(tables, nullptr, 0, const_cast<float *>(norm), max_norm, stream);  // only read: no partial sums are given
 }
 
 dg_status_t launch_grad_clip(const GradList &g, const float *norm, float max_norm, cudaStream_t stream) {
-    float *n = const_cast<float *>(norm);  // only read: no partial sums are given
-    return with_elements(g) <= kSmallTable ? clip<kSmallTable>(g, nullptr, 0, n, max_norm, stream)
-                                           : clip<kTable>(g, nullptr, 0, n, max_norm, stream);
+    const int64_t n = with_elements(g);
+    if (n <= kSmallTable) return clip_by<kSmallTable>(g, norm, max_norm, stream);
+    return n <= kMiddleTable ? clip_by<kMiddleTable>(g, norm, max_norm, stream) : clip_by<kTable>(g, norm, max_norm, stream);
 }
 
 dg_status_t launch_grad_norm_clip(const GradList &g, float max_norm, float *norm, void *workspace, cudaStream_t stream) {
     double *part = static_cast<double *>(workspace);
-    int parts = 0;
     const int64_t n = with_elements(g);
     if (n == 0) return launch_grad_norm(g, norm, workspace, stream);
-    dg_status_t st = n <= kSmallTable ? squares<kSmallTable>(g, part, parts, stream) : squares<kTable>(g, part, parts, stream);
-    if (st != DG_OK) return st;
-    return n <= kSmallTable ? clip<kSmallTable>(g, part, parts, norm, max_norm, stream)
-                            : clip<kTable>(g, part, parts, norm, max_norm, stream);
+    if (n <= kSmallTable) return clip_list<kSmallTable>(g, max_norm, norm, part, stream);
+    return n <= kMiddleTable ? clip_list<kMiddleTable>(g, max_norm, norm, part, stream)
+                             : clip_list<kTable>(g, max_norm, norm, part, stream);
 }
 
 }  // namespace dg

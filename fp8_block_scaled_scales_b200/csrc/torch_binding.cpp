@@ -644,7 +644,7 @@ struct Grads {
             const Tensor &t = tensor(g.items[i], "a gradient");
             if (i == 0) dev = device_of(t, "a gradient", t.dim());
             bf16.push_back(t.scalar_type() == kBF16);
-            in.push_back(checked(t, "a gradient", bf16.back() ? kBF16 : kF32, t.sizes(), dev));
+            in.push_back(address(t, "a gradient", bf16.back() ? kBF16 : kF32));
             sizes.push_back(t.numel());
         }
         if (g.size == 0) dev = c10::cuda::current_device();
@@ -653,15 +653,26 @@ struct Grads {
         const Items o(outs, "out");
         TORCH_CHECK_VALUE(o.size == g.size, "out must hold ", g.size, " tensors, not ", o.size);
         out.reserve(o.size);
-        for (Py_ssize_t i = 0; i < o.size; ++i)
-            out.push_back(checked(tensor(o.items[i], "an output"), "an output", bf16[i] ? kBF16 : kF32,
-                                  tensor(g.items[i], "a gradient").sizes(), dev));
+        for (Py_ssize_t i = 0; i < o.size; ++i) {
+            const Tensor &t = tensor(o.items[i], "an output"), &like = THPVariable_Unpack(g.items[i]);
+            out.push_back(address(t, "an output", bf16[i] ? kBF16 : kF32));
+            TORCH_CHECK_VALUE(t.sizes() == like.sizes(), "an output must have shape ", like.sizes(), ", not ", t.sizes());
+        }
     }
 
     int64_t count() const { return static_cast<int64_t>(in.size()); }
     void *const *outs() const { return in_place ? nullptr : out.data(); }
 
 private:
+    // checked() without the shape: a step has hundreds of these.
+    void *address(const Tensor &t, const char *name, at::ScalarType type) const {
+        TORCH_CHECK_VALUE(t.scalar_type() == type, name, " must be ", type, ", not ", t.scalar_type());
+        TORCH_CHECK_VALUE(t.is_cuda() && t.get_device() == dev, name, " must be on cuda:", dev,
+                          ", the current device and that of the other tensors");
+        TORCH_CHECK_VALUE(t.is_contiguous(), name, " must be contiguous (row-major)");
+        return t.unsafeGetTensorImpl()->mutable_data();
+    }
+
     struct Items {  // a list or tuple, held while it is read
         PyObject *held, **items;
         Py_ssize_t size;
