@@ -498,50 +498,83 @@ __device__ __forceinline__ void store_score(void *out, bool bf16, int64_t at, fl
 // ROWS: every expert's score matters (the balance loss, or softmax without renormalization);
 // otherwise only the chosen experts have a gradient, and only their scores are read.
 template <int PER, bool ROWS>
-__global__ void __launch_bounds__(256) route_backward_kernel(const RouteBackwardParams p) {
+__global__ void __launch_bounds__(256, PER <= 8 ? 4 : 1) route_backward_kernel(const RouteBackwardParams p) {
     const int lane = lane_id();
     const int warps = static_cast<int>(blockDim.x) >> 5, warp = static_cast<int>(threadIdx.x) >> 5;
     grid_dep_wait();
     grid_dep_launch_dependents();
     float dp[PER];
-    const float dloss = p.dprob ? __ldg(p.dloss) : 0.0f;
+    const float dloss = ROWS && p.dprob ? __ldg(p.dloss) : 0.0f;
+    if (ROWS) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) dp[i] = p.dprob && lane + 32 * i < p.G ? __ldg(p.dprob + lane + 32 * i) * dloss : 0.0f;
+        for (int i = 0; i < PER; ++i) dp[i] = p.dprob && lane + 32 * i < p.G ? __ldg(p.dprob + lane + 32 * i) * dloss : 0.0f;
+    }
 
     const int64_t stride = static_cast<int64_t>(gridDim.x) * warps;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * warps + warp; t < p.T; t += stride) {
         const int64_t row = t * p.G;
         const int id = lane < p.k ? __ldg(p.ids + t * p.k + lane) : -1;
-        const bool ok = id >= 0 && id < p.G;
-        const bool routed = __any_sync(kAll, ok);
-        float z[PER];
+        const float given = lane < p.k && p.dweights ? __ldg(p.dweights + t * p.k + lane) : 0.0f;
+        float q[PER], ns[PER];  // what p is proportional to, and 1 - sigmoid
         if (ROWS) {
+            if (p.bf16) {
+                const uint16_t *at = static_cast<const uint16_t *>(p.logits) + row + lane;
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                z[i] = lane + 32 * i < p.G ? load_score(p.logits, p.bf16, row + lane + 32 * i) : -CUDART_INF_F;
+                for (int i = 0; i < PER; ++i)
+                    q[i] = lane + 32 * i < p.G ? __uint_as_float(static_cast<uint32_t>(__ldg(at + 32 * i)) << 16) : -CUDART_INF_F;
+            } else {
+                const float *at = static_cast<const float *>(p.logits) + row + lane;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) q[i] = lane + 32 * i < p.G ? __ldg(at + 32 * i) : -CUDART_INF_F;
+            }
         }
+        const bool ok = id >= 0 && id < p.G;
         const float z_id = ok ? load_score(p.logits, p.bf16, row + id) : 0.0f;
-        const float dw = ok && p.dweights ? __ldg(p.dweights + t * p.k + lane) : 0.0f;
+        const bool routed = __any_sync(kAll, ok);
+        const float dw = ok ? given : 0.0f;
         float top = -CUDART_INF_F, r = 0.0f, base = 0.0f;
         bool exponential = !p.sigmoid;
-        float q[PER];
         if (ROWS && routed) {
+            float sum = 0.0f, dot = 0.0f;
+            if (!exponential) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) top = fmaxf(top, z[i]);
-            top = warp_max(top);
-            exponential = exponential || top < kFarBelow;
-            float sum = 0.0f;
+                for (int i = 0; i < PER; ++i) {
+                    const float z = q[i], e = fminf(exp_fast(-z), 0x1p125f);  // the bound: e times its reciprocal is 1
+                    q[i] = reciprocal(1.0f + e);
+                    ns[i] = e * q[i];
+                    if (z == -CUDART_INF_F) q[i] = 0.0f;  // an expert that is left out, or none
+                    sum += q[i];
+                    dot = fmaf(dp[i], q[i], dot);
+                    top = fmaxf(top, z);
+                }
+                sum = warp_sum(sum);
+                exponential = sum < 0x1p-80f;
+                if (exponential) {  // all far below 0: ratios of exponentials
+                    sum = dot = 0.0f;
+                    top = warp_max(top);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                q[i] = unnormalized(z[i], top, exponential);
-                if (lane + 32 * i >= p.G) q[i] = 0.0f;
-                sum += q[i];
+                    for (int i = 0; i < PER; ++i) {
+                        const float z = lane + 32 * i < p.G ? load_score(p.logits, p.bf16, row + lane + 32 * i) : -CUDART_INF_F;
+                        q[i] = exp_fast(z - top);
+                        sum += q[i];
+                        dot = fmaf(dp[i], q[i], dot);
+                    }
+                    sum = warp_sum(sum);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) top = fmaxf(top, q[i]);
+                top = warp_max(top);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    q[i] = exp_fast(q[i] - top);
+                    sum += q[i];
+                    dot = fmaf(dp[i], q[i], dot);
+                }
+                sum = warp_sum(sum);
             }
-            r = 1.0f / warp_sum(sum);
-            float dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) dot += dp[i] * (q[i] * r);
-            base = warp_sum(dot);
+            r = 1.0f / sum;
+            if (p.dprob) base = warp_sum(dot) * r;
         }
         float a = 0.0f;  // lane j: A_j
         if (routed) {
@@ -550,25 +583,31 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteBackward
                 const float mean = warp_sum(ok ? dw * v : 0.0f);
                 a = ok ? p.scale * v * (dw - mean) : 0.0f;
             } else {
-                float s;
-                if (p.sigmoid) {
-                    s = sigmoid_of(z_id);
-                } else {
-                    s = expf(z_id - top) * r;
-                }
+                const float s = p.sigmoid ? sigmoid_of(z_id) : expf(z_id - top) * r;
                 a = ok ? p.scale * dw * s : 0.0f;
                 if (!p.sigmoid) base += warp_sum(a);
             }
         }
         // every expert's part, then the chosen ones' whole gradient over it
+        float v[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            float v = 0.0f;
+            v[i] = 0.0f;
             if (ROWS && routed) {
-                v = q[i] * r * (dp[i] - base);
-                if (p.sigmoid) v *= sigmoid_fast(-z[i]);
+                v[i] = q[i] * r * (dp[i] - base);
+                if (p.sigmoid) v[i] *= ns[i];
             }
-            if (lane + 32 * i < p.G) store_score(p.dlogits, p.bf16, row + lane + 32 * i, v);
+        }
+        if (p.bf16) {
+            __nv_bfloat16 *at = static_cast<__nv_bfloat16 *>(p.dlogits) + row + lane;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (lane + 32 * i < p.G) at[32 * i] = __float2bfloat16(v[i]);
+        } else {
+            float *at = static_cast<float *>(p.dlogits) + row + lane;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (lane + 32 * i < p.G) at[32 * i] = v[i];
         }
         if (routed) {
             // an expert that a token names twice gets both slots' parts
@@ -581,14 +620,17 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const RouteBackward
                 }
                 a = both;
             }
-            float v = a;
+            float g = a;
             if (ROWS && ok) {
                 const float d = p.dprob ? __ldg(p.dprob + id) * dloss : 0.0f;
-                v += unnormalized(z_id, top, exponential) * r * (d - base);
+                g += unnormalized(z_id, top, exponential) * r * (d - base);
             }
-            if (p.sigmoid) v *= sigmoid_of(-z_id);
+            if (p.sigmoid) {
+                const float e = fminf(exp_fast(-z_id), 0x1p125f);
+                g *= e * reciprocal(1.0f + e);
+            }
             __syncwarp();  // the row's stores come first
-            if (ok) store_score(p.dlogits, p.bf16, row + id, v);
+            if (ok) store_score(p.dlogits, p.bf16, row + id, g);
         }
     }
 }
@@ -695,7 +737,7 @@ static dg_status_t launch_route_backward_per(const RouteBackwardParams &p, int g
 dg_status_t launch_route_backward(const RouteBackwardArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
     RouteBackwardParams p = {a.logits, a.ids, a.dweights, a.dprob, a.dloss, a.T, a.G, a.k,
                              a.bf16, a.sigmoid, a.renormalize, a.scale, a.dlogits};
-    const int64_t want = (a.T + 7) / 8, most = 8 * static_cast<int64_t>(dev.num_sms);
+    const int64_t want = (a.T + 7) / 8, most = 4 * static_cast<int64_t>(dev.num_sms);
     const int grid = static_cast<int>(want < most ? want : most);
     switch (per_lane(a.G)) {
     case 1: return launch_route_backward_per<1>(p, grid, stream);
