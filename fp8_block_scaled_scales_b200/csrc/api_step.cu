@@ -118,7 +118,8 @@ dg_status_t dg_moe_route(const void *logits, int logits_bf16, const dg_route_opt
     if ((loss != nullptr) != balance || (dprob != nullptr) != balance) return DG_ERR_INVALID_ARG;
     if (T == 0 && !balance) return DG_OK;
     if (T > 0 && (!logits || !topk_ids || !weights)) return DG_ERR_INVALID_ARG;
-    if (balance && (!workspace || workspace_bytes < route_workspace(T, G))) return DG_ERR_INVALID_ARG;
+    const int64_t need = balance ? route_workspace(T, G) : 0;
+    if ((need > 0 && !workspace) || workspace_bytes < need) return DG_ERR_INVALID_ARG;
     if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(weights, 4) ||
         !aligned(counts, 4) || !aligned(loss, 4) || !aligned(dprob, 4) || !aligned(workspace, 16))
         return DG_ERR_ALIGNMENT;

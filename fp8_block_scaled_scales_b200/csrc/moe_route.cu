@@ -16,6 +16,8 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "dg_device.cuh"
 #include "train_internal.h"
 
@@ -23,7 +25,18 @@ namespace dg {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kFinishCtas = 8;
+constexpr int kClusterCtas = 16;  // of the cluster that takes few tokens alone
 constexpr int kFinishThreads = 512;
+
+// How the tokens are shared out: `per` to each warp, one more to the first `extra`; and lanes for
+// a token's slots when they are finished side by side, 2^shift of them.
+struct WarpShare {
+    int64_t per;
+    int extra, shift;
+
+    __device__ __forceinline__ int64_t first(int warp) const { return warp * per + (warp < extra ? warp : extra); }
+    __device__ __forceinline__ int64_t count(int warp) const { return per + (warp < extra ? 1 : 0); }
+};
 
 struct RouteParams {
     const void *logits;
@@ -31,6 +44,7 @@ struct RouteParams {
     const uint8_t *mask;
     int64_t T;
     int G, k;
+    WarpShare share;
     bool bf16, sigmoid, renormalize;
     float scale;
     int32_t *ids;
@@ -38,6 +52,9 @@ struct RouteParams {
     // partial sums of a CTA: [grid][G] of p, [grid][G] slots, [grid] tokens
     float *part_p;
     int32_t *part_count, *part_tokens;
+    // part_p null: the grid is one cluster, which writes the results itself
+    int32_t *counts;
+    float *loss, *dprob;
 };
 
 // Floats as integers of the same order; -0 must have been made +0.
@@ -96,13 +113,26 @@ __device__ __forceinline__ float sigmoid_of(float z) {
     return (z >= 0.0f ? 1.0f : e) / (1.0f + e);
 }
 
-// Lane j's share of the chosen scores' sum, in FP32 without common under- or overflow; lanes
-// with ok == false hold no slot.
-__device__ __forceinline__ float share_of_chosen(float z, bool ok, bool sigmoid) {
-    const float m = warp_max(ok ? z : -CUDART_INF_F);
-    float s = 0.0f;
-    if (ok) s = !sigmoid || m < kFarBelow ? expf(z - m) : sigmoid_of(z);
-    return s / warp_sum(s);  // 0 / 0 where no lane holds a slot: the caller's ok is false then
+// A warp's lanes as segments of `width` (a power of two), one token's slots in each.
+__device__ __forceinline__ float segment_sum(float v, int width) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < width) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float segment_max(float v, int width) {  // a NaN loses
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < width) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+
+// A slot's share of its token's chosen scores, in FP32 without common under- or overflow; lanes
+// with ok == false hold no slot.  m: the segment's largest chosen score.
+__device__ __forceinline__ float share_of_chosen(float z, bool ok, bool sigmoid, float m, int width) {
+    const float s = ok ? (!sigmoid || m < kFarBelow ? expf(z - m) : sigmoid_of(z)) : 0.0f;
+    return s / segment_sum(s, width);  // 0 / 0 where the segment holds no slot: ok is false then
 }
 
 // A key in FP64: z itself without a bias (top and sum: of a row's exponentials).
@@ -204,15 +234,85 @@ __device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
                     }
 }
 
+template <typename T>
+__device__ __forceinline__ T from_cta(const T *shared, uint32_t rank) {
+    T v;
+    const uint32_t at = mapa_shared(smem_u32(shared), rank);
+    if constexpr (sizeof(T) == 8)
+        asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(at) : "memory");
+    else if constexpr (std::is_same<T, float>::value)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    else
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// The loss from what the threads of a cluster of CTAS hold of it, in FP64 and a fixed order; called by
+// all of them.  The CTAs' shares go to the first one, so nobody reads another CTA's memory at the end.
+template <int CTAS>
+__device__ __forceinline__ void loss_of_cluster(double mine, double *warp_loss, double *cta_loss, float *loss) {
+    const int warps = static_cast<int>(blockDim.x) >> 5, lane = lane_id();
+    mine = warp_sum(mine);
+    if (lane == 0) warp_loss[threadIdx.x >> 5] = mine;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        mine = warp_sum(lane < warps ? warp_loss[lane] : 0.0);
+        if (lane == 0)
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa_shared(smem_u32(cta_loss + cluster_ctarank()), 0)), "d"(mine)
+                         : "memory");
+    }
+    cluster_sync();
+    if (cluster_ctarank() == 0 && threadIdx.x < 32) {
+        mine = warp_sum(lane < CTAS ? cta_loss[lane] : 0.0);
+        if (lane == 0) *loss = static_cast<float>(mine);
+    }
+}
+
+// counts, dprob and the loss from the CTAs' shared memory: sums [G] of p, counts [G] and the tokens.
+// A lane for each CTA of the cluster, half a warp an expert.
+__device__ __forceinline__ void finish_in_cluster(const RouteParams &p, const float *sums, const int *counts) {
+    static_assert(kClusterCtas == 16, "half a warp");
+    __shared__ double warp_loss[32], cta_loss[kClusterCtas];
+    cluster_sync();
+    const int half = static_cast<int>(threadIdx.x) >> 4, halves = static_cast<int>(blockDim.x) >> 4;
+    const uint32_t r = threadIdx.x & 15u;
+    int n = from_cta(counts + p.G, r);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
+    const double nd = n > 0 ? static_cast<double>(n) : 1.0;
+    const double unit = static_cast<double>(p.G) / (static_cast<double>(p.k) * nd * nd);
+    double mine = 0.0;
+    const int share = (p.G + kClusterCtas - 1) / kClusterCtas, e0 = static_cast<int>(cluster_ctarank()) * share;
+    const int end = e0 + share < p.G ? e0 + share : p.G;
+    for (int base = e0; base < end; base += halves) {  // the same for the whole CTA
+        const int e = base + half;
+        double s = e < end ? static_cast<double>(from_cta(sums + e, r)) : 0.0;
+        int c = e < end ? from_cta(counts + e, r) : 0;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(kAll, s, o);
+            c += __shfl_xor_sync(kAll, c, o);
+        }
+        if (e < end && r == 0) {
+            const double d = unit * c;
+            p.counts[e] = c;
+            p.dprob[e] = static_cast<float>(d);
+            mine += d * s;
+        }
+    }
+    loss_of_cluster<kClusterCtas>(mine, warp_loss, cta_loss, p.loss);
+}
+
 // A warp chooses by 32-bit keys whose low bits are the expert's id, inverted: one maximum over the
 // warp gives key and id, the lowest id among equals, and no two keys are the same.  The id takes the place of
 // the key's last 5 to 10 bits, so the choice is settled only where neighbours in the order differ
 // by more than those (and, with a bias, by more than the key's own FP32 error); otherwise (a token
 // in thirty) the candidates are put in order by FP64 keys.  BF16 logits without a bias have the bits to spare.
-// 16384 tokens x 256 experts, k = 8, with bias and balance loss: see launch_route.
+// Bound by instruction issue, most of it the sort and the k + 1 rounds: 16384 tokens x 256 experts, k = 8,
+// FP32 sigmoid scores 10.7 us, with balance loss 15.4, with bias too 18.7 (the logits alone: 2.6).
 constexpr int route_max_threads(int per) { return per <= 8 ? 1024 : 512; }
 
-template <int PER, bool BIAS, bool BALANCE>
+template <int PER, bool BIAS, bool BALANCE, bool CLUSTER>
 __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const RouteParams p) {
     extern __shared__ float sums[];  // BALANCE: [warps][G] of p, then [G] counts, then the tokens
     constexpr uint32_t kIdBits = 32 * PER - 1;
@@ -225,18 +325,33 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
     }
     grid_dep_wait();
     grid_dep_launch_dependents();
-    float psum[PER], b[PER];
+    // sums of p: in registers, or, where those run out, in the warp's shared memory
+    constexpr bool kSumsInRegisters = PER <= 8;
+    float psum[kSumsInRegisters ? PER : 1];
+    if (BALANCE) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        psum[i] = 0.0f;
-        b[i] = (BIAS && lane + 32 * i < p.G ? __ldg(p.bias + lane + 32 * i) : 0.0f) + 0.0f;
+        for (int i = 0; i < PER; ++i) {
+            if constexpr (kSumsInRegisters)
+                psum[i] = 0.0f;
+            else if (lane + 32 * i < p.G)
+                sums[warp * p.G + lane + 32 * i] = 0.0f;
+        }
     }
+    auto bias = [&](int i) { return lane + 32 * i < p.G ? __ldg(p.bias + lane + 32 * i) + 0.0f : 0.0f; };  // from L1; never -0
     const bool exact_keys = !BIAS && p.bf16;
     const int rounds = exact_keys || p.k == p.G ? p.k : p.k + 1;  // the next one too: is the last one settled?
     int tokens = 0;
 
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * warps;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * warps + warp; t < p.T; t += stride) {
+    // the warp's tokens, 32 / width at a time: each is chosen for by the whole warp, their slots are
+    // finished side by side
+    const int me = static_cast<int>(blockIdx.x) * warps + warp, width = 1 << p.share.shift;
+    const int segment = lane >> p.share.shift, slot = lane & (width - 1);
+    int64_t t = p.share.first(me);
+    const int64_t end = t + p.share.count(me);
+    int my_id = -1;  // slot `slot` of the batch's token `segment`
+    float my_top = 0.0f, my_sum = 1.0f;
+    int held = 0;
+    for (; t < end; ++t) {
         const int64_t row = t * p.G;
         int id = -1;  // lane j: slot j
         float top = 0.0f, sum = 1.0f;
@@ -283,7 +398,7 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
                     if (BIAS) {
 #pragma unroll
                         for (int i = 0; i < PER; ++i) {
-                            const float c = q[i] + b[i];  // never -0: b is not
+                            const float c = q[i] + bias(i);
                             key[i] = keyed(c, z[i] > -CUDART_INF_F && c > -CUDART_INF_F, i);
                         }
                     }
@@ -297,7 +412,7 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
                         const float r = reciprocal(sum);
 #pragma unroll
                         for (int i = 0; i < PER; ++i) {
-                            const float c = fmaf(q[i], r, b[i]);
+                            const float c = fmaf(q[i], r, bias(i));
                             key[i] = keyed(c, z[i] > -CUDART_INF_F && c > -CUDART_INF_F, i);
                         }
                     }
@@ -306,7 +421,12 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
                     const float r = reciprocal(sum);
                     if (top > -CUDART_INF_F) {  // for sigmoids 0, unless no expert has a score
 #pragma unroll
-                        for (int i = 0; i < PER; ++i) psum[i] = fmaf(q[i], r, psum[i]);
+                        for (int i = 0; i < PER; ++i) {
+                            if constexpr (kSumsInRegisters)
+                                psum[i] = fmaf(q[i], r, psum[i]);
+                            else if (lane + 32 * i < p.G)
+                                sums[warp * p.G + lane + 32 * i] += q[i] * r;
+                        }
                     }
                 }
             }
@@ -359,39 +479,55 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
                 id = static_cast<int>(kIdBits - (mine & kIdBits));
             }
         }
-        const bool ok = id >= 0;
-        const bool routed = __any_sync(kAll, ok);
-        float w = 0.0f;
-        if (routed) {
-            const float z = ok ? load_score(p.logits, p.bf16, row + id) : 0.0f;
-            if (p.renormalize)
-                w = share_of_chosen(z, ok, p.sigmoid);
-            else
-                w = p.sigmoid ? sigmoid_of(z) : expf(z - top) / sum;
+        if (BALANCE) tokens += __any_sync(kAll, id >= 0) ? 1 : 0;
+        const int moved = __shfl_sync(kAll, id, slot);
+        if (segment == held) {
+            my_id = moved;
+            my_top = top;
+            my_sum = sum;
         }
-        if (lane < p.k) {
-            p.ids[t * p.k + lane] = id;
-            p.weights[t * p.k + lane] = ok ? w * p.scale : 0.0f;
+        if (++held < (32 >> p.share.shift) && t + 1 < end) continue;
+        // the batch's slots
+        const int64_t first = t + 1 - held;
+        const bool ok = segment < held && my_id >= 0;
+        const float z = ok ? load_score(p.logits, p.bf16, (first + segment) * p.G + my_id) : 0.0f;
+        float w;
+        if (p.renormalize)
+            w = share_of_chosen(z, ok, p.sigmoid, segment_max(ok ? z : -CUDART_INF_F, width), width);
+        else
+            w = p.sigmoid ? sigmoid_of(z) : expf(z - my_top) / my_sum;
+        if (segment < held && slot < p.k) {
+            const int64_t at = (first + segment) * p.k + slot;
+            p.ids[at] = ok ? my_id : -1;
+            p.weights[at] = ok ? w * p.scale : 0.0f;
         }
-        if (BALANCE) {
-            if (ok) atomicAdd(&counts[id], 1);
-            tokens += routed ? 1 : 0;
-        }
+        if (BALANCE && ok) atomicAdd(&counts[my_id], 1);
+        held = 0;
     }
     if (BALANCE) {
+        if constexpr (kSumsInRegisters) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (lane + 32 * i < p.G) sums[warp * p.G + lane + 32 * i] = psum[i];
+            for (int i = 0; i < PER; ++i)
+                if (lane + 32 * i < p.G) sums[warp * p.G + lane + 32 * i] = psum[i];
+        }
         if (lane == 0) atomicAdd(&counts[p.G], tokens);
         __syncthreads();
         const int64_t at = static_cast<int64_t>(blockIdx.x) * p.G;
         for (int e = static_cast<int>(threadIdx.x); e < p.G; e += static_cast<int>(blockDim.x)) {
             float s = 0.0f;
             for (int w = 0; w < warps; ++w) s += sums[w * p.G + e];
-            p.part_p[at + e] = s;
-            p.part_count[at + e] = counts[e];
+            if constexpr (!CLUSTER) {
+                p.part_p[at + e] = s;
+                p.part_count[at + e] = counts[e];
+            } else {
+                sums[e] = s;  // read by no other thread until the cluster has met
+            }
         }
-        if (threadIdx.x == 0) p.part_tokens[blockIdx.x] = counts[p.G];
+        if constexpr (!CLUSTER) {
+            if (threadIdx.x == 0) p.part_tokens[blockIdx.x] = counts[p.G];
+        } else {
+            finish_in_cluster(p, sums, counts);
+        }
     }
 }
 
@@ -402,7 +538,7 @@ __global__ void __cluster_dims__(kFinishCtas, 1, 1) __launch_bounds__(kFinishThr
                         const int32_t *__restrict__ part_tokens, int parts, int G, int k,
                         int32_t *__restrict__ counts, float *__restrict__ loss, float *__restrict__ dprob) {
     constexpr int kWarps = kFinishThreads / 32;
-    __shared__ double warp_p[kWarps][32], cta_loss;
+    __shared__ double warp_p[kWarps][32], warp_loss[kWarps], cta_loss[kFinishCtas];
     __shared__ int warp_count[kWarps][32], warp_tokens[kWarps];
     grid_dep_wait();
     grid_dep_launch_dependents();
@@ -460,21 +596,7 @@ __global__ void __cluster_dims__(kFinishCtas, 1, 1) __launch_bounds__(kFinishThr
         }
         __syncthreads();
     }
-    if (warp == 0) {
-        mine = warp_sum(mine);
-        if (lane == 0) cta_loss = mine;
-    }
-    cluster_sync();
-    if (rank == 0 && tid == 0) {
-        double s = 0.0;
-        for (int r = 0; r < kFinishCtas; ++r) {
-            double v;
-            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(smem_u32(&cta_loss), r)) : "memory");
-            s += v;
-        }
-        *loss = static_cast<float>(s);
-    }
-    cluster_sync();  // no CTA leaves while rank 0 reads its sum
+    loss_of_cluster<kFinishCtas>(mine, warp_loss, cta_loss, loss);
 }
 
 struct RouteBackwardParams {
@@ -483,6 +605,7 @@ struct RouteBackwardParams {
     const float *dweights, *dprob, *dloss;
     int64_t T;
     int G, k;
+    WarpShare share;
     bool bf16, sigmoid, renormalize;
     float scale;
     void *dlogits;
@@ -510,128 +633,140 @@ __global__ void __launch_bounds__(256, PER <= 8 ? 4 : 1) route_backward_kernel(c
         for (int i = 0; i < PER; ++i) dp[i] = p.dprob && lane + 32 * i < p.G ? __ldg(p.dprob + lane + 32 * i) * dloss : 0.0f;
     }
 
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * warps;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * warps + warp; t < p.T; t += stride) {
-        const int64_t row = t * p.G;
-        const int id = lane < p.k ? __ldg(p.ids + t * p.k + lane) : -1;
-        const float given = lane < p.k && p.dweights ? __ldg(p.dweights + t * p.k + lane) : 0.0f;
-        float q[PER], ns[PER];  // what p is proportional to, and 1 - sigmoid
-        if (ROWS) {
-            if (p.bf16) {
-                const uint16_t *at = static_cast<const uint16_t *>(p.logits) + row + lane;
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    q[i] = lane + 32 * i < p.G ? __uint_as_float(static_cast<uint32_t>(__ldg(at + 32 * i)) << 16) : -CUDART_INF_F;
-            } else {
-                const float *at = static_cast<const float *>(p.logits) + row + lane;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) q[i] = lane + 32 * i < p.G ? __ldg(at + 32 * i) : -CUDART_INF_F;
-            }
-        }
+    // the warp's tokens, 32 / width at a time: their slots side by side, their rows one after another
+    const int me = static_cast<int>(blockIdx.x) * warps + warp, width = 1 << p.share.shift, batch = 32 >> p.share.shift;
+    const int segment = lane >> p.share.shift, slot = lane & (width - 1);
+    int64_t t0 = p.share.first(me);
+    const int64_t end = t0 + p.share.count(me);
+    for (; t0 < end; t0 += batch) {
+        const int tokens = static_cast<int>(end - t0 < batch ? end - t0 : batch);
+        const bool here = segment < tokens && slot < p.k;
+        const int64_t at_slot = (t0 + segment) * p.k + slot;
+        const int id = here ? __ldg(p.ids + at_slot) : -1;
         const bool ok = id >= 0 && id < p.G;
-        const float z_id = ok ? load_score(p.logits, p.bf16, row + id) : 0.0f;
-        const bool routed = __any_sync(kAll, ok);
-        const float dw = ok ? given : 0.0f;
-        float top = -CUDART_INF_F, r = 0.0f, base = 0.0f;
-        bool exponential = !p.sigmoid;
-        if (ROWS && routed) {
-            float sum = 0.0f, dot = 0.0f;
-            if (!exponential) {
+        const float dw = ok && p.dweights ? __ldg(p.dweights + at_slot) : 0.0f;
+        const float z_id = ok ? load_score(p.logits, p.bf16, (t0 + segment) * p.G + id) : 0.0f;
+        const uint32_t oks = __ballot_sync(kAll, ok);
+        const float m = p.renormalize || !p.sigmoid ? segment_max(ok ? z_id : -CUDART_INF_F, width) : 0.0f;
+        float a, token_a = 0.0f;  // A_j; softmax without renormalization: over e^(m - top) / sum, with its sum over the slots
+        if (p.renormalize) {
+            const float v = share_of_chosen(z_id, ok, p.sigmoid, m, width);
+            const float mean = segment_sum(ok ? dw * v : 0.0f, width);
+            a = ok ? p.scale * v * (dw - mean) : 0.0f;
+        } else {
+            a = ok ? p.scale * dw * (p.sigmoid ? sigmoid_of(z_id) : expf(z_id - m)) : 0.0f;
+            if (!p.sigmoid) token_a = segment_sum(a, width);
+        }
+        float my_r = 0.0f, my_base = 0.0f, my_top = 0.0f;  // of the lane's token
+        bool my_exponential = false;
+        const uint32_t segment_lanes = width == 32 ? kAll : (1u << width) - 1u;
+        for (int b = 0; b < tokens; ++b) {
+            const int64_t row = (t0 + b) * p.G;
+            const bool routed = (oks >> (b * width)) & segment_lanes;
+            float q[PER], ns[PER];  // what p is proportional to, and 1 - sigmoid; then the gradient
+            float top = -CUDART_INF_F, r = 0.0f, base = 0.0f;
+            bool exponential = !p.sigmoid;
+            if (ROWS && routed) {
+                if (p.bf16) {
+                    const uint16_t *at = static_cast<const uint16_t *>(p.logits) + row + lane;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const float z = q[i], e = fminf(exp_fast(-z), 0x1p125f);  // the bound: e times its reciprocal is 1
-                    q[i] = reciprocal(1.0f + e);
-                    ns[i] = e * q[i];
-                    if (z == -CUDART_INF_F) q[i] = 0.0f;  // an expert that is left out, or none
-                    sum += q[i];
-                    dot = fmaf(dp[i], q[i], dot);
-                    top = fmaxf(top, z);
+                    for (int i = 0; i < PER; ++i)
+                        q[i] = lane + 32 * i < p.G ? __uint_as_float(static_cast<uint32_t>(__ldg(at + 32 * i)) << 16) : -CUDART_INF_F;
+                } else {
+                    const float *at = static_cast<const float *>(p.logits) + row + lane;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) q[i] = lane + 32 * i < p.G ? __ldg(at + 32 * i) : -CUDART_INF_F;
                 }
-                sum = warp_sum(sum);
-                exponential = sum < 0x1p-80f;
-                if (exponential) {  // all far below 0: ratios of exponentials
-                    sum = dot = 0.0f;
+                float sum = 0.0f, dot = 0.0f;
+                if (!exponential) {
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const float z = q[i], e = fminf(exp_fast(-z), 0x1p125f);  // the bound: e times its reciprocal is 1
+                        q[i] = reciprocal(1.0f + e);
+                        ns[i] = e * q[i];
+                        if (z == -CUDART_INF_F) q[i] = 0.0f;  // an expert that is left out, or none
+                        sum += q[i];
+                        dot = fmaf(dp[i], q[i], dot);
+                        top = fmaxf(top, z);
+                    }
+                    sum = warp_sum(sum);
+                    exponential = sum < 0x1p-80f;
+                    if (exponential) {  // all far below 0: ratios of exponentials
+                        sum = dot = 0.0f;
+                        top = warp_max(top);
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const float z = lane + 32 * i < p.G ? load_score(p.logits, p.bf16, row + lane + 32 * i) : -CUDART_INF_F;
+                            q[i] = exp_fast(z - top);
+                            sum += q[i];
+                            dot = fmaf(dp[i], q[i], dot);
+                        }
+                        sum = warp_sum(sum);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) top = fmaxf(top, q[i]);
                     top = warp_max(top);
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
-                        const float z = lane + 32 * i < p.G ? load_score(p.logits, p.bf16, row + lane + 32 * i) : -CUDART_INF_F;
-                        q[i] = exp_fast(z - top);
+                        q[i] = exp_fast(q[i] - top);
                         sum += q[i];
                         dot = fmaf(dp[i], q[i], dot);
                     }
                     sum = warp_sum(sum);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) top = fmaxf(top, q[i]);
-                top = warp_max(top);
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    q[i] = exp_fast(q[i] - top);
-                    sum += q[i];
-                    dot = fmaf(dp[i], q[i], dot);
+                r = 1.0f / sum;
+                if (p.dprob) base = warp_sum(dot) * r;
+                if (!p.sigmoid && !p.renormalize)
+                    base += __shfl_sync(kAll, token_a, b * width) * (expf(__shfl_sync(kAll, m, b * width) - top) * r);
+                if (segment == b) {
+                    my_r = r;
+                    my_base = base;
+                    my_top = top;
+                    my_exponential = exponential;
                 }
-                sum = warp_sum(sum);
             }
-            r = 1.0f / sum;
-            if (p.dprob) base = warp_sum(dot) * r;
-        }
-        float a = 0.0f;  // lane j: A_j
-        if (routed) {
-            if (p.renormalize) {
-                const float v = share_of_chosen(z_id, ok, p.sigmoid);
-                const float mean = warp_sum(ok ? dw * v : 0.0f);
-                a = ok ? p.scale * v * (dw - mean) : 0.0f;
+            // every expert's part; the chosen ones' whole gradient follows over it
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                q[i] = ROWS && routed ? q[i] * r * (dp[i] - base) : 0.0f;
+                if (ROWS && routed && p.sigmoid) q[i] *= ns[i];
+            }
+            if (p.bf16) {
+                __nv_bfloat16 *at = static_cast<__nv_bfloat16 *>(p.dlogits) + row + lane;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (lane + 32 * i < p.G) at[32 * i] = __float2bfloat16(q[i]);
             } else {
-                const float s = p.sigmoid ? sigmoid_of(z_id) : expf(z_id - top) * r;
-                a = ok ? p.scale * dw * s : 0.0f;
-                if (!p.sigmoid) base += warp_sum(a);
-            }
-        }
-        // every expert's part, then the chosen ones' whole gradient over it
-        float v[PER];
+                float *at = static_cast<float *>(p.dlogits) + row + lane;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            v[i] = 0.0f;
-            if (ROWS && routed) {
-                v[i] = q[i] * r * (dp[i] - base);
-                if (p.sigmoid) v[i] *= ns[i];
+                for (int i = 0; i < PER; ++i)
+                    if (lane + 32 * i < p.G) at[32 * i] = q[i];
             }
         }
-        if (p.bf16) {
-            __nv_bfloat16 *at = static_cast<__nv_bfloat16 *>(p.dlogits) + row + lane;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (lane + 32 * i < p.G) at[32 * i] = __float2bfloat16(v[i]);
-        } else {
-            float *at = static_cast<float *>(p.dlogits) + row + lane;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (lane + 32 * i < p.G) at[32 * i] = v[i];
+        if (oks == 0u) continue;
+        if (!p.renormalize && !p.sigmoid) a *= expf(m - my_top) * my_r;
+        // an expert that a token names twice gets both slots' parts
+        const uint32_t same = __match_any_sync(kAll, ok ? segment * 1024 + id : -1 - lane);
+        if (__any_sync(kAll, (same & (same - 1)) != 0)) {
+            float both = 0.0f;
+            for (int j = 0; j < 32; ++j) {
+                const float other = __shfl_sync(kAll, a, j);
+                if ((same >> j) & 1u) both += other;
+            }
+            a = both;
         }
-        if (routed) {
-            // an expert that a token names twice gets both slots' parts
-            const uint32_t same = __match_any_sync(kAll, ok ? id : -1 - lane);
-            if (__any_sync(kAll, (same & (same - 1)) != 0)) {
-                float both = 0.0f;
-                for (int j = 0; j < 32; ++j) {
-                    const float other = __shfl_sync(kAll, a, j);
-                    if ((same >> j) & 1u) both += other;
-                }
-                a = both;
-            }
-            float g = a;
-            if (ROWS && ok) {
-                const float d = p.dprob ? __ldg(p.dprob + id) * dloss : 0.0f;
-                g += unnormalized(z_id, top, exponential) * r * (d - base);
-            }
-            if (p.sigmoid) {
-                const float e = fminf(exp_fast(-z_id), 0x1p125f);
-                g *= e * reciprocal(1.0f + e);
-            }
-            __syncwarp();  // the row's stores come first
-            if (ok) store_score(p.dlogits, p.bf16, row + id, g);
+        float g = a;
+        if (ROWS && ok) {
+            const float d = p.dprob ? __ldg(p.dprob + id) * dloss : 0.0f;
+            g += unnormalized(z_id, my_top, my_exponential) * my_r * (d - my_base);
         }
+        if (p.sigmoid) {
+            const float e = fminf(exp_fast(-z_id), 0x1p125f);
+            g *= e * reciprocal(1.0f + e);
+        }
+        __syncwarp();  // the rows' stores come first
+        if (ok) store_score(p.dlogits, p.bf16, (t0 + segment) * p.G + id, g);
     }
 }
 
@@ -650,26 +785,44 @@ struct RouteShape {
     int threads, grid;
 };
 
+// Few tokens are taken by one cluster of sixteen CTAs alone, where a pass is bound by host time: a launch and an
+// allocation less (1000 tokens of 64 experts: 14.2 -> 9.5 us of host time, 5.9 -> 8.0 us on the GPU; 100 tokens 5.0 -> 4.6).
+// With more experts or tokens the cluster itself takes longer than that (1000 of 256: 15 us).
+bool one_cluster(int64_t T, int G) { return T * per_lane(G) <= 2048; }
+
 // A CTA per SM with as many warps as there are tokens for, up to 32: fewer parts to add up.
 RouteShape balance_shape(int64_t T, int G) {
     const int64_t most = route_max_threads(per_lane(G)) / 32;
+    if (one_cluster(T, G)) {
+        const int64_t warps = (T + kClusterCtas - 1) / kClusterCtas;
+        return {static_cast<int>(warps < 4 ? 4 : warps > most ? most : warps) * 32, kClusterCtas};
+    }
     int64_t warps = (T + kSms - 1) / kSms;
     warps = warps < 4 ? 4 : warps > most ? most : warps;
     const int64_t grid = (T + warps - 1) / warps, limit = kSms * (32 / most);
     return {static_cast<int>(warps) * 32, static_cast<int>(grid < 1 ? 1 : grid > limit ? limit : grid)};
 }
 
+// As few lanes for a token's slots as hold them, and at least as many as leave a warp no more
+// tokens at a time than it has.
+WarpShare share_out(int64_t T, int k, int64_t warps) {
+    int shift = 0;
+    while ((1 << shift) < k || (shift < 5 && (T + warps - 1) / warps <= (16 >> shift))) ++shift;
+    return {T / warps, static_cast<int>(T % warps), shift};
+}
+
 }  // namespace
 
 // As many parts as any T up to this one gives: a workspace for the largest batch serves smaller ones.
 int64_t route_workspace(int64_t T, int G) {
-    const int64_t most = T < 4 ? 1 : (T + 3) / 4, limit = kSms * (32 * 32 / route_max_threads(per_lane(G)));
+    if (one_cluster(T, G)) return 0;
+    const int64_t most = (T + 3) / 4, limit = kSms * (32 * 32 / route_max_threads(per_lane(G)));
     return (most < limit ? most : limit) * (G * 8 + 4);
 }
 
-template <int PER, bool BIAS, bool BALANCE>
+template <int PER, bool BIAS, bool BALANCE, bool CLUSTER>
 static dg_status_t launch_route_impl(const RouteParams &p, const RouteShape &s, cudaStream_t stream) {
-    auto kernel = route_kernel<PER, BIAS, BALANCE>;
+    auto kernel = route_kernel<PER, BIAS, BALANCE, CLUSTER>;
     const size_t smem = BALANCE ? (static_cast<size_t>(s.threads / 32) * p.G + p.G + 1) * 4 : 0;
     if (smem > 48 * 1024) {
         static thread_local int configured_device = -1;
@@ -677,14 +830,39 @@ static dg_status_t launch_route_impl(const RouteParams &p, const RouteShape &s, 
                                           configured_device);
         if (st != DG_OK) return st;
     }
-    return launch_pdl(kernel, s.grid, s.threads, smem, stream, p);
+    if (!CLUSTER) return launch_pdl(kernel, s.grid, s.threads, smem, stream, p);
+    static thread_local int wide_device = -1;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return DG_ERR_CUDA;
+    if (wide_device != device) {  // clusters of more than eight need the kernel's consent
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return DG_ERR_CUDA;
+        wide_device = device;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(s.grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(s.threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(s.grid);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+template <int PER, bool BIAS>
+static dg_status_t launch_route_per(const RouteParams &p, bool balance, const RouteShape &s, cudaStream_t stream) {
+    if (!balance) return launch_route_impl<PER, BIAS, false, false>(p, s, stream);
+    return p.part_p ? launch_route_impl<PER, BIAS, true, false>(p, s, stream) : launch_route_impl<PER, BIAS, true, true>(p, s, stream);
 }
 
 template <int PER>
 static dg_status_t launch_route_per(const RouteParams &p, bool balance, const RouteShape &s, cudaStream_t stream) {
-    if (p.bias)
-        return balance ? launch_route_impl<PER, true, true>(p, s, stream) : launch_route_impl<PER, true, false>(p, s, stream);
-    return balance ? launch_route_impl<PER, false, true>(p, s, stream) : launch_route_impl<PER, false, false>(p, s, stream);
+    return p.bias ? launch_route_per<PER, true>(p, balance, s, stream) : launch_route_per<PER, false>(p, balance, s, stream);
 }
 
 dg_status_t launch_route(const RouteArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
@@ -705,13 +883,19 @@ dg_status_t launch_route(const RouteArgs &a, const DeviceInfo &dev, cudaStream_t
     RouteShape s;
     if (balance) {
         s = balance_shape(a.T, a.G);
-        p.part_p = static_cast<float *>(a.workspace);
-        p.part_count = reinterpret_cast<int32_t *>(p.part_p + static_cast<int64_t>(s.grid) * a.G);
-        p.part_tokens = p.part_count + static_cast<int64_t>(s.grid) * a.G;
+        p.counts = a.counts;
+        p.loss = a.loss;
+        p.dprob = a.dprob;
+        if (!one_cluster(a.T, a.G)) {
+            p.part_p = static_cast<float *>(a.workspace);
+            p.part_count = reinterpret_cast<int32_t *>(p.part_p + static_cast<int64_t>(s.grid) * a.G);
+            p.part_tokens = p.part_count + static_cast<int64_t>(s.grid) * a.G;
+        }
     } else {
-        const int64_t want = (a.T + 3) / 4, most = 16 * static_cast<int64_t>(dev.num_sms);
+        const int64_t want = (a.T + 3) / 4, most = 8 * static_cast<int64_t>(dev.num_sms);
         s = {128, static_cast<int>(want < most ? want : most)};
     }
+    p.share = share_out(a.T, a.k, static_cast<int64_t>(s.grid) * (s.threads / 32));
     dg_status_t st;
     switch (per_lane(a.G)) {
     case 1: st = launch_route_per<1>(p, balance, s, stream); break;
@@ -721,7 +905,7 @@ dg_status_t launch_route(const RouteArgs &a, const DeviceInfo &dev, cudaStream_t
     case 16: st = launch_route_per<16>(p, balance, s, stream); break;
     default: st = launch_route_per<32>(p, balance, s, stream); break;
     }
-    if (st != DG_OK || !balance) return st;
+    if (st != DG_OK || !p.part_p) return st;
     return launch_pdl(route_finish_kernel, kFinishCtas, kFinishThreads, 0, stream, static_cast<const float *>(p.part_p),
                       static_cast<const int32_t *>(p.part_count), static_cast<const int32_t *>(p.part_tokens), s.grid, a.G,
                       a.k, a.counts, a.loss, a.dprob);
@@ -735,10 +919,11 @@ static dg_status_t launch_route_backward_per(const RouteBackwardParams &p, int g
 }
 
 dg_status_t launch_route_backward(const RouteBackwardArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    RouteBackwardParams p = {a.logits, a.ids, a.dweights, a.dprob, a.dloss, a.T, a.G, a.k,
-                             a.bf16, a.sigmoid, a.renormalize, a.scale, a.dlogits};
     const int64_t want = (a.T + 7) / 8, most = 4 * static_cast<int64_t>(dev.num_sms);
     const int grid = static_cast<int>(want < most ? want : most);
+    const RouteBackwardParams p = {a.logits, a.ids, a.dweights, a.dprob, a.dloss, a.T, a.G, a.k,
+                                   share_out(a.T, a.k, static_cast<int64_t>(grid) * 8),
+                                   a.bf16, a.sigmoid, a.renormalize, a.scale, a.dlogits};
     switch (per_lane(a.G)) {
     case 1: return launch_route_backward_per<1>(p, grid, stream);
     case 2: return launch_route_backward_per<2>(p, grid, stream);

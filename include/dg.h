@@ -567,8 +567,8 @@ typedef struct {
  * 1 <= G <= 1024, 1 <= k <= min(G, 32), T * k <= 2^30.  T == 0 writes counts, dprob and
  * loss of 0 when they are asked for.
  * workspace : device scratch of at least dg_moe_route_workspace(T, G) bytes, 16-byte aligned,
- *             where counts are asked for; else it may be null.  Not shared with a call that
- *             may run at the same time.
+ *             where counts are asked for; may be null where that is 0 (few tokens), or without
+ *             counts.  Not shared with a call that may run at the same time.
  */
 dg_status_t dg_moe_route(const void *logits, int logits_bf16, const dg_route_options_t *options,
                          const float *bias, const uint8_t *mask, int64_t T, int G, int k,

@@ -45,16 +45,18 @@ def test_route_refusals(lib):
         assert call(**bad) == SHAPE, bad
     for bad in (dict(z=NULL), dict(ids=NULL), dict(w=NULL), dict(o=NULL), dict(o=ref(RouteOptions(2, 1, 1.0))),
                 dict(o=ref(RouteOptions(0, 1, math.inf))), dict(o=ref(RouteOptions(0, 1, math.nan))), dict(c=P),
-                dict(loss=P), dict(d=P), dict(c=P, loss=P), dict(c=P, loss=P, d=P)):
+                dict(loss=P), dict(d=P), dict(c=P, loss=P)):
         assert call(**bad) == ARG, bad
-    need = lib.dg_moe_route_workspace(8, 16)
-    full = dict(c=P, loss=P, d=P, ws=P, n=need)
-    assert need > 0 and call(**{**full, "n": need - 1}) == ARG
+    # more tokens than one cluster takes: a workspace of the size that the library names
+    need = lib.dg_moe_route_workspace(8000, 16)
+    full = dict(T=8000, c=P, loss=P, d=P, ws=P, n=need)
+    assert need > 0 and lib.dg_moe_route_workspace(8, 16) == 0
+    assert call(**{**full, "n": need - 1}) == ARG and call(**{**full, "ws": NULL}) == ARG
     for bad in (dict(z=ODD), dict(z=ctypes.c_void_p(0x10002)), dict(bias=ODD), dict(ids=ODD), dict(w=ODD),
                 dict(full, c=ODD), dict(full, loss=ODD), dict(full, d=ODD), dict(full, ws=ODD)):
         assert call(**bad) == ALIGN, bad
     assert call(z=ctypes.c_void_p(0x10002), bf16=1, ids=ODD) == ALIGN and call(T=0, z=NULL, ids=NULL, w=NULL) == OK
-    assert lib.dg_moe_route_workspace(-1, 16) == lib.dg_moe_route_workspace(8, 1025) == 0
+    assert lib.dg_moe_route_workspace(-1, 16) == lib.dg_moe_route_workspace(8000, 1025) == 0
     # the workspace never shrinks as the sizes grow
     assert all(lib.dg_moe_route_workspace(T, 64) <= lib.dg_moe_route_workspace(T + 1, 64) for T in range(0, 9000, 7))
 
