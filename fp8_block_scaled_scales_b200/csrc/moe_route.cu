@@ -620,8 +620,11 @@ __device__ __forceinline__ void store_score(void *out, bool bf16, int64_t at, fl
 
 // ROWS: every expert's score matters (the balance loss, or softmax without renormalization);
 // otherwise only the chosen experts have a gradient, and only their scores are read.
+// CTAs of an SM, as the registers allow: none waits for another to end.
+constexpr int backward_ctas(int per) { return per <= 8 ? 4 : per <= 16 ? 2 : 1; }
+
 template <int PER, bool ROWS>
-__global__ void __launch_bounds__(256, PER <= 8 ? 4 : 1) route_backward_kernel(const RouteBackwardParams p) {
+__global__ void __launch_bounds__(256, backward_ctas(PER)) route_backward_kernel(const RouteBackwardParams p) {
     const int lane = lane_id();
     const int warps = static_cast<int>(blockDim.x) >> 5, warp = static_cast<int>(threadIdx.x) >> 5;
     grid_dep_wait();
@@ -919,7 +922,7 @@ static dg_status_t launch_route_backward_per(const RouteBackwardParams &p, int g
 }
 
 dg_status_t launch_route_backward(const RouteBackwardArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    const int64_t want = (a.T + 7) / 8, most = 4 * static_cast<int64_t>(dev.num_sms);
+    const int64_t want = (a.T + 7) / 8, most = backward_ctas(per_lane(a.G)) * static_cast<int64_t>(dev.num_sms);
     const int grid = static_cast<int>(want < most ? want : most);
     const RouteBackwardParams p = {a.logits, a.ids, a.dweights, a.dprob, a.dloss, a.T, a.G, a.k,
                                    share_out(a.T, a.k, static_cast<int64_t>(grid) * 8),
