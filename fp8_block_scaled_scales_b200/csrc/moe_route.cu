@@ -309,7 +309,7 @@ __device__ __forceinline__ void finish_in_cluster(const RouteParams &p, const fl
 // by more than those (and, with a bias, by more than the key's own FP32 error); otherwise (a token
 // in thirty) the candidates are put in order by FP64 keys.  BF16 logits without a bias have the bits to spare.
 // Bound by instruction issue, most of it the sort and the k + 1 rounds: 16384 tokens x 256 experts, k = 8,
-// FP32 sigmoid scores 10.7 us, with balance loss 15.4, with bias too 18.7 (the logits alone: 2.6).
+// FP32 sigmoid scores 10.7 us, with balance loss 15.4, with bias too 18.7 (the logits alone: 2.6); over 512 experts 31, 42 and 54.
 constexpr int route_max_threads(int per) { return per <= 8 ? 1024 : 512; }
 
 template <int PER, bool BIAS, bool BALANCE, bool CLUSTER>
@@ -802,7 +802,7 @@ RouteShape balance_shape(int64_t T, int G) {
     }
     int64_t warps = (T + kSms - 1) / kSms;
     warps = warps < 4 ? 4 : warps > most ? most : warps;
-    const int64_t grid = (T + warps - 1) / warps, limit = kSms * (32 / most);
+    const int64_t grid = (T + warps - 1) / warps, limit = kSms;
     return {static_cast<int>(warps) * 32, static_cast<int>(grid < 1 ? 1 : grid > limit ? limit : grid)};
 }
 
@@ -819,7 +819,7 @@ WarpShare share_out(int64_t T, int k, int64_t warps) {
 // As many parts as any T up to this one gives: a workspace for the largest batch serves smaller ones.
 int64_t route_workspace(int64_t T, int G) {
     if (one_cluster(T, G)) return 0;
-    const int64_t most = (T + 3) / 4, limit = kSms * (32 * 32 / route_max_threads(per_lane(G)));
+    const int64_t most = (T + 3) / 4, limit = kSms;
     return (most < limit ? most : limit) * (G * 8 + 4);
 }
 
