@@ -276,18 +276,25 @@ __device__ __forceinline__ void finish_in_cluster(const RouteParams &p, const fl
     cluster_sync();
     const int half = static_cast<int>(threadIdx.x) >> 4, halves = static_cast<int>(blockDim.x) >> 4;
     const uint32_t r = threadIdx.x & 15u;
-    int n = from_cta(counts + p.G, r);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
-    const double nd = n > 0 ? static_cast<double>(n) : 1.0;
-    const double unit = static_cast<double>(p.G) / (static_cast<double>(p.k) * nd * nd);
-    double mine = 0.0;
     const int share = (p.G + kClusterCtas - 1) / kClusterCtas, e0 = static_cast<int>(cluster_ctarank()) * share;
     const int end = e0 + share < p.G ? e0 + share : p.G;
-    for (int base = e0; base < end; base += halves) {  // the same for the whole CTA
+    int n = from_cta(counts + p.G, r);
+    double unit = 0.0, mine = 0.0;
+    for (int base = e0; base < end || base == e0; base += halves) {  // the same for the whole CTA
         const int e = base + half;
-        double s = e < end ? static_cast<double>(from_cta(sums + e, r)) : 0.0;
-        int c = e < end ? from_cta(counts + e, r) : 0;
+        float part = 0.0f;
+        int c = 0;
+        if (e < end) {
+            part = from_cta(sums + e, r);
+            c = from_cta(counts + e, r);
+        }
+        if (base == e0) {  // under the loads
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
+            const double nd = n > 0 ? static_cast<double>(n) : 1.0;
+            unit = static_cast<double>(p.G) / (static_cast<double>(p.k) * nd * nd);
+        }
+        double s = static_cast<double>(part);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) {
             s += __shfl_xor_sync(kAll, s, o);
@@ -515,6 +522,7 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
         const int64_t at = static_cast<int64_t>(blockIdx.x) * p.G;
         for (int e = static_cast<int>(threadIdx.x); e < p.G; e += static_cast<int>(blockDim.x)) {
             float s = 0.0f;
+#pragma unroll 8
             for (int w = 0; w < warps; ++w) s += sums[w * p.G + e];
             if constexpr (!CLUSTER) {
                 p.part_p[at + e] = s;
@@ -789,7 +797,7 @@ struct RouteShape {
 };
 
 // Few tokens are taken by one cluster of sixteen CTAs alone, where a pass is bound by host time: a launch and an
-// allocation less (1000 tokens of 64 experts: 14.2 -> 9.5 us of host time, 5.9 -> 8.0 us on the GPU; 100 tokens 5.0 -> 4.6).
+// allocation less (1000 tokens of 64 experts: 10.2 -> 8.2 us a call among others, though 5.9 -> 7.7 on the GPU; 100 tokens 5.0 -> 4.5 there).
 // With more experts or tokens the cluster itself takes longer than that (1000 of 256: 15 us).
 bool one_cluster(int64_t T, int G) { return T * per_lane(G) <= 2048; }
 
@@ -809,9 +817,11 @@ RouteShape balance_shape(int64_t T, int G) {
 // As few lanes for a token's slots as hold them, and at least as many as leave a warp no more
 // tokens at a time than it has.
 WarpShare share_out(int64_t T, int k, int64_t warps) {
+    const int64_t per = T / warps;
+    const int extra = static_cast<int>(T - per * warps), most = per < 16 ? static_cast<int>(per) + (extra != 0) : 16;
     int shift = 0;
-    while ((1 << shift) < k || (shift < 5 && (T + warps - 1) / warps <= (16 >> shift))) ++shift;
-    return {T / warps, static_cast<int>(T % warps), shift};
+    while ((1 << shift) < k || (shift < 5 && most <= (16 >> shift))) ++shift;
+    return {per, extra, shift};
 }
 
 }  // namespace
