@@ -199,7 +199,7 @@ struct WalkShape {
 static WalkShape walk_shape(int64_t T, int64_t H, int arrays, int threads_per_sm, int most_stages) {
     WalkShape s;
     s.ctas = H <= kWalkCols ? 1 : H <= 2 * kWalkCols ? 2 : 4;
-    s.cols = s.ctas == 1 ? static_cast<int>(H) : static_cast<int>((H / s.ctas + 15) / 16 * 16);
+    s.cols = s.ctas == 1 ? static_cast<int>(H) : static_cast<int>((H / s.ctas + 127) / 128 * 128);  // whole groups
     s.threads = (s.cols / kVec + 31) / 32 * 32;
     const int per_sm = threads_per_sm / s.threads;
     const int stage = arrays * s.cols * 2;

@@ -80,6 +80,14 @@ def test_forward(T, H, y, post, gate, vec):
     assert ((s.double() - want).abs() <= off / 448 + U * want).all()
 
 
+@pytest.mark.parametrize("T,H", [(601, 4112), (640, 6000), (601, 8176), (620, 8208), (601, 12304), (601, 16368), (2001, 272),
+                                 (1203, 3984)])
+@pytest.mark.parametrize("y,post,gate", FORMS)
+def test_many_rows_of_odd_widths(T, H, y, post, gate):
+    """Rows that several CTAs share, and that end inside a group of 128 columns."""
+    test_forward(T, H, y, post, gate, torch.float32)
+
+
 def test_codes_are_those_of_the_quantizer():
     """With a weight of powers of two and rows whose norm is a power of two, n is a BF16 number:
     quantize_1x128 of it gives the same codes and scales, bit for bit."""
