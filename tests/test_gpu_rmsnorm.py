@@ -162,7 +162,8 @@ def test_backward(T, H, y, post, gate, dr):
     check_backward(T, H, y, post, gate, dr=dr, vec=torch.bfloat16 if dr else torch.float32)
 
 
-@pytest.mark.parametrize("T,H", [(5000, 1024), (9001, 128), (1500, 8192), (700, 16384), (4001, 4096)])
+@pytest.mark.parametrize("T,H", [(5000, 1024), (9001, 128), (1500, 8192), (700, 16384), (4001, 4096),
+                                 (700, 6000), (500, 12304), (900, 4112)])
 def test_backward_of_many_rows_repeats_bit_for_bit(T, H):
     a = check_backward(T, H, True, True, True)
     b = check_backward(T, H, True, True, True, stream=torch.cuda.Stream())

@@ -164,6 +164,37 @@ def test_route_backward(T, G, k, score, dtype):
         check_backward(z, k, score, renormalize, None, mask=mask)
 
 
+# several tokens a warp, whose slots are finished side by side
+MANY = [(20011, 8, 2), (9001, 64, 1), (12000, 40, 3), (6007, 300, 8), (5003, 1000, 32), (11000, 33, 31), (10000, 128, 16)]
+
+
+@pytest.mark.parametrize("T,G,k", MANY)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_tokens(T, G, k, score):
+    dtype = torch.bfloat16 if T % 2 else torch.float32
+    z = logits(T, G, T + k, dtype)
+    bias = (torch.rand((G,), generator=torch.Generator().manual_seed(G)) - 0.5) * 0.3
+    mask = torch.arange(T) % 7 != 3
+    check(z, k, score, bias=bias, mask=mask, renormalize=False, scale=2.5)
+    ids = check(z, k, score)
+    dw = torch.randn((T, k), generator=torch.Generator().manual_seed(T))
+    for renormalize in (True, False):
+        check_backward(z, k, score, renormalize, dw, ids=ids)
+        check_backward(z, k, score, renormalize, dw, balance=False, mask=mask)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_tokens_with_ids_named_twice(score):
+    T, G = 15000, 50
+    z = logits(T, G, 3)
+    ids = torch.randint(-2, 53, (T, 5), generator=torch.Generator().manual_seed(4), dtype=torch.int32)
+    ids[::50] = -1
+    dw = torch.randn((T, 5), generator=torch.Generator().manual_seed(6))
+    for renormalize in (True, False):
+        for balance in (True, False):
+            check_backward(z, 5, score, renormalize, dw, balance=balance, ids=ids.cuda())
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_backward_of_ids_named_twice_and_out_of_range(score):
     z = logits(300, 50, 3)
