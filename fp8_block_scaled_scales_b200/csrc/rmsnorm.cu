@@ -439,8 +439,10 @@ static dg_status_t launch_walk_form(const NormWalkParams &p, const WalkShape &s,
     return launch_walk_forward<true, false, false, CODES>(p, s, stream);
 }
 
-// Above this many rows they are walked over.
-constexpr int64_t kWalkRows = 600;
+// Above this many rows they are walked over.  A CTA a row has no ring to fill first: 1500 x 1024 with post and gate
+// as codes 5.3 us against 6.9 walked over, 700 x 256 3.1 against 4.5, about the same from 3000 rows on.  Of wider
+// rows fewer run at once: 601 x 7168 17 us against 13, 1000 x 2048 8.1 against 7.3.
+static int64_t walk_rows(int64_t H) { return H <= 1024 ? 3000 : 600; }
 
 dg_status_t launch_rmsnorm(const NormArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
     NormParams p;
@@ -461,7 +463,7 @@ dg_status_t launch_rmsnorm(const NormArgs &a, const DeviceInfo &dev, cudaStream_
     p.rstd = a.rstd;
     p.rstd_y = a.rstd_y;
     const bool codes = a.q != nullptr;
-    if (a.T > kWalkRows) {
+    if (a.T > walk_rows(a.H)) {
         // Reads far ahead of the writes cost bandwidth: 16384 x 4096 with a post and a gate, two CTAs an SM, takes
         // 87 us with three rows in the ring, 94 with four, 101 with six (one CTA: 104).  With less arithmetic one
         // CTA and four rows keep up: 86 us without post, against 107 with two CTAs and three rows.

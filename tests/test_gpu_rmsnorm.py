@@ -80,7 +80,7 @@ def test_forward(T, H, y, post, gate, vec):
     assert ((s.double() - want).abs() <= off / 448 + U * want).all()
 
 
-@pytest.mark.parametrize("T,H", [(601, 4112), (640, 6000), (601, 8176), (620, 8208), (601, 12304), (601, 16368), (2001, 272),
+@pytest.mark.parametrize("T,H", [(601, 4112), (640, 6000), (601, 8176), (620, 8208), (601, 12304), (601, 16368), (2001, 272), (3100, 272), (3001, 16), (3000, 1024),
                                  (1203, 3984)])
 @pytest.mark.parametrize("y,post,gate", FORMS)
 def test_many_rows_of_odd_widths(T, H, y, post, gate):
