@@ -459,10 +459,12 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
             auto unsettled = [&](uint32_t a, uint32_t b) {
                 if (b == 0u) return false;
                 if (!BIAS) return (a ^ b) <= kIdBits;
-                // keys are off by less than 2^-18 max(1, |key|): 2^-21 in s (37 additions of softmax's
-                // sum among them) and a rounding of s + b
+                // keys are off by less than 2^-18 max(s, |key|), s the row's largest score (1 for sigmoids):
+                // 2^-21 of s in a score (37 additions of softmax's sum among them, and an exponential's error,
+                // which grows slower than the exponential falls) and a rounding of s + b
                 const float x = from_ordered(a & ~kIdBits), y = from_ordered(b | kIdBits);
-                return !(x - y > 0x1p-17f * fmaxf(1.0f, fabsf(x)));  // infinite keys too
+                const float s = p.sigmoid ? 1.0f : reciprocal(sum);
+                return !(x - y > 0x1p-17f * fmaxf(s, fabsf(x)));  // infinite keys too
             };
             while (found < rounds) next();
             if (!exact_keys) {

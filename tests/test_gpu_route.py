@@ -83,6 +83,9 @@ def test_keys_that_float32_cannot_tell_apart(score, G):
     s = plain.probabilities(z[:1].double(), score)[0][0]
     check(z[:1].repeat(50, 1), min(G, 12), score, bias=(0.75 - s).float())
     check(z, min(G, 12), score, bias=(0.75 - s).float())
+    # the same around sums far below the scores themselves
+    check(z[:1].repeat(50, 1), min(G, 12), score, bias=(1e-3 - s).float())
+    check(z, min(G, 12), score, bias=(1e-3 - s).float())
 
 
 def test_experts_and_tokens_left_out():
