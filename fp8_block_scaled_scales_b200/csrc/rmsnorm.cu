@@ -517,10 +517,12 @@ __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
 // CTAS CTAs (a cluster) walk rows together, each over up to 4096 columns, eight a thread.  The
 // vectors and the per-column sums stay in registers; rows come through a ring of bulk copies.
 // The loop takes a row's sums one iteration before it uses them, so that one barrier a row
-// publishes the next row's sums and frees the last row's stage, and the reduction of one row
-// runs under the arithmetic of the other.  In a cluster each warp stores its share into every
-// CTA asynchronously, counted by that CTA's barrier of the row's parity: the cluster's own
-// barrier would wait for the row's stores to global memory (8192 x 8192: 232 us with it).  A share of row
+// publishes the next row's sums and frees a stage.  A row's pieces stay in registers from its sums to its outputs,
+// and the next row's are read behind these (16384 x 4096: 140 -> 131 us, 8192 x 8192 156 -> 147); clusters of
+// four take the next row's sums first and read the row at hand from the ring once more, so that the shares' way
+// passes under its arithmetic (4000 x 16384: 201 us as in smaller clusters, 190 so).  In a cluster each warp
+// stores its share into every CTA asynchronously, counted by that CTA's barrier of the row's parity: the
+// cluster's own barrier would wait for the row's stores to global memory (8192 x 8192: 232 us with it).  A share of row
 // i + 2 cannot overtake a reader of row i: it is sent after all shares of row i + 1 have come, and a warp
 // sends its share of row i + 1 after it has read row i.
 // VECTOR: y has a post or a gate (POST implies it).
@@ -531,6 +533,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
     uint64_t *shared_sums = full + kWalkMaxStages;  // [2], in a cluster: a row's shares have come
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + 64);
     constexpr int kWords = 16 * CTAS;  // warps of the cluster
+    constexpr bool kAhead = CTAS == 4;
     float *red = reinterpret_cast<float *>(smem + kWalkSums);  // [2][4][kWords]
     uint8_t *ring = smem + kWalkHeader;
     constexpr int kSumsKept = 1 + VECTOR;
@@ -588,9 +591,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
         for (; asked < p.stages && first + static_cast<int64_t>(asked) * step < p.T; ++asked)
             ask(first + static_cast<int64_t>(asked) * step, asked);
 
-    auto piece = [&](int s, int array, float2(&out)[4]) {
-        bf16x8_to_f32(reinterpret_cast<const uint4 *>(ring + s * stage_bytes + array * row_bytes)[tid], out);
-    };
+    uint4 held[4];  // the thread's pieces of the row whose sums were taken last: dn, r, y, dr
+    auto take = [&](int s, int array) { return reinterpret_cast<const uint4 *>(ring + s * stage_bytes + array * row_bytes)[tid]; };
     // the warp's share of a row's sums (g r, dr q, g q, r q), to every CTA of the cluster
     auto sum_row = [&](int it, int s, uint32_t parity) {
         if (!mbar_wait(&full[s], parity, abort_flag, p.timeout_ns)) {
@@ -600,9 +602,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
         }
         float2 gr = zero, dq = zero, gq = zero, rq = zero;
         if (mine) {
+            held[0] = take(s, 0);
+            held[1] = take(s, 1);
+            if (Y) held[2] = take(s, 2);
+            if (p.dr) held[3] = take(s, 2 + Y);
             float2 g[4], r[4];
-            piece(s, 0, g);
-            piece(s, 1, r);
+            bf16x8_to_f32(held[0], g);
+            bf16x8_to_f32(held[1], r);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 g[j] = __fmul2_rn(g[j], w[j]);
@@ -610,7 +616,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
             }
             if (POST) {
                 float2 q[4];
-                piece(s, 2, q);
+                bf16x8_to_f32(held[2], q);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     q[j] = __fmul2_rn(q[j], gp[j]);
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
                     rq = __ffma2_rn(r[j], q[j], rq);
                 }
                 if (p.dr) {
-                    piece(s, 2 + Y, r);
+                    bf16x8_to_f32(held[3], r);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) dq = __ffma2_rn(r[j], q[j], dq);
                 }
@@ -663,6 +669,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
     float rstd = scale_of_row(p.rstd, t), rstd_y = POST ? scale_of_row(p.rstd_y, t) : 1.0f;
     if (t < p.T) sum_row(0, 0, 0u);
     __syncthreads();
+    auto refill = [&](int64_t row, int s) {  // the stage that it was read from
+        const int64_t later = row + static_cast<int64_t>(p.stages) * step;
+        if (tid == 0 && later < p.T && !*abort_flag) {
+            ask(later, s);
+            ++asked;
+        }
+    };
+    if (!kAhead) refill(t, 0);
     if (t < p.T) read_sums(0, rstd, rstd_y);
     int s = 0, next_s = 1;  // at least two stages
     uint32_t next_parity = 0u;
@@ -673,15 +687,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
         const int64_t next = t + step;
         const float later_rstd = scale_of_row(p.rstd, next + step);
         const float later_rstd_y = POST ? scale_of_row(p.rstd_y, next + step) : 1.0f;
-        if (next < p.T) sum_row(it + 1, next_s, next_parity);
+        if (kAhead && next < p.T) sum_row(it + 1, next_s, next_parity);
         if (mine) {
+            auto piece = [&](int i, int array, float2(&v)[4]) { bf16x8_to_f32(kAhead ? take(s, array) : held[i], v); };
             const float2 rs = make_float2(rstd, rstd), ry = make_float2(rstd_y, rstd_y), alpha2 = make_float2(p.alpha, p.alpha);
             const float2 back2 = make_float2(back, back), back_y2 = make_float2(back_y, back_y);
             float2 m[4], r[4], d[4];
-            piece(s, 0, m);
-            piece(s, 1, r);
+            piece(0, 0, m);
+            piece(1, 1, r);
             if (p.dr) {
-                piece(s, 2 + Y, d);
+                piece(3, 2 + Y, d);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[j] = zero;
@@ -697,7 +712,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
             p.dx[out] = pack8(m);
             if (Y) {
                 if (VECTOR) {
-                    piece(s, 2, r);
+                    piece(2, 2, r);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (POST) d[j] = __fmul2_rn(d[j], ry);
@@ -709,12 +724,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
                 p.dy[out] = pack8(d);
             }
         }
-        __syncthreads();  // the row's stage has been read, and the next row's sums are there
-        const int64_t refill = t + static_cast<int64_t>(p.stages) * step;
-        if (tid == 0 && refill < p.T && !*abort_flag) {
-            ask(refill, s);
-            ++asked;
-        }
+        if (!kAhead && next < p.T) sum_row(it + 1, next_s, next_parity);
+        __syncthreads();  // a stage has been read by all, and the next row's sums are there
+        refill(kAhead ? t : next, kAhead ? s : next_s);
         rstd = next_rstd;
         rstd_y = next_rstd_y;
         next_rstd = later_rstd;
