@@ -466,9 +466,11 @@ dg_status_t launch_rmsnorm(const NormArgs &a, const DeviceInfo &dev, cudaStream_
     if (a.T > walk_rows(a.H)) {
         // Reads far ahead of the writes cost bandwidth: 16384 x 4096 with a post and a gate, two CTAs an SM, takes
         // 87 us with three rows in the ring, 94 with four, 101 with six (one CTA: 104).  With less arithmetic one
-        // CTA and four rows keep up: 86 us without post, against 107 with two CTAs and three rows.
-        const bool heavy = codes || a.post;
-        const WalkShape s = walk_shape(a.T, a.H, 1 + (a.y != nullptr), heavy ? 2 * kWalkThreads : kWalkThreads, heavy ? 3 : 4);
+        // CTA and four rows keep up: 86 us without post, against 107 with two CTAs and three rows; in clusters two
+        // CTAs and two rows do (16384 x 8192 164 us, with three rows 193, one CTA and four rows 188; 4000 x 16384
+        // 93, 94 and 146).
+        const bool heavy = codes || a.post, two = heavy || a.H > kWalkCols;
+        const WalkShape s = walk_shape(a.T, a.H, 1 + (a.y != nullptr), two ? 2 * kWalkThreads : kWalkThreads, heavy ? 3 : two ? 2 : 4);
         const KernelControl ctl = kernel_control();
         const NormWalkParams wp = {p, s.cols, s.stages, ctl.timeout_ns, ctl.status};
         return codes ? launch_walk_form<true>(wp, s, stream) : launch_walk_form<false>(wp, s, stream);
@@ -814,7 +816,7 @@ int64_t rmsnorm_backward_workspace(int64_t T, int64_t H, bool post, bool gate) {
 dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
     (void)dev;
     const bool y = a.y != nullptr, post = a.post != nullptr, gate = a.gate != nullptr;
-    // four rows in the ring: 16384 x 4096 with all vectors 140 us, with three 146, with six 142
+    // four rows in the ring: 16384 x 4096 with all vectors 131.5 us, with three 131.1, with six 133; 4000 x 16384 194, 195, 197
     const WalkShape s = walk_shape(a.T, a.H, 2 + y + (a.dr != nullptr), kWalkThreads, 4);
     const KernelControl ctl = kernel_control();
     NormBackwardParams p;
