@@ -14,7 +14,7 @@ using namespace dg;
 namespace {
 
 constexpr int64_t kMaxSlots = 1LL << 30;
-constexpr int64_t kMaxWidth = 16384;             // of a normed row: two CTAs hold its column sums
+constexpr int64_t kMaxWidth = 16384;             // of a normed row: four CTAs of 4096 columns
 constexpr int64_t kMaxElements = 1LL << 42;      // of a gradient: its chunks are counted with 32 bits
 constexpr int64_t kMaxTensors = 1LL << 24;
 
@@ -56,10 +56,10 @@ dg_status_t check_grads(const GradList &g) {
     return DG_OK;
 }
 
-// A tensor that is written overlaps no other one: the kernel's CTAs run in no order.  What is
+// A tensor that is written overlaps no other one, nor the norm: the kernel's CTAs run in no order.  What is
 // written is put in order and drawn together into spans with gaps of less than 4 KB; a tensor
 // that is only read seldom meets one, and only then is looked up among the written ones.
-dg_status_t check_overlap(const GradList &g) try {
+dg_status_t check_overlap(const GradList &g, const float *norm, bool norm_written) try {
     struct Range {
         uintptr_t begin, end;
     };
@@ -67,8 +67,14 @@ dg_status_t check_overlap(const GradList &g) try {
     written.reserve(static_cast<size_t>(g.count));
     auto bytes = [&](int64_t i) { return static_cast<uintptr_t>(g.sizes[i]) * (g.bf16[i] ? 2 : 4); };
     auto target = [&](int64_t i) { return reinterpret_cast<uintptr_t>(g.out ? g.out[i] : g.in[i]); };
-    for (int64_t i = 0; i < g.count; ++i)
-        if (g.sizes[i] != 0) written.push_back({target(i), target(i) + bytes(i)});
+    const uintptr_t norm_at = reinterpret_cast<uintptr_t>(norm);
+    const auto holds_norm = [&](uintptr_t begin, uintptr_t n) { return norm_at < begin + n && begin < norm_at + 4; };
+    for (int64_t i = 0; i < g.count; ++i) {
+        if (g.sizes[i] == 0) continue;
+        written.push_back({target(i), target(i) + bytes(i)});
+        if (holds_norm(target(i), bytes(i))) return DG_ERR_INVALID_ARG;
+        if (norm_written && holds_norm(reinterpret_cast<uintptr_t>(g.in[i]), bytes(i))) return DG_ERR_INVALID_ARG;
+    }
     const auto before = [](const Range &a, const Range &b) { return a.begin < b.begin; };
     if (!std::is_sorted(written.begin(), written.end(), before)) std::sort(written.begin(), written.end(), before);
     for (size_t i = 1; i < written.size(); ++i)
@@ -237,7 +243,7 @@ dg_status_t dg_grad_clip(const void *const *grads, const int64_t *sizes, const u
     if (st != DG_OK) return st;
     if (!norm || bad_limit(max_norm)) return DG_ERR_INVALID_ARG;
     if (!aligned(norm, 4)) return DG_ERR_ALIGNMENT;
-    st = check_overlap(g);
+    st = check_overlap(g, norm, false);
     if (st != DG_OK) return st;
     DeviceInfo dev;
     st = b200(&dev);
@@ -253,7 +259,7 @@ dg_status_t dg_grad_norm_clip(const void *const *grads, const int64_t *sizes, co
     if (st != DG_OK) return st;
     if (bad_limit(max_norm)) return DG_ERR_INVALID_ARG;
     st = check_norm_workspace(count, norm, workspace, workspace_bytes);
-    if (st == DG_OK) st = check_overlap(g);
+    if (st == DG_OK) st = check_overlap(g, norm, true);
     if (st != DG_OK) return st;
     DeviceInfo dev;
     st = b200(&dev);

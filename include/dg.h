@@ -671,7 +671,8 @@ int64_t dg_grad_norm_workspace(int64_t count);
  * grads.  A norm that is not finite clips nothing, so that the caller can see it and drop the
  * step.  out null: in place, and without a write where nothing is clipped.  out[i] is grads[i],
  * or a tensor of the same type and size that overlaps no other tensor of the call (written in
- * any case); tensors that are written must not overlap each other (DG_ERR_INVALID_ARG).
+ * any case); tensors that are written must not overlap each other or the norm, nor, where the
+ * norm is written too, may it lie in a tensor that is read (DG_ERR_INVALID_ARG).
  * max_norm : HOST address of the limit, read before the call returns; finite, at least 0.
  */
 dg_status_t dg_grad_clip(const void *const *grads, const int64_t *sizes, const uint8_t *bf16,

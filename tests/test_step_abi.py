@@ -133,7 +133,7 @@ def test_gradient_norm_refusals(lib):
     need = lib.dg_grad_norm_workspace(2)
     limit = ctypes.c_float(1.0)
 
-    def both(addresses, sizes, types=(0, 1), out=None, norm=P, ws=P, n=need, m=limit):
+    def both(addresses, sizes, types=(0, 1), out=None, norm=ctypes.c_void_p(0x90000), ws=P, n=need, m=limit):
         a, s, t, count = arrays(addresses, sizes, types)
         o = NULL if out is None else vp((ctypes.c_void_p * count)(*out))
         got = [lib.dg_grad_norm_clip(vp(a), vp(s), vp(t), count, vp(ctypes.pointer(m)), o, norm, ws, n, NULL),
@@ -154,7 +154,13 @@ def test_gradient_norm_refusals(lib):
     assert both([0x10000, 0x10000], [4, 4]) == ARG and both([0x10000, 0x1000E], [4, 4]) == ARG
     assert both([0x10000, 0x10008], [100, 2]) == ARG and both(ok, [4, 4], out=[0x20000, 0x30000]) == ARG
     assert both(ok, [4, 4], out=[0x10004, 0x30000]) == ARG and both(ok, [4, 4], out=[0x30000, 0x30000]) == ARG
+    # a norm inside a tensor that is written, or, where it is written itself, that is read
+    assert both(ok, [4, 4], norm=ctypes.c_void_p(0x1000C)) == ARG and both(ok, [4, 4], norm=ctypes.c_void_p(0x20004)) == ARG
+    assert both(ok, [4, 4], out=[0x30000, 0x40000], norm=ctypes.c_void_p(0x30008)) == ARG
     a, s, t, count = arrays(ok, [4, 4], [0, 1])
+    o = vp((ctypes.c_void_p * 2)(0x30000, 0x40000))
+    assert lib.dg_grad_norm_clip(vp(a), vp(s), vp(t), 2, vp(ctypes.pointer(limit)), o, ctypes.c_void_p(0x10008), P, need,
+                                 NULL) == ARG
     assert lib.dg_grad_norm(vp(a), vp(s), vp(t), -1, P, P, need, NULL) == SHAPE
     assert lib.dg_grad_norm(NULL, vp(s), vp(t), 2, P, P, need, NULL) == ARG
     assert lib.dg_grad_norm(vp(a), vp(s), vp(t), 2, P, NULL, need, NULL) == ARG
