@@ -248,7 +248,8 @@ __device__ __forceinline__ T from_cta(const T *shared, uint32_t rank) {
 }
 
 // The loss from what the threads of a cluster of CTAS hold of it, in FP64 and a fixed order; called by
-// all of them.  The CTAs' shares go to the first one, so nobody reads another CTA's memory at the end.
+// all of them, after every CTA has met the others once: the shared memory of a CTA that may not have started yet
+// must not be written.  The CTAs' shares go to the first one, so nobody reads another CTA's memory at the end.
 template <int CTAS>
 __device__ __forceinline__ void loss_of_cluster(double mine, double *warp_loss, double *cta_loss, float *loss) {
     const int warps = static_cast<int>(blockDim.x) >> 5, lane = lane_id();
@@ -550,6 +551,7 @@ __global__ void __cluster_dims__(kFinishCtas, 1, 1) __launch_bounds__(kFinishThr
     constexpr int kWarps = kFinishThreads / 32;
     __shared__ double warp_p[kWarps][32], warp_loss[kWarps], cta_loss[kFinishCtas];
     __shared__ int warp_count[kWarps][32], warp_tokens[kWarps];
+    cluster_arrive_relaxed();  // this CTA runs
     grid_dep_wait();
     grid_dep_launch_dependents();
     const int tid = static_cast<int>(threadIdx.x), lane = lane_id(), warp = tid >> 5;
@@ -606,6 +608,7 @@ __global__ void __cluster_dims__(kFinishCtas, 1, 1) __launch_bounds__(kFinishThr
         }
         __syncthreads();
     }
+    cluster_wait();  // all of them do: a CTA without experts comes here at once
     loss_of_cluster<kFinishCtas>(mine, warp_loss, cta_loss, loss);
 }
 
