@@ -465,7 +465,7 @@ def rmsnorm_residual_backward(dn, r, rstd, weight, dr=None, y=None, rstd_y=None,
 
 
 def grad_norm(grads, norm=None, stream=None):
-    """sqrt of the sum of squares over all tensors of grads (a sequence; float32 or bfloat16, contiguous):
+    """sqrt of the sum of squares over all tensors of grads (a sequence or iterator; float32 or bfloat16, contiguous):
     float32, 0-dim, on the device."""
     return (_ext or _native()).grad_norm(grads, norm, stream)
 

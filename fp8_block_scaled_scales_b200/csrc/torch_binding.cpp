@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -629,32 +630,35 @@ PyObject *rmsnorm_residual_backward(PyObject *, PyObject *const *a, Py_ssize_t) 
     END_HANDLE_TH_ERRORS
 }
 
-// A sequence of gradients as the C interface's host arrays; `out` None: in place.
-struct Grads {
+// A sequence of gradients as the C interface's host arrays; `out` None: in place.  The sequences live as long as
+// this does: of an iterable that is neither list nor tuple, nobody else may hold the tensors, and their memory must
+// not serve for the call's own outputs and scratch.
+class Grads {
+public:
     std::vector<void *> in, out;
     std::vector<int64_t> sizes;
     std::vector<uint8_t> bf16;
     int dev = -1;  // the tensors', which has to be the current one
     bool in_place = true;
 
-    Grads(PyObject *grads, PyObject *outs) {
-        const Items g(grads, "grads");
-        in.reserve(g.size), sizes.reserve(g.size), bf16.reserve(g.size);
-        for (Py_ssize_t i = 0; i < g.size; ++i) {
-            const Tensor &t = tensor(g.items[i], "a gradient");
+    // Both are iterated over before either is read: an iterator is Python code, which could change the other one.
+    Grads(PyObject *grads, PyObject *outs) : g_(grads, "grads"), o_(outs, "out", true) {
+        const Py_ssize_t n = g_.size();
+        in.reserve(n), sizes.reserve(n), bf16.reserve(n);
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            const Tensor &t = tensor(g_[i], "a gradient");
             if (i == 0) dev = device_of(t, "a gradient", t.dim());
             bf16.push_back(t.scalar_type() == kBF16);
             in.push_back(address(t, "a gradient", bf16.back() ? kBF16 : kF32));
             sizes.push_back(t.numel());
         }
-        if (g.size == 0) dev = c10::cuda::current_device();
+        if (n == 0) dev = c10::cuda::current_device();
         if (outs == Py_None) return;
         in_place = false;
-        const Items o(outs, "out");
-        TORCH_CHECK_VALUE(o.size == g.size, "out must hold ", g.size, " tensors, not ", o.size);
-        out.reserve(o.size);
-        for (Py_ssize_t i = 0; i < o.size; ++i) {
-            const Tensor &t = tensor(o.items[i], "an output"), &like = THPVariable_Unpack(g.items[i]);
+        TORCH_CHECK_VALUE(o_.size() == n, "out must hold ", n, " tensors, not ", o_.size());
+        out.reserve(n);
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            const Tensor &t = tensor(o_[i], "an output"), &like = THPVariable_Unpack(g_[i]);
             out.push_back(address(t, "an output", bf16[i] ? kBF16 : kF32));
             TORCH_CHECK_VALUE(t.sizes() == like.sizes(), "an output must have shape ", like.sizes(), ", not ", t.sizes());
         }
@@ -662,6 +666,14 @@ struct Grads {
 
     int64_t count() const { return static_cast<int64_t>(in.size()); }
     void *const *outs() const { return in_place ? nullptr : out.data(); }
+
+    // After the launch, on the call's stream: tensors that only this holds are not given out anew before its work is done.
+    void launched() const {
+        const auto stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev));
+        for (const Items *items : {&g_, &o_})
+            for (Py_ssize_t i = 0; items->ours() && i < items->size(); ++i)
+                c10::cuda::CUDACachingAllocator::recordStream(THPVariable_Unpack((*items)[i]).storage().data_ptr(), stream);
+    }
 
 private:
     // checked() without the shape: a step has hundreds of these.
@@ -673,19 +685,27 @@ private:
         return t.unsafeGetTensorImpl()->mutable_data();
     }
 
-    struct Items {  // a list or tuple, held while it is read
-        PyObject *held, **items;
-        Py_ssize_t size;
-        Items(PyObject *o, const char *name) {
+    class Items {  // the caller's list or tuple, or a list of what an iterable yields; nothing for an optional None
+    public:
+        Items(PyObject *o, const char *name, bool optional = false) {
+            if (optional && o == Py_None) return;
             TORCH_CHECK_TYPE(!THPVariable_Check(o), name, " must be a sequence of tensors");
-            held = PySequence_Fast(o, "expected a sequence of tensors");
-            if (!held) throw python_error();
-            items = PySequence_Fast_ITEMS(held);
-            size = PySequence_Fast_GET_SIZE(held);
+            held_ = PySequence_Fast(o, "expected a sequence of tensors");
+            if (!held_) throw python_error();
+            ours_ = held_ != o;
         }
-        ~Items() { Py_DECREF(held); }
+        ~Items() { Py_XDECREF(held_); }
         Items(const Items &) = delete;
+        Items &operator=(const Items &) = delete;
+        Py_ssize_t size() const { return held_ ? PySequence_Fast_GET_SIZE(held_) : 0; }
+        PyObject *operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(held_, i); }
+        bool ours() const { return ours_; }
+
+    private:
+        PyObject *held_ = nullptr;
+        bool ours_ = false;
     };
+    const Items g_, o_;
 };
 
 // (grads, norm, stream)
@@ -698,6 +718,7 @@ PyObject *grad_norm(PyObject *, PyObject *const *a, Py_ssize_t) {
     status(dg_grad_norm(g.in.data(), g.sizes.data(), g.bf16.data(), g.count(), ptr<float>(norm),
                         ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, st),
            "dg_grad_norm");
+    g.launched();
     return wrap(norm);
     END_HANDLE_TH_ERRORS
 }
@@ -710,6 +731,7 @@ PyObject *grad_clip(PyObject *, PyObject *const *a, Py_ssize_t) {
     const auto *norm = in<float>(a[1], "norm", kF32, {}, g.dev);
     const auto limit = number(a[2], "max_norm");
     status(dg_grad_clip(g.in.data(), g.sizes.data(), g.bf16.data(), g.count(), norm, &limit, g.outs(), st), "dg_grad_clip");
+    g.launched();
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -725,6 +747,7 @@ PyObject *clip_grad_norm(PyObject *, PyObject *const *a, Py_ssize_t) {
     status(dg_grad_norm_clip(g.in.data(), g.sizes.data(), g.bf16.data(), g.count(), &limit, g.outs(), ptr<float>(norm),
                              ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, st),
            "dg_grad_norm_clip");
+    g.launched();
     return wrap(norm);
     END_HANDLE_TH_ERRORS
 }

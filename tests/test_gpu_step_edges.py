@@ -1,6 +1,8 @@
 """GPU tests of routing, the norms around a block and clipping where a call is allowed but unusual:
 few experts beside other work, rows that reach no expert, extreme magnitudes, gradients given by
 an iterator."""
+import weakref
+
 import pytest
 import torch
 
@@ -44,3 +46,68 @@ def test_balance_loss_of_few_experts_beside_other_work(G):
     assert torch.equal(outs[0][2].cpu().long(), counts)
     assert ((outs[0][4].cpu().double() - dprob).abs() <= 2 * U * dprob).all()
     assert abs(float(outs[0][3]) - float(loss)) <= (2 * (2.4 * top + 4) + 40 + 2 + 34 + 2) * U * float(loss)
+
+
+class WatchedStream:
+    """A stream that counts, when a call asks for its handle, which of some tensors are still there."""
+
+    def __init__(self, stream):
+        self.stream, self.made, self.alive = stream, [], None
+
+    def yielding(self, tensors):
+        for t in tensors:
+            t = t.clone()
+            self.made.append(weakref.ref(t))
+            yield t
+            del t
+        self.stream.wait_stream(torch.cuda.current_stream())
+
+    @property
+    def cuda_stream(self):
+        self.alive = sum(r() is not None for r in self.made)
+        return self.stream.cuda_stream
+
+
+def test_gradients_that_only_an_iterator_holds():
+    """The call keeps them: their memory is neither its workspace nor its outputs, on any stream."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    # some as large as the workspace, some as the norm
+    grads = [torch.randn((n,), generator=g, device="cuda") for n in [1184] * 30 + [1, 128] * 10 + [300000]]
+    norm = binding.grad_norm(grads)
+    clipped = [torch.empty_like(t) for t in grads]
+    binding.clip_grad_norm(grads, 0.5, out=clipped)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.current_stream(), side):
+        for _ in range(5):
+            outs = [torch.zeros_like(t) for t in grads]
+            torch.cuda.synchronize()
+            w = WatchedStream(stream)
+            assert torch.equal(binding.grad_norm(w.yielding(grads), stream=w).cpu(), norm.cpu())
+            assert w.alive == len(grads) and all(r() is None for r in w.made)
+            stream.synchronize()
+            w = WatchedStream(stream)
+            binding.clip_grad_norm(w.yielding(grads), 0.5, out=(t for t in outs), stream=w)
+            assert w.alive == len(grads)
+            stream.synchronize()
+            for a, b in zip(outs, clipped):
+                assert torch.equal(a, b)
+            outs = [t.clone() for t in grads]
+            torch.cuda.synchronize()
+            binding.grad_clip(iter(outs), norm, 0.5, stream=stream)  # in place
+            stream.synchronize()
+            for a, b in zip(outs, clipped):
+                assert torch.equal(a, b)
+
+
+def test_an_iterator_that_changes_the_other_sequence():
+    grads = [torch.ones(8, device="cuda"), torch.ones(3, device="cuda")]
+    outs = [torch.zeros(8, device="cuda"), torch.zeros(3, device="cuda")]
+
+    def dropping():
+        for t in outs:
+            grads.clear()
+            yield t
+
+    with pytest.raises(ValueError):
+        binding.clip_grad_norm(grads, 1.0, out=dropping())
