@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
                     }
                     if (BALANCE) {
                         sum = warp_sum(sum);
-                        if (sum < 0x1p-80f) exponentials();  // all far below 0: ratios of exponentials
+                        // all far below 0: ratios of exponentials; with a NaN, for `top`
+                        if (!(sum >= 0x1p-80f)) exponentials();
                     }
                 } else {
                     exponentials();
@@ -427,7 +428,16 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
                 }
                 if (BALANCE) {
                     const float r = reciprocal(sum);
-                    if (top > -CUDART_INF_F) {  // for sigmoids 0, unless no expert has a score
+                    // a token that reaches no expert has no part in the loss: without a score above -inf (for
+                    // sigmoids whose sum is a number, and not 0, `top` is 0), or where the bias leaves no key
+                    bool routed = top > -CUDART_INF_F;
+                    if (BIAS) {
+                        uint32_t keys = 0u;
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) keys |= key[i];
+                        routed = __any_sync(kAll, keys != 0u);
+                    }
+                    if (routed) {
 #pragma unroll
                         for (int i = 0; i < PER; ++i) {
                             if constexpr (kSumsInRegisters)

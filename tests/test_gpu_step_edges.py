@@ -1,6 +1,7 @@
 """GPU tests of routing, the norms around a block and clipping where a call is allowed but unusual:
 few experts beside other work, rows that reach no expert, extreme magnitudes, gradients given by
 an iterator."""
+import math
 import weakref
 
 import pytest
@@ -9,9 +10,11 @@ import torch
 from fp8_block_scaled_scales_b200 import binding
 
 import plain_step as plain
-from plain_step import U
+from plain_step import BF, U
+from test_gpu_route import check, check_backward
 
 pytestmark = pytest.mark.gpu
+INF, NAN = math.inf, math.nan
 
 
 def logits(T, G, seed):
@@ -111,3 +114,51 @@ def test_an_iterator_that_changes_the_other_sequence():
 
     with pytest.raises(ValueError):
         binding.clip_grad_norm(grads, 1.0, out=dropping())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,G", [(40, 40), (60, 24), (3000, 40), (2500, 200), (700, 300), (300, 600)])
+def test_tokens_that_reach_no_expert_stay_out_of_the_balance_loss(T, G, score):
+    """Rows of nothing but NaN and -inf, and rows whose finite logits are those of experts that the bias takes out: no
+    expert, no share in the loss, no gradient; in one cluster and over the whole GPU."""
+    k = 6
+    z = logits(T, G, T + G)
+    gone = torch.arange(G) % 5 == 2        # by their bias
+    z[3] = NAN
+    z[5, ::2], z[5, 1::2] = NAN, -INF
+    z[7] = -INF
+    z[9, ~gone] = -INF                     # finite only where the bias takes the expert out
+    z[11, ~gone] = -INF
+    z[11, 2] = 80.0                        # a large share of one expert
+    z[13, ~gone] = -INF
+    z[13, 4] = 0.25                        # one expert is left
+    z[15, gone] = -INF
+    bias = (torch.rand((G,), generator=torch.Generator().manual_seed(G)) - 0.5) * 0.3
+    bias[gone] = -INF
+    bias[7] = NAN
+    mask = torch.arange(T) % 11 != 4
+    dw = torch.randn((T, k), generator=torch.Generator().manual_seed(T))
+    for kw in (dict(), dict(renormalize=False, mask=mask), dict(bias=bias), dict(bias=bias, mask=mask, renormalize=False, scale=2.5)):
+        ids = check(z, k, score, **kw)
+        none = [3, 5, 7] + ([9, 11] if "bias" in kw else [])
+        assert (ids.cpu()[none] == -1).all()
+        dz = check_backward(z, k, score, kw.get("renormalize", True), dw, mask=kw.get("mask"), ids=ids)
+        assert not dz.cpu()[none].any()
+    # nothing but such rows
+    lost = z[[3, 5, 7, 9, 11]].repeat(T // 5, 1)
+    ids, w, counts, loss, dprob = binding.moe_route(lost.cuda(), k, score=score, bias=bias.cuda(), balance=True)
+    assert bool((ids == -1).all()) and not w.any() and not counts.any() and not dprob.any() and float(loss) == 0.0
+    # a softmax's sum is NaN with a single NaN, and with a bias so are all keys
+    if score == "softmax":
+        one = z.clone()
+        one[20, 1] = NAN
+        got = binding.moe_route(one.cuda(), k, bias=bias.cuda(), balance=True)
+        without = torch.arange(T) != 20
+        want = binding.moe_route(z.cuda(), k, bias=bias.cuda(), mask=without.cuda(), balance=True)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        assert (got[0][20] == -1).all() and bool(torch.isfinite(got[3]))
+    # a row that reaches an expert and has a NaN: by the definition the loss has one too
+    z[20, 1] = NAN
+    ids, _, _, loss, _ = binding.moe_route(z.cuda(), k, score=score, balance=True)
+    assert int(ids[20, 0]) >= 0 and bool(torch.isnan(loss))
