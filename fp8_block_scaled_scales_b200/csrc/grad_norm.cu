@@ -178,6 +178,9 @@ __global__ void __launch_bounds__(kNormThreads) grad_clip_kernel(const __grid_co
     const float n = part ? norm_of(part, parts, red) : *norm;
     if (part && write && blockIdx.x == 0 && tid == 0) *norm = n;
     const float coef = n > max_norm && n <= 3.402823466e38f ? __fdiv_rn(max_norm, n) : 1.0f;
+    // a subnormal quotient has lost bits that the product still needs: FP64 then, element by element
+    const bool tiny = coef < 0x1p-126f && max_norm > 0.0f;
+    const double ratio = tiny ? static_cast<double>(max_norm) / static_cast<double>(n) : 0.0;
     for (int c = t.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= static_cast<int>(gridDim.x)) {
         const Chunk k = find_chunk(t, c);
         if (coef == 1.0f && k.in == k.out) continue;
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(kNormThreads) grad_clip_kernel(const __grid_co
         const uint8_t *in = static_cast<const uint8_t *>(k.in) + k.first * size;
         uint8_t *out = static_cast<uint8_t *>(k.out) + k.first * size;
         int done = 0;
-        if (((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
+        if (!tiny && ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
             const uint4 *v = reinterpret_cast<const uint4 *>(in);
             uint4 *o = reinterpret_cast<uint4 *>(out);
             const int pieces = k.count / per;
@@ -208,7 +211,8 @@ __global__ void __launch_bounds__(kNormThreads) grad_clip_kernel(const __grid_co
             done = pieces * per;
         }
         for (int i = done + tid; i < k.count; i += kNormThreads) {
-            const float x = element(k, k.first + i) * coef;
+            float x = element(k, k.first + i);
+            x = tiny ? static_cast<float>(x * ratio) : x * coef;
             if (k.bf16)
                 reinterpret_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16(x);
             else

@@ -162,3 +162,30 @@ def test_tokens_that_reach_no_expert_stay_out_of_the_balance_loss(T, G, score):
     z[20, 1] = NAN
     ids, _, _, loss, _ = binding.moe_route(z.cuda(), k, score=score, balance=True)
     assert int(ids[20, 0]) >= 0 and bool(torch.isnan(loss))
+
+
+@pytest.mark.parametrize("norm,limit", [(2e38, 1e-3), (1e38, 1e-8), (3e30, 2e-9), (1e20, 1e-30), (1e25, 1e-40), (1e-3, 1e-42),
+                                        (2e38, 1e-38), (1e38, 0.0), (1e38, 2.0)])
+def test_clipping_by_factors_beyond_float32(norm, limit):
+    """max_norm / norm below the smallest normal number: the clipped gradients are ordinary numbers all the same."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    sizes = [9000, 1, 300000, 4099, 64]
+    ts = [torch.randn((n + 1,), generator=g, device="cuda") for n in sizes]
+    ts = [t * (norm / math.sqrt(sum(sizes))) for t in ts]
+    ts = [t.to(torch.bfloat16) if i % 2 else t for i, t in enumerate(ts)]
+    ts = [t[1:] if i == 3 else t[:-1] for i, t in enumerate(ts)]
+    want = math.sqrt(sum(float((t.double() ** 2).sum()) for t in ts))
+    coef = min(1.0, float(torch.tensor(limit)) / want)  # the limit as float32
+    outs = [torch.full_like(t, 7.0) for t in ts]
+    n = binding.clip_grad_norm(ts, limit, out=outs)
+    # 32 squares are added in float32, a root of these, a rounding
+    assert abs(float(n) - want) <= 20 * U * want
+    for t, o in zip(ts, outs):
+        ref = t.double() * coef
+        half, least = (BF, 2.0 ** -134) if t.dtype == torch.bfloat16 else (U, 2.0 ** -150)  # least: half a subnormal step
+        assert ((o.double() - ref).abs() <= (20 * U + 3 * U + half) * ref.abs() + 2 * least).all()
+    mine, again = [t.clone() for t in ts], [t.clone() for t in ts]
+    binding.clip_grad_norm(mine, limit)
+    binding.grad_clip(again, n, limit)
+    for a, b, c in zip(outs, mine, again):
+        assert torch.equal(a, b) and torch.equal(a, c)
