@@ -520,8 +520,8 @@ __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
 // vectors and the per-column sums stay in registers; rows come through a ring of bulk copies.
 // The loop takes a row's sums one iteration before it uses them, so that one barrier a row
 // publishes the next row's sums and frees a stage.  A row's pieces stay in registers from its sums to its outputs,
-// and the next row's are read behind these (16384 x 4096: 140 -> 131 us, 8192 x 8192 156 -> 147); clusters of
-// four take the next row's sums first and read the row at hand from the ring once more, so that the shares' way
+// and the next row's are read behind these (16384 x 4096: 133 us, 8192 x 8192 150; a second read of the ring cost 9 us of
+// either); clusters of four take the next row's sums first and read the row at hand from the ring once more, so that the shares' way
 // passes under its arithmetic (4000 x 16384: 201 us as in smaller clusters, 190 so).  In a cluster each warp
 // stores its share into every CTA asynchronously, counted by that CTA's barrier of the row's parity: the
 // cluster's own barrier would wait for the row's stores to global memory (8192 x 8192: 232 us with it).  A share of row
@@ -593,7 +593,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
         for (; asked < p.stages && first + static_cast<int64_t>(asked) * step < p.T; ++asked)
             ask(first + static_cast<int64_t>(asked) * step, asked);
 
-    uint4 held[4];  // the thread's pieces of the row whose sums were taken last: dn, r, y, dr
+    uint4 held[4];     // the thread's pieces of the row whose sums were taken last: dn, r, y, dr
+    float2 held_g[4];  // and dn w
     auto take = [&](int s, int array) { return reinterpret_cast<const uint4 *>(ring + s * stage_bytes + array * row_bytes)[tid]; };
     // the warp's share of a row's sums (g r, dr q, g q, r q), to every CTA of the cluster
     auto sum_row = [&](int it, int s, uint32_t parity) {
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
             held[1] = take(s, 1);
             if (Y) held[2] = take(s, 2);
             if (p.dr) held[3] = take(s, 2 + Y);
-            float2 g[4], r[4];
+            float2 r[4], (&g)[4] = held_g;
             bf16x8_to_f32(held[0], g);
             bf16x8_to_f32(held[1], r);
 #pragma unroll
@@ -642,7 +643,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
                 store_share(word, v, &shared_sums[it & 1], lane & 7);
         }
     };
-    float back = 0.0f, back_y = 0.0f;  // -rstd^2 c1 and -rstd_y^2 c2 of the row
+    // -c1 and -c2 of the row.  They and the normed rows rh and yh are of the size of what they are made from.  rstd^2 c1
+    // in their place saves a product an element and sum (16384 x 4096 131.6 us against 132.7, 8192 x 8192 147 against
+    // 149), but it leaves FP32 in rows whose mean square FP32 holds (from an RMS of 1e13 on, and below 1e-13).
+    float back = 0.0f, back_y = 0.0f;
     const float inv_h = 1.0f / static_cast<float>(p.H);
     auto read_sums = [&](int it, float rstd, float rstd_y) {  // in the same order in every warp and CTA
         if (CTAS > 1 && !mbar_wait(&shared_sums[it & 1], static_cast<uint32_t>(it >> 1) & 1u, abort_flag, p.timeout_ns)) {
@@ -659,10 +663,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
         v *= inv_h;
-        back = -rstd * rstd * rstd * __shfl_sync(0xFFFFFFFFu, v, 0);
+        back = -rstd * __shfl_sync(0xFFFFFFFFu, v, 0);
         if (POST) {
             const float dq = __shfl_sync(0xFFFFFFFFu, v, 8), gq = __shfl_sync(0xFFFFFFFFu, v, 16), rq = __shfl_sync(0xFFFFFFFFu, v, 24);
-            back_y = -rstd_y * rstd_y * rstd_y * fmaf(back, rq, fmaf(rstd, gq, dq));
+            back_y = -rstd_y * fmaf(rstd, fmaf(back, rstd * rq, gq), dq);
         }
     };
     auto scale_of_row = [&](const float *v, int64_t t) { return t < p.T ? __ldg(v + t) : 0.0f; };
@@ -705,10 +709,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                m[j] = __fmul2_rn(m[j], rs);
+                r[j] = __fmul2_rn(r[j], rs);  // rh
                 acc_w[j] = __ffma2_rn(m[j], r[j], acc_w[j]);
-                d[j] = __ffma2_rn(m[j], w[j], d[j]);
-                d[j] = __ffma2_rn(r[j], back2, d[j]);  // dR
+                m[j] = __ffma2_rn(r[j], back2, kAhead ? __fmul2_rn(m[j], w[j]) : held_g[j]);
+                d[j] = __ffma2_rn(m[j], rs, d[j]);  // dR
                 m[j] = __fmul2_rn(d[j], alpha2);
             }
             p.dx[out] = pack8(m);
@@ -717,10 +721,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) rmsnorm_backward_kernel(const
                     piece(2, 2, r);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (POST) d[j] = __fmul2_rn(d[j], ry);
+                        if (POST) r[j] = __fmul2_rn(r[j], ry);  // yh
                         acc_e[j] = __ffma2_rn(d[j], r[j], acc_e[j]);
                         d[j] = __fmul2_rn(d[j], gp[j]);
-                        if (POST) d[j] = __ffma2_rn(r[j], back_y2, d[j]);
+                        if (POST) d[j] = __fmul2_rn(__ffma2_rn(r[j], back_y2, d[j]), ry);
                     }
                 }
                 p.dy[out] = pack8(d);

@@ -189,3 +189,52 @@ def test_clipping_by_factors_beyond_float32(norm, limit):
     binding.grad_clip(again, n, limit)
     for a, b, c in zip(outs, mine, again):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+NORM_FORMS = [(False, False, False), (True, False, False), (True, True, False), (True, False, True), (True, True, True)]
+
+
+@pytest.mark.parametrize("H", [16, 256, 784, 4096, 8192, 16384])
+@pytest.mark.parametrize("y,post,gate", NORM_FORMS)
+@pytest.mark.parametrize("grad", [1.0, 1e-6])
+@pytest.mark.parametrize("small", [True, False])
+def test_norm_gradient_of_rows_of_any_magnitude(H, y, post, gate, grad, small):
+    """Rows whose mean square float32 holds: rstd^3 does not have to lie in float32, nor rstd^2 times a small gradient."""
+    T, alpha, eps = 44, 0.5 if y else 1.0, 0.0 if small else 1e-6
+    g = torch.Generator().manual_seed(H)
+    sign = -1 if small else 1
+    powers = torch.tensor([0, 6, 10, 12, 13, 14, 15, 15.5, 16, 16.5, 17])
+    scale_r = 10.0 ** (sign * powers.repeat_interleave(4))
+    scale_y = 10.0 ** (sign * powers.repeat(4))
+
+    def rows(std, scale):
+        return (torch.randn((T, H), generator=g) * std * scale[:, None]).to(torch.bfloat16).cuda()
+
+    def vector(mean):
+        return (mean + 0.3 * torch.randn((H,), generator=g)).cuda()
+
+    one = torch.ones(T)
+    # without a norm of its own y is no larger than the rest
+    r, Y = rows(1.0, scale_r), rows(0.7, scale_y if post else one) if y else None
+    dn, dr = rows(grad, one), rows(grad, one / scale_r.double()) if H % 3 else None
+    w, P, A = vector(1.0), vector(1.0) if post else None, vector(0.5) if gate else None
+
+    def rstd_of(v):
+        return ((v.double() ** 2).mean(1) + eps).pow(-0.5).float()
+
+    rstd, rstd_y = rstd_of(r), rstd_of(Y) if post else None
+    got = binding.rmsnorm_residual_backward(dn, r, rstd, w, dr=dr, y=Y, rstd_y=rstd_y, gate=A, post_weight=P, alpha=alpha)
+
+    def d(t):
+        return None if t is None else t.double()
+
+    want = plain.norm_backward(d(dn), d(dr), d(r), d(rstd), d(Y), d(rstd_y), d(w), d(P), d(A), alpha)
+    for name, t in zip(("dx", "dy", "dweight", "dgate", "dpost_weight"), got):
+        assert (t is not None) == (name in want), name
+        if t is None:
+            continue
+        ref, bound = want[name]
+        half, least = (BF, 2.0 ** -134) if t.dtype == torch.bfloat16 else (U, 2.0 ** -150)
+        assert bool(torch.isfinite(t).all()), name
+        # the bounds count roundings of normal numbers; what is subnormal in the output is rounded to its step
+        assert ((t.double() - ref).abs() <= bound * (1 + half) + half * ref.abs() + least).all(), name
