@@ -794,8 +794,8 @@ __global__ void __launch_bounds__(512) rmsnorm_columns_kernel(const float *__res
             dweight[c] = s;
         } else {
             const int64_t h = c - H;
-            auto times = [&](const void *v) {  // one element of a vector, or 1
-                if (!v) return 1.0f;
+            auto times = [&](const void *v) {  // one element of a vector, or 1; no rows: the sum is 0 whatever that holds
+                if (!v || parts == 0) return 1.0f;
                 return vec_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(v)[h]) : static_cast<const float *>(v)[h];
             };
             if (dgate) dgate[h] = s * times(post);

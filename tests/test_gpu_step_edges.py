@@ -238,3 +238,14 @@ def test_norm_gradient_of_rows_of_any_magnitude(H, y, post, gate, grad, small):
         assert bool(torch.isfinite(t).all()), name
         # the bounds count roundings of normal numbers; what is subnormal in the output is rounded to its step
         assert ((t.double() - ref).abs() <= bound * (1 + half) + half * ref.abs() + least).all(), name
+
+
+def test_norm_gradient_of_no_rows_is_zero_whatever_the_vectors_hold():
+    x, w = torch.zeros((0, 256), dtype=torch.bfloat16, device="cuda"), torch.ones(256, device="cuda")
+    bad = torch.full((256,), INF, device="cuda")
+    bad[::2] = NAN
+    stat = torch.zeros(0, device="cuda")
+    outs = [torch.full((256,), 7.0, device="cuda") for _ in range(3)]
+    binding.rmsnorm_residual_backward(x, x, stat, bad, y=x, rstd_y=stat, gate=bad, post_weight=bad, dweight=outs[0],
+                                      dgate=outs[1], dpost_weight=outs[2])
+    assert not any(bool((t != 0).any()) for t in outs)
