@@ -644,9 +644,10 @@ public:
     // Both are iterated over before either is read: an iterator is Python code, which could change the other one.
     Grads(PyObject *grads, PyObject *outs) : g_(grads, "grads"), o_(outs, "out", true) {
         const Py_ssize_t n = g_.size();
+        PyObject *const *const g = g_.items();
         in.reserve(n), sizes.reserve(n), bf16.reserve(n);
         for (Py_ssize_t i = 0; i < n; ++i) {
-            const Tensor &t = tensor(g_[i], "a gradient");
+            const Tensor &t = tensor(g[i], "a gradient");
             if (i == 0) dev = device_of(t, "a gradient", t.dim());
             bf16.push_back(t.scalar_type() == kBF16);
             in.push_back(address(t, "a gradient", bf16.back() ? kBF16 : kF32));
@@ -657,8 +658,9 @@ public:
         in_place = false;
         TORCH_CHECK_VALUE(o_.size() == n, "out must hold ", n, " tensors, not ", o_.size());
         out.reserve(n);
+        PyObject *const *const o = o_.items();
         for (Py_ssize_t i = 0; i < n; ++i) {
-            const Tensor &t = tensor(o_[i], "an output"), &like = THPVariable_Unpack(g_[i]);
+            const Tensor &t = tensor(o[i], "an output"), &like = THPVariable_Unpack(g[i]);
             out.push_back(address(t, "an output", bf16[i] ? kBF16 : kF32));
             TORCH_CHECK_VALUE(t.sizes() == like.sizes(), "an output must have shape ", like.sizes(), ", not ", t.sizes());
         }
@@ -669,10 +671,11 @@ public:
 
     // After the launch, on the call's stream: tensors that only this holds are not given out anew before its work is done.
     void launched() const {
+        if (!g_.ours() && !o_.ours()) return;
         const auto stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev));
-        for (const Items *items : {&g_, &o_})
-            for (Py_ssize_t i = 0; items->ours() && i < items->size(); ++i)
-                c10::cuda::CUDACachingAllocator::recordStream(THPVariable_Unpack((*items)[i]).storage().data_ptr(), stream);
+        for (const Items *list : {&g_, &o_})
+            for (Py_ssize_t i = 0; list->ours() && i < list->size(); ++i)
+                c10::cuda::CUDACachingAllocator::recordStream(THPVariable_Unpack(list->items()[i]).storage().data_ptr(), stream);
     }
 
 private:
@@ -698,7 +701,7 @@ private:
         Items(const Items &) = delete;
         Items &operator=(const Items &) = delete;
         Py_ssize_t size() const { return held_ ? PySequence_Fast_GET_SIZE(held_) : 0; }
-        PyObject *operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(held_, i); }
+        PyObject *const *items() const { return held_ ? PySequence_Fast_ITEMS(held_) : nullptr; }
         bool ours() const { return ours_; }
 
     private:
