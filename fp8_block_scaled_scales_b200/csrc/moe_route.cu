@@ -247,6 +247,12 @@ __device__ __forceinline__ T from_cta(const T *shared, uint32_t rank) {
     return v;
 }
 
+// The cluster's barrier in two parts, where the other CTAs only have to have started: nothing written before the first
+// part is visible after the second.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // The loss from what the threads of a cluster of CTAS hold of it, in FP64 and a fixed order; called by
 // all of them, after every CTA has met the others once: the shared memory of a CTA that may not have started yet
 // must not be written.  The CTAs' shares go to the first one, so nobody reads another CTA's memory at the end.
