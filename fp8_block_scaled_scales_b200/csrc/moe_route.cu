@@ -323,7 +323,8 @@ __device__ __forceinline__ void finish_in_cluster(const RouteParams &p, const fl
 // by more than those (and, with a bias, by more than the key's own FP32 error); otherwise (a token
 // in thirty) the candidates are put in order by FP64 keys.  BF16 logits without a bias have the bits to spare.
 // Bound by instruction issue, most of it the sort and the k + 1 rounds: 16384 tokens x 256 experts, k = 8,
-// FP32 sigmoid scores 10.7 us, with balance loss 15.4, with bias too 18.7 (the logits alone: 2.6); over 512 experts 31, 42 and 54.
+// FP32 sigmoid scores 11.0 us, with balance loss 15.8, with bias too 19.0 (the logits alone: 2.6); over 512 experts 32, 42 and 51, over 1024 98, 116 and 159.
+// The last of these forms spills 92 and 116 bytes at 256 experts (the loss's sums live beside the keys); past 512 every form spills.
 constexpr int route_max_threads(int per) { return per <= 8 ? 1024 : 512; }
 
 template <int PER, bool BIAS, bool BALANCE, bool CLUSTER>
@@ -476,9 +477,13 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
             auto unsettled = [&](uint32_t a, uint32_t b) {
                 if (b == 0u) return false;
                 if (!BIAS) return (a ^ b) <= kIdBits;
-                // keys are off by less than 2^-18 max(s, |key|), s the row's largest score (1 for sigmoids):
-                // 2^-21 of s in a score (37 additions of softmax's sum among them, and an exponential's error,
-                // which grows slower than the exponential falls) and a rounding of s + b
+                // s: the row's largest score (1 for sigmoids).  Two keys' difference is off by less than 2^-17.8 of s:
+                // - softmax's sum and its reciprocal move both scores alike, so that the difference of the scores takes
+                //   their error: 37 additions and a unit, 2^-18.7, and the exponentials', 2 + 1.7 |x| units with the rounding
+                //   of x = z - top, averaged over the sum, where |x| is 4.5 at most (1024 experts): 2^-19.7;
+                // - each score alone is off by 2 units of s (an exponential falls faster than its error grows; for
+                //   sigmoids (2 + 1.2 |z|) s (1 - s) units, a sum and a reciprocal), 2^-21 for both keys;
+                // and by a rounding of each s + b, 2^-23 of the larger key for both
                 const float x = from_ordered(a & ~kIdBits), y = from_ordered(b | kIdBits);
                 const float s = p.sigmoid ? 1.0f : reciprocal(sum);
                 return !(x - y > 0x1p-17f * fmaxf(s, fabsf(x)));  // infinite keys too
@@ -491,10 +496,10 @@ __global__ void __launch_bounds__(route_max_threads(PER)) route_kernel(const Rou
                     // more candidates, until the next one certainly comes after them
                     while (p.k < p.G && found < 32 && unsettled(prev, last)) next();
                     const int n = p.k == p.G ? p.k : found - 1;
-                    const uint32_t held = __ballot_sync(kAll, lane < n && mine != 0u);
+                    const uint32_t candidates = __ballot_sync(kAll, lane < n && mine != 0u);
                     id = static_cast<int>(kIdBits - (mine & kIdBits));
                     if (p.k == p.G || !unsettled(prev, last))
-                        id = order_exactly<BIAS>(p.logits, p.bias, row, p.G, p.bf16, p.sigmoid, id, __popc(held));
+                        id = order_exactly<BIAS>(p.logits, p.bias, row, p.G, p.bf16, p.sigmoid, id, __popc(candidates));
                     else
                         id = choose_exactly<PER, BIAS>(p.logits, p.bias, row, p.G, p.k, p.bf16, p.sigmoid);
                     if (lane >= p.k) id = -1;

@@ -13,6 +13,8 @@
 //     c1 = rstd mean(g r),  c2 = rstd_y (mean(dr q) + rstd mean(g q) - rstd^2 c1 mean(r q)),
 //   all four sums come out of one reduction.  dgate and dpost have one sum in common:
 //     E = sum_t dR yh,  dgate = post E,  dpost = gate E   (yh = y without post).
+// The two forward kernels round alike in kind but not in order: a CTA a row multiplies u by post and gate one after the
+// other and divides by H, walking CTAs hold gate * post and 1 / H, and their sums run over other threads' shares.
 #include <cuda_bf16.h>
 
 #include "dg_device.cuh"
@@ -441,7 +443,10 @@ static dg_status_t launch_walk_form(const NormWalkParams &p, const WalkShape &s,
 
 // Above this many rows they are walked over.  A CTA a row has no ring to fill first: 1500 x 1024 with post and gate
 // as codes 5.3 us against 6.9 walked over, 700 x 256 3.1 against 4.5, about the same from 3000 rows on.  Of wider
-// rows fewer run at once: 601 x 7168 17 us against 13, 1000 x 2048 8.1 against 7.3.
+// rows fewer run at once, and the forms cross earlier, between 160 and 300 rows with post and gate: 601 x 7168 as codes 17 us
+// against 13 walked over, 300 x 7168 9.8 and 8.4, 300 x 4096 7.3 and 6.7, 160 x 4096 4.0 and 5.1; without them 300 x 4096
+// 5.2 and 4.8, 500 x 7168 8.2 and 9.5, 500 x 16384 16.2 and 18.2.  The bound is the row count from which the walk
+// is no slower in any of them but wide rows without vectors; a finer one would have to follow the form too.
 static int64_t walk_rows(int64_t H) { return H <= 1024 ? 3000 : 600; }
 
 dg_status_t launch_rmsnorm(const NormArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
@@ -821,6 +826,7 @@ dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo 
     (void)dev;
     const bool y = a.y != nullptr, post = a.post != nullptr, gate = a.gate != nullptr;
     // four rows in the ring: 16384 x 4096 with all vectors 131.5 us, with three 131.1, with six 133; 4000 x 16384 194, 195, 197
+    // (with two products a row fewer than now)
     const WalkShape s = walk_shape(a.T, a.H, 2 + y + (a.dr != nullptr), kWalkThreads, 4);
     const KernelControl ctl = kernel_control();
     NormBackwardParams p;

@@ -558,7 +558,10 @@ typedef struct {
  *   loss = sum_e dprob[e] * sum_t p[t][e],
  * that is G * sum_e (share of the n * k slots) * (mean p); 1 when both are even.  dprob is the
  * gradient of loss with respect to every p[t][e] (counts have none), as
- * dg_moe_route_backward takes it.
+ * dg_moe_route_backward takes it.  A token that reaches no expert adds nothing to any of them.
+ * FP32 arithmetic; the order of the keys is exact.  Weights come from library exponentials and quotients; p, and 1 - s in
+ * the gradient, from the hardware's exponential and reciprocal, which are off by up to (4 + 1.7 |x|) * 2^-23 of their
+ * value at a distance x (of z from the row's largest, or from 0 for sigmoids).
  *
  * logits : [T][G] FP32, or BF16 when logits_bf16 is not 0; aligned to its type.
  * bias   : FP32 [G] or null.        mask : bytes [T] or null; 0 leaves the token out.
@@ -597,7 +600,10 @@ dg_status_t dg_moe_route_backward(const void *logits, int logits_bf16, const dg_
  *   u = Y * rstd_y * post,  rstd_y[t] = 1 / sqrt(mean_h Y[t]^2 + eps)   (post null: u = Y)
  *   r = alpha * X + gate * u                                            (gate null: of ones)
  *   N = r * rstd * weight,  rstd[t] = 1 / sqrt(mean_h r[t]^2 + eps)
- * in FP32; R is r rounded to BF16, N is computed from r before that rounding.
+ * in FP32; R is r rounded to BF16, N is computed from r before that rounding.  The sums of squares are FP32 too: they have
+ * to lie in it (an RMS up to 1e19 / sqrt(H); with an eps of 0 from 1e-18 on).  Few rows and many are taken by two
+ * kernels whose roundings differ in order, so a row's last bits may depend on how many rows the call has, never on what
+ * the others hold.
  * Y null (before the first block): r = X; R, post, gate and rstd_y must be null and alpha 1.
  *
  * X_bf16, Y_bf16 : [T][H] BF16.   weight, post, gate : [H].   N_bf16 : [T][H] BF16 out.   R_bf16 : [T][H] BF16 out; R may be X.
@@ -650,8 +656,9 @@ dg_status_t dg_rmsnorm_residual_backward(const void *dN_bf16, const void *dR_bf1
 int64_t dg_rmsnorm_residual_backward_workspace(int64_t T, int64_t H, int has_post, int has_gate);
 
 /*
- * The global norm of a step's gradients, sqrt(sum over all tensors of sum g^2): squares are
- * taken in FP32 where that loses nothing, else in FP64, and added up in FP64 in a fixed order,
+ * The global norm of a step's gradients, sqrt(sum over all tensors of sum g^2): up to 32 squares at
+ * a time are added in FP32 where they neither overflow nor vanish there (the norm is then off by less than 2^-19 of
+ * itself), else in FP64, and the rest in FP64 in a fixed order,
  * so a finite norm does not overflow on the way.  A NaN or an infinity in a gradient shows in it.
  *
  * grads, sizes, bf16 : HOST arrays of `count` device addresses, element counts and types (0 FP32,
@@ -668,8 +675,8 @@ int64_t dg_grad_norm_workspace(int64_t count);
 
 /*
  * Clipping by a norm (device): out = grads * (max_norm / norm) where norm > max_norm, else
- * grads.  A norm that is not finite clips nothing, so that the caller can see it and drop the
- * step.  out null: in place, and without a write where nothing is clipped.  out[i] is grads[i],
+ * grads.  A norm that is not finite (that of finite gradients past FP32's largest number too) clips nothing, so
+ * that the caller can see it and drop the step.  A factor below FP32's smallest normal number is taken in FP64.  out null: in place, and without a write where nothing is clipped.  out[i] is grads[i],
  * or a tensor of the same type and size that overlaps no other tensor of the call (written in
  * any case); tensors that are written must not overlap each other or the norm, nor, where the
  * norm is written too, may it lie in a tensor that is read (DG_ERR_INVALID_ARG).
