@@ -826,7 +826,7 @@ dg_status_t launch_rmsnorm_backward(const NormBackwardArgs &a, const DeviceInfo 
     (void)dev;
     const bool y = a.y != nullptr, post = a.post != nullptr, gate = a.gate != nullptr;
     // four rows in the ring: 16384 x 4096 with all vectors 131.5 us, with three 131.1, with six 133; 4000 x 16384 194, 195, 197
-    // (with two products a row fewer than now)
+    // (measured with rstd^2 c1 and rstd_y^2 c2 in place of c1 and c2)
     const WalkShape s = walk_shape(a.T, a.H, 2 + y + (a.dr != nullptr), kWalkThreads, 4);
     const KernelControl ctl = kernel_control();
     NormBackwardParams p;
